@@ -90,6 +90,84 @@ _SIGS = {
                                      _c_vp, _c_sz]),
 }
 
+
+
+# --- host structs of the serving operators (same members as include/gguf_mm.h) ---
+
+GGUF_ROPE_NORM, GGUF_ROPE_NEOX = 0, 1
+
+
+def _dt_of(t):
+    import torch
+    return {torch.float32: GGUF_DT_F32, torch.float16: GGUF_DT_F16, torch.bfloat16: GGUF_DT_BF16}[t.dtype]
+
+
+class gguf_kv_cache(ctypes.Structure):
+    """A layer's paged cache from two tensors [page, head, slot, dim] of any strides whose last is 1."""
+    _fields_ = [("k", _c_vp), ("v", _c_vp), ("dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("n_pages", _c_i64),
+                ("page_stride", _c_i64), ("head_stride", _c_i64), ("token_stride", _c_i64)]
+
+    def __init__(self, k, v):
+        if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.dim() != 4 or k.stride(3) != 1:
+            raise ValueError("k and v are [page, head, slot, dim] tensors of one type and the same strides, the last 1")
+        n, h, p, d = k.shape
+        super().__init__(k.data_ptr(), v.data_ptr(), _dt_of(k), p, h, d, n, k.stride(0), k.stride(1), k.stride(2))
+        self._keep = (k, v)
+        self._ref = ctypes.addressof(self)
+
+
+class gguf_kv_batch(ctypes.Structure):
+    """A ragged batch: q_start [n_seq + 1], kv_len [n_seq], pages [n_seq, width] (int32 tensors on the device)."""
+    _fields_ = [("q_start", _c_vp), ("kv_len", _c_vp), ("pages", _c_vp), ("n_seq", _c_i64), ("n_tokens", _c_i64),
+                ("pages_stride", _c_i64), ("max_q_len", _c_i64), ("max_kv_len", _c_i64)]
+
+    def __init__(self, q_start, kv_len, pages, n_tokens, max_q_len, max_kv_len):
+        if q_start.numel() != kv_len.numel() + 1 or pages.shape[0] != kv_len.numel() or pages.stride(1) != 1:
+            raise ValueError("q_start has one entry more than kv_len, and pages a row of stride 1 for each sequence")
+        for t in (q_start, kv_len, pages):
+            if "int32" not in str(t.dtype):
+                raise ValueError("q_start, kv_len and pages are int32")
+        stride = pages.stride(0) if pages.shape[0] > 1 else pages.shape[1]
+        super().__init__(_p(q_start), _p(kv_len), _p(pages), kv_len.numel(), n_tokens, stride, max_q_len, max_kv_len)
+        self._keep = (q_start, kv_len, pages)
+        self._ref = ctypes.addressof(self)
+
+
+class gguf_rope(ctypes.Structure):
+    """Rotary positions: freqs f32 [rot_dim / 2] in radians a position, positions int32 [n_tokens] or None."""
+    _fields_ = [("freqs", _c_vp), ("positions", _c_vp), ("rot_dim", ctypes.c_int32), ("style", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+    def __init__(self, freqs, rot_dim, style=GGUF_ROPE_NORM, scale=1.0, positions=None):
+        super().__init__(_p(freqs), _p(positions), rot_dim, style, scale)
+        self._keep = (freqs, positions)
+        self._ref = ctypes.addressof(self)
+
+
+class gguf_logit_rules(ctypes.Structure):
+    """Rules on a batch of logits; what is None is not used."""
+    _fields_ = [("hist", _c_vp), ("hist_start", _c_vp), ("repeat", _c_vp), ("frequency", _c_vp), ("presence", _c_vp),
+                ("bias_ids", _c_vp), ("bias", _c_vp), ("bias_start", _c_vp), ("allow", _c_vp), ("allow_stride", _c_i64)]
+
+    def __init__(self, hist=None, hist_start=None, repeat=None, frequency=None, presence=None, bias_ids=None, bias=None,
+                 bias_start=None, allow=None):
+        stride = 0 if allow is None else allow.stride(0) if allow.shape[0] > 1 else allow.shape[1]
+        super().__init__(*(_p(t) for t in (hist, hist_start, repeat, frequency, presence, bias_ids, bias, bias_start,
+                                           allow)), stride)
+        self._keep = (hist, hist_start, repeat, frequency, presence, bias_ids, bias, bias_start, allow)
+        self._ref = ctypes.addressof(self)
+
+
+_SIGS.update({
+    "gguf_kv_append": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_vp, _c_vp, _c_vp,
+                                _c_vp, _c_i64, _c_vp]),
+    "gguf_paged_attn": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_vp, ctypes.c_float, _c_int, _c_i64, _c_vp, _c_i64,
+                                 _c_vp, _c_vp, _c_sz, _c_vp]),
+    "gguf_paged_attn_workspace_size": (_c_sz, [_c_vp, _c_vp, _c_i64]),
+    "gguf_logits_adjust": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_int, _c_i64, _c_vp]),
+})
+
 _lib = None
 
 
@@ -260,6 +338,34 @@ def gguf_mm_debug_moe_mv_terms(w_experts, qtype, n_expert, N, K, x, xdt, T, ids,
 
 def gguf_mm_debug_timeout(spin_limit, stream=None):
     return _check("gguf_mm_debug_timeout", load_library().gguf_mm_debug_timeout(spin_limit, _s(stream)))
+
+
+# --- serving operators --------------------------------------------------------
+
+def _ref(struct):
+    return None if struct is None else struct._ref
+
+
+def gguf_kv_append(q, ldq, k, ldk, v, ldv, xdt, heads, rope, batch, cache, q_out, ldqo, stream=None):
+    return _check("gguf_kv_append", load_library().gguf_kv_append(
+        _p(q), ldq, _p(k), ldk, _p(v), ldv, xdt, heads, _ref(rope), _ref(batch), _ref(cache), _p(q_out), ldqo,
+        _s(stream)))
+
+
+def gguf_paged_attn(q, ldq, heads, batch, cache, scale, causal, window, out, ldo, lse=None, workspace=None, ws_bytes=0,
+                    stream=None):
+    return _check("gguf_paged_attn", load_library().gguf_paged_attn(
+        _p(q), ldq, heads, _ref(batch), _ref(cache), scale, causal, window, _p(out), ldo, _p(lse), _p(workspace),
+        ws_bytes, _s(stream)))
+
+
+def gguf_paged_attn_workspace_size(batch, cache, heads) -> int:
+    return load_library().gguf_paged_attn_workspace_size(_ref(batch), _ref(cache), heads)
+
+
+def gguf_logits_adjust(logits, dt, ld, rows, vocab, rules, out, odt, ldo, stream=None):
+    return _check("gguf_logits_adjust", load_library().gguf_logits_adjust(
+        _p(logits), dt, ld, rows, vocab, _ref(rules), _p(out), odt, ldo, _s(stream)))
 
 
 # --- GGUF container reader (host only) ---------------------------------------

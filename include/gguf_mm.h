@@ -75,7 +75,8 @@ typedef enum { GGUF_PATH_AUTO = 0, GGUF_PATH_GEMV = 1, GGUF_PATH_FUSED = 2 } ggu
 
 typedef enum {
     GGUF_OK = 0,
-    GGUF_ERR_INVALID_ARG = -1,  /* null pointer, non-positive size, K not a multiple of the block */
+    GGUF_ERR_INVALID_ARG = -1,  /* null pointer, non-positive size, K not a multiple of the block; from
+                                   check_errors: an index array led outside its buffer */
     GGUF_ERR_UNSUPPORTED = -2,  /* type / layout / dtype / size combination not implemented */
     GGUF_ERR_MISALIGNED = -3,   /* a pointer is not 16-byte aligned */
     GGUF_ERR_WORKSPACE = -4,    /* workspace missing or smaller than gguf_mm_workspace_size() */
@@ -278,9 +279,165 @@ int gguf_dense_gemm_noalloc(const void* wdense, int wdt, int64_t ld, int64_t N, 
                             const void* x, int xdt, int64_t M, const void* residual, void* y, int ydt,
                             gguf_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Between the products of a serving step: rotary positions and the paged
+ * key/value cache, attention over it, and the rules on the logits
+ *
+ * The queries, keys and values that a QKV projection gives are rotated and
+ * appended with gguf_kv_append, gguf_paged_attn attends over the cache (its
+ * output is the next projection's input), and after the last product
+ * gguf_logits_adjust applies penalties, biases and a grammar's mask.
+ *
+ * A batch is ragged: sequence b's new tokens are rows q_start[b] ..
+ * q_start[b+1]-1 of the packed inputs, and kv_len[b] counts its keys, the new
+ * ones included, so that its j-th new token (of n_b) has the position
+ *   p = kv_len[b] - n_b + j.
+ * Key t of sequence b lives in page pages[b][t / page_size], slot t % page_size.
+ * The three structs are HOST memory, read during the call; the arrays they
+ * point to are device memory, read when the work runs.  Nothing in them is
+ * kept past the call.
+ *
+ * An index that leads outside the caller's buffers is never followed: a page
+ * id outside [0, n_pages) where a key is read or written, a position past the
+ * page table's row, q_start out of order or past n_tokens.  Such a token's or
+ * sequence's results are undefined, and gguf_mm_check_errors() reports
+ * GGUF_ERR_INVALID_ARG.
+ * ------------------------------------------------------------------------- */
+
+/* A layer's cache.  K[page][head][slot][d] is at k + page * page_stride +
+ * head * head_stride + slot * token_stride + d, V likewise (strides in
+ * elements, the same for both), so any order of the axes whose last is dense
+ * is possible, K and V in one allocation among them.
+ *   dtype      F16 or BF16
+ *   page_size  tokens in a page: 16, 32, 64, 128 or 256
+ *   head_dim   a multiple of 16 up to 128
+ * k and v are 16-byte aligned and the strides multiples of 8 elements. */
+typedef struct {
+    void* k;
+    void* v;
+    int32_t dtype;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int64_t n_pages;
+    int64_t page_stride, head_stride, token_stride;
+} gguf_kv_cache;
+
+/* A batch of sequences.  Rows of the packed inputs at and after q_start[n_seq]
+ * are left alone, so n_tokens may be an upper bound (a captured graph's).
+ *   q_start  [n_seq + 1] int32, non-decreasing, q_start[0] >= 0, q_start[n_seq] <= n_tokens
+ *   kv_len   [n_seq] int32 (0: no keys at all)
+ *   pages    [n_seq][pages_stride] int32; entries past a sequence's last page
+ *            are not read (attention under a window also reads none before it)
+ *   max_q_len, max_kv_len  bounds on the sequences' new tokens and keys, known
+ *            on the host: they shape the launch.  max_kv_len <= pages_stride *
+ *            page_size; a sequence that exceeds one is an index out of range. */
+typedef struct {
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* pages;
+    int64_t n_seq, n_tokens, pages_stride;
+    int64_t max_q_len, max_kv_len;
+} gguf_kv_batch;
+
+/* Rotary positions: pair i of a head, i < rot_dim / 2, turns by the angle
+ * p * freqs[i] (radians, freqs f32 [rot_dim / 2]; base, scaling and per-channel
+ * factors are in them) and is multiplied by `scale` (1 without scaling).
+ * The product p * freqs[i] is taken in 64 bits, so far positions keep their digits.
+ *   style      GGUF_ROPE_NORM: pair i is values 2i, 2i+1;
+ *              GGUF_ROPE_NEOX: values i, i + rot_dim / 2
+ *   rot_dim    even, 2 .. head_dim; the values from rot_dim on are copied
+ *   positions  int32 [n_tokens], used instead of p, or NULL (the angles alone
+ *              follow it: keys are stored by p) */
+enum { GGUF_ROPE_NORM = 0, GGUF_ROPE_NEOX = 1 };
+typedef struct {
+    const float* freqs;
+    const int32_t* positions;
+    int32_t rot_dim;
+    int32_t style;
+    float scale;
+} gguf_rope;
+
+/* Rotates the new tokens' q and k and appends k and v to the cache, in one
+ * kernel.  q [n_tokens][heads][head_dim], k and v [n_tokens][kv_heads]
+ * [head_dim] of xdt (F32, F16 or BF16); token t's heads start at q + t * ldq
+ * (k + t * ldk, v + t * ldv; elements), so the three may be the columns of one
+ * fused projection.  q_out [n_tokens][heads][head_dim] of the cache's dtype,
+ * token t at q_out + t * ldqo; it may be q itself when the types agree.  The
+ * rotation is computed in f32 and each value rounded once.
+ *   rope  NULL: nothing is rotated (values are converted and stored)
+ *   q     NULL (with q_out NULL): keys and values only
+ * All pointers 16-byte aligned, every row stride a multiple of 16 bytes.
+ * A token whose position is negative (more new tokens than keys) is not stored.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, NO_DEVICE, CUDA. */
+int gguf_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, int xdt,
+                   int64_t heads, const gguf_rope* rope, const gguf_kv_batch* batch, const gguf_kv_cache* cache,
+                   void* q_out, int64_t ldqo, gguf_stream_t stream);
+
+/* Attention of the new tokens over the paged cache (their own keys appended):
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K[j][h']) V[j][h'],  h' = h * kv_heads / heads,
+ * over the keys 0 <= j < kv_len[b] with, where `causal` is set, j <= p, and
+ * where window > 0, j > p - window.  A row that sees no key gives zeros.  What
+ * the cache holds in slots that no row of the sequence sees, and in pages
+ * before the window, has no influence (NaN and infinities included).
+ *   q, out  [n_tokens][heads][head_dim] of the cache's dtype, token t at
+ *           t * ldq (ldo) elements; out may not overlap q
+ *   heads   a multiple of kv_heads, at most 128 query heads to a key head
+ *   scale   positive and finite
+ *   lse     [n_tokens][heads] f32 or NULL: log sum_j exp(scale * q . K[j]),
+ *           -inf for a row that sees no key (joins partial results)
+ * Scores, softmax statistics and sums are f32; the weights are rounded to the
+ * cache's dtype for the product with V.  The result does not depend on timing.
+ * All pointers 16-byte aligned (lse: 4), ldq and ldo multiples of 8.
+ * Workspace: gguf_paged_attn_workspace_size() bytes.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, NO_DEVICE, CUDA. */
+int gguf_paged_attn(const void* q, int64_t ldq, int64_t heads, const gguf_kv_batch* batch, const gguf_kv_cache* cache,
+                    float scale, int causal, int64_t window, void* out, int64_t ldo, float* lse, void* workspace,
+                    size_t ws_bytes, gguf_stream_t stream);
+
+/* Bytes of workspace gguf_paged_attn needs for a batch of these bounds (n_seq,
+ * n_tokens, max_q_len, max_kv_len; the arrays are not read), whatever the mask:
+ * 0 = none, or invalid arguments. */
+size_t gguf_paged_attn_workspace_size(const gguf_kv_batch* batch, const gguf_kv_cache* cache, int64_t heads);
+
+/* The rules on a batch of logits; a NULL member is a rule that is not used.
+ *   hist, hist_start    row r's earlier tokens: hist[hist_start[r] .. hist_start[r+1])
+ *                       (int32; ids outside [0, vocab) count nowhere)
+ *   repeat, frequency, presence  f32 [rows], for the tokens in the history
+ *   bias_ids, bias, bias_start   row r's biased tokens and what is added to
+ *                       each, laid out as the history; an id that comes twice gets both
+ *   allow               bit v % 32 of word v / 32 of row r (allow + r *
+ *                       allow_stride words): token v may come next */
+typedef struct {
+    const int32_t* hist;
+    const int32_t* hist_start;
+    const float* repeat;
+    const float* frequency;
+    const float* presence;
+    const int32_t* bias_ids;
+    const float* bias;
+    const int32_t* bias_start;
+    const uint32_t* allow;
+    int64_t allow_stride;
+} gguf_logit_rules;
+
+/* Applies the rules to logits [rows][vocab] (row r at logits + r * ld) and
+ * writes out (row r at out + r * ldo).  For a token v that comes c times in the
+ * row's history, x its logit in f32:
+ *   c > 0:  x = (x > 0 ? x / repeat[r] : x * repeat[r]) - (c * frequency[r] + presence[r])
+ * then the biases of v are added in the order of the list, and a token that
+ * `allow` leaves out becomes -inf.  dt and odt: F32, F16 or BF16; out may be
+ * logits itself when the types and strides agree.  logits and out 16-byte
+ * aligned (rows may start anywhere).  The result does not depend on timing.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, NO_DEVICE, CUDA. */
+int gguf_logits_adjust(const void* logits, int dt, int64_t ld, int64_t rows, int64_t vocab,
+                       const gguf_logit_rules* rules, void* out, int odt, int64_t ldo, gguf_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the device status word of the
  * current device: GGUF_OK, GGUF_ERR_TIMEOUT (a bounded wait in a kernel expired;
- * that kernel's outputs are undefined), or GGUF_ERR_CUDA for a pending CUDA error. */
+ * that kernel's outputs are undefined), GGUF_ERR_INVALID_ARG (an index array of a
+ * gguf_kv_* or gguf_paged_attn call led outside its buffer), or GGUF_ERR_CUDA for
+ * a pending CUDA error. */
 int gguf_mm_check_errors(gguf_stream_t stream);
 
 /* Static string for a status code. */
