@@ -1,0 +1,98 @@
+// Pieces shared by the attention kernels: the rows and keys of a block's work,
+// tensor maps of the cache, partial results and their joining.
+#pragma once
+#include "serving.cuh"
+#include "tc.cuh"
+
+namespace gg {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_fast(float x) {   // 2 units of 2^-23; exp2(-inf) = 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The query heads of one key head and a sequence's new tokens are the rows of
+// one attention problem, token by token: row r is token r / group, head
+// r % group of the group.  Rows [r0, r0 + rows) of a sequence, the keys
+// [lo, hi) that any of them sees, and each row's own limits:
+struct RowSpan {
+    int seq, t0, n, len;   // sequence, its first packed row, new tokens, keys
+    int lo, hi;
+};
+
+// Sequence `seq`'s numbers; false where it has no rows at r0, or indexes out
+// of range (reported).  Every thread gets the same answer.
+__device__ __forceinline__ bool row_span(const AttnParams& p, int seq, int r0, int rows, RowSpan& s) {
+    const int a = p.b.q_start[seq], e = p.b.q_start[seq + 1], len = p.b.kv_len[seq];
+    const int64_t room = p.b.pages_stride << p.c.page_shift;
+    s.seq = seq;
+    s.t0 = a;
+    s.n = e - a;
+    s.len = len;
+    if (a < 0 || e < a || e > p.b.n_tokens || s.n > p.b.max_q || len > room || len > p.b.max_kv) {
+        if (threadIdx.x == 0) report(p.status, GGUF_ERR_INVALID_ARG);
+        return false;
+    }
+    if (r0 >= s.n * p.group) return false;
+    const int first = len - s.n + r0 / p.group;                          // positions of the first and last token
+    const int last = len - s.n + min(s.n - 1, (r0 + rows - 1) / p.group);
+    s.hi = max(0, p.causal ? min(len, last + 1) : len);
+    s.lo = p.window ? (int)min((int64_t)s.hi, max((int64_t)0, first - p.window + 1)) : 0;
+    return true;
+}
+
+// Keys [lo, hi) that the token of this position sees.
+__device__ __forceinline__ void row_keys(const AttnParams& p, const RowSpan& s, int pos, int& lo, int& hi) {
+    hi = p.causal ? min(s.len, pos + 1) : s.len;
+    lo = p.window ? (int)max((int64_t)0, pos - p.window + 1) : 0;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if (BF16) {
+        __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&v);
+    }
+    __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// A box of 64 values x `rows` tokens of one head and page, swizzled in 128-byte rows.
+__device__ __forceinline__ void tma_load_kv(uint32_t smem_dst, const CUtensorMap* map, int d, int slot, int head,
+                                            int page, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+            "r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(slot), "r"(head), "r"(page), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Tensor map over K or V: (d, slot, head, page), box 64 x rows x 1 x 1; values
+// past head_dim read as zeros.
+int make_kv_map(CUtensorMap* map, const void* base, const CacheParams& c, int rows);
+// Tensor map over q: (d, head, token), box 64 x heads x tokens.
+int make_q_map(CUtensorMap* map, const AttnParams& p, int heads, int tokens);
+
+// Partial results of a call that splits its keys: for split i, packed row
+// (token * heads + head): o[i][row][dim], unnormalised f32 sums at the
+// exponents of m[i][row], and l[i][row] (ml holds m and l in pairs).
+struct Partials {
+    float* o;
+    float2* ml;
+    int splits;
+};
+
+struct AttnPlan {
+    int few;        // the few-rows form
+    int tiles;      // row tiles of a sequence and key head
+    int cluster;    // blocks that split a tile's keys and join in their cluster
+    int splits;     // clusters to a tile, joined through the workspace where there are several
+};
+
+int attn_few_launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int pdl, cudaStream_t s);
+
+}  // namespace gg

@@ -56,6 +56,10 @@ __device__ __forceinline__ void tc_epilogue(const TcEpilogue& ep, uint32_t tmem,
     }
 }
 
+// Tensor map of `rank` (2..5) dimensions, innermost first; strides in bytes,
+// rank - 1 of them (the innermost dimension is dense).
+int make_tmap(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int rank, const uint64_t* dims,
+              const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swz);
 int make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t inner,
                  uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
                  CUtensorMapSwizzle swz);
