@@ -94,5 +94,6 @@ struct AttnPlan {
 };
 
 int attn_few_launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int pdl, cudaStream_t s);
+int attn_many_launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int pdl, cudaStream_t s);
 
 }  // namespace gg

@@ -1,9 +1,10 @@
-// Attention of new tokens over a paged key/value cache.
+// Attention of new tokens over a paged key/value cache: the form a call takes,
+// its tensor maps, and the joining of split keys.
 //
-//   out = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),  s_j = scale * q . K_j,
-// with m the running maximum of the scores seen so far: when it grows, what
-// has been summed is multiplied by exp(old m - new m), so one pass over the
-// keys is enough.
+//   out = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m),  s_j = scale * q . K_j.
+// With m the running maximum of the scores seen so far, multiplying what has
+// been summed by exp(old m - new m) when it grows makes one pass over the keys
+// enough, and partial results over disjoint keys join in the same way.
 #include "attn.cuh"
 #include "tc_gemm.cuh"
 
@@ -13,70 +14,9 @@ namespace {
 
 constexpr int kWarps = 8;
 
-template <class T> __device__ __forceinline__ float to_f(T v);
-template <> __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <class T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
-
-// One warp to a (token, head): the lanes hold the head's values, d = lane + 32 i.
-template <class T>
-__global__ void __launch_bounds__(32 * kWarps) attn_rows_kernel(const AttnParams p) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int t = (int)(row / p.heads), h = (int)(row % p.heads);
-    if (t >= p.b.n_tokens) return;
-    int seq = -1;
-    for (int i = lane; i < p.b.n_seq; i += 32)
-        if (p.b.q_start[i] <= t && t < p.b.q_start[i + 1]) seq = i;
-    seq = __reduce_max_sync(0xffffffffu, seq);
-    if (seq < 0) return;
-    const int len = p.b.kv_len[seq], pos = len - p.b.q_start[seq + 1] + t;
-    int hi = p.causal ? min(len, pos + 1) : len;
-    const int lo = p.window ? (int)max((int64_t)0, pos - p.window + 1) : 0;
-    if (hi > p.b.pages_stride << p.c.page_shift) {
-        hi = (int)(p.b.pages_stride << p.c.page_shift);
-        if (lane == 0) report(p.status, GGUF_ERR_INVALID_ARG);
-    }
-    const int D = p.c.dim;
-    float q[4], o[4] = {0.f, 0.f, 0.f, 0.f};
-    const T* qr = static_cast<const T*>(p.q) + t * p.ldq + h * D;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = lane + 32 * i < D ? to_f(qr[lane + 32 * i]) * p.scale : 0.f;
-    float m = -INFINITY, l = 0.f;
-    for (int j = lo; j < hi; ++j) {
-        const int page = p.b.pages[seq * p.b.pages_stride + (j >> p.c.page_shift)];
-        if ((unsigned)page >= (unsigned)p.c.n_pages) {
-            if (lane == 0) report(p.status, GGUF_ERR_INVALID_ARG);
-            break;
-        }
-        const int64_t at = page * p.c.page_stride + (h / p.group) * p.c.head_stride +
-                           (j & ((1 << p.c.page_shift) - 1)) * p.c.token_stride;
-        const T* k = static_cast<const T*>(p.c.k) + at;
-        const T* v = static_cast<const T*>(p.c.v) + at;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < D) s += q[i] * to_f(k[lane + 32 * i]);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        const float top = fmaxf(m, s);
-        const float old = m == -INFINITY ? 0.f : __expf(m - top), w = top == -INFINITY ? 0.f : __expf(s - top);
-        l = l * old + w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < D) o[i] = o[i] * old + w * to_f(v[lane + 32 * i]);
-        m = top;
-    }
-    T* out = static_cast<T*>(p.out) + t * p.ldo + h * D;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < D) out[lane + 32 * i] = from_f<T>(l > 0.f ? o[i] / l : 0.f);
-    if (p.lse && lane == 0) p.lse[(int64_t)t * p.heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
-}
 
 // One warp to a row: joins the splits' partial sums, in their order.
 template <class T>
@@ -107,21 +47,30 @@ __global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(const AttnParams
     if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
+// The form and the split of a call, from its sizes alone.
 AttnPlan make_plan(const AttnParams& p, int num_sms) {
     AttnPlan a{};
     const int64_t rows = (int64_t)p.b.max_q * p.group;
-    a.few = rows <= 64;
-    a.tiles = (int)ceil_div(rows, 16);
-    // keys in units of one chunk to each warp of a block
-    int64_t span = p.b.max_kv;
+    int64_t span = p.b.max_kv;                        // keys that a row tile may see
     if (p.window && p.causal) span = std::min<int64_t>(span, p.window + p.b.max_q);
-    const int64_t units = std::max<int64_t>(1, ceil_div(span, 64)), pairs = (int64_t)p.b.n_seq * p.c.kv_heads * a.tiles;
-    // two blocks to an SM; sequences of different lengths in shares of about a thousand keys
-    int64_t want = std::max(ceil_div(2 * num_sms, pairs), std::min<int64_t>(16, ceil_div(units, 16)));
-    want = std::min(want, units);
-    a.cluster = 1;
-    while (a.cluster < 16 && a.cluster < want) a.cluster *= 2;
-    a.splits = (int)ceil_div(want, a.cluster);
+    a.few = rows <= 64;
+    if (a.few) {
+        a.tiles = (int)ceil_div(rows, 16);
+        // keys in units of one chunk to each warp of a block
+        const int64_t units = std::max<int64_t>(1, ceil_div(span, 64)), pairs = (int64_t)p.b.n_seq * p.c.kv_heads * a.tiles;
+        // two blocks to an SM; sequences of different lengths in shares of about a thousand keys
+        int64_t want = std::max(ceil_div(2 * num_sms, pairs), std::min<int64_t>(16, ceil_div(units, 16)));
+        want = std::min(want, units);
+        a.cluster = 1;
+        while (a.cluster < 16 && a.cluster < want) a.cluster *= 2;
+        a.splits = (int)ceil_div(want, a.cluster);
+    } else {
+        a.tiles = (int)ceil_div(p.b.max_q, 2 * (128 / p.group));
+        // the keys are split where the tiles alone leave SMs idle
+        const int64_t units = std::max<int64_t>(1, ceil_div(span, 128)), pairs = (int64_t)p.b.n_seq * p.c.kv_heads * a.tiles;
+        a.cluster = 1;
+        a.splits = (int)std::min(units, std::max<int64_t>(1, num_sms / pairs));
+    }
     return a;
 }
 
@@ -135,28 +84,30 @@ int make_kv_map(CUtensorMap* map, const void* base, const CacheParams& c, int ro
                      strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+int make_q_map(CUtensorMap* map, const AttnParams& p, int heads, int tokens) {
+    const uint64_t dims[3] = {(uint64_t)p.c.dim, (uint64_t)p.heads, (uint64_t)p.b.n_tokens};
+    const uint64_t strides[2] = {(uint64_t)p.c.dim * 2, (uint64_t)p.ldq * 2};
+    const uint32_t box[3] = {64, (uint32_t)heads, (uint32_t)tokens};
+    return make_tmap(map, p.q, p.c.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, dims,
+                     strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 size_t paged_attn_workspace_bytes(const AttnParams& p, int num_sms) {
     const AttnPlan a = make_plan(p, num_sms);
-    if (!a.few || a.splits <= 1) return 0;
-    return (size_t)a.splits * p.b.n_tokens * p.heads * (p.c.dim * 4 + 8);
+    return a.splits > 1 ? (size_t)a.splits * p.b.n_tokens * p.heads * (p.c.dim * 4 + 8) : 0;
 }
 
 int paged_attn_launch(const AttnParams& p, void* workspace, int num_sms, int pdl, cudaStream_t s) {
     const AttnPlan a = make_plan(p, num_sms);
-    if (a.few) {
-        const int64_t rows = (int64_t)p.b.n_tokens * p.heads;
-        Partials part{static_cast<float*>(workspace), nullptr, a.splits};
-        part.ml = reinterpret_cast<float2*>(part.o + (int64_t)a.splits * rows * p.c.dim);
-        const int st = attn_few_launch(p, a, part, pdl, s);
-        if (st != GGUF_OK || a.splits == 1) return st;
-        const dim3 grid((unsigned)ceil_div(rows, kWarps));
-        const cudaError_t e = p.c.bf16 ? launch_pdl(attn_join_kernel<__nv_bfloat16>, grid, dim3(32 * kWarps), 0, s, pdl, p, part)
-                                       : launch_pdl(attn_join_kernel<__half>, grid, dim3(32 * kWarps), 0, s, pdl, p, part);
-        return e == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
-    }
-    const dim3 grid((unsigned)ceil_div((int64_t)p.b.n_tokens * p.heads, kWarps));
-    const cudaError_t e = p.c.bf16 ? launch_pdl(attn_rows_kernel<__nv_bfloat16>, grid, dim3(32 * kWarps), 0, s, pdl, p)
-                                   : launch_pdl(attn_rows_kernel<__half>, grid, dim3(32 * kWarps), 0, s, pdl, p);
+    if (a.tiles * (a.few ? (int64_t)p.c.kv_heads : 1) > 65535) return GGUF_ERR_UNSUPPORTED;   // a grid's limit
+    const int64_t rows = (int64_t)p.b.n_tokens * p.heads;
+    Partials part{static_cast<float*>(workspace), nullptr, a.splits};
+    part.ml = reinterpret_cast<float2*>(part.o + (int64_t)a.splits * rows * p.c.dim);
+    const int st = a.few ? attn_few_launch(p, a, part, pdl, s) : attn_many_launch(p, a, part, pdl, s);
+    if (st != GGUF_OK || a.splits == 1) return st;
+    const dim3 grid((unsigned)ceil_div(rows, kWarps));
+    const cudaError_t e = p.c.bf16 ? launch_pdl(attn_join_kernel<__nv_bfloat16>, grid, dim3(32 * kWarps), 0, s, pdl, p, part)
+                                   : launch_pdl(attn_join_kernel<__half>, grid, dim3(32 * kWarps), 0, s, pdl, p, part);
     return e == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
 }
 
