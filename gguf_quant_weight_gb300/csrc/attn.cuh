@@ -25,8 +25,8 @@ struct RowSpan {
 };
 
 // Sequence `seq`'s numbers; false where it has no rows at r0, or indexes out
-// of range (reported).  Every thread gets the same answer.
-__device__ __forceinline__ bool row_span(const AttnParams& p, int seq, int r0, int rows, RowSpan& s) {
+// of range (reported where tell is set).
+__device__ __forceinline__ bool row_span(const AttnParams& p, int seq, int r0, int rows, RowSpan& s, bool tell) {
     const int a = p.b.q_start[seq], e = p.b.q_start[seq + 1], len = p.b.kv_len[seq];
     const int64_t room = p.b.pages_stride << p.c.page_shift;
     s.seq = seq;
@@ -34,7 +34,7 @@ __device__ __forceinline__ bool row_span(const AttnParams& p, int seq, int r0, i
     s.n = e - a;
     s.len = len;
     if (a < 0 || e < a || e > p.b.n_tokens || s.n > p.b.max_q || len > room || len > p.b.max_kv) {
-        if (threadIdx.x == 0) report(p.status, GGUF_ERR_INVALID_ARG);
+        if (tell) report(p.status, GGUF_ERR_INVALID_ARG);
         return false;
     }
     if (r0 >= s.n * p.group) return false;
@@ -88,12 +88,14 @@ struct Partials {
 
 struct AttnPlan {
     int few;        // the few-rows form
-    int tiles;      // row tiles of a sequence and key head
-    int cluster;    // blocks that split a tile's keys and join in their cluster
-    int splits;     // clusters to a tile, joined through the workspace where there are several
+    int tiles;      // row tiles of a sequence and key head (of 16 rows, or pairs of up to 128)
+    int cluster;    // few rows, small calls: blocks of a cluster that split the keys
+    int blocks;     // few rows, large calls: blocks among whose warps all keys are dealt out; else 0
+    int splits;     // many rows: shares of the keys, joined through the workspace where there are several
 };
 
-int attn_few_launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int pdl, cudaStream_t s);
+size_t attn_line_bytes(const AttnParams& p, const AttnPlan& plan);
+int attn_few_launch(const AttnParams& p, const AttnPlan& plan, void* workspace, int pdl, cudaStream_t s);
 int attn_many_launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int pdl, cudaStream_t s);
 
 }  // namespace gg

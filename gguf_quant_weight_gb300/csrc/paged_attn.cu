@@ -47,6 +47,8 @@ __global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(const AttnParams
     if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
+constexpr int64_t kLineChunks = 4096;
+
 // The form and the split of a call, from its sizes alone.
 AttnPlan make_plan(const AttnParams& p, int num_sms) {
     AttnPlan a{};
@@ -56,14 +58,15 @@ AttnPlan make_plan(const AttnParams& p, int num_sms) {
     a.few = rows <= 64;
     if (a.few) {
         a.tiles = (int)ceil_div(rows, 16);
-        // keys in units of one chunk to each warp of a block
-        const int64_t units = std::max<int64_t>(1, ceil_div(span, 64)), pairs = (int64_t)p.b.n_seq * p.c.kv_heads * a.tiles;
-        // two blocks to an SM; sequences of different lengths in shares of about a thousand keys
-        int64_t want = std::max(ceil_div(2 * num_sms, pairs), std::min<int64_t>(16, ceil_div(units, 16)));
-        want = std::min(want, units);
-        a.cluster = 1;
-        while (a.cluster < 16 && a.cluster < want) a.cluster *= 2;
-        a.splits = (int)ceil_div(want, a.cluster);
+        const int64_t pairs = (int64_t)p.b.n_seq * p.c.kv_heads * a.tiles, chunks = std::max<int64_t>(1, ceil_div(span, 16));
+        a.cluster = a.splits = 1;
+        if (pairs * chunks > kLineChunks) {
+            a.blocks = 2 * num_sms;
+        } else {
+            // blocks enough for two to an SM, with a chunk to each warp
+            const int64_t want = std::min(ceil_div(2 * num_sms, pairs), ceil_div(chunks, 4));
+            while (a.cluster < 16 && a.cluster < want) a.cluster *= 2;
+        }
     } else {
         a.tiles = (int)ceil_div(p.b.max_q, 2 * (128 / p.group));
         // the keys are split where the tiles alone leave SMs idle
@@ -94,16 +97,18 @@ int make_q_map(CUtensorMap* map, const AttnParams& p, int heads, int tokens) {
 
 size_t paged_attn_workspace_bytes(const AttnParams& p, int num_sms) {
     const AttnPlan a = make_plan(p, num_sms);
+    if (a.blocks) return attn_line_bytes(p, a);
     return a.splits > 1 ? (size_t)a.splits * p.b.n_tokens * p.heads * (p.c.dim * 4 + 8) : 0;
 }
 
 int paged_attn_launch(const AttnParams& p, void* workspace, int num_sms, int pdl, cudaStream_t s) {
     const AttnPlan a = make_plan(p, num_sms);
     if (a.tiles * (a.few ? (int64_t)p.c.kv_heads : 1) > 65535) return GGUF_ERR_UNSUPPORTED;   // a grid's limit
+    if (a.few) return attn_few_launch(p, a, workspace, pdl, s);
     const int64_t rows = (int64_t)p.b.n_tokens * p.heads;
     Partials part{static_cast<float*>(workspace), nullptr, a.splits};
     part.ml = reinterpret_cast<float2*>(part.o + (int64_t)a.splits * rows * p.c.dim);
-    const int st = a.few ? attn_few_launch(p, a, part, pdl, s) : attn_many_launch(p, a, part, pdl, s);
+    const int st = attn_many_launch(p, a, part, pdl, s);
     if (st != GGUF_OK || a.splits == 1) return st;
     const dim3 grid((unsigned)ceil_div(rows, kWarps));
     const cudaError_t e = p.c.bf16 ? launch_pdl(attn_join_kernel<__nv_bfloat16>, grid, dim3(32 * kWarps), 0, s, pdl, p, part)

@@ -12,11 +12,14 @@
 //   * scores S = Q K^T with the queries in registers as the first operand; the
 //     accumulator's layout of S is the layout that the weights need as first
 //     operand of P V, so they never leave the registers.
-//   * the keys of a (sequence, key head) are split over the blocks of a
-//     cluster, and where those do not fill the GPU over several clusters.  A
-//     block's four partial results are joined in shared memory, a cluster's
-//     through distributed shared memory, several clusters' by the joining
-//     kernel: always in the same order.
+//   * small calls split the keys of a (sequence, key head) over the blocks of a
+//     cluster; the warps' results are joined in shared memory, the blocks'
+//     through distributed shared memory, in one launch.
+//   * large calls deal out the batch's keys in equal shares to all the warps
+//     that the GPU holds, across sequences, so that a warp's copies never
+//     pause and the sequences' lengths do not matter.  A second kernel joins
+//     what was cut.
+// Partial results are always joined in the same order.
 #include "attn.cuh"
 
 namespace gg {
@@ -27,6 +30,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kChunk = 16;      // keys a warp takes at a time
 constexpr int kRows = 16;
+constexpr int kCluster = 16;    // blocks of a cluster, at most
 
 template <int DP> struct FewCfg {
     static constexpr int BOX = kChunk * 128;                 // 16 keys x 64 values
@@ -65,17 +69,169 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
     return v;
 }
 
+// The workspace of a call in equal shares: sums and statistics in places of
+// `rows` rows, two to a worker, and where each sequence begins in the line.
+struct LineSpace {
+    float* o;
+    float2* ml;
+    int64_t* begin;
+    int rows;
+};
+LineSpace line_space(const AttnParams& p, const AttnPlan& plan, void* base) {
+    LineSpace ws;
+    ws.rows = (int)std::min<int64_t>(kRows, (int64_t)p.b.max_q * p.group);
+    const int64_t places = 2 * (int64_t)plan.blocks * kWarps * ws.rows;
+    ws.o = static_cast<float*>(base);
+    ws.ml = reinterpret_cast<float2*>(ws.o + places * p.c.dim);
+    ws.begin = reinterpret_cast<int64_t*>(ws.ml + places);
+    return ws;
+}
+
 template <bool BF16> struct Elem { using T = __half; };
 template <> struct Elem<true> { using T = __nv_bfloat16; };
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Block (x, y, z): split x (cluster x / cluster size) of the keys, key head and
-// row tile y, sequence z.
+// One warp's work on 16 rows: the queries as first operand (rows lane / 4 and
+// lane / 4 + 8), the sums, and the rows' statistics (m in units of ln 2).
+template <int DP, bool BF16>
+struct Rows16 {
+    using C = FewCfg<DP>;
+    using T = typename Elem<BF16>::T;
+    uint32_t q[DP / 16][4];
+    float o[DP / 8][4];
+    float m[2], l[2];
+    int lo[2], hi[2];
+
+    __device__ __forceinline__ void begin(const AttnParams& p, const RowSpan& s, int kvh, int r0, int lane) {
+        const int D = p.c.dim, steps = D / 16;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = r0 + lane / 4 + 8 * x, tok = r / p.group;
+            const bool is = tok < s.n;
+            lo[x] = hi[x] = 0;
+            if (is) row_keys(p, s, s.len - s.n + tok, lo[x], hi[x]);
+            const T* src = static_cast<const T*>(p.q) + (int64_t)(s.t0 + tok) * p.ldq + (kvh * p.group + r % p.group) * D +
+                           lane % 4 * 2;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+                q[k][x] = is && k < steps ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
+                q[k][2 + x] = is && k < steps ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
+            }
+            m[x] = -INFINITY;
+            l[x] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    }
+
+    // The 16 keys from j0 in the ring's slot at kb (K, then V).
+    __device__ __forceinline__ void take(const RowSpan& s, uint32_t kb, int j0, float c2, int lane) {
+        const uint32_t vb = kb + DP / 64 * C::BOX;
+        if (j0 + kChunk > s.hi || j0 < s.lo) {
+            // values that no row sees may be anything: 0 x NaN must not reach the sums
+            for (int e = lane; e < kChunk * 8 * (DP / 64); e += 32) {
+                const int row = e / 8 % kChunk;
+                if (j0 + row >= s.hi || j0 + row < s.lo)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + e / (8 * kChunk) * C::BOX +
+                                                                                 row * 128 + e % 8 * 16),
+                                 "r"(0)
+                                 : "memory");
+            }
+            fence_proxy_async_smem();                                // before the slot's next copy
+            __syncwarp();
+        }
+        float sc[2][4] = {};                                         // scores: two tiles of 8 keys
+        const int kr = (lane & 7) + (lane >> 4) * 8, kc = lane >> 3 & 1;         // key, and which 8 values
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+            uint32_t b[4];
+            ldsm4(kb + k / 4 * C::BOX + kr * 128 + (((k % 4 * 2 + kc) ^ (kr & 7)) << 4), b);
+            mma16816<BF16>(sc[0], q[k], b[0], b[1]);
+            mma16816<BF16>(sc[1], q[k], b[2], b[3]);
+        }
+        float top[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float t = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int j = j0 + 8 * n + lane % 4 * 2 + y;
+                    float& v = sc[n][2 * x + y];
+                    v = j >= lo[x] && j < hi[x] ? v * c2 : -INFINITY;
+                    t = fmaxf(t, v);
+                }
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+            top[x] = fmaxf(m[x], t);
+        }
+        if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float f = top[x] > m[x] ? exp2_fast(m[x] - top[x]) : 1.f;
+                m[x] = top[x];
+                l[x] *= f;
+#pragma unroll
+                for (int d = 0; d < DP / 8; ++d) {
+                    o[d][2 * x] *= f;
+                    o[d][2 * x + 1] *= f;
+                }
+            }
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const float base = m[x] == -INFINITY ? 0.f : m[x];       // a row that has seen nothing yet
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float a = exp2_fast(sc[n][2 * x] - base), b = exp2_fast(sc[n][2 * x + 1] - base);
+                l[x] += a + b;
+                w[2 * n + x] = pack2<BF16>(a, b);
+            }
+        }
+        const int vr = (lane & 7) + (lane >> 3 & 1) * 8, vc = lane >> 4;
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) {
+            uint32_t b[4];
+            ldsm4t(vb + d / 4 * C::BOX + vr * 128 + (((d % 4 * 2 + vc) ^ (vr & 7)) << 4), b);
+            mma16816<BF16>(o[2 * d], w, b[0], b[1]);
+            mma16816<BF16>(o[2 * d + 1], w, b[2], b[3]);
+        }
+    }
+
+    // The lanes' shares of the rows' sums of weights, together.
+    __device__ __forceinline__ void end() {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+        }
+    }
+};
+
+template <int DP>
+__device__ __forceinline__ void load_chunk(uint32_t at, const CUtensorMap* tmK, const CUtensorMap* tmV, int slot, int kvh,
+                                           int page, uint64_t* bar) {
+    using C = FewCfg<DP>;
+    mbar_arrive_expect_tx(bar, C::SLOT);
+#pragma unroll
+    for (int h = 0; h < DP / 64; ++h) {
+        tma_load_kv(at + h * C::BOX, tmK, 64 * h, slot, kvh, page, bar);
+        tma_load_kv(at + (DP / 64 + h) * C::BOX, tmV, 64 * h, slot, kvh, page, bar);
+    }
+}
+
+// ------------------------------------------------------------------ keys split over a cluster
+
+// Block (x, y, z): the x-th block of the cluster, key head and row tile y, sequence z.
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(kThreads)
-    attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p,
-                    const Partials part, int tiles, int cluster) {
+    attn_few_cluster_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                            const AttnParams p, int tiles) {
     using C = FewCfg<DP>;
     using T = typename Elem<BF16>::T;
     extern __shared__ uint8_t smem_raw[];
@@ -83,7 +239,7 @@ __global__ void __launch_bounds__(kThreads)
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];       // the warps' statistics
     __shared__ float2 s_ml[kRows];                                  // the block's
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cluster = gridDim.x;
     uint64_t* full = s_full + warp * C::STAGES;
     if (lane == 0) {
         if (warp == 0) {
@@ -99,77 +255,44 @@ __global__ void __launch_bounds__(kThreads)
 
     const int kvh = blockIdx.y / tiles, r0 = (blockIdx.y % tiles) * kRows;
     RowSpan s;
-    if (!row_span(p, blockIdx.z, r0, kRows, s)) return;             // the whole cluster alike
+    if (!row_span(p, blockIdx.z, r0, kRows, s, threadIdx.x == 0)) return;       // the whole cluster alike
 
-    // this block's chunks of 16 keys, in equal shares
+    // this block's chunks of 16 keys, in equal shares; the warps take them in turn
     const int c_lo = s.lo / kChunk, c_n = s.hi > s.lo ? (s.hi + kChunk - 1) / kChunk - c_lo : 0;
-    const int shares = gridDim.x;
-    const int c0 = c_lo + (int)((int64_t)c_n * blockIdx.x / shares), c1 = c_lo + (int)((int64_t)c_n * (blockIdx.x + 1) / shares);
+    const int c0 = c_lo + (int)((int64_t)c_n * blockIdx.x / cluster), c1 = c_lo + (int)((int64_t)c_n * (blockIdx.x + 1) / cluster);
     const int mine = c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;   // chunks c0 + warp + 4 i
     const int32_t* pages = p.b.pages + s.seq * p.b.pages_stride;
     const int per_page = p.c.page_shift - 4;                         // log2 of the chunks in a page
     const uint32_t slots = smem_u32(ring) + warp * C::STAGES * C::SLOT;
 
-    // lane i holds the page of the warp's chunk 32 j + i
-    int page_of = 0;
-    auto fetch_pages = [&](int from) {
-        const int i = from + lane;
-        page_of = -1;
-        if (i < mine) {
-            page_of = pages[(c0 + warp + kWarps * i) >> per_page];
-            if ((unsigned)page_of >= (unsigned)p.c.n_pages) {
-                report(p.status, GGUF_ERR_INVALID_ARG);
-                page_of = -1;
+    int page_of = 0;          // lane i: the page of the warp's chunk 32 j + i
+    uint32_t have = 0;        // bit i % 32: chunk i was loaded
+    auto issue = [&](int i) {
+        if (i >= mine) return;
+        if ((i & 31) == 0) {
+            page_of = -1;
+            if (i + lane < mine) {
+                page_of = pages[(c0 + warp + kWarps * (i + lane)) >> per_page];
+                if ((unsigned)page_of >= (unsigned)p.c.n_pages) {
+                    report(p.status, GGUF_ERR_INVALID_ARG);
+                    page_of = -1;
+                }
             }
         }
-    };
-    // whether chunk i was loaded, kept for its use: bit i % 32
-    uint32_t have = 0;
-    auto issue = [&](int i) {                                        // whole warp
-        if (i >= mine) return;
-        if ((i & 31) == 0) fetch_pages(i);
         const int page = __shfl_sync(0xffffffffu, page_of, i & 31);
         const uint32_t bit = 1u << (i & 31);
         have = page >= 0 ? have | bit : have & ~bit;
         if (page < 0 || lane != 0) return;
         const int st = i % C::STAGES;
-        const int slot = ((c0 + warp + kWarps * i) & ((1 << per_page) - 1)) * kChunk;
-        const uint32_t at = slots + st * C::SLOT;
-        mbar_arrive_expect_tx(&full[st], C::SLOT);
-#pragma unroll
-        for (int h = 0; h < DP / 64; ++h) {
-            tma_load_kv(at + h * C::BOX, &tmK, 64 * h, slot, kvh, page, &full[st]);
-            tma_load_kv(at + (DP / 64 + h) * C::BOX, &tmV, 64 * h, slot, kvh, page, &full[st]);
-        }
+        load_chunk<DP>(slots + st * C::SLOT, &tmK, &tmV, ((c0 + warp + kWarps * i) & ((1 << per_page) - 1)) * kChunk, kvh,
+                       page, &full[st]);
     };
 #pragma unroll 1
     for (int i = 0; i < C::STAGES; ++i) issue(i);
 
-    // the queries as first operand: rows lane / 4 and lane / 4 + 8
-    const int D = p.c.dim, steps = D / 16;
-    uint32_t q[DP / 16][4];
-    int lo[2], hi[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int r = r0 + lane / 4 + 8 * x, tok = r / p.group;
-        const bool is = tok < s.n;
-        lo[x] = hi[x] = 0;
-        if (is) row_keys(p, s, s.len - s.n + tok, lo[x], hi[x]);
-        const T* src = static_cast<const T*>(p.q) + (int64_t)(s.t0 + tok) * p.ldq + (kvh * p.group + r % p.group) * D + lane % 4 * 2;
-#pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-            q[k][x] = is && k < steps ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
-            q[k][2 + x] = is && k < steps ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
-        }
-    }
+    Rows16<DP, BF16> w;
+    w.begin(p, s, kvh, r0, lane);
     const float c2 = p.scale * kLog2e;
-    float o[DP / 8][4];
-#pragma unroll
-    for (int i = 0; i < DP / 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};          // m: of the scores in units of ln 2
-
     uint32_t phase = 0;                                              // bit st: the parity that slot st waits for
     bool ok = true;
 #pragma unroll 1
@@ -181,80 +304,7 @@ __global__ void __launch_bounds__(kThreads)
                 break;
             }
             phase ^= 1u << st;
-            const uint32_t kb = slots + st * C::SLOT, vb = kb + DP / 64 * C::BOX;
-            const int j0 = (c0 + warp + kWarps * i) * kChunk;
-            if (j0 + kChunk > s.hi || j0 < s.lo) {
-                // values that no row sees may be anything: 0 x NaN must not reach the sums
-                for (int e = lane; e < kChunk * 8 * (DP / 64); e += 32) {
-                    const int row = e / 8 % kChunk;
-                    if (j0 + row >= s.hi || j0 + row < s.lo)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         vb + e / (8 * kChunk) * C::BOX + row * 128 + e % 8 * 16),
-                                     "r"(0)
-                                     : "memory");
-                }
-                fence_proxy_async_smem();                            // before the slot's next copy
-                __syncwarp();
-            }
-            // scores of 16 keys: two tiles of 8
-            float sc[2][4] = {};
-            const int kr = (lane & 7) + (lane >> 4) * 8, kc = lane >> 3 & 1;     // key, and which 8 values
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-                uint32_t b[4];
-                ldsm4(kb + k / 4 * C::BOX + kr * 128 + (((k % 4 * 2 + kc) ^ (kr & 7)) << 4), b);
-                mma16816<BF16>(sc[0], q[k], b[0], b[1]);
-                mma16816<BF16>(sc[1], q[k], b[2], b[3]);
-            }
-            float top[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float t = -INFINITY;
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int j = j0 + 8 * n + lane % 4 * 2 + y;
-                        float& v = sc[n][2 * x + y];
-                        v = j >= lo[x] && j < hi[x] ? v * c2 : -INFINITY;
-                        t = fmaxf(t, v);
-                    }
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                top[x] = fmaxf(m[x], t);
-            }
-            if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float f = top[x] > m[x] ? exp2_fast(m[x] - top[x]) : 1.f;
-                    m[x] = top[x];
-                    l[x] *= f;
-#pragma unroll
-                    for (int d = 0; d < DP / 8; ++d) {
-                        o[d][2 * x] *= f;
-                        o[d][2 * x + 1] *= f;
-                    }
-                }
-            }
-            uint32_t w[4];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float base = m[x] == -INFINITY ? 0.f : m[x];   // a row that has seen nothing yet
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float a = exp2_fast(sc[n][2 * x] - base), b = exp2_fast(sc[n][2 * x + 1] - base);
-                    l[x] += a + b;
-                    w[2 * n + x] = pack2<BF16>(a, b);
-                }
-            }
-            const int vr = (lane & 7) + (lane >> 3 & 1) * 8, vc = lane >> 4;
-#pragma unroll
-            for (int d = 0; d < DP / 16; ++d) {
-                uint32_t b[4];
-                ldsm4t(vb + d / 4 * C::BOX + vr * 128 + (((d % 4 * 2 + vc) ^ (vr & 7)) << 4), b);
-                mma16816<BF16>(o[2 * d], w, b[0], b[1]);
-                mma16816<BF16>(o[2 * d + 1], w, b[2], b[3]);
-            }
+            w.take(s, slots + st * C::SLOT, (c0 + warp + kWarps * i) * kChunk, c2, lane);
             __syncwarp();
         }
         issue(i + C::STAGES);
@@ -266,15 +316,13 @@ __global__ void __launch_bounds__(kThreads)
 
     // join the block's warps: the sums at the largest maximum, in the ring's place
     float* so = reinterpret_cast<float*>(ring);                      // [warp][row][DP], the block's result in warp 0's
+    w.end();
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    for (int x = 0; x < 2; ++x)
         if (lane % 4 == 0) {
-            s_m[warp][lane / 4 + 8 * x] = m[x];
-            s_l[warp][lane / 4 + 8 * x] = l[x];
+            s_m[warp][lane / 4 + 8 * x] = w.m[x];
+            s_l[warp][lane / 4 + 8 * x] = w.l[x];
         }
-    }
     __syncthreads();                                                 // every ring is done with
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -282,11 +330,11 @@ __global__ void __launch_bounds__(kThreads)
         float top = -INFINITY;
 #pragma unroll
         for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_m[v][row]);
-        const float f = m[x] == -INFINITY ? 0.f : exp2_fast(m[x] - top);
+        const float f = w.m[x] == -INFINITY ? 0.f : exp2_fast(w.m[x] - top);
 #pragma unroll
         for (int d = 0; d < DP / 8; ++d)
             *reinterpret_cast<float2*>(so + (warp * kRows + row) * DP + 8 * d + lane % 4 * 2) =
-                make_float2(o[d][2 * x] * f, o[d][2 * x + 1] * f);
+                make_float2(w.o[d][2 * x] * f, w.o[d][2 * x + 1] * f);
         if (warp == 0 && lane % 4 == 0) {
             float sum = 0.f;
 #pragma unroll
@@ -310,21 +358,30 @@ __global__ void __launch_bounds__(kThreads)
     }
 
     // join the cluster's blocks: each takes its share of the elements
-    const int rank = cluster > 1 ? (int)cluster_rank() : 0;
-    const int split = blockIdx.x / cluster;
+    const int D = p.c.dim;
     const uint32_t so_a = smem_u32(so), ml_a = smem_u32(s_ml);
-    for (int e = rank * kThreads + threadIdx.x; e < rows * D; e += cluster * kThreads) {
+    for (int e = blockIdx.x * kThreads + threadIdx.x; e < rows * D; e += cluster * kThreads) {
         const int row = e / D, d = e - row * D;
         float top = -INFINITY, sum = 0.f, v = 0.f;
         if (cluster > 1) {
-            for (int c = 0; c < cluster; ++c) top = fmaxf(top, ld_cluster_f32(cluster_map(ml_a + 8 * row, c)));
-            for (int c = 0; c < cluster; ++c) {
+            float mc[kCluster], lc[kCluster], vc[kCluster];          // every block's, all loads in flight at once
+#pragma unroll
+            for (int c = 0; c < kCluster; ++c) {
+                mc[c] = -INFINITY;
+                lc[c] = vc[c] = 0.f;
+                if (c >= cluster) continue;
                 const uint32_t a = cluster_map(ml_a + 8 * row, c);
-                const float mc = ld_cluster_f32(a);
-                if (mc == -INFINITY) continue;
-                const float f = exp2_fast(mc - top);
-                sum += f * ld_cluster_f32(a + 4);
-                v += f * ld_cluster_f32(cluster_map(so_a + 4 * (row * DP + d), c));
+                mc[c] = ld_cluster_f32(a);
+                lc[c] = ld_cluster_f32(a + 4);
+                vc[c] = ld_cluster_f32(cluster_map(so_a + 4 * (row * DP + d), c));
+            }
+#pragma unroll
+            for (int c = 0; c < kCluster; ++c) top = fmaxf(top, mc[c]);
+#pragma unroll
+            for (int c = 0; c < kCluster; ++c) {
+                const float f = mc[c] == -INFINITY ? 0.f : exp2_fast(mc[c] - top);
+                sum += f * lc[c];
+                v += f * vc[c];
             }
         } else {
             top = s_ml[row].x;
@@ -332,14 +389,8 @@ __global__ void __launch_bounds__(kThreads)
             v = so[row * DP + d];
         }
         const int r = r0 + row, tok = s.t0 + r / p.group, head = kvh * p.group + r % p.group;
-        const int64_t at = (int64_t)tok * p.heads + head;
-        if (part.splits > 1) {
-            part.o[((int64_t)split * p.b.n_tokens * p.heads + at) * D + d] = v;
-            if (d == 0) part.ml[(int64_t)split * p.b.n_tokens * p.heads + at] = make_float2(top, sum);
-        } else {
-            put(static_cast<T*>(p.out) + (int64_t)tok * p.ldo + head * D + d, sum > 0.f ? v / sum : (sum == 0.f ? 0.f : sum));
-            if (p.lse && d == 0) p.lse[at] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
-        }
+        put(static_cast<T*>(p.out) + (int64_t)tok * p.ldo + head * D + d, sum > 0.f ? v / sum : (sum == 0.f ? 0.f : sum));
+        if (p.lse && d == 0) p.lse[(int64_t)tok * p.heads + head] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
     }
     if (cluster > 1) {                                               // nobody leaves while another reads its memory
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -347,17 +398,341 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// ------------------------------------------------------------------ keys in equal shares to every warp
+//
+// All chunks of the batch stand in one line: sequence by sequence, row tile by
+// row tile, key head by key head.  Of `total` chunks worker w of W, as many as
+// there are warps or chunks, takes [total w / W, total (w + 1) / W), whatever
+// sequences they belong to.  A
+// (sequence, tile, head) whose chunks one worker has alone is written at once;
+// of the others each worker leaves its sums in the workspace -- in place 2 w
+// where its share begins inside the item, 2 w + 1 where the item begins in its
+// share -- and the joining kernel adds them in the line's order.
+
+__device__ __forceinline__ int64_t share_begin(int64_t total, int w, int workers) { return total * w / workers; }
+// The worker that has chunk x.
+__device__ __forceinline__ int share_of(int64_t total, int64_t x, int workers) {
+    return (int)(((x + 1) * workers + total - 1) / total) - 1;
+}
+
+// Chunks of one row tile of a sequence; a tile that sees no key has one, empty.
+__device__ __forceinline__ int tile_chunks(const RowSpan& s) {
+    return s.hi > s.lo ? (s.hi + kChunk - 1) / kChunk - s.lo / kChunk : 1;
+}
+__device__ __forceinline__ int seq_chunks(const AttnParams& p, int seq) {
+    int n = 0;
+    RowSpan s;
+    for (int r0 = 0; row_span(p, seq, r0, kRows, s, false); r0 += kRows) n += tile_chunks(s);
+    return n * p.c.kv_heads;
+}
+
+// A place in the line.
+struct Cursor {
+    RowSpan s;
+    int r0, kvh;
+    int c, n;          // chunk of the item, and how many it has
+};
+
+// The first item with rows at or after (seq, r0) -- false at the end.
+__device__ __forceinline__ bool settle(const AttnParams& p, Cursor& k, int seq, int r0) {
+    for (; seq < p.b.n_seq; ++seq, r0 = 0)
+        if (row_span(p, seq, r0, kRows, k.s, false)) {
+            k.r0 = r0;
+            k.n = tile_chunks(k.s);
+            k.kvh = k.c = 0;
+            return true;
+        }
+    return false;
+}
+__device__ __forceinline__ bool next_item(const AttnParams& p, Cursor& k) {
+    k.c = 0;
+    if (++k.kvh < p.c.kv_heads) return true;
+    return settle(p, k, k.s.seq, k.r0 + kRows);
+}
+
 template <int DP, bool BF16>
-int launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int pdl, cudaStream_t s) {
+__global__ void __launch_bounds__(kThreads)
+    attn_few_line_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p,
+                         const LineSpace ws) {
+    using C = FewCfg<DP>;
+    using T = typename Elem<BF16>::T;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_full[kWarps * C::STAGES];
+    __shared__ int64_t s_sum[kWarps], s_at[kWarps];
+    __shared__ int s_seq[kWarps];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, me = blockIdx.x * kWarps + warp;
+    uint64_t* full = s_full + warp * C::STAGES;
+    if (lane == 0) {
+        if (warp == 0) {
+            prefetch_tmap(&tmK);
+            prefetch_tmap(&tmV);
+        }
+        for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+        s_seq[warp] = p.b.n_seq;
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // the line's length, then the sequence in which each warp's share begins
+    int64_t total = 0;
+    int workers = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        const int64_t length = total;
+        workers = (int)min((int64_t)(gridDim.x * kWarps), length);
+        total = 0;
+#pragma unroll 1
+        for (int b0 = 0; b0 < p.b.n_seq; b0 += kThreads) {
+            const int b = b0 + threadIdx.x;
+            int64_t sum = b < p.b.n_seq ? seq_chunks(p, b) : 0;
+            const int64_t own = sum;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += v;
+            }
+            if (lane == 31) s_sum[warp] = sum;
+            __syncthreads();
+            int64_t before = total + sum - own;
+            for (int v = 0; v < kWarps; ++v) {
+                if (v < warp) before += s_sum[v];
+                total += s_sum[v];
+            }
+            if (pass == 1) {
+                for (int v = 0; v < kWarps; ++v) {
+                    if (blockIdx.x * kWarps + v >= workers) break;
+                    const int64_t x = share_begin(length, blockIdx.x * kWarps + v, workers);
+                    if (own && before <= x && x < before + own) {
+                        s_seq[v] = b;
+                        s_at[v] = x - before;
+                    }
+                }
+                if (blockIdx.x == 0 && b < p.b.n_seq) {
+                    ws.begin[b] = before;
+                    RowSpan s;
+                    row_span(p, b, 0, kRows, s, true);               // reports what is out of range
+                }
+            }
+            __syncthreads();
+        }
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) ws.begin[p.b.n_seq] = total;
+    if (me >= workers) return;
+    const int64_t x0 = share_begin(total, me, workers);
+    int left = (int)(share_begin(total, me + 1, workers) - x0);       // chunks of this warp's share, at least one
+
+    // two places in the line: what is consumed, and what is loaded, STAGES chunks on
+    Cursor use;
+    {
+        int64_t at = s_at[warp];
+        settle(p, use, s_seq[warp], 0);
+        while (at >= (int64_t)use.n * p.c.kv_heads) {
+            at -= (int64_t)use.n * p.c.kv_heads;
+            settle(p, use, use.s.seq, use.r0 + kRows);
+        }
+        use.kvh = (int)(at / use.n);
+        use.c = (int)(at - (int64_t)use.kvh * use.n);
+    }
+    Cursor get = use;
+    int to_get = left;
+    const int per_page = p.c.page_shift - 4;
+    const uint32_t slots = smem_u32(ring) + warp * C::STAGES * C::SLOT;
+    int page_of = -1, page_from = -1;                                // lane i: the page of the item's chunk page_from + i
+    uint32_t have = 0;
+    int st_get = 0;
+    auto issue = [&]() {
+        if (to_get == 0) return;
+        const int first = get.s.lo / kChunk;
+        if (page_from < 0 || get.c >= page_from + 32) {
+            page_from = get.c;
+            page_of = -1;
+            const int c = get.c + lane;
+            if (c < get.n && get.s.hi > get.s.lo) {
+                page_of = p.b.pages[get.s.seq * p.b.pages_stride + ((first + c) >> per_page)];
+                if ((unsigned)page_of >= (unsigned)p.c.n_pages) {
+                    report(p.status, GGUF_ERR_INVALID_ARG);
+                    page_of = -1;
+                }
+            }
+        }
+        const int page = __shfl_sync(0xffffffffu, page_of, get.c - page_from);
+        have = page >= 0 ? have | 1u << st_get : have & ~(1u << st_get);
+        if (page >= 0 && lane == 0)
+            load_chunk<DP>(slots + st_get * C::SLOT, &tmK, &tmV, ((first + get.c) & ((1 << per_page) - 1)) * kChunk, get.kvh,
+                           page, &full[st_get]);
+        st_get = st_get + 1 == C::STAGES ? 0 : st_get + 1;
+        if (--to_get && ++get.c == get.n) {
+            next_item(p, get);
+            page_from = -1;
+        }
+    };
+#pragma unroll 1
+    for (int i = 0; i < C::STAGES; ++i) issue();
+
+    const float c2 = p.scale * kLog2e;
+    const int D = p.c.dim;
+    uint32_t phase = 0;
+    int st = 0;
+    bool inside = use.c > 0;                                         // the share begins inside an item
+    Rows16<DP, BF16> w;
+    w.begin(p, use.s, use.kvh, use.r0, lane);
+#pragma unroll 1
+    while (left > 0) {
+        if (have >> st & 1) {
+            if (!mbar_wait(&full[st], phase >> st & 1, p.status)) break;
+            phase ^= 1u << st;
+            w.take(use.s, slots + st * C::SLOT, (use.s.lo / kChunk + use.c) * kChunk, c2, lane);
+            __syncwarp();
+        }
+        st = st + 1 == C::STAGES ? 0 : st + 1;
+        issue();
+        --left;
+        ++use.c;
+        if (use.c < use.n && left > 0) continue;
+        // the item's end, or the share's
+        w.end();
+        const bool whole = !inside && use.c == use.n;
+        const int64_t place = 2 * me + (inside ? 0 : 1);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int row = lane / 4 + 8 * x, r = use.r0 + row;
+            if (r >= use.s.n * p.group) continue;
+            const int tok = use.s.t0 + r / p.group, head = use.kvh * p.group + r % p.group;
+            if (whole) {
+                T* out = static_cast<T*>(p.out) + (int64_t)tok * p.ldo + head * D + lane % 4 * 2;
+                const float inv = w.l[x] > 0.f ? 1.f / w.l[x] : (w.l[x] == 0.f ? 0.f : w.l[x]);
+#pragma unroll
+                for (int d = 0; d < DP / 8; ++d)
+                    if (8 * d < D)
+                        *reinterpret_cast<uint32_t*>(out + 8 * d) = pack2<BF16>(w.o[d][2 * x] * inv, w.o[d][2 * x + 1] * inv);
+                if (p.lse && lane % 4 == 0)
+                    p.lse[(int64_t)tok * p.heads + head] = w.l[x] == 0.f ? -INFINITY : w.m[x] * kLn2 + logf(w.l[x]);
+            } else {
+                float* po = ws.o + (place * ws.rows + row) * D + lane % 4 * 2;
+#pragma unroll
+                for (int d = 0; d < DP / 8; ++d)
+                    if (8 * d < D) *reinterpret_cast<float2*>(po + 8 * d) = make_float2(w.o[d][2 * x], w.o[d][2 * x + 1]);
+                if (lane % 4 == 0) ws.ml[place * ws.rows + row] = make_float2(w.m[x], w.l[x]);
+            }
+        }
+        if (left > 0) {
+            next_item(p, use);
+            inside = false;
+            w.begin(p, use.s, use.kvh, use.r0, lane);
+        }
+    }
+    if (left > 0)        // a wait ran out: let the copies in flight land
+        for (int i = 0; i < C::STAGES; ++i) mbar_wait(&full[i], phase >> i & 1, p.status, 1 << 12);
+}
+
+// Joins the items that several workers had: block (x, y, z) key head and row
+// tile x of sequence y, of it rows [rb (z / parts), + rb) and the z % parts-th
+// `db` values.  Each thread adds four values of a row over every per-th worker;
+// then the sums are added in pairs.
+constexpr int kJoin = 512;
+template <bool BF16>
+__global__ void __launch_bounds__(kJoin) attn_line_join_kernel(const AttnParams p, const LineSpace ws, int workers /* warps of the grid */,
+                                                               int rb, int db) {
+    using T = typename Elem<BF16>::T;
+    __shared__ float4 s_v[kJoin];
+    __shared__ float2 s_ml[kJoin];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tile = blockIdx.x / p.c.kv_heads, kvh = blockIdx.x % p.c.kv_heads, seq = blockIdx.y, D = p.c.dim;
+    RowSpan s;
+    if (!row_span(p, seq, tile * kRows, kRows, s, false)) return;
+    int64_t x = ws.begin[seq];
+    for (int t = 0; t < tile; ++t) {
+        RowSpan u;
+        row_span(p, seq, t * kRows, kRows, u, false);
+        x += (int64_t)tile_chunks(u) * p.c.kv_heads;
+    }
+    const int n = tile_chunks(s);
+    x += (int64_t)n * kvh;
+    const int64_t total = ws.begin[p.b.n_seq];
+    workers = (int)min((int64_t)workers, total);
+    const int w0 = share_of(total, x, workers), w1 = share_of(total, x + n - 1, workers);
+    if (w0 == w1) return;                                            // one worker had it and wrote it
+    const int parts = D / db, row0 = blockIdx.z / parts * rb;
+    const int rows = min(min(kRows, s.n * p.group - tile * kRows) - row0, rb);
+    if (rows <= 0) return;
+    const int work = rb * db / 4, per = blockDim.x / work;
+    const int g = threadIdx.x / work, e = threadIdx.x - g * work, in = e / (db / 4), row = row0 + in;
+    const int d = blockIdx.z % parts * db + (e - in * (db / 4)) * 4;
+    float top = -INFINITY, sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float2 ml, float4 o) {
+        if (ml.x == -INFINITY) return;
+        const float t = fmaxf(top, ml.x), a = exp2_fast(top - t), b = exp2_fast(ml.x - t);
+        top = t;
+        sum = sum * a + ml.y * b;
+        v = make_float4(v.x * a + o.x * b, v.y * a + o.y * b, v.z * a + o.z * b, v.w * a + o.w * b);
+    };
+    if (g < per && in < rows) {
+        for (int w = w0 + g; w <= w1; w += 4 * per) {
+            float2 ml[4];
+            float4 o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ml[i] = make_float2(-INFINITY, 0.f);
+                if (w + i * per > w1) continue;
+                const int64_t at = (2 * (int64_t)(w + i * per) + (w + i * per == w0)) * ws.rows + row;
+                ml[i] = ws.ml[at];
+                o[i] = *reinterpret_cast<const float4*>(ws.o + at * D + d);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) add(ml[i], o[i]);
+        }
+    }
+    for (int h = per; h > 1;) {                                      // pairs (g, g + ceil(h / 2))
+        const int to = (h + 1) / 2;
+        if (g >= to && g < h) {
+            s_v[threadIdx.x] = v;
+            s_ml[threadIdx.x] = make_float2(top, sum);
+        }
+        __syncthreads();
+        if (g + to < h) add(s_ml[threadIdx.x + to * work], s_v[threadIdx.x + to * work]);
+        h = to;
+    }
+    if (g != 0 || in >= rows) return;
+    const int r = tile * kRows + row, tok = s.t0 + r / p.group, head = kvh * p.group + r % p.group;
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    T* out = static_cast<T*>(p.out) + (int64_t)tok * p.ldo + head * D + d;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
+    if (p.lse && d == 0) p.lse[(int64_t)tok * p.heads + head] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+}
+
+template <int DP, bool BF16>
+int launch_line(const AttnParams& p, const AttnPlan& plan, void* workspace, int pdl, cudaStream_t s) {
     CUtensorMap k, v;
     if (make_kv_map(&k, p.c.k, p.c, kChunk) != GGUF_OK || make_kv_map(&v, p.c.v, p.c, kChunk) != GGUF_OK)
         return GGUF_ERR_UNSUPPORTED;
-    auto f = attn_few_kernel<DP, BF16>;
+    const LineSpace ws = line_space(p, plan, workspace);
+    auto f = attn_few_line_kernel<DP, BF16>;
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<DP>::SMEM) != cudaSuccess ||
+        launch_pdl(f, dim3(plan.blocks), dim3(kThreads), FewCfg<DP>::SMEM, s, pdl, k, v, p, ws) != cudaSuccess)
+        return GGUF_ERR_CUDA;
+    // few items, each cut into many shares: a block to 16 values of a row; else a block to an item
+    const bool many = plan.blocks * kWarps > 8 * (int64_t)p.b.n_seq * p.c.kv_heads * plan.tiles;
+    const int rb = many ? 1 : ws.rows, db = many ? 16 : p.c.dim;
+    const int threads = many ? kJoin : (int)ceil_div(rb * db / 4, 32) * 32;
+    return launch_pdl(attn_line_join_kernel<BF16>, dim3(p.c.kv_heads * plan.tiles, p.b.n_seq, ceil_div(ws.rows, rb) * (p.c.dim / db)),
+                      dim3(threads), 0, s, pdl, p, ws, plan.blocks * kWarps, rb, db) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
+}
+
+template <int DP, bool BF16>
+int launch_cluster(const AttnParams& p, const AttnPlan& plan, int pdl, cudaStream_t s) {
+    CUtensorMap k, v;
+    if (make_kv_map(&k, p.c.k, p.c, kChunk) != GGUF_OK || make_kv_map(&v, p.c.v, p.c, kChunk) != GGUF_OK)
+        return GGUF_ERR_UNSUPPORTED;
+    auto f = attn_few_cluster_kernel<DP, BF16>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<DP>::SMEM) != cudaSuccess ||
         cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return GGUF_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(plan.cluster * plan.splits, p.c.kv_heads * plan.tiles, p.b.n_seq);
+    cfg.gridDim = dim3(plan.cluster, p.c.kv_heads * plan.tiles, p.b.n_seq);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = FewCfg<DP>::SMEM;
     cfg.stream = s;
@@ -369,14 +744,24 @@ int launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int 
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, f, k, v, p, part, plan.tiles, plan.cluster) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, f, k, v, p, plan.tiles) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
 }
 
 }  // namespace
 
-int attn_few_launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int pdl, cudaStream_t s) {
-    if (p.c.dim > 64) return p.c.bf16 ? launch<128, true>(p, plan, part, pdl, s) : launch<128, false>(p, plan, part, pdl, s);
-    return p.c.bf16 ? launch<64, true>(p, plan, part, pdl, s) : launch<64, false>(p, plan, part, pdl, s);
+size_t attn_line_bytes(const AttnParams& p, const AttnPlan& plan) {
+    const LineSpace ws = line_space(p, plan, nullptr);
+    return (size_t)reinterpret_cast<uintptr_t>(ws.begin + p.b.n_seq + 1);
+}
+
+template <int DP, bool BF16>
+static int run(const AttnParams& p, const AttnPlan& plan, void* workspace, int pdl, cudaStream_t s) {
+    return plan.blocks ? launch_line<DP, BF16>(p, plan, workspace, pdl, s) : launch_cluster<DP, BF16>(p, plan, pdl, s);
+}
+
+int attn_few_launch(const AttnParams& p, const AttnPlan& plan, void* workspace, int pdl, cudaStream_t s) {
+    if (p.c.dim > 64) return p.c.bf16 ? run<128, true>(p, plan, workspace, pdl, s) : run<128, false>(p, plan, workspace, pdl, s);
+    return p.c.bf16 ? run<64, true>(p, plan, workspace, pdl, s) : run<64, false>(p, plan, workspace, pdl, s);
 }
 
 }  // namespace gg

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kvh = blockIdx.x / part.splits, split = blockIdx.x % part.splits;
     const int r0 = (gridDim.y - 1 - blockIdx.y) * 2 * geo.rows;
     RowSpan s;
-    if (!row_span(p, blockIdx.z, r0, 2 * geo.rows, s)) return;
+    if (!row_span(p, blockIdx.z, r0, 2 * geo.rows, s, threadIdx.x == 0)) return;
 
     // this split's tiles of keys, and how many of them each tile of rows needs
     const int k_lo = s.lo / kKeys, k_n = s.hi > s.lo ? (s.hi + kKeys - 1) / kKeys - k_lo : 0;

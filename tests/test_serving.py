@@ -253,6 +253,11 @@ def check_attn(c, group, causal=1, window=0, scale=None, spread=1.0, ref_cache=N
     return out, lse
 
 
+# bounds that make a call a large one: its keys are dealt out to all warps
+LARGE = dict(max_kv_len=16 * 6000)
+LARGE_WIDE = 6000          # pages of 16
+
+
 # (new tokens, keys) of each sequence: single tokens, chunks, more tokens than
 # keys, no keys, no tokens, lengths on both sides of pages and tiles
 RAGGED = [(1, 1), (1, 16), (1, 17), (5, 5), (0, 9), (3, 200), (1, 129), (2, 0), (4, 2), (33, 64), (1, 255)]
@@ -263,6 +268,14 @@ RAGGED = [(1, 1), (1, 16), (1, 17), (5, 5), (0, 9), (3, 200), (1, 129), (2, 0), 
 @pytest.mark.parametrize("causal", [0, 1])
 def test_attn_ragged(dt, dim, causal):
     check_attn(Case(RAGGED, 2, dim, dt, page=16, extra_rows=3, seed=dim), 4, causal)
+
+
+@pytest.mark.parametrize("dt,dim", [("bf16", 128), ("f16", 64), ("bf16", 80), ("f16", 16)])
+@pytest.mark.parametrize("causal,window", [(1, 0), (0, 0), (1, 21), (0, 130)])
+@pytest.mark.parametrize("seqs,group", [(RAGGED[:6] + RAGGED[6:9], 1), ([(1, 2000)], 4), ([(3, 700), (16, 900)], 3),
+                                        ([(1, 0), (1, 0)], 2), ([(1, 1 + 37 * i % 90) for i in range(300)], 1)])
+def test_attn_keys_dealt_out(dt, dim, causal, window, seqs, group):
+    check_attn(Case(seqs, 2, dim, dt, page=16, seed=dim + window, wide=LARGE_WIDE), group, causal, window, **LARGE)
 
 
 @pytest.mark.parametrize("group", [1, 2, 3, 5, 7, 8, 16, 20])
