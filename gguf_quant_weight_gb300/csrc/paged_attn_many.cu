@@ -61,9 +61,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     using C = ManyCfg<DP>;
     using T = typename Elem<BF16>::T;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t s_full[C::STAGES], s_empty[C::STAGES], s_q, s_score[2], s_weight[2], s_sum[2];
+    __shared__ __align__(8) uint64_t s_full[C::STAGES], s_empty[C::STAGES], s_q, s_score[2], s_weight[2][2], s_sum[2];
     __shared__ uint32_t s_tmem;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sq = smem_u32(base), ring = sq + 2 * C::TILE;
 
@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&s_q, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_score[i], 1);
-            mbar_init(&s_weight[i], 4);
+            mbar_init(&s_weight[i][0], 4);
+            mbar_init(&s_weight[i][1], 4);
             mbar_init(&s_sum[i], 1);
         }
         fence_mbar_init();
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;            // S of the two tiles at 0 and 128, O at 256 and 384
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);            // S of the two tiles at 0 and 128, O at 256 and 384
 
     if (warp == 8) {
         // ---- copies: Q, then K and V of each tile of keys through the ring
@@ -155,47 +156,68 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(&s_full[d % C::STAGES], d / C::STAGES & 1, p.status);
         }
     } else if (warp == 9) {
-        // ---- products, issued by one thread
-        if (lane == 0 && n > 0) {
-            const int D = p.c.dim, steps = D / 16;
-            const uint32_t id_s = idesc_f16(128, 128, BF16), id_o = idesc_f16(128, D, BF16) | kIdescBMajorMn;
+        // ---- products.  The warp's own instructions are what the tensor cores
+        // wait for between products: it goes through them together, descriptors
+        // advance by additions, and nothing is divided.
+        if (n > 0) {
+            const int steps = p.c.dim / 16;
+            const uint32_t id_s = idesc_f16(128, 128, BF16), id_o = idesc_f16(128, p.c.dim, BF16) | kIdescBMajorMn;
+            constexpr uint32_t kHi = (1024 >> 4) | 1u << 14 | 2u << 29;          // both layouts' upper words are the same
+            const uint32_t q_lo = sq >> 4 | 1u << 16, k_lo = ring >> 4 | 1u << 16, v_lo = ring >> 4 | (C::HALF >> 4) << 16;
             bool ok = mbar_wait(&s_q, 0, p.status);
-            auto wait_tile = [&](int d) { ok = ok && mbar_wait(&s_full[d % C::STAGES], d / C::STAGES & 1, p.status); };
-            auto scores = [&](int t, int d) {
-                const uint32_t a = sq + t * C::TILE, b = ring + d % C::STAGES * C::TILE;
-                for (int k = 0; k < steps; ++k)
-                    umma_f16(tmem + 128 * t, sw128_desc(a + k / 4 * C::HALF + k % 4 * 32),
-                             sw128_desc(b + k / 4 * C::HALF + k % 4 * 32), id_s, k != 0);
-                umma_commit(&s_score[t]);
+            auto scores = [&](int t, int st) {
+                const uint32_t a = q_lo + t * (C::TILE >> 4), b = k_lo + st * (C::TILE >> 4), d = tmem + 128 * t;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    if (k < steps) {
+                        const uint32_t at = (k / 4 * C::HALF + k % 4 * 32) >> 4;
+                        umma_f16_warp(d, a + at, b + at, kHi, id_s, k != 0);
+                    }
+                umma_commit_warp(&s_score[t]);
             };
-            auto sums = [&](int t, int i) {
-                const uint32_t b = ring + (2 * i + 1) % C::STAGES * C::TILE;
-                for (int k = 0; k < kKeys / 16; ++k)
-                    umma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, sw128_mn_desc(b + k * 2048, C::HALF), id_o,
-                                (i | k) != 0);
-                umma_commit(&s_sum[t]);
+            // in halves of 64 keys, as their weights come
+            auto sums = [&](int t, int st, uint32_t parity, bool first) {
+                const uint32_t b = v_lo + st * (C::TILE >> 4), a = tmem + 128 * t, d = tmem + 256 + 128 * t;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    ok = mbar_wait(&s_weight[t][h], parity, p.status);
+                    if (!ok) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 4 * h; k < 4 * h + 4; ++k)
+                        umma_f16_ts_warp(d, a + 8 * k, b + k * (2048 >> 4), kHi, id_o, k != 0 || !first);
+                }
+                umma_commit_warp(&s_sum[t]);
             };
-            wait_tile(0);
+            int st = 0;                          // the ring's next stage, and its parity
+            uint32_t turn = 0;
+            auto next = [&]() {
+                const int now = st;
+                ok = ok && mbar_wait(&s_full[now], turn, p.status);
+                if (++st == C::STAGES) {
+                    st = 0;
+                    turn ^= 1;
+                }
+                return now;
+            };
+            const int k_st = next();
             if (ok) {
                 tc_fence_after();
+#pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    if (tiles[t] > 0) scores(t, 0);
-                umma_commit(&s_empty[0]);
+                    if (tiles[t] > 0) scores(t, k_st);
+                umma_commit_warp(&s_empty[k_st]);
             }
+#pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
-                wait_tile(2 * i + 1);
-                if (i + 1 < n) wait_tile(2 * i + 2);
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (i < tiles[t]) {
-                        ok = mbar_wait(&s_weight[t], i & 1, p.status);
-                        if (!ok) break;
-                        tc_fence_after();
-                        sums(t, i);
-                    }
-                    if (i + 1 < tiles[t]) scores(t, 2 * i + 2);
+                const int v_st = next(), k_next = i + 1 < n ? next() : 0;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (i < tiles[t] && ok) sums(t, v_st, i & 1, i == 0);
+                    if (i + 1 < tiles[t] && ok) scores(t, k_next);
                 }
-                umma_commit(&s_empty[(2 * i + 1) % C::STAGES]);
-                if (i + 1 < n) umma_commit(&s_empty[(2 * i + 2) % C::STAGES]);
+                umma_commit_warp(&s_empty[v_st]);
+                if (i + 1 < n) umma_commit_warp(&s_empty[k_next]);
             }
         }
         __syncwarp();
@@ -234,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < 128; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(v[j]));
+            for (int j = 0; j < 128; j += 2)
+                top[j >> 1 & 3] = max3(top[j >> 1 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
             const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             const bool raise = mx > m && (m == -INFINITY || (mx - m) * c2 > kRaise);
             if (__any_sync(0xffffffffu, raise)) {
@@ -256,21 +279,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st_wait();
                 }
             }
-            const float mb = m == -INFINITY ? 0.f : m * c2;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                for (int j = 64 * c; j < 64 * c + 64; j += 2) {
-                    const float a = exp2_fast(fmaf(__uint_as_float(v[j]), c2, -mb));
-                    const float b = exp2_fast(fmaf(__uint_as_float(v[j + 1]), c2, -mb));
-                    sum[j & 2] += a;
-                    sum[(j & 2) + 1] += b;
-                    v[j / 2] = pack2<BF16>(a, b);
-                }
-                tmem_st32(ts + 32 * c, v + 32 * c);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             // values that no row of the block sees may be anything: 0 x NaN must
             // not reach the sums.  The products of the first tile of rows come first.
             if ((j0 < s.lo || j0 + kKeys > s.hi) && (t == 0 || i >= tiles[0])) {
@@ -284,10 +292,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      : "memory");
                 fence_proxy_async_smem();
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_weight[t]);
+            const float mb = m == -INFINITY ? 0.f : -m * c2;
+            const f32x2 cc = {c2, c2}, bb = {mb, mb};
+            f32x2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int j = 64 * c; j < 64 * c + 64; j += 2) {
+                    const f32x2 x = fma2({__uint_as_float(v[j]), __uint_as_float(v[j + 1])}, cc, bb);
+                    const f32x2 w = {exp2_fast(x.x), exp2_fast(x.y)};
+                    sum[j >> 1 & 1] = add2(sum[j >> 1 & 1], w);
+                    v[j / 2] = pack2<BF16>(w.x, w.y);
+                }
+                tmem_st32(ts + 32 * c, v + 32 * c);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_weight[t][c]);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
         if (mine > 0) ok = ok && mbar_wait(&s_sum[t], (mine - 1) & 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
