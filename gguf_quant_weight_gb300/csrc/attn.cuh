@@ -71,6 +71,9 @@ __device__ __forceinline__ bool row_span(const AttnParams& p, int seq, int r0, i
     return true;
 }
 
+// Whether the few-rows form takes a sequence of n new tokens.
+__device__ __forceinline__ bool is_few(const AttnParams& p, int n) { return (int64_t)n * p.group <= p.few_rows; }
+
 // Keys [lo, hi) that the token of this position sees.
 __device__ __forceinline__ void row_keys(const AttnParams& p, const RowSpan& s, int pos, int& lo, int& hi) {
     hi = p.causal ? min(s.len, pos + 1) : s.len;

@@ -101,9 +101,11 @@ size_t paged_attn_workspace_bytes(const AttnParams& p, int num_sms) {
     return a.splits > 1 ? (size_t)a.splits * p.b.n_tokens * p.heads * (p.c.dim * 4 + 8) : 0;
 }
 
-int paged_attn_launch(const AttnParams& p, void* workspace, int num_sms, int pdl, cudaStream_t s) {
+int paged_attn_launch(const AttnParams& call, void* workspace, int num_sms, int pdl, cudaStream_t s) {
+    AttnParams p = call;
     const AttnPlan a = make_plan(p, num_sms);
     if (a.tiles * (a.few ? (int64_t)p.c.kv_heads : 1) > 65535) return GGUF_ERR_UNSUPPORTED;   // a grid's limit
+    p.few_rows = a.few ? INT32_MAX : 0;
     if (a.few) return attn_few_launch(p, a, workspace, pdl, s);
     const int64_t rows = (int64_t)p.b.n_tokens * p.heads;
     Partials part{static_cast<float*>(workspace), nullptr, a.splits};

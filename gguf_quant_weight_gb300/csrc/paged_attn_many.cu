@@ -5,9 +5,9 @@
 // query heads of the group, token by token -- through their keys, 128 at a
 // time.  Per tile of keys
 //   S = Q K^T   both operands from shared memory, 128 x 128 sums in TMEM
-//   P = exp2(c S - c m), c = scale log2 e: one thread to a row, which holds the
-//               128 scores in registers, so a row's maximum and sum take no
-//               exchange; the weights, in 16 bits, replace the scores in TMEM
+//   P = exp2(c S - c m), c = scale log2 e: one thread to a row, so a row's
+//               maximum and sum take no exchange; the weights, in 16 bits,
+//               replace the scores in TMEM
 //   O += P V    P from TMEM, V from shared memory as it lies in the cache
 //               (its rows are the keys: an MN-major operand), sums in TMEM.
 // While one tile's threads take exponentials, the tensor cores work on the
@@ -16,6 +16,10 @@
 // equally precise, and O keeps its scale; so O is rescaled a few times in all.
 //
 // Warps 0-3 and 4-7: the two tiles' rows; warp 8 issues copies, warp 9 products.
+// A block that is done takes over one that has not begun (its index comes from
+// the launch's own queue), so its copies and products of the next tiles start
+// while the last rows are written; blocks stand in the order of their work, the
+// longest first.
 // What bounds it: 4 x 128 x 128 x D operations a tile pair and key tile on the
 // tensor cores, and 2 x 128 x 128 exponentials.
 #include "attn.cuh"
@@ -47,13 +51,79 @@ __device__ __forceinline__ void tma_load_q(uint32_t smem_dst, const CUtensorMap*
         : "memory");
 }
 
+__device__ __forceinline__ void store32(void* to, const uint32_t* v) {   // 32 bytes, aligned to as many
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 struct Geometry {
     int rows;        // rows of a tile: whole tokens, at most 128
     int box;         // tokens of a cache box
 };
 
-// Block (x, y, z): key head x / splits, split x % splits of the keys; the y-th
-// pair of tiles from the end (the longest first); sequence z.
+// A pair of row tiles and its share of the keys, from a block's index (x, y, z):
+// key head x / splits, split x % splits of the keys; the y-th pair from the
+// end; sequence z.
+struct Item {
+    RowSpan s;
+    int kvh, split, r0;
+    int k0;             // first tile of keys
+    int tiles[2], n;    // tiles of keys that each tile of rows needs, and the larger number
+    int more;           // 1: an item with rows, 0: one without, -1: the end
+};
+
+__device__ __forceinline__ bool find_item(const AttnParams& p, int splits, const Geometry& geo, uint3 at, Item& w, bool tell) {
+    w.kvh = at.x / splits;
+    w.split = at.x - w.kvh * splits;
+    w.r0 = (gridDim.y - 1 - at.y) * 2 * geo.rows;
+    w.n = w.tiles[0] = w.tiles[1] = 0;
+    if (!row_span(p, at.z, w.r0, 2 * geo.rows, w.s, tell) || is_few(p, w.s.n)) return false;
+    const RowSpan& s = w.s;
+    const int lo = s.lo / kKeys, all = s.hi > s.lo ? (s.hi + kKeys - 1) / kKeys - lo : 0;
+    w.k0 = lo;
+    int k1 = lo + all;
+    if (splits > 1) {
+        w.k0 = lo + (int)((int64_t)all * w.split / splits);
+        k1 = lo + (int)((int64_t)all * (w.split + 1) / splits);
+    }
+    w.tiles[0] = k1 - w.k0;
+    if (w.r0 + geo.rows < s.n * p.group) {
+        w.tiles[1] = w.tiles[0];
+        if (p.causal) {          // the first tile's last token sees up to here
+            const int hi = min(s.len, s.len - s.n + (w.r0 + geo.rows) / p.group);
+            w.tiles[0] = max(0, min(k1, (hi + kKeys - 1) / kKeys) - w.k0);
+        }
+    }
+    w.n = max(w.tiles[0], w.tiles[1]);
+    return true;
+}
+
+// Asks for the index of a block that has not begun, which then never does: 16
+// bytes arrive at `to` and on the barrier.
+__device__ __forceinline__ void take_block(uint4* to, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(to)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ bool taken_block(const uint4* from, uint3& at) {
+    uint32_t got, x, y, z;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+        "ld.shared.b128 h, [%4];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, h;\n\t}"
+        : "=r"(got), "=r"(x), "=r"(y), "=r"(z)
+        : "r"(smem_u32(from))
+        : "memory");
+    at = make_uint3(x, y, z);
+    return got != 0;
+}
+
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_many_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -61,30 +131,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     using C = ManyCfg<DP>;
     using T = typename Elem<BF16>::T;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t s_full[C::STAGES], s_empty[C::STAGES], s_q, s_score[2], s_weight[2][2], s_sum[2];
+    // copies of K and V; Q; scores, weights (halves) and sums of a tile; the next block's index
+    __shared__ __align__(8) uint64_t s_full[C::STAGES], s_empty[C::STAGES], s_q[2], s_qfree[2], s_score[2], s_weight[2][2],
+        s_sum[2], s_next, s_item[2], s_read[2];
+    __shared__ uint4 s_answer;
+    __shared__ Item s_work[2];
     __shared__ uint32_t s_tmem;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sq = smem_u32(base), ring = sq + 2 * C::TILE;
-
-    pdl_wait();
-    pdl_launch_dependents();
-    const int kvh = blockIdx.x / part.splits, split = blockIdx.x % part.splits;
-    const int r0 = (gridDim.y - 1 - blockIdx.y) * 2 * geo.rows;
-    RowSpan s;
-    if (!row_span(p, blockIdx.z, r0, 2 * geo.rows, s, threadIdx.x == 0)) return;
-
-    // this split's tiles of keys, and how many of them each tile of rows needs
-    const int k_lo = s.lo / kKeys, k_n = s.hi > s.lo ? (s.hi + kKeys - 1) / kKeys - k_lo : 0;
-    const int k0 = k_lo + (int)((int64_t)k_n * split / part.splits), k1 = k_lo + (int)((int64_t)k_n * (split + 1) / part.splits);
-    int tiles[2];
-    tiles[0] = k1 - k0;
-    tiles[1] = r0 + geo.rows < s.n * p.group ? k1 - k0 : 0;
-    if (p.causal && tiles[1]) {
-        const int hi = min(s.len, s.len - s.n + (r0 + geo.rows) / p.group);    // the first tile's last token sees up to here
-        tiles[0] = max(0, min(k1, (hi + kKeys - 1) / kKeys) - k0);
-    }
-    const int n = max(tiles[0], tiles[1]);
 
     if (threadIdx.x == 0) {
         prefetch_tmap(&tmQ);
@@ -94,260 +149,405 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], 1);
         }
-        mbar_init(&s_q, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_q[i], 1);
+            mbar_init(&s_qfree[i], 1);
             mbar_init(&s_score[i], 1);
             mbar_init(&s_weight[i][0], 4);
             mbar_init(&s_weight[i][1], 4);
             mbar_init(&s_sum[i], 1);
+            mbar_init(&s_item[i], 1);
+            mbar_init(&s_read[i], 9);                                // warps that read it
         }
+        mbar_init(&s_next, 1);
         fence_mbar_init();
     }
     if (warp == 9) tmem_alloc(&s_tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);            // S of the two tiles at 0 and 128, O at 256 and 384
+    // all 512 columns, so the address is 0: S of the two tiles at 0 and 128, O at 256 and 384
+    constexpr uint32_t tmem = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    bool ok = true;
+    // the k-th item of this block, as warp 8 found it
+    auto next_item = [&](int k) -> const Item& {
+        ok = mbar_wait(&s_item[k & 1], k >> 1 & 1, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        return s_work[k & 1];
+    };
+    auto item_done = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_read[k & 1]);
+    };
 
     if (warp == 8) {
         // ---- copies: Q, then K and V of each tile of keys through the ring
-        const int32_t* pages = p.b.pages + s.seq * p.b.pages_stride;
         const int nbox = kKeys / geo.box;    // boxes of a tile: a page each, or half of one
-        if (lane == 0 && n > 0) {
-            const int per = geo.rows / p.group, heads = tiles[1] ? 2 : 1;
-            mbar_arrive_expect_tx(&s_q, heads * (DP / 64) * geo.rows * 128);
-            for (int t = 0; t < heads; ++t)
-                for (int h = 0; h < DP / 64; ++h)
-                    tma_load_q(sq + t * C::TILE + h * C::HALF, &tmQ, 64 * h, kvh * p.group,
-                               s.t0 + r0 / p.group + t * per, &s_q);
-        }
-        int done = 0;                        // stages whose copies were started
-        bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
-            const int j0 = (k0 + i) * kKeys + lane * geo.box;     // lane's first key
-            int page = -1;
-            if (lane < nbox && j0 < s.hi && j0 + geo.box > s.lo) {
-                page = pages[j0 >> p.c.page_shift];
-                if ((unsigned)page >= (unsigned)p.c.n_pages) {
-                    report(p.status, GGUF_ERR_INVALID_ARG);
-                    page = -1;
-                }
-            }
-            const int count = __popc(__ballot_sync(0xffffffffu, page >= 0));
-            for (int kv = 0; kv < 2; ++kv, ++done) {
-                const int st = done % C::STAGES;
-                ok = mbar_wait(&s_empty[st], (done / C::STAGES & 1) ^ 1, p.status);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&s_full[st], count * (DP / 64) * geo.box * 128);
+        int st = 0, quse[2] = {0, 0};        // the ring's next stage; copies of Q so far
+        uint32_t turn = 1, loaded = 0;       // the parity of an empty stage; bit st: the stage was ever loaded
+        uint3 at = blockIdx;
+        Item w;
+        for (int k = 0;; ++k) {
+            if (k > 0) {
+                ok = ok && mbar_wait(&s_next, k - 1 & 1, p.status);
+                ok = __all_sync(0xffffffffu, ok);
+                w.more = ok && taken_block(&s_answer, at) ? 0 : -1;
+                fence_proxy_async_smem();
                 __syncwarp();
-                if (page >= 0)
-                    for (int h = 0; h < DP / 64; ++h)
-                        tma_load_kv(ring + st * C::TILE + h * C::HALF + lane * geo.box * 128, kv ? &tmV : &tmK, 64 * h,
-                                    j0 & ((1 << p.c.page_shift) - 1), kvh, page, &s_full[st]);
+            } else {
+                w.more = 0;
             }
+            if (w.more == 0) {
+                if (lane == 0) take_block(&s_answer, &s_next);
+                w.more = find_item(p, part.splits, geo, at, w, lane == 0) ? 1 : 0;
+            }
+            if (k >= 2) ok = ok && mbar_wait(&s_read[k & 1], (k >> 1) - 1 & 1, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                s_work[k & 1] = w;
+                mbar_arrive(&s_item[k & 1]);
+            }
+            if (w.more < 0) break;
+            if (w.more == 0) continue;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (w.tiles[t] == 0) continue;
+                if (quse[t] > 0) ok = ok && mbar_wait(&s_qfree[t], quse[t] - 1 & 1, p.status);
+                ++quse[t];
+                if (lane == 0 && ok) {
+                    mbar_arrive_expect_tx(&s_q[t], (DP / 64) * geo.rows * 128);
+                    for (int h = 0; h < DP / 64; ++h)
+                        tma_load_q(sq + t * C::TILE + h * C::HALF, &tmQ, 64 * h, w.kvh * p.group,
+                                   w.s.t0 + (w.r0 + t * geo.rows) / p.group, &s_q[t]);
+                }
+            }
+            const int32_t* pages = p.b.pages + w.s.seq * p.b.pages_stride;
+            ok = __all_sync(0xffffffffu, ok);
+            for (int i = 0; i < w.n && ok; ++i) {
+                const int j0 = (w.k0 + i) * kKeys + lane * geo.box;   // lane's first key
+                int page = -1;
+                if (lane < nbox && j0 < w.s.hi && j0 + geo.box > w.s.lo) {
+                    page = pages[j0 >> p.c.page_shift];
+                    if ((unsigned)page >= (unsigned)p.c.n_pages) {
+                        report(p.status, GGUF_ERR_INVALID_ARG);
+                        page = -1;
+                    }
+                }
+                const int count = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                for (int kv = 0; kv < 2; ++kv) {
+                    ok = mbar_wait(&s_empty[st], turn, p.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&s_full[st], count * (DP / 64) * geo.box * 128);
+                    __syncwarp();
+                    if (page >= 0)
+                        for (int h = 0; h < DP / 64; ++h)
+                            tma_load_kv(ring + st * C::TILE + h * C::HALF + lane * geo.box * 128, kv ? &tmV : &tmK, 64 * h,
+                                        j0 & ((1 << p.c.page_shift) - 1), w.kvh, page, &s_full[st]);
+                    loaded |= 1u << st;
+                    if (++st == C::STAGES) {
+                        st = 0;
+                        turn ^= 1;
+                    }
+                }
+            }
+            if (!ok) break;
         }
-        // nothing of this block is in flight when it ends, also after a wait that ran out
+        // nothing of this block is in flight when it ends, also after a wait that
+        // ran out: the last copy of every stage and of Q (the answer has been read)
         if (lane == 0) {
-            if (n > 0) mbar_wait(&s_q, 0, p.status);
-            for (int d = max(0, done - C::STAGES); d < done; ++d)
-                mbar_wait(&s_full[d % C::STAGES], d / C::STAGES & 1, p.status);
+            for (int i = 0; i < C::STAGES; ++i)
+                if (loaded >> i & 1) mbar_wait(&s_full[i], i < st ? turn ^ 1 : turn, p.status);
+            for (int t = 0; t < 2; ++t)
+                if (quse[t] > 0) mbar_wait(&s_q[t], quse[t] - 1 & 1, p.status);
+            if (!ok) mbar_wait(&s_next, 0, p.status), mbar_wait(&s_next, 1, p.status);
         }
     } else if (warp == 9) {
         // ---- products.  The warp's own instructions are what the tensor cores
         // wait for between products: it goes through them together, descriptors
         // advance by additions, and nothing is divided.
-        if (n > 0) {
-            const int steps = p.c.dim / 16;
-            const uint32_t id_s = idesc_f16(128, 128, BF16), id_o = idesc_f16(128, p.c.dim, BF16) | kIdescBMajorMn;
-            constexpr uint32_t kHi = (1024 >> 4) | 1u << 14 | 2u << 29;          // both layouts' upper words are the same
-            const uint32_t q_lo = sq >> 4 | 1u << 16, k_lo = ring >> 4 | 1u << 16, v_lo = ring >> 4 | (C::HALF >> 4) << 16;
-            bool ok = mbar_wait(&s_q, 0, p.status);
-            auto scores = [&](int t, int st) {
-                const uint32_t a = q_lo + t * (C::TILE >> 4), b = k_lo + st * (C::TILE >> 4), d = tmem + 128 * t;
+        const int steps = p.c.dim / 16;
+        const uint32_t id_s = idesc_f16(128, 128, BF16), id_o = idesc_f16(128, p.c.dim, BF16) | kIdescBMajorMn;
+        constexpr uint32_t kHi = (1024 >> 4) | 1u << 14 | 2u << 29;          // both layouts' upper words are the same
+        const uint32_t q_lo = sq >> 4 | 1u << 16, k_lo = ring >> 4 | 1u << 16, v_lo = ring >> 4 | (C::HALF >> 4) << 16;
+        int st = 0;                          // the ring's next stage, and its parity
+        uint32_t turn = 0, quse = 0, weights = 0;   // bit t: parity of the next Q, and of the next weights
+        // once a wait has run out there are no more: what follows is worthless, but ends
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status));
+        };
+        auto scores = [&](int t, int from, bool last) {
+            // (a shuffle's result is known to be the same in all lanes)
+            const uint32_t b = __shfl_sync(0xffffffffu, k_lo + from * (C::TILE >> 4), 0);
+            const uint32_t a = q_lo + t * (C::TILE >> 4), d = tmem + 128 * t;
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    if (k < steps) {
-                        const uint32_t at = (k / 4 * C::HALF + k % 4 * 32) >> 4;
-                        umma_f16_warp(d, a + at, b + at, kHi, id_s, k != 0);
-                    }
-                umma_commit_warp(&s_score[t]);
-            };
-            // in halves of 64 keys, as their weights come
-            auto sums = [&](int t, int st, uint32_t parity, bool first) {
-                const uint32_t b = v_lo + st * (C::TILE >> 4), a = tmem + 128 * t, d = tmem + 256 + 128 * t;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    ok = mbar_wait(&s_weight[t][h], parity, p.status);
-                    if (!ok) return;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 4 * h; k < 4 * h + 4; ++k)
-                        umma_f16_ts_warp(d, a + 8 * k, b + k * (2048 >> 4), kHi, id_o, k != 0 || !first);
+            for (int k = 0; k < DP / 16; ++k)
+                if (k < steps) {
+                    const uint32_t off = (k / 4 * C::HALF + k % 4 * 32) >> 4;
+                    umma_f16_warp(d, a + off, b + off, kHi, id_s, k != 0);
                 }
-                umma_commit_warp(&s_sum[t]);
-            };
-            int st = 0;                          // the ring's next stage, and its parity
-            uint32_t turn = 0;
-            auto next = [&]() {
-                const int now = st;
-                ok = ok && mbar_wait(&s_full[now], turn, p.status);
-                if (++st == C::STAGES) {
-                    st = 0;
-                    turn ^= 1;
-                }
-                return now;
-            };
-            const int k_st = next();
-            if (ok) {
+            umma_commit_warp(&s_score[t]);
+            if (last) umma_commit_warp(&s_qfree[t]);
+        };
+        // in halves of 64 keys, as their weights come
+        auto sums = [&](int t, int from, bool first) {
+            const uint32_t b = __shfl_sync(0xffffffffu, v_lo + from * (C::TILE >> 4), 0);
+            const uint32_t a = tmem + 128 * t, d = tmem + 256 + 128 * t;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                wait(&s_weight[t][h], weights >> t & 1);
                 tc_fence_after();
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (tiles[t] > 0) scores(t, k_st);
-                umma_commit_warp(&s_empty[k_st]);
+                for (int k = 4 * h; k < 4 * h + 4; ++k)
+                    umma_f16_ts_warp(d, a + 8 * k, b + k * (2048 >> 4), kHi, id_o, k != 0 || !first);
             }
+            weights ^= 1u << t;
+            umma_commit_warp(&s_sum[t]);
+        };
+        auto next = [&]() {
+            const int now = st;
+            wait(&s_full[now], turn);
+            if (++st == C::STAGES) {
+                st = 0;
+                turn ^= 1;
+            }
+            return now;
+        };
+        for (int k = 0;; ++k) {
+            const Item& w = next_item(k);
+            if (!ok) break;
+            const int more = __shfl_sync(0xffffffffu, w.more, 0), n = __shfl_sync(0xffffffffu, w.n, 0);
+            const int tiles[2] = {__shfl_sync(0xffffffffu, w.tiles[0], 0), __shfl_sync(0xffffffffu, w.tiles[1], 0)};
+            item_done(k);
+            if (more < 0) break;
+            if (more == 0 || n == 0) continue;
+            const int first = next();
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (tiles[t] > 0) {
+                    wait(&s_q[t], quse >> t & 1);
+                    quse ^= 1u << t;
+                    tc_fence_after();
+                    scores(t, first, tiles[t] == 1);
+                }
+            umma_commit_warp(&s_empty[first]);
+            int v_st = next();
+            // every wait stands behind products enough to cover it
 #pragma unroll 1
             for (int i = 0; i < n && ok; ++i) {
-                const int v_st = next(), k_next = i + 1 < n ? next() : 0;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (i < tiles[t] && ok) sums(t, v_st, i & 1, i == 0);
-                    if (i + 1 < tiles[t] && ok) scores(t, k_next);
-                }
+                const bool more_keys = i + 1 < n;
+                int k_st = 0, v_next = 0;
+                if (i < tiles[0]) sums(0, v_st, i == 0);
+                if (more_keys) k_st = next();
+                if (i + 1 < tiles[0]) scores(0, k_st, i + 2 == tiles[0]);
+                if (i < tiles[1]) sums(1, v_st, i == 0);
                 umma_commit_warp(&s_empty[v_st]);
-                if (i + 1 < n) umma_commit_warp(&s_empty[k_next]);
+                if (more_keys) v_next = next();
+                if (i + 1 < tiles[1]) scores(1, k_st, i + 2 == tiles[1]);
+                if (more_keys) umma_commit_warp(&s_empty[k_st]);
+                v_st = v_next;
             }
+            if (!ok) break;
         }
-        __syncwarp();
     } else {
-        // ---- rows: thread `at` of four warps has row at of the tile
-        const int t = warp >> 2, at = threadIdx.x & 127;
+        // ---- rows: thread `in` of four warps has row `in` of the tile
+        const int t = warp >> 2, in = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 128 * t + lanes;
-        const int r = r0 + t * geo.rows + at, tok = r / p.group;
-        const bool is = at < geo.rows && tok < s.n;
-        int lo = 0, hi = INT32_MAX;         // a row that is none: any scores, never stored
-        if (is) row_keys(p, s, s.len - s.n + tok, lo, hi);
         const float c2 = p.scale * kLog2e;
-        float m = -INFINITY, l = 0.f;
-        bool ok = true;
-        const int mine = tiles[t];
+        int stage0 = 1;             // the ring's stage of the item's first V, and its parity
+        uint32_t turn0 = 0;
+        uint32_t par = 0;           // parity of the tile's next scores, weights and sums
+        for (int k = 0;; ++k) {
+            const Item& w = next_item(k);
+            if (!ok || w.more < 0) break;
+            if (w.more == 0) {
+                item_done(k);
+                continue;
+            }
+            const int r = w.r0 + t * geo.rows + in, tok = r / p.group;
+            const bool is = in < geo.rows && tok < w.s.n;
+            int lo = 0, hi = INT32_MAX;     // a row that is none: any scores, never stored
+            if (is) row_keys(p, w.s, w.s.len - w.s.n + tok, lo, hi);
+            // the keys that all the warp's rows see need no mask (a warp without rows
+            // still has its part in clearing V's edge)
+            const int all_lo = max(w.s.lo, __reduce_max_sync(0xffffffffu, lo));
+            const int all_hi = min(w.s.hi, __reduce_min_sync(0xffffffffu, hi));
+            float m = -INFINITY, l = 0.f;
+            const int mine = w.tiles[t], k0 = w.k0;
+            int v_st = stage0;              // the ring's stage of this tile of V
+            uint32_t v_turn = turn0;
 #pragma unroll 1
-        for (int i = 0; i < mine; ++i) {
-            const int j0 = (k0 + i) * kKeys;
-            ok = mbar_wait(&s_score[t], i & 1, p.status);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t v[128];
+            for (int i = 0; i < mine; ++i) {
+                const int j0 = (k0 + i) * kKeys;
+                ok = mbar_wait(&s_score[t], par, p.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                // Two passes over the scores, 32 at a time with the next 32 on their
+                // way: the maximum, then the weights.  They come from TMEM twice
+                // (about 90 cycles a pass), for short loops: straight-line code over
+                // 128 scores runs from beyond the nearest instruction cache.
+                uint32_t x[32], y[32];
+                tmem_ld32(ts, x);
+                const bool edge = j0 < all_lo || j0 + kKeys > all_hi;
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto maxima = [&](uint32_t* v, int c) {
+                    if (edge) {
+                        // keys [from, to) of the 32 are seen; what is not goes back as -inf
+                        const int from = max(0, min(32, lo - j0 - c)), to_ = max(0, min(32, hi - j0 - c));
+                        const uint32_t seen = (to_ == 32 ? 0xffffffffu : (1u << to_) - 1) & ~(from == 32 ? 0xffffffffu : (1u << from) - 1);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, v + 32 * c);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 8; ++c) tmem_ld_regs(v + 16 * c);
-            if (__any_sync(0xffffffffu, j0 < lo || j0 + kKeys > hi)) {
-#pragma unroll
-                for (int j = 0; j < 128; ++j)
-                    if (j0 + j < lo || j0 + j >= hi) v[j] = 0xff800000u;      // -inf
-            }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int j = 0; j < 128; j += 2)
-                top[j >> 1 & 3] = max3(top[j >> 1 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            const bool raise = mx > m && (m == -INFINITY || (mx - m) * c2 > kRaise);
-            if (__any_sync(0xffffffffu, raise)) {
-                const float f = raise ? exp2_fast((m - mx) * c2) : 1.f;
-                if (raise) m = mx;
-                l *= f;
-                if (i > 0) {
-                    ok = mbar_wait(&s_sum[t], (i - 1) & 1, p.status);
-                    tc_fence_after();
-                    for (int c = 0; c < DP / 16; ++c) {
-                        uint32_t w[16];
-                        tmem_ld16(to + 16 * c, w);
-                        tmem_ld_wait();
-                        tmem_ld_regs(w);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * f);
-                        tmem_st16(to + 16 * c, w);
+                        for (int j = 0; j < 32; ++j)
+                            if (!(seen >> j & 1)) v[j] = 0xff800000u;
+                        tmem_st32(ts + c, v);
                     }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        top[j >> 1 & 3] = max3(top[j >> 1 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                };
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64) {
+                    tmem_ld_wait();
+                    tmem_ld_regs(x);
+                    tmem_ld_regs(x + 16);
+                    tmem_ld32(ts + c + 32, y);
+                    maxima(x, c);
+                    tmem_ld_wait();
+                    tmem_ld_regs(y);
+                    tmem_ld_regs(y + 16);
+                    if (c == 0) tmem_ld32(ts + 64, x);
+                    maxima(y, c + 32);
+                }
+                if (edge) {
                     tmem_st_wait();
+                    // values that no row of the item sees may be anything: 0 x NaN must
+                    // not reach the sums.  The products of the first tile of rows come first.
+                    if ((j0 < w.s.lo || j0 + kKeys > w.s.hi) && (t == 0 || i >= w.tiles[0])) {
+                        mbar_wait(&s_full[v_st], v_turn, p.status);
+                        if (j0 + in < w.s.lo || j0 + in >= w.s.hi)
+#pragma unroll 1
+                            for (int e = 0; e < DP / 8; ++e)
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                 ring + v_st * C::TILE + e / 8 * C::HALF + in * 128 + e % 8 * 16),
+                                             "r"(0)
+                                             : "memory");
+                        fence_proxy_async_smem();
+                    }
+                }
+                tmem_ld32(ts, x);
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                const bool raise = mx > m && (m == -INFINITY || (mx - m) * c2 > kRaise);
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float f = raise ? exp2_fast((m - mx) * c2) : 1.f;
+                    if (raise) m = mx;
+                    l *= f;
+                    if (i > 0) {
+                        mbar_wait(&s_sum[t], par ^ 1, p.status);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < DP; c += 16) {
+                            tmem_ld16(to + c, y);
+                            tmem_ld_wait();
+                            tmem_ld_regs(y);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                            tmem_st16(to + c, y);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float mb = m == -INFINITY ? 0.f : -m * c2;
+                const f32x2 cc = {c2, c2}, bb = {mb, mb};
+                f32x2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                auto weights = [&](uint32_t* v, int c) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const f32x2 u = fma2({__uint_as_float(v[j]), __uint_as_float(v[j + 1])}, cc, bb);
+                        const f32x2 e = {exp2_fast(u.x), exp2_fast(u.y)};
+                        sum[j >> 1 & 1] = add2(sum[j >> 1 & 1], e);
+                        v[j / 2] = pack2<BF16>(e.x, e.y);
+                    }
+                    tmem_st16(ts + c / 2, v);       // over scores that have been read
+                };
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64) {
+                    tmem_ld_wait();
+                    tmem_ld_regs(x);
+                    tmem_ld_regs(x + 16);
+                    tmem_ld32(ts + c + 32, y);
+                    weights(x, c);
+                    tmem_ld_wait();
+                    tmem_ld_regs(y);
+                    tmem_ld_regs(y + 16);
+                    if (c == 0) tmem_ld32(ts + 64, x);
+                    weights(y, c + 32);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_weight[t][c >> 6]);
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                par ^= 1;
+                if ((v_st += 2) >= C::STAGES) {
+                    v_st -= C::STAGES;
+                    v_turn ^= 1;
                 }
             }
-            // values that no row of the block sees may be anything: 0 x NaN must
-            // not reach the sums.  The products of the first tile of rows come first.
-            if ((j0 < s.lo || j0 + kKeys > s.hi) && (t == 0 || i >= tiles[0])) {
-                const int d = 2 * i + 1;
-                ok = mbar_wait(&s_full[d % C::STAGES], d / C::STAGES & 1, p.status);
-                if (j0 + at < s.lo || j0 + at >= s.hi)
-                    for (int e = 0; e < DP / 8; ++e)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         ring + d % C::STAGES * C::TILE + e / 8 * C::HALF + at * 128 + e % 8 * 16),
-                                     "r"(0)
-                                     : "memory");
-                fence_proxy_async_smem();
-            }
-            const float mb = m == -INFINITY ? 0.f : -m * c2;
-            const f32x2 cc = {c2, c2}, bb = {mb, mb};
-            f32x2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            // the next item's first V
+            stage0 += 2 * w.n;
+            turn0 ^= stage0 / C::STAGES & 1;
+            stage0 %= C::STAGES;
+            if (mine > 0) ok = ok && mbar_wait(&s_sum[t], par ^ 1, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const int D = p.c.dim, head = w.kvh * p.group + r % p.group;
+            const int64_t row = (int64_t)(w.s.t0 + tok) * p.heads + head;
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+            // 32 bytes of its row at a time from each thread: whole sectors
+            T* out = static_cast<T*>(p.out) + (int64_t)(w.s.t0 + tok) * p.ldo + head * D;
+            float* po = part.o + ((int64_t)w.split * p.b.n_tokens * p.heads + row) * D;
+            const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.ldo * 2) & 31) == 0;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                uint32_t y[16];
+                if (mine > 0) {
+                    tmem_ld16(to + c, y);
+                    tmem_ld_wait();
+                    tmem_ld_regs(y);
+                } else {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                for (int j = 64 * c; j < 64 * c + 64; j += 2) {
-                    const f32x2 x = fma2({__uint_as_float(v[j]), __uint_as_float(v[j + 1])}, cc, bb);
-                    const f32x2 w = {exp2_fast(x.x), exp2_fast(x.y)};
-                    sum[j >> 1 & 1] = add2(sum[j >> 1 & 1], w);
-                    v[j / 2] = pack2<BF16>(w.x, w.y);
+                    for (int j = 0; j < 16; ++j) y[j] = 0u;
                 }
-                tmem_st32(ts + 32 * c, v + 32 * c);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_weight[t][c]);
-            }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        }
-        if (mine > 0) ok = ok && mbar_wait(&s_sum[t], (mine - 1) & 1, p.status);
-        ok = __all_sync(0xffffffffu, ok);
-        tc_fence_after();
-        const int D = p.c.dim, head = kvh * p.group + r % p.group;
-        const int64_t row = (int64_t)(s.t0 + tok) * p.heads + head;
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        T* out = static_cast<T*>(p.out) + (int64_t)(s.t0 + tok) * p.ldo + head * D;
-        float* po = part.o + ((int64_t)split * p.b.n_tokens * p.heads + row) * D;
-        for (int c = 0; c < DP / 16; ++c) {
-            uint32_t w[16];
-            if (mine > 0 && ok) {
-                tmem_ld16(to + 16 * c, w);
-                tmem_ld_wait();
-                tmem_ld_regs(w);
-            } else {
+                if (!is) continue;
+                if (part.splits > 1) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = 0u;
-            }
-            if (!is || 16 * c >= D) continue;
-            if (part.splits > 1) {
-#pragma unroll
-                for (int j = 0; j < 16; j += 4)
-                    *reinterpret_cast<uint4*>(po + 16 * c + j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
-            } else {
-                uint32_t h[8];
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<uint4*>(po + c + j) = make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                    continue;
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    h[j] = l == 0.f ? 0u : pack2<BF16>(__uint_as_float(w[2 * j]) * inv, __uint_as_float(w[2 * j + 1]) * inv);
-                *reinterpret_cast<uint4*>(out + 16 * c) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(out + 16 * c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+                    y[j] = l == 0.f ? 0u : pack2<BF16>(__uint_as_float(y[2 * j]) * inv, __uint_as_float(y[2 * j + 1]) * inv);
+                if (wide) {
+                    store32(out + c, y);
+                } else {
+                    *reinterpret_cast<uint4*>(out + c) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+                }
             }
+            if (is && part.splits > 1)
+                part.ml[(int64_t)w.split * p.b.n_tokens * p.heads + row] = make_float2(l == 0.f ? -INFINITY : m * c2, l);
+            else if (is && p.lse)
+                p.lse[row] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+            tc_fence_before();
+            item_done(k);
         }
-        if (is && part.splits > 1)
-            part.ml[(int64_t)split * p.b.n_tokens * p.heads + row] = make_float2(l == 0.f ? -INFINITY : m * c2, l);
-        else if (is && p.lse)
-            p.lse[row] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
     }
     tc_fence_before();
     __syncthreads();

@@ -51,6 +51,7 @@ struct AttnParams {
     float scale;
     int causal;
     int64_t window;          // 0: none
+    int few_rows;            // sequences of up to so many rows (tokens x group) take the few-rows form
     int* status;
 };
 
