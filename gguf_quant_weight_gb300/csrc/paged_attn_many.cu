@@ -5,9 +5,8 @@
 // query heads of the group, token by token -- through their keys, 128 at a
 // time.  Per tile of keys
 //   S = Q K^T   both operands from shared memory, 128 x 128 sums in TMEM
-//   P = exp2(c S - c m), c = scale log2 e: one thread to a row, so a row's
-//               maximum and sum take no exchange; the weights, in 16 bits,
-//               replace the scores in TMEM
+//   P = exp2(c S - c m), c = scale log2 e: two threads to a row, 64 scores each
+//               in registers; the weights, in 16 bits, replace the scores in TMEM
 //   O += P V    P from TMEM, V from shared memory as it lies in the cache
 //               (its rows are the keys: an MN-major operand), sums in TMEM.
 // While one tile's threads take exponentials, the tensor cores work on the
@@ -15,7 +14,7 @@
 // pass it by 2^8: below that the weights and sums stay far from overflow and
 // equally precise, and O keeps its scale; so O is rescaled a few times in all.
 //
-// Warps 0-3 and 4-7: the two tiles' rows; warp 8 issues copies, warp 9 products.
+// Warps 0-7 and 8-15: the two tiles' rows; warp 16 issues copies, warp 17 products.
 // A block that is done takes over one that has not begun (its index comes from
 // the launch's own queue), so its copies and products of the next tiles start
 // while the last rows are written; blocks stand in the order of their work, the
@@ -28,7 +27,7 @@ namespace gg {
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 576;
 constexpr int kKeys = 128;          // keys of a tile
 constexpr float kRaise = 8.f;       // log2 of how far scores may pass the maximum in use
 
@@ -36,7 +35,7 @@ template <int DP> struct ManyCfg {
     static constexpr int HALF = 128 * 128;                 // bytes of 128 rows x 64 values
     static constexpr int TILE = DP / 64 * HALF;            // 128 rows x DP values
     static constexpr int STAGES = DP == 128 ? 5 : 8;
-    static constexpr int SMEM = (2 + STAGES) * TILE + 1024;
+    static constexpr int SMEM = (2 + STAGES) * TILE;       // 224 KB at 128 values; the static part has 3 KB
 };
 
 template <bool BF16> struct Elem { using T = __half; };
@@ -130,17 +129,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmV, const AttnParams p, const Partials part, const Geometry geo) {
     using C = ManyCfg<DP>;
     using T = typename Elem<BF16>::T;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     // copies of K and V; Q; scores, weights (halves) and sums of a tile; the next block's index
     __shared__ __align__(8) uint64_t s_full[C::STAGES], s_empty[C::STAGES], s_q[2], s_qfree[2], s_score[2], s_weight[2][2],
         s_sum[2], s_next, s_item[2], s_read[2];
     __shared__ uint4 s_answer;
     __shared__ Item s_work[2];
+    __shared__ float s_pair[2][2][128];          // two threads of a row
     __shared__ uint32_t s_tmem;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sq = smem_u32(base), ring = sq + 2 * C::TILE;
+    const uint32_t sq = smem_u32(smem_raw), ring = sq + 2 * C::TILE;
 
+    if (sq & 1023) {            // the swizzle's unit; the alignment asked for gives it
+        if (threadIdx.x == 0) report(p.status, GGUF_ERR_CUDA);
+        return;
+    }
     if (threadIdx.x == 0) {
         prefetch_tmap(&tmQ);
         prefetch_tmap(&tmK);
@@ -157,12 +160,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s_weight[i][1], 4);
             mbar_init(&s_sum[i], 1);
             mbar_init(&s_item[i], 1);
-            mbar_init(&s_read[i], 9);                                // warps that read it
+            mbar_init(&s_read[i], 17);                               // warps that read it
         }
         mbar_init(&s_next, 1);
         fence_mbar_init();
     }
-    if (warp == 9) tmem_alloc(&s_tmem, 512);
+    if (warp == 17) tmem_alloc(&s_tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
 
     bool ok = true;
-    // the k-th item of this block, as warp 8 found it
+    // the k-th item of this block, as warp 16 found it
     auto next_item = [&](int k) -> const Item& {
         ok = mbar_wait(&s_item[k & 1], k >> 1 & 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&s_read[k & 1]);
     };
 
-    if (warp == 8) {
+    if (warp == 16) {
         // ---- copies: Q, then K and V of each tile of keys through the ring
         const int nbox = kKeys / geo.box;    // boxes of a tile: a page each, or half of one
         int st = 0, quse[2] = {0, 0};        // the ring's next stage; copies of Q so far
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (quse[t] > 0) mbar_wait(&s_q[t], quse[t] - 1 & 1, p.status);
             if (!ok) mbar_wait(&s_next, 0, p.status), mbar_wait(&s_next, 1, p.status);
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ---- products.  The warp's own instructions are what the tensor cores
         // wait for between products: it goes through them together, descriptors
         // advance by additions, and nothing is divided.
@@ -354,14 +357,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
         }
     } else {
-        // ---- rows: thread `in` of four warps has row `in` of the tile
-        const int t = warp >> 2, in = threadIdx.x & 127;
+        // ---- rows: two threads to a row, in warps of the same TMEM lanes; thread
+        // (in, half) has the row's scores 64 half .. 64 half + 63
+        const int t = warp >> 3, half = warp >> 2 & 1, in = 32 * (warp & 3) + lane, pair = 1 + t * 4 + (warp & 3);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 128 * t + lanes;
         const float c2 = p.scale * kLog2e;
         int stage0 = 1;             // the ring's stage of the item's first V, and its parity
         uint32_t turn0 = 0;
         uint32_t par = 0;           // parity of the tile's next scores, weights and sums
+        // the row's two threads' values, to both
+        auto exchange = [&](float x) {
+            s_pair[t][half][in] = x;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+            return s_pair[t][half ^ 1][in];
+        };
         for (int k = 0;; ++k) {
             const Item& w = next_item(k);
             if (!ok || w.more < 0) break;
@@ -388,59 +398,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                // Two passes over the scores, 32 at a time with the next 32 on their
-                // way: the maximum, then the weights.  They come from TMEM twice
-                // (about 90 cycles a pass), for short loops: straight-line code over
-                // 128 scores runs from beyond the nearest instruction cache.
-                uint32_t x[32], y[32];
-                tmem_ld32(ts, x);
-                const bool edge = j0 < all_lo || j0 + kKeys > all_hi;
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                auto maxima = [&](uint32_t* v, int c) {
-                    if (edge) {
-                        // keys [from, to) of the 32 are seen; what is not goes back as -inf
-                        const int from = max(0, min(32, lo - j0 - c)), to_ = max(0, min(32, hi - j0 - c));
-                        const uint32_t seen = (to_ == 32 ? 0xffffffffu : (1u << to_) - 1) & ~(from == 32 ? 0xffffffffu : (1u << from) - 1);
+                uint32_t v[64];
+                tmem_ld32(ts + 64 * half, v);
+                tmem_ld32(ts + 64 * half + 32, v + 32);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 64; c += 16) tmem_ld_regs(v + c);
+                if (j0 < all_lo || j0 + kKeys > all_hi) {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        // keys [from, to) of the 32 are seen
+                        const int j1 = j0 + 64 * half + c, from = max(0, min(32, lo - j1)), end = max(0, min(32, hi - j1));
+                        const uint32_t seen = (end == 32 ? 0xffffffffu : (1u << end) - 1) & ~(from == 32 ? 0xffffffffu : (1u << from) - 1);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (!(seen >> j & 1)) v[j] = 0xff800000u;
-                        tmem_st32(ts + c, v);
+                            if (!(seen >> j & 1)) v[c + j] = 0xff800000u;         // -inf
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        top[j >> 1 & 3] = max3(top[j >> 1 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                };
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 64) {
-                    tmem_ld_wait();
-                    tmem_ld_regs(x);
-                    tmem_ld_regs(x + 16);
-                    tmem_ld32(ts + c + 32, y);
-                    maxima(x, c);
-                    tmem_ld_wait();
-                    tmem_ld_regs(y);
-                    tmem_ld_regs(y + 16);
-                    if (c == 0) tmem_ld32(ts + 64, x);
-                    maxima(y, c + 32);
-                }
-                if (edge) {
-                    tmem_st_wait();
                     // values that no row of the item sees may be anything: 0 x NaN must
-                    // not reach the sums.  The products of the first tile of rows come first.
+                    // not reach the sums.  The products of the first tile of rows come
+                    // first, and those of 64 keys wait for the warps that clear them here.
                     if ((j0 < w.s.lo || j0 + kKeys > w.s.hi) && (t == 0 || i >= w.tiles[0])) {
                         mbar_wait(&s_full[v_st], v_turn, p.status);
-                        if (j0 + in < w.s.lo || j0 + in >= w.s.hi)
+                        const int row = 64 * half + (in >> 1);
+                        if (j0 + row < w.s.lo || j0 + row >= w.s.hi)
 #pragma unroll 1
-                            for (int e = 0; e < DP / 8; ++e)
+                            for (int e = in & 1; e < DP / 8; e += 2)
                                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                                 ring + v_st * C::TILE + e / 8 * C::HALF + in * 128 + e % 8 * 16),
+                                                 ring + v_st * C::TILE + e / 8 * C::HALF + row * 128 + e % 8 * 16),
                                              "r"(0)
                                              : "memory");
                         fence_proxy_async_smem();
                     }
                 }
-                tmem_ld32(ts, x);
-                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 64; j += 2)
+                    top[j >> 1 & 3] = max3(top[j >> 1 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // (and both have their scores: weights may replace them.  The next value
+                // follows products that needed both threads' weights: this one is read.)
+                mx = fmaxf(mx, exchange(mx));
                 const bool raise = mx > m && (m == -INFINITY || (mx - m) * c2 > kRaise);
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? exp2_fast((m - mx) * c2) : 1.f;
@@ -450,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_wait(&s_sum[t], par ^ 1, p.status);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < DP; c += 16) {
+                        for (int c = 16 * half; c < DP; c += 32) {
+                            uint32_t y[16];
                             tmem_ld16(to + c, y);
                             tmem_ld_wait();
                             tmem_ld_regs(y);
@@ -464,33 +462,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float mb = m == -INFINITY ? 0.f : -m * c2;
                 const f32x2 cc = {c2, c2}, bb = {mb, mb};
                 f32x2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-                auto weights = [&](uint32_t* v, int c) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const f32x2 u = fma2({__uint_as_float(v[j]), __uint_as_float(v[j + 1])}, cc, bb);
-                        const f32x2 e = {exp2_fast(u.x), exp2_fast(u.y)};
-                        sum[j >> 1 & 1] = add2(sum[j >> 1 & 1], e);
-                        v[j / 2] = pack2<BF16>(e.x, e.y);
-                    }
-                    tmem_st16(ts + c / 2, v);       // over scores that have been read
-                };
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 64) {
-                    tmem_ld_wait();
-                    tmem_ld_regs(x);
-                    tmem_ld_regs(x + 16);
-                    tmem_ld32(ts + c + 32, y);
-                    weights(x, c);
-                    tmem_ld_wait();
-                    tmem_ld_regs(y);
-                    tmem_ld_regs(y + 16);
-                    if (c == 0) tmem_ld32(ts + 64, x);
-                    weights(y, c + 32);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_weight[t][c >> 6]);
+                for (int j = 0; j < 64; j += 2) {
+                    const f32x2 u = fma2({__uint_as_float(v[j]), __uint_as_float(v[j + 1])}, cc, bb);
+                    const f32x2 e = {exp2_fast(u.x), exp2_fast(u.y)};
+                    sum[j >> 1 & 1] = add2(sum[j >> 1 & 1], e);
+                    v[j / 2] = pack2<BF16>(e.x, e.y);
                 }
+                tmem_st32(ts + 32 * half, v);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_weight[t][half]);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 par ^= 1;
                 if ((v_st += 2) >= C::STAGES) {
@@ -505,6 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mine > 0) ok = ok && mbar_wait(&s_sum[t], par ^ 1, p.status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+            l += exchange(l);
+            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
             tc_fence_after();
             const int D = p.c.dim, head = w.kvh * p.group + r % p.group;
             const int64_t row = (int64_t)(w.s.t0 + tok) * p.heads + head;
@@ -514,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* po = part.o + ((int64_t)w.split * p.b.n_tokens * p.heads + row) * D;
             const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.ldo * 2) & 31) == 0;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
+            for (int c = 16 * half; c < D; c += 32) {
                 uint32_t y[16];
                 if (mine > 0) {
                     tmem_ld16(to + c, y);
@@ -541,9 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(y[4], y[5], y[6], y[7]);
                 }
             }
-            if (is && part.splits > 1)
+            if (!is || half != 0) {
+            } else if (part.splits > 1)
                 part.ml[(int64_t)w.split * p.b.n_tokens * p.heads + row] = make_float2(l == 0.f ? -INFINITY : m * c2, l);
-            else if (is && p.lse)
+            else if (p.lse)
                 p.lse[row] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
             tc_fence_before();
             item_done(k);
@@ -552,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 template <int DP, bool BF16>
