@@ -35,9 +35,9 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {   // NaN where one is
     float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -116,8 +116,10 @@ struct Partials {
 };
 
 struct AttnPlan {
-    int few;        // the few-rows form
+    int few;        // all sequences in the few-rows form
+    int mixed;      // those of few rows in it, the others in the many-rows form
     int tiles;      // row tiles of a sequence and key head (of 16 rows, or pairs of up to 128)
+    int few_tiles;  // mixed: row tiles of 16 of the sequences of few rows
     int cluster;    // few rows, small calls: blocks of a cluster that split the keys
     int blocks;     // few rows, large calls: blocks among whose warps all keys are dealt out; else 0
     int splits;     // many rows: shares of the keys, joined through the workspace where there are several

@@ -13,6 +13,7 @@ namespace gg {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kAtOnce = 8;
 
 template <class T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
@@ -31,14 +32,26 @@ __global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(const AttnParams
     for (int i = lane; i < part.splits; i += 32) top = fmaxf(top, part.ml[i * rows + row].x);
 #pragma unroll
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    for (int i = 0; i < part.splits; ++i) {
-        const float2 ml = part.ml[i * rows + row];
-        if (ml.x == -INFINITY) continue;
-        const float f = exp2_fast(ml.x - top);
-        sum += f * ml.y;
+    for (int i0 = 0; i0 < part.splits; i0 += kAtOnce) {        // so many splits' loads in flight
+        float2 ml[kAtOnce];
+        float v[kAtOnce][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (lane + 32 * k < D) o[k] += f * part.o[(i * rows + row) * D + lane + 32 * k];
+        for (int j = 0; j < kAtOnce; ++j) {
+            ml[j] = make_float2(-INFINITY, 0.f);
+            if (i0 + j >= part.splits) continue;
+            ml[j] = part.ml[(i0 + j) * rows + row];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[j][k] = lane + 32 * k < D ? part.o[((i0 + j) * rows + row) * D + lane + 32 * k] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            if (ml[j].x == -INFINITY) continue;
+            const float f = exp2_fast(ml[j].x - top);
+            sum += f * ml[j].y;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] += f * v[j][k];
+        }
     }
     T* out = static_cast<T*>(p.out) + t * p.ldo + h * D;
 #pragma unroll
@@ -47,7 +60,8 @@ __global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(const AttnParams
     if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
-constexpr int64_t kLineChunks = 4096;
+constexpr int kFewRows = 64;            // rows of a sequence up to which the few-rows form takes it
+constexpr int64_t kLineChunks = 4096;   // chunks of 16 keys from which a call deals its keys out to all warps
 
 // The form and the split of a call, from its sizes alone.
 AttnPlan make_plan(const AttnParams& p, int num_sms) {
@@ -55,11 +69,12 @@ AttnPlan make_plan(const AttnParams& p, int num_sms) {
     const int64_t rows = (int64_t)p.b.max_q * p.group;
     int64_t span = p.b.max_kv;                        // keys that a row tile may see
     if (p.window && p.causal) span = std::min<int64_t>(span, p.window + p.b.max_q);
-    a.few = rows <= 64;
+    const int64_t chunks = std::max<int64_t>(1, ceil_div(span, 16));
+    a.cluster = a.splits = 1;
+    a.few = rows <= kFewRows;
     if (a.few) {
         a.tiles = (int)ceil_div(rows, 16);
-        const int64_t pairs = (int64_t)p.b.n_seq * p.c.kv_heads * a.tiles, chunks = std::max<int64_t>(1, ceil_div(span, 16));
-        a.cluster = a.splits = 1;
+        const int64_t pairs = (int64_t)p.b.n_seq * p.c.kv_heads * a.tiles;
         if (pairs * chunks > kLineChunks) {
             a.blocks = 2 * num_sms;
         } else {
@@ -71,8 +86,13 @@ AttnPlan make_plan(const AttnParams& p, int num_sms) {
         a.tiles = (int)ceil_div(p.b.max_q, 2 * (128 / p.group));
         // the keys are split where the tiles alone leave SMs idle
         const int64_t units = std::max<int64_t>(1, ceil_div(span, 128)), pairs = (int64_t)p.b.n_seq * p.c.kv_heads * a.tiles;
-        a.cluster = 1;
         a.splits = (int)std::min(units, std::max<int64_t>(1, num_sms / pairs));
+        // among several sequences some may have few rows
+        a.mixed = p.b.n_seq > 1 && a.splits == 1 && p.group <= kFewRows;
+        if (a.mixed) {
+            a.few_tiles = (int)ceil_div((int64_t)(kFewRows / p.group) * p.group, 16);
+            while (a.cluster < 8 && 64 * a.cluster < chunks) a.cluster *= 2;      // about a thousand keys a block
+        }
     }
     return a;
 }
@@ -104,13 +124,15 @@ size_t paged_attn_workspace_bytes(const AttnParams& p, int num_sms) {
 int paged_attn_launch(const AttnParams& call, void* workspace, int num_sms, int pdl, cudaStream_t s) {
     AttnParams p = call;
     const AttnPlan a = make_plan(p, num_sms);
-    if (a.tiles * (a.few ? (int64_t)p.c.kv_heads : 1) > 65535) return GGUF_ERR_UNSUPPORTED;   // a grid's limit
-    p.few_rows = a.few ? INT32_MAX : 0;
+    if (a.tiles * (a.few ? (int64_t)p.c.kv_heads : 1) > 65535 || a.few_tiles * p.c.kv_heads > 65535) return GGUF_ERR_UNSUPPORTED;   // a grid's limit
+    p.few_rows = a.few ? INT32_MAX : a.mixed ? kFewRows : 0;
     if (a.few) return attn_few_launch(p, a, workspace, pdl, s);
     const int64_t rows = (int64_t)p.b.n_tokens * p.heads;
     Partials part{static_cast<float*>(workspace), nullptr, a.splits};
     part.ml = reinterpret_cast<float2*>(part.o + (int64_t)a.splits * rows * p.c.dim);
-    const int st = attn_many_launch(p, a, part, pdl, s);
+    int st = GGUF_OK;
+    if (a.mixed) st = attn_few_launch(p, a, workspace, pdl, s);
+    if (st == GGUF_OK) st = attn_many_launch(p, a, part, pdl, s);
     if (st != GGUF_OK || a.splits == 1) return st;
     const dim3 grid((unsigned)ceil_div(rows, kWarps));
     const cudaError_t e = p.c.bf16 ? launch_pdl(attn_join_kernel<__nv_bfloat16>, grid, dim3(32 * kWarps), 0, s, pdl, p, part)

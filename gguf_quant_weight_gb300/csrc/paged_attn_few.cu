@@ -255,7 +255,8 @@ __global__ void __launch_bounds__(kThreads)
 
     const int kvh = blockIdx.y / tiles, r0 = (blockIdx.y % tiles) * kRows;
     RowSpan s;
-    if (!row_span(p, blockIdx.z, r0, kRows, s, threadIdx.x == 0)) return;       // the whole cluster alike
+    // the whole cluster alike
+    if (!row_span(p, blockIdx.z, r0, kRows, s, threadIdx.x == 0) || !is_few(p, s.n)) return;
 
     // this block's chunks of 16 keys, in equal shares; the warps take them in turn
     const int c_lo = s.lo / kChunk, c_n = s.hi > s.lo ? (s.hi + kChunk - 1) / kChunk - c_lo : 0;
@@ -714,10 +715,13 @@ int launch_line(const AttnParams& p, const AttnPlan& plan, void* workspace, int 
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<DP>::SMEM) != cudaSuccess ||
         launch_pdl(f, dim3(plan.blocks), dim3(kThreads), FewCfg<DP>::SMEM, s, pdl, k, v, p, ws) != cudaSuccess)
         return GGUF_ERR_CUDA;
-    // few items, each cut into many shares: a block to 16 values of a row; else a block to an item
-    const bool many = plan.blocks * kWarps > 8 * (int64_t)p.b.n_seq * p.c.kv_heads * plan.tiles;
-    const int rb = many ? 1 : ws.rows, db = many ? 16 : p.c.dim;
-    const int threads = many ? kJoin : (int)ceil_div(rb * db / 4, 32) * 32;
+    // a block to a row of an item, with threads for four shares each; where few
+    // items are cut into a great many, a block to 16 values of a row
+    const int64_t cuts = plan.blocks * kWarps / ((int64_t)p.b.n_seq * p.c.kv_heads * plan.tiles) + 1;
+    const int rb = 1, db = cuts >= 64 ? 16 : p.c.dim;
+    int per = 1;
+    while (per < 16 && per * 4 < cuts) per *= 2;
+    const int threads = cuts >= 64 ? kJoin : (int)ceil_div(db / 4 * per, 32) * 32;
     return launch_pdl(attn_line_join_kernel<BF16>, dim3(p.c.kv_heads * plan.tiles, p.b.n_seq, ceil_div(ws.rows, rb) * (p.c.dim / db)),
                       dim3(threads), 0, s, pdl, p, ws, plan.blocks * kWarps, rb, db) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
 }
@@ -732,7 +736,8 @@ int launch_cluster(const AttnParams& p, const AttnPlan& plan, int pdl, cudaStrea
         cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return GGUF_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(plan.cluster, p.c.kv_heads * plan.tiles, p.b.n_seq);
+    const int tiles = plan.mixed ? plan.few_tiles : plan.tiles;
+    cfg.gridDim = dim3(plan.cluster, p.c.kv_heads * tiles, p.b.n_seq);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = FewCfg<DP>::SMEM;
     cfg.stream = s;
@@ -744,7 +749,7 @@ int launch_cluster(const AttnParams& p, const AttnPlan& plan, int pdl, cudaStrea
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, f, k, v, p, plan.tiles) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, f, k, v, p, tiles) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
 }
 
 }  // namespace

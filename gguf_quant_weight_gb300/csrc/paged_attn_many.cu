@@ -59,6 +59,7 @@ __device__ __forceinline__ void store32(void* to, const uint32_t* v) {   // 32 b
 struct Geometry {
     int rows;        // rows of a tile: whole tokens, at most 128
     int box;         // tokens of a cache box
+    int beside;      // the few-rows kernel was launched just before
 };
 
 // A pair of row tiles and its share of the keys, from a block's index (x, y, z):
@@ -171,7 +172,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     // all 512 columns, so the address is 0: S of the two tiles at 0 and 128, O at 256 and 384
     constexpr uint32_t tmem = 0;
-    pdl_wait();
+    // Beside the few-rows kernel of the same call, which has waited for what came
+    // before, this one waits at its end, so that what comes after waits for both.
+    if (!geo.beside) pdl_wait();
     pdl_launch_dependents();
 
     bool ok = true;
@@ -433,15 +436,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int j = 0; j < 64; j += 2)
-                    top[j >> 1 & 3] = max3(top[j >> 1 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    top[j >> 1 & 3] = max3_nan(top[j >> 1 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                float mx = max3_nan(max3_nan(top[0], top[1], top[2]), top[3], top[3]);
                 // (and both have their scores: weights may replace them.  The next value
                 // follows products that needed both threads' weights: this one is read.)
-                mx = fmaxf(mx, exchange(mx));
-                const bool raise = mx > m && (m == -INFINITY || (mx - m) * c2 > kRaise);
+                const float other = exchange(mx);
+                mx = max3_nan(mx, other, other);
+                const bool raise = !(mx <= m) && !((mx - m) * c2 <= kRaise);
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? exp2_fast((m - mx) * c2) : 1.f;
-                    if (raise) m = mx;
+                    if (raise) m = mx < INFINITY ? mx : NAN;     // the row has no finite sum: all of it is NaN
                     l *= f;
                     if (i > 0) {
                         mbar_wait(&s_sum[t], par ^ 1, p.status);
@@ -535,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             item_done(k);
         }
     }
+    if (geo.beside) pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -547,6 +552,7 @@ int launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int 
     const int tokens = 128 / p.group;
     geo.rows = tokens * p.group;
     geo.box = std::min(kKeys, 1 << p.c.page_shift);
+    geo.beside = plan.mixed;
     CUtensorMap q, k, v;
     if (make_q_map(&q, p, p.group, tokens) != GGUF_OK || make_kv_map(&k, p.c.k, p.c, geo.box) != GGUF_OK ||
         make_kv_map(&v, p.c.v, p.c, geo.box) != GGUF_OK)

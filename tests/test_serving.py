@@ -330,12 +330,23 @@ def test_attn_extreme_keys():
     near(lse.cpu().numpy(), rlse, "f32", 1e-4)
 
 
-def test_attn_nan_in_a_seen_key_reaches_only_its_sequence():
-    c = Case([(1, 20), (1, 20)], 1, 64, "bf16", page=16, seed=14)
-    c.v[int(c.pages[0, 0]), 0, 2, 7] = math.nan
-    q = c.values((2, 1, 64))
+@pytest.mark.parametrize("n", [1, 130])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+@pytest.mark.parametrize("where", range(12, 20))
+def test_attn_nan_in_a_seen_key_reaches_its_rows_alone(n, what, where):
+    # a value: one column of the rows that see it; a key: all of them, wherever it stands
+    c = Case([(n, n + 20), (n, n + 20)], 1, 64, "bf16", page=16, seed=14)
+    at = int(c.pages[0, where // 16]), 0, where % 16
+    q = c.values((2 * n, 1, 64)).abs() + 0.5
+    keep = c.v[at][7].clone()
+    c.v[at][7] = what
     out, _ = run_attn(c, q)
-    assert torch.isnan(out[0, 0, 7]) and torch.isfinite(out[1]).all()
+    assert not torch.isfinite(out[:n, 0, 7]).any() and torch.isfinite(out[n:]).all()
+    assert torch.isfinite(out[:n, 0, :7]).all() and torch.isfinite(out[:n, 0, 8:]).all()
+    c.v[at][7] = keep
+    c.k[at][:] = what
+    out, lse = run_attn(c, q)
+    assert torch.isnan(out[:n]).all() and torch.isfinite(out[n:]).all() and torch.isfinite(lse[n:]).all()
 
 
 def test_attn_strided_queries():
