@@ -90,19 +90,21 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// A box of 64 values x `rows` tokens of one head and page, swizzled in 128-byte rows.
+// One box of the cache, swizzled in 128-byte rows: values d.. of tokens slot..
 __device__ __forceinline__ void tma_load_kv(uint32_t smem_dst, const CUtensorMap* map, int d, int slot, int head,
                                             int page, uint64_t* bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::
             "r"(smem_dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(slot), "r"(head), "r"(page), "r"(smem_u32(bar))
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(slot), "r"(0), "r"(head), "r"(page), "r"(smem_u32(bar))
         : "memory");
 }
 
-// Tensor map over K or V: (d, slot, head, page), box 64 x rows x 1 x 1; values
-// past head_dim read as zeros.
-int make_kv_map(CUtensorMap* map, const void* base, const CacheParams& c, int rows);
+// Tensor map over K or V: (d, slot, block of 64 values, head, page), box 64 x
+// rows x blocks x 1 x 1.  With blocks = 1 the third dimension is nothing, and
+// values past head_dim read as zeros; with blocks = head_dim / 64 the box brings
+// whole heads, one block of 64 values after the other.
+int make_kv_map(CUtensorMap* map, const void* base, const CacheParams& c, int rows, int blocks);
 // Tensor map over q: (d, head, token), box 64 x heads x tokens.
 int make_q_map(CUtensorMap* map, const AttnParams& p, int heads, int tokens);
 
@@ -116,10 +118,10 @@ struct Partials {
 };
 
 struct AttnPlan {
-    int few;        // all sequences in the few-rows form
-    int mixed;      // those of few rows in it, the others in the many-rows form
-    int tiles;      // row tiles of a sequence and key head (of 16 rows, or pairs of up to 128)
-    int few_tiles;  // mixed: row tiles of 16 of the sequences of few rows
+    int few;        // few rows: of a tile (8 or 16); 0: all sequences in the many-rows form
+    int mixed;      // sequences of few rows in the few-rows form, the others in the many-rows form
+    int tiles;      // row tiles of a sequence and key head (or pairs of tiles of up to 128 rows)
+    int few_tiles;  // mixed: row tiles of the sequences of few rows
     int cluster;    // few rows, small calls: blocks of a cluster that split the keys
     int blocks;     // few rows, large calls: blocks among whose warps all keys are dealt out; else 0
     int splits;     // many rows: shares of the keys, joined through the workspace where there are several

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(const AttnParams
     if (p.lse && lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
-constexpr int kFewRows = 64;            // rows of a sequence up to which the few-rows form takes it
+constexpr int kFewRows = 16;            // rows of a sequence up to which the few-rows form takes it
 constexpr int64_t kLineChunks = 4096;   // chunks of 16 keys from which a call deals its keys out to all warps
 
 // The form and the split of a call, from its sizes alone.
@@ -71,9 +71,9 @@ AttnPlan make_plan(const AttnParams& p, int num_sms) {
     if (p.window && p.causal) span = std::min<int64_t>(span, p.window + p.b.max_q);
     const int64_t chunks = std::max<int64_t>(1, ceil_div(span, 16));
     a.cluster = a.splits = 1;
-    a.few = rows <= kFewRows;
-    if (a.few) {
-        a.tiles = (int)ceil_div(rows, 16);
+    if (rows <= kFewRows) {
+        a.few = rows <= 8 ? 8 : 16;
+        a.tiles = (int)ceil_div(rows, a.few);
         const int64_t pairs = (int64_t)p.b.n_seq * p.c.kv_heads * a.tiles;
         if (pairs * chunks > kLineChunks) {
             a.blocks = 2 * num_sms;
@@ -90,8 +90,9 @@ AttnPlan make_plan(const AttnParams& p, int num_sms) {
         // among several sequences some may have few rows
         a.mixed = p.b.n_seq > 1 && a.splits == 1 && p.group <= kFewRows;
         if (a.mixed) {
-            a.few_tiles = (int)ceil_div((int64_t)(kFewRows / p.group) * p.group, 16);
-            while (a.cluster < 8 && 64 * a.cluster < chunks) a.cluster *= 2;      // about a thousand keys a block
+            a.few = 16;
+            a.few_tiles = (int)ceil_div((int64_t)(kFewRows / p.group) * p.group, a.few);
+            while (a.cluster < 8 && 256 * a.cluster < chunks) a.cluster *= 2;     // about four thousand keys a block
         }
     }
     return a;
@@ -99,11 +100,12 @@ AttnPlan make_plan(const AttnParams& p, int num_sms) {
 
 }  // namespace
 
-int make_kv_map(CUtensorMap* map, const void* base, const CacheParams& c, int rows) {
-    const uint64_t dims[4] = {(uint64_t)c.dim, uint64_t(1) << c.page_shift, (uint64_t)c.kv_heads, (uint64_t)c.n_pages};
-    const uint64_t strides[3] = {(uint64_t)c.token_stride * 2, (uint64_t)c.head_stride * 2, (uint64_t)c.page_stride * 2};
-    const uint32_t box[4] = {64, (uint32_t)rows, 1, 1};
-    return make_tmap(map, base, c.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, dims,
+int make_kv_map(CUtensorMap* map, const void* base, const CacheParams& c, int rows, int blocks) {
+    const uint64_t dims[5] = {(uint64_t)(blocks > 1 ? 64 : c.dim), uint64_t(1) << c.page_shift, (uint64_t)blocks,
+                              (uint64_t)c.kv_heads, (uint64_t)c.n_pages};
+    const uint64_t strides[4] = {(uint64_t)c.token_stride * 2, 128, (uint64_t)c.head_stride * 2, (uint64_t)c.page_stride * 2};
+    const uint32_t box[5] = {64, (uint32_t)rows, (uint32_t)blocks, 1, 1};
+    return make_tmap(map, base, c.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, dims,
                      strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -124,9 +126,9 @@ size_t paged_attn_workspace_bytes(const AttnParams& p, int num_sms) {
 int paged_attn_launch(const AttnParams& call, void* workspace, int num_sms, int pdl, cudaStream_t s) {
     AttnParams p = call;
     const AttnPlan a = make_plan(p, num_sms);
-    if (a.tiles * (a.few ? (int64_t)p.c.kv_heads : 1) > 65535 || a.few_tiles * p.c.kv_heads > 65535) return GGUF_ERR_UNSUPPORTED;   // a grid's limit
-    p.few_rows = a.few ? INT32_MAX : a.mixed ? kFewRows : 0;
-    if (a.few) return attn_few_launch(p, a, workspace, pdl, s);
+    if (a.tiles * (a.few && !a.mixed ? (int64_t)p.c.kv_heads : 1) > 65535 || a.few_tiles * p.c.kv_heads > 65535) return GGUF_ERR_UNSUPPORTED;   // a grid's limit
+    p.few_rows = a.mixed ? kFewRows : a.few ? INT32_MAX : 0;
+    if (a.few && !a.mixed) return attn_few_launch(p, a, workspace, pdl, s);
     const int64_t rows = (int64_t)p.b.n_tokens * p.heads;
     Partials part{static_cast<float*>(workspace), nullptr, a.splits};
     part.ml = reinterpret_cast<float2*>(part.o + (int64_t)a.splits * rows * p.c.dim);

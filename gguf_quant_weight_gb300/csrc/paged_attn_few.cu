@@ -63,6 +63,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Element (i, j) of an 8 x 8 matrix of 16-bit values to (j, i); lane: row lane / 4, two values.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
@@ -79,7 +85,7 @@ struct LineSpace {
 };
 LineSpace line_space(const AttnParams& p, const AttnPlan& plan, void* base) {
     LineSpace ws;
-    ws.rows = (int)std::min<int64_t>(kRows, (int64_t)p.b.max_q * p.group);
+    ws.rows = (int)std::min<int64_t>(plan.few, (int64_t)p.b.max_q * p.group);
     const int64_t places = 2 * (int64_t)plan.blocks * kWarps * ws.rows;
     ws.o = static_cast<float*>(base);
     ws.ml = reinterpret_cast<float2*>(ws.o + places * p.c.dim);
@@ -92,24 +98,61 @@ template <> struct Elem<true> { using T = __nv_bfloat16; };
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Values of the 16 keys from j0 that no row sees may be anything, and 0 x NaN
+// must not reach the sums.
+template <int DP>
+__device__ __forceinline__ void clear_unseen(const RowSpan& s, uint32_t vb, int j0, int lane) {
+    using C = FewCfg<DP>;
+    if (j0 >= s.lo && j0 + kChunk <= s.hi) return;
+#pragma unroll 1
+    for (int e = lane; e < kChunk * 8 * (DP / 64); e += 32) {
+        const int row = e / 8 % kChunk;
+        if (j0 + row >= s.hi || j0 + row < s.lo)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + e / (8 * kChunk) * C::BOX + row * 128 +
+                                                                         e % 8 * 16),
+                         "r"(0)
+                         : "memory");
+    }
+    fence_proxy_async_smem();                                        // before the slot's next copy
+    __syncwarp();
+}
+
 // One warp's work on 16 rows: the queries as first operand (rows lane / 4 and
 // lane / 4 + 8), the sums, and the rows' statistics (m in units of ln 2).
 template <int DP, bool BF16>
 struct Rows16 {
     using C = FewCfg<DP>;
     using T = typename Elem<BF16>::T;
+    static constexpr int ROWS = 16;
     uint32_t q[DP / 16][4];
     float o[DP / 8][4];
     float m[2], l[2];
     int lo[2], hi[2];
+    int all_lo, all_hi;          // keys that every row sees
+
+    static __device__ __forceinline__ int row(int x, int lane) { return lane / 4 + 8 * x; }
+    // Whether this lane speaks for its rows' statistics.
+    static __device__ __forceinline__ bool speaks(int lane) { return lane % 4 == 0; }
+    // f(row's index x, d, value) for each of the lane's sums.
+    template <class F>
+    __device__ __forceinline__ void each(int lane, F f) const {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) {
+                f(x, 8 * i + lane % 4 * 2, o[i][2 * x]);
+                f(x, 8 * i + lane % 4 * 2 + 1, o[i][2 * x + 1]);
+            }
+    }
 
     __device__ __forceinline__ void begin(const AttnParams& p, const RowSpan& s, int kvh, int r0, int lane) {
         const int D = p.c.dim, steps = D / 16;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int r = r0 + lane / 4 + 8 * x, tok = r / p.group;
+            const int r = r0 + row(x, lane), tok = r / p.group;
             const bool is = tok < s.n;
-            lo[x] = hi[x] = 0;
+            lo[x] = 0;
+            hi[x] = INT32_MAX;           // a row that is none: zeros as queries, never stored
             if (is) row_keys(p, s, s.len - s.n + tok, lo[x], hi[x]);
             const T* src = static_cast<const T*>(p.q) + (int64_t)(s.t0 + tok) * p.ldq + (kvh * p.group + r % p.group) * D +
                            lane % 4 * 2;
@@ -121,6 +164,8 @@ struct Rows16 {
             m[x] = -INFINITY;
             l[x] = 0.f;
         }
+        all_lo = max(s.lo, __reduce_max_sync(0xffffffffu, max(lo[0], lo[1])));
+        all_hi = min(s.hi, __reduce_min_sync(0xffffffffu, min(hi[0], hi[1])));
 #pragma unroll
         for (int i = 0; i < DP / 8; ++i)
 #pragma unroll
@@ -130,19 +175,8 @@ struct Rows16 {
     // The 16 keys from j0 in the ring's slot at kb (K, then V).
     __device__ __forceinline__ void take(const RowSpan& s, uint32_t kb, int j0, float c2, int lane) {
         const uint32_t vb = kb + DP / 64 * C::BOX;
-        if (j0 + kChunk > s.hi || j0 < s.lo) {
-            // values that no row sees may be anything: 0 x NaN must not reach the sums
-            for (int e = lane; e < kChunk * 8 * (DP / 64); e += 32) {
-                const int row = e / 8 % kChunk;
-                if (j0 + row >= s.hi || j0 + row < s.lo)
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + e / (8 * kChunk) * C::BOX +
-                                                                                 row * 128 + e % 8 * 16),
-                                 "r"(0)
-                                 : "memory");
-            }
-            fence_proxy_async_smem();                                // before the slot's next copy
-            __syncwarp();
-        }
+        const bool edge = j0 < all_lo || j0 + kChunk > all_hi;
+        if (edge) clear_unseen<DP>(s, vb, j0, lane);
         float sc[2][4] = {};                                         // scores: two tiles of 8 keys
         const int kr = (lane & 7) + (lane >> 4) * 8, kc = lane >> 3 & 1;         // key, and which 8 values
 #pragma unroll
@@ -162,7 +196,7 @@ struct Rows16 {
                 for (int y = 0; y < 2; ++y) {
                     const int j = j0 + 8 * n + lane % 4 * 2 + y;
                     float& v = sc[n][2 * x + y];
-                    v = j >= lo[x] && j < hi[x] ? v * c2 : -INFINITY;
+                    v = edge && (j < lo[x] || j >= hi[x]) ? -INFINITY : v * c2;
                     t = fmaxf(t, v);
                 }
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
@@ -213,22 +247,151 @@ struct Rows16 {
     }
 };
 
+// The same on up to 8 rows, the products turned around: S^T = K Q^T has the 16
+// keys as rows and the 8 queries as columns, O^T = V^T P^T the values' places as
+// rows, so that no half of a 16-row product is spent on rows that are not there.
+// The weights pass from accumulator to second operand by transposing two 8 x 8
+// matrices.  Lane: queries lane % 4 * 2 + x.
+template <int DP, bool BF16>
+struct Rows8 {
+    using C = FewCfg<DP>;
+    using T = typename Elem<BF16>::T;
+    static constexpr int ROWS = 8;
+    uint32_t q[DP / 16][2];
+    float o[DP / 16][4];
+    float m[2], l[2];
+    int lo[2], hi[2];
+    int all_lo, all_hi;
+
+    static __device__ __forceinline__ int row(int x, int lane) { return lane % 4 * 2 + x; }
+    static __device__ __forceinline__ bool speaks(int lane) { return lane < 4; }
+    template <class F>
+    __device__ __forceinline__ void each(int lane, F f) const {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+                f(x, 16 * i + lane / 4, o[i][x]);
+                f(x, 16 * i + lane / 4 + 8, o[i][2 + x]);
+            }
+    }
+
+    __device__ __forceinline__ void begin(const AttnParams& p, const RowSpan& s, int kvh, int r0, int lane) {
+        const int D = p.c.dim, steps = D / 16;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int tok = (r0 + row(x, lane)) / p.group;
+            lo[x] = 0;
+            hi[x] = INT32_MAX;
+            if (tok < s.n) row_keys(p, s, s.len - s.n + tok, lo[x], hi[x]);
+            m[x] = -INFINITY;
+            l[x] = 0.f;
+        }
+        all_lo = max(s.lo, __reduce_max_sync(0xffffffffu, max(lo[0], lo[1])));
+        all_hi = min(s.hi, __reduce_min_sync(0xffffffffu, min(hi[0], hi[1])));
+        // as second operand: query lane / 4, values lane % 4 * 2 and 8 further
+        const int r = r0 + lane / 4, tok = r / p.group;
+        const bool is = tok < s.n;
+        const T* src = static_cast<const T*>(p.q) + (int64_t)(s.t0 + tok) * p.ldq + (kvh * p.group + r % p.group) * D +
+                       lane % 4 * 2;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                q[k][h] = is && k < steps ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8 * h) : 0u;
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    }
+
+    __device__ __forceinline__ void take(const RowSpan& s, uint32_t kb, int j0, float c2, int lane) {
+        const uint32_t vb = kb + DP / 64 * C::BOX;
+        const bool edge = j0 < all_lo || j0 + kChunk > all_hi;
+        if (edge) clear_unseen<DP>(s, vb, j0, lane);
+        float sc[2][4] = {};                                         // two sums, to halve the chain
+        const int kr = (lane & 7) + (lane >> 3 & 1) * 8, kc = lane >> 4;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+            uint32_t a[4];
+            ldsm4(kb + k / 4 * C::BOX + kr * 128 + (((k % 4 * 2 + kc) ^ (kr & 7)) << 4), a);
+            mma16816<BF16>(sc[k & 1], a, q[k][0], q[k][1]);
+        }
+        float e[4], top[2];                                          // [2 y + x]: key lane / 4 + 8 y
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int j = j0 + lane / 4 + 8 * y;
+                const float v = sc[0][2 * y + x] + sc[1][2 * y + x];
+                e[2 * y + x] = edge && (j < lo[x] || j >= hi[x]) ? -INFINITY : v * c2;
+            }
+            float t = fmaxf(e[x], e[2 + x]);
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+            top[x] = fmaxf(m[x], t);
+        }
+        if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float f = top[x] > m[x] ? exp2_fast(m[x] - top[x]) : 1.f;
+                m[x] = top[x];
+                l[x] *= f;
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    o[i][x] *= f;
+                    o[i][2 + x] *= f;
+                }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const float base = m[x] == -INFINITY ? 0.f : m[x];
+            e[x] = exp2_fast(e[x] - base);
+            e[2 + x] = exp2_fast(e[2 + x] - base);
+            l[x] += e[x] + e[2 + x];
+        }
+        const uint32_t w0 = transpose8(pack2<BF16>(e[0], e[1])), w1 = transpose8(pack2<BF16>(e[2], e[3]));
+        const int vr = (lane & 7) + (lane >> 4) * 8, vc = lane >> 3 & 1;
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+            uint32_t a[4];
+            ldsm4t(vb + i / 4 * C::BOX + vr * 128 + (((i % 4 * 2 + vc) ^ (vr & 7)) << 4), a);
+            mma16816<BF16>(o[i], a, w0, w1);
+        }
+    }
+
+    __device__ __forceinline__ void end() {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) l[x] += __shfl_xor_sync(0xffffffffu, l[x], d);
+    }
+};
+
+// Whether one copy brings 16 whole keys: the fewer copies, the nearer to the
+// memory's rate they come.  (A head that ends inside 64 values takes two, so
+// that what is past it reads as zeros.)
+__host__ __device__ inline bool whole_heads(const AttnParams& p) { return p.c.dim % 64 == 0; }
+
 template <int DP>
-__device__ __forceinline__ void load_chunk(uint32_t at, const CUtensorMap* tmK, const CUtensorMap* tmV, int slot, int kvh,
-                                           int page, uint64_t* bar) {
+__device__ __forceinline__ void load_chunk(uint32_t at, const CUtensorMap* tmK, const CUtensorMap* tmV, bool whole, int slot,
+                                           int kvh, int page, uint64_t* bar) {
     using C = FewCfg<DP>;
     mbar_arrive_expect_tx(bar, C::SLOT);
-#pragma unroll
-    for (int h = 0; h < DP / 64; ++h) {
-        tma_load_kv(at + h * C::BOX, tmK, 64 * h, slot, kvh, page, bar);
-        tma_load_kv(at + (DP / 64 + h) * C::BOX, tmV, 64 * h, slot, kvh, page, bar);
+    tma_load_kv(at, tmK, 0, slot, kvh, page, bar);
+    tma_load_kv(at + DP / 64 * C::BOX, tmV, 0, slot, kvh, page, bar);
+    if (DP == 128 && !whole) {
+        tma_load_kv(at + C::BOX, tmK, 64, slot, kvh, page, bar);
+        tma_load_kv(at + 3 * C::BOX, tmV, 64, slot, kvh, page, bar);
     }
 }
 
 // ------------------------------------------------------------------ keys split over a cluster
 
 // Block (x, y, z): the x-th block of the cluster, key head and row tile y, sequence z.
-template <int DP, bool BF16>
+template <int DP, bool BF16, class W>
 __global__ void __launch_bounds__(kThreads)
     attn_few_cluster_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const AttnParams p, int tiles) {
@@ -253,10 +416,10 @@ __global__ void __launch_bounds__(kThreads)
     pdl_wait();
     pdl_launch_dependents();
 
-    const int kvh = blockIdx.y / tiles, r0 = (blockIdx.y % tiles) * kRows;
+    const int kvh = blockIdx.y / tiles, r0 = (blockIdx.y % tiles) * W::ROWS;
     RowSpan s;
     // the whole cluster alike
-    if (!row_span(p, blockIdx.z, r0, kRows, s, threadIdx.x == 0) || !is_few(p, s.n)) return;
+    if (!row_span(p, blockIdx.z, r0, W::ROWS, s, threadIdx.x == 0) || !is_few(p, s.n)) return;
 
     // this block's chunks of 16 keys, in equal shares; the warps take them in turn
     const int c_lo = s.lo / kChunk, c_n = s.hi > s.lo ? (s.hi + kChunk - 1) / kChunk - c_lo : 0;
@@ -285,13 +448,13 @@ __global__ void __launch_bounds__(kThreads)
         have = page >= 0 ? have | bit : have & ~bit;
         if (page < 0 || lane != 0) return;
         const int st = i % C::STAGES;
-        load_chunk<DP>(slots + st * C::SLOT, &tmK, &tmV, ((c0 + warp + kWarps * i) & ((1 << per_page) - 1)) * kChunk, kvh,
+        load_chunk<DP>(slots + st * C::SLOT, &tmK, &tmV, whole_heads(p), ((c0 + warp + kWarps * i) & ((1 << per_page) - 1)) * kChunk, kvh,
                        page, &full[st]);
     };
 #pragma unroll 1
     for (int i = 0; i < C::STAGES; ++i) issue(i);
 
-    Rows16<DP, BF16> w;
+    W w;
     w.begin(p, s, kvh, r0, lane);
     const float c2 = p.scale * kLog2e;
     uint32_t phase = 0;                                              // bit st: the parity that slot st waits for
@@ -316,39 +479,38 @@ __global__ void __launch_bounds__(kThreads)
     }
 
     // join the block's warps: the sums at the largest maximum, in the ring's place
-    float* so = reinterpret_cast<float*>(ring);                      // [warp][row][DP], the block's result in warp 0's
+    constexpr int LD = DP + 4;
+    float* so = reinterpret_cast<float*>(ring);                      // [warp][row][LD], the block's result in warp 0's
     w.end();
 #pragma unroll
     for (int x = 0; x < 2; ++x)
-        if (lane % 4 == 0) {
-            s_m[warp][lane / 4 + 8 * x] = w.m[x];
-            s_l[warp][lane / 4 + 8 * x] = w.l[x];
+        if (W::speaks(lane)) {
+            s_m[warp][W::row(x, lane)] = w.m[x];
+            s_l[warp][W::row(x, lane)] = w.l[x];
         }
     __syncthreads();                                                 // every ring is done with
+    float f[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        const int row = lane / 4 + 8 * x;
+        const int row = W::row(x, lane);
         float top = -INFINITY;
 #pragma unroll
         for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_m[v][row]);
-        const float f = w.m[x] == -INFINITY ? 0.f : exp2_fast(w.m[x] - top);
-#pragma unroll
-        for (int d = 0; d < DP / 8; ++d)
-            *reinterpret_cast<float2*>(so + (warp * kRows + row) * DP + 8 * d + lane % 4 * 2) =
-                make_float2(w.o[d][2 * x] * f, w.o[d][2 * x + 1] * f);
-        if (warp == 0 && lane % 4 == 0) {
+        f[x] = w.m[x] == -INFINITY ? 0.f : exp2_fast(w.m[x] - top);
+        if (warp == 0 && W::speaks(lane)) {
             float sum = 0.f;
 #pragma unroll
             for (int v = 0; v < kWarps; ++v) sum += s_m[v][row] == -INFINITY ? 0.f : s_l[v][row] * exp2_fast(s_m[v][row] - top);
             s_ml[row] = make_float2(top, sum);
         }
     }
+    w.each(lane, [&](int x, int d, float v) { so[(warp * W::ROWS + W::row(x, lane)) * LD + d] = v * f[x]; });
     __syncthreads();
-    const int rows = min(kRows, s.n * p.group - r0);
-    for (int e = threadIdx.x; e < rows * DP; e += kThreads) {
+    const int rows = min(W::ROWS, s.n * p.group - r0);
+    for (int e = threadIdx.x; e < rows * LD; e += kThreads) {
         float v = so[e];
 #pragma unroll
-        for (int x = 1; x < kWarps; ++x) v += so[x * kRows * DP + e];
+        for (int x = 1; x < kWarps; ++x) v += so[x * W::ROWS * LD + e];
         so[e] = v;
     }
     if (cluster > 1) {
@@ -374,7 +536,7 @@ __global__ void __launch_bounds__(kThreads)
                 const uint32_t a = cluster_map(ml_a + 8 * row, c);
                 mc[c] = ld_cluster_f32(a);
                 lc[c] = ld_cluster_f32(a + 4);
-                vc[c] = ld_cluster_f32(cluster_map(so_a + 4 * (row * DP + d), c));
+                vc[c] = ld_cluster_f32(cluster_map(so_a + 4 * (row * LD + d), c));
             }
 #pragma unroll
             for (int c = 0; c < kCluster; ++c) top = fmaxf(top, mc[c]);
@@ -387,7 +549,7 @@ __global__ void __launch_bounds__(kThreads)
         } else {
             top = s_ml[row].x;
             sum = s_ml[row].y;
-            v = so[row * DP + d];
+            v = so[row * LD + d];
         }
         const int r = r0 + row, tok = s.t0 + r / p.group, head = kvh * p.group + r % p.group;
         put(static_cast<T*>(p.out) + (int64_t)tok * p.ldo + head * D + d, sum > 0.f ? v / sum : (sum == 0.f ? 0.f : sum));
@@ -416,14 +578,15 @@ __device__ __forceinline__ int share_of(int64_t total, int64_t x, int workers) {
     return (int)(((x + 1) * workers + total - 1) / total) - 1;
 }
 
-// Chunks of one row tile of a sequence; a tile that sees no key has one, empty.
+// (ROWS: rows of a tile.)  Chunks of one row tile of a sequence; a tile that sees no key has one, empty.
 __device__ __forceinline__ int tile_chunks(const RowSpan& s) {
     return s.hi > s.lo ? (s.hi + kChunk - 1) / kChunk - s.lo / kChunk : 1;
 }
+template <int ROWS>
 __device__ __forceinline__ int seq_chunks(const AttnParams& p, int seq) {
     int n = 0;
     RowSpan s;
-    for (int r0 = 0; row_span(p, seq, r0, kRows, s, false); r0 += kRows) n += tile_chunks(s);
+    for (int r0 = 0; row_span(p, seq, r0, ROWS, s, false); r0 += ROWS) n += tile_chunks(s);
     return n * p.c.kv_heads;
 }
 
@@ -435,9 +598,10 @@ struct Cursor {
 };
 
 // The first item with rows at or after (seq, r0) -- false at the end.
+template <int ROWS>
 __device__ __forceinline__ bool settle(const AttnParams& p, Cursor& k, int seq, int r0) {
     for (; seq < p.b.n_seq; ++seq, r0 = 0)
-        if (row_span(p, seq, r0, kRows, k.s, false)) {
+        if (row_span(p, seq, r0, ROWS, k.s, false)) {
             k.r0 = r0;
             k.n = tile_chunks(k.s);
             k.kvh = k.c = 0;
@@ -445,13 +609,14 @@ __device__ __forceinline__ bool settle(const AttnParams& p, Cursor& k, int seq, 
         }
     return false;
 }
+template <int ROWS>
 __device__ __forceinline__ bool next_item(const AttnParams& p, Cursor& k) {
     k.c = 0;
     if (++k.kvh < p.c.kv_heads) return true;
-    return settle(p, k, k.s.seq, k.r0 + kRows);
+    return settle<ROWS>(p, k, k.s.seq, k.r0 + ROWS);
 }
 
-template <int DP, bool BF16>
+template <int DP, bool BF16, class W>
 __global__ void __launch_bounds__(kThreads)
     attn_few_line_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p,
                          const LineSpace ws) {
@@ -476,49 +641,56 @@ __global__ void __launch_bounds__(kThreads)
     pdl_wait();
     pdl_launch_dependents();
 
-    // the line's length, then the sequence in which each warp's share begins
-    int64_t total = 0;
+    // the line's length, then the sequence in which each warp's share begins: one
+    // reading of the batch's arrays where a block's threads cover the sequences
+    int64_t total = 0, before = 0, own = 0;
     int workers = 0;
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-        const int64_t length = total;
-        workers = (int)min((int64_t)(gridDim.x * kWarps), length);
-        total = 0;
-#pragma unroll 1
-        for (int b0 = 0; b0 < p.b.n_seq; b0 += kThreads) {
-            const int b = b0 + threadIdx.x;
-            int64_t sum = b < p.b.n_seq ? seq_chunks(p, b) : 0;
-            const int64_t own = sum;
+    auto scan = [&](int b0) {
+        const int b = b0 + threadIdx.x;
+        own = b < p.b.n_seq ? seq_chunks<W::ROWS>(p, b) : 0;
+        int64_t sum = own;
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += v;
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += v;
+        }
+        if (lane == 31) s_sum[warp] = sum;
+        __syncthreads();
+        before = total + sum - own;
+        for (int v = 0; v < kWarps; ++v) {
+            if (v < warp) before += s_sum[v];
+            total += s_sum[v];
+        }
+        __syncthreads();
+    };
+    auto find = [&](int b0, int64_t length) {
+        const int b = b0 + threadIdx.x;
+        workers = (int)min((int64_t)(gridDim.x * kWarps), length);
+        for (int v = 0; v < kWarps && blockIdx.x * kWarps + v < workers; ++v) {
+            const int64_t x = share_begin(length, blockIdx.x * kWarps + v, workers);
+            if (own && before <= x && x < before + own) {
+                s_seq[v] = b;
+                s_at[v] = x - before;
             }
-            if (lane == 31) s_sum[warp] = sum;
-            __syncthreads();
-            int64_t before = total + sum - own;
-            for (int v = 0; v < kWarps; ++v) {
-                if (v < warp) before += s_sum[v];
-                total += s_sum[v];
-            }
-            if (pass == 1) {
-                for (int v = 0; v < kWarps; ++v) {
-                    if (blockIdx.x * kWarps + v >= workers) break;
-                    const int64_t x = share_begin(length, blockIdx.x * kWarps + v, workers);
-                    if (own && before <= x && x < before + own) {
-                        s_seq[v] = b;
-                        s_at[v] = x - before;
-                    }
-                }
-                if (blockIdx.x == 0 && b < p.b.n_seq) {
-                    ws.begin[b] = before;
-                    RowSpan s;
-                    row_span(p, b, 0, kRows, s, true);               // reports what is out of range
-                }
-            }
-            __syncthreads();
+        }
+        if (blockIdx.x == 0 && b < p.b.n_seq) {
+            ws.begin[b] = before;
+            RowSpan s;
+            row_span(p, b, 0, W::ROWS, s, true);                     // reports what is out of range
+        }
+    };
+    for (int b0 = 0; b0 < p.b.n_seq; b0 += kThreads) scan(b0);
+    if (p.b.n_seq <= kThreads) {
+        find(0, total);
+    } else {
+        const int64_t length = total;
+        total = 0;
+        for (int b0 = 0; b0 < p.b.n_seq; b0 += kThreads) {
+            scan(b0);
+            find(b0, length);
         }
     }
+    __syncthreads();
     if (blockIdx.x == 0 && threadIdx.x == 0) ws.begin[p.b.n_seq] = total;
     if (me >= workers) return;
     const int64_t x0 = share_begin(total, me, workers);
@@ -528,10 +700,10 @@ __global__ void __launch_bounds__(kThreads)
     Cursor use;
     {
         int64_t at = s_at[warp];
-        settle(p, use, s_seq[warp], 0);
+        settle<W::ROWS>(p, use, s_seq[warp], 0);
         while (at >= (int64_t)use.n * p.c.kv_heads) {
             at -= (int64_t)use.n * p.c.kv_heads;
-            settle(p, use, use.s.seq, use.r0 + kRows);
+            settle<W::ROWS>(p, use, use.s.seq, use.r0 + W::ROWS);
         }
         use.kvh = (int)(at / use.n);
         use.c = (int)(at - (int64_t)use.kvh * use.n);
@@ -561,11 +733,11 @@ __global__ void __launch_bounds__(kThreads)
         const int page = __shfl_sync(0xffffffffu, page_of, get.c - page_from);
         have = page >= 0 ? have | 1u << st_get : have & ~(1u << st_get);
         if (page >= 0 && lane == 0)
-            load_chunk<DP>(slots + st_get * C::SLOT, &tmK, &tmV, ((first + get.c) & ((1 << per_page) - 1)) * kChunk, get.kvh,
+            load_chunk<DP>(slots + st_get * C::SLOT, &tmK, &tmV, whole_heads(p), ((first + get.c) & ((1 << per_page) - 1)) * kChunk, get.kvh,
                            page, &full[st_get]);
         st_get = st_get + 1 == C::STAGES ? 0 : st_get + 1;
         if (--to_get && ++get.c == get.n) {
-            next_item(p, get);
+            next_item<W::ROWS>(p, get);
             page_from = -1;
         }
     };
@@ -577,7 +749,7 @@ __global__ void __launch_bounds__(kThreads)
     uint32_t phase = 0;
     int st = 0;
     bool inside = use.c > 0;                                         // the share begins inside an item
-    Rows16<DP, BF16> w;
+    W w;
     w.begin(p, use.s, use.kvh, use.r0, lane);
 #pragma unroll 1
     while (left > 0) {
@@ -596,30 +768,23 @@ __global__ void __launch_bounds__(kThreads)
         w.end();
         const bool whole = !inside && use.c == use.n;
         const int64_t place = 2 * me + (inside ? 0 : 1);
+        int64_t to[2];                                               // where the lane's rows go, -1: nowhere
+        float inv[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int row = lane / 4 + 8 * x, r = use.r0 + row;
+            const int row = W::row(x, lane), r = use.r0 + row, tok = use.s.t0 + r / p.group, head = use.kvh * p.group + r % p.group;
+            to[x] = -1;
+            inv[x] = w.l[x] > 0.f ? 1.f / w.l[x] : (w.l[x] == 0.f ? 0.f : w.l[x]);
             if (r >= use.s.n * p.group) continue;
-            const int tok = use.s.t0 + r / p.group, head = use.kvh * p.group + r % p.group;
-            if (whole) {
-                T* out = static_cast<T*>(p.out) + (int64_t)tok * p.ldo + head * D + lane % 4 * 2;
-                const float inv = w.l[x] > 0.f ? 1.f / w.l[x] : (w.l[x] == 0.f ? 0.f : w.l[x]);
-#pragma unroll
-                for (int d = 0; d < DP / 8; ++d)
-                    if (8 * d < D)
-                        *reinterpret_cast<uint32_t*>(out + 8 * d) = pack2<BF16>(w.o[d][2 * x] * inv, w.o[d][2 * x + 1] * inv);
-                if (p.lse && lane % 4 == 0)
-                    p.lse[(int64_t)tok * p.heads + head] = w.l[x] == 0.f ? -INFINITY : w.m[x] * kLn2 + logf(w.l[x]);
-            } else {
-                float* po = ws.o + (place * ws.rows + row) * D + lane % 4 * 2;
-#pragma unroll
-                for (int d = 0; d < DP / 8; ++d)
-                    if (8 * d < D) *reinterpret_cast<float2*>(po + 8 * d) = make_float2(w.o[d][2 * x], w.o[d][2 * x + 1]);
-                if (lane % 4 == 0) ws.ml[place * ws.rows + row] = make_float2(w.m[x], w.l[x]);
-            }
+            to[x] = whole ? (int64_t)tok * p.ldo + head * D : (place * ws.rows + row) * D;
+            if (!W::speaks(lane)) continue;
+            if (!whole) ws.ml[place * ws.rows + row] = make_float2(w.m[x], w.l[x]);
+            else if (p.lse) p.lse[(int64_t)tok * p.heads + head] = w.l[x] == 0.f ? -INFINITY : w.m[x] * kLn2 + logf(w.l[x]);
         }
+        if (whole) w.each(lane, [&](int x, int d, float v) { if (to[x] >= 0 && d < D) put(static_cast<T*>(p.out) + to[x] + d, v * inv[x]); });
+        else w.each(lane, [&](int x, int d, float v) { if (to[x] >= 0 && d < D) ws.o[to[x] + d] = v; });
         if (left > 0) {
-            next_item(p, use);
+            next_item<W::ROWS>(p, use);
             inside = false;
             w.begin(p, use.s, use.kvh, use.r0, lane);
         }
@@ -635,29 +800,31 @@ __global__ void __launch_bounds__(kThreads)
 constexpr int kJoin = 512;
 template <bool BF16>
 __global__ void __launch_bounds__(kJoin) attn_line_join_kernel(const AttnParams p, const LineSpace ws, int workers /* warps of the grid */,
-                                                               int rb, int db) {
+                                                               int rb, int db, int ROWS) {
     using T = typename Elem<BF16>::T;
     __shared__ float4 s_v[kJoin];
     __shared__ float2 s_ml[kJoin];
-    pdl_wait();
-    pdl_launch_dependents();
+    // what the batch's arrays say stands since before the kernel this one follows
     const int tile = blockIdx.x / p.c.kv_heads, kvh = blockIdx.x % p.c.kv_heads, seq = blockIdx.y, D = p.c.dim;
     RowSpan s;
-    if (!row_span(p, seq, tile * kRows, kRows, s, false)) return;
-    int64_t x = ws.begin[seq];
-    for (int t = 0; t < tile; ++t) {
+    const bool is = row_span(p, seq, tile * ROWS, ROWS, s, false);
+    int64_t x = 0;
+    for (int t = 0; is && t < tile; ++t) {
         RowSpan u;
-        row_span(p, seq, t * kRows, kRows, u, false);
+        row_span(p, seq, t * ROWS, ROWS, u, false);
         x += (int64_t)tile_chunks(u) * p.c.kv_heads;
     }
+    pdl_wait();
+    pdl_launch_dependents();
+    if (!is) return;
     const int n = tile_chunks(s);
-    x += (int64_t)n * kvh;
+    x += ws.begin[seq] + (int64_t)n * kvh;
     const int64_t total = ws.begin[p.b.n_seq];
     workers = (int)min((int64_t)workers, total);
     const int w0 = share_of(total, x, workers), w1 = share_of(total, x + n - 1, workers);
     if (w0 == w1) return;                                            // one worker had it and wrote it
     const int parts = D / db, row0 = blockIdx.z / parts * rb;
-    const int rows = min(min(kRows, s.n * p.group - tile * kRows) - row0, rb);
+    const int rows = min(min(ROWS, s.n * p.group - tile * ROWS) - row0, rb);
     if (rows <= 0) return;
     const int work = rb * db / 4, per = blockDim.x / work;
     const int g = threadIdx.x / work, e = threadIdx.x - g * work, in = e / (db / 4), row = row0 + in;
@@ -698,20 +865,20 @@ __global__ void __launch_bounds__(kJoin) attn_line_join_kernel(const AttnParams 
         h = to;
     }
     if (g != 0 || in >= rows) return;
-    const int r = tile * kRows + row, tok = s.t0 + r / p.group, head = kvh * p.group + r % p.group;
+    const int r = tile * ROWS + row, tok = s.t0 + r / p.group, head = kvh * p.group + r % p.group;
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
     T* out = static_cast<T*>(p.out) + (int64_t)tok * p.ldo + head * D + d;
     *reinterpret_cast<uint2*>(out) = make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
     if (p.lse && d == 0) p.lse[(int64_t)tok * p.heads + head] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
-template <int DP, bool BF16>
+template <int DP, bool BF16, class W>
 int launch_line(const AttnParams& p, const AttnPlan& plan, void* workspace, int pdl, cudaStream_t s) {
     CUtensorMap k, v;
-    if (make_kv_map(&k, p.c.k, p.c, kChunk) != GGUF_OK || make_kv_map(&v, p.c.v, p.c, kChunk) != GGUF_OK)
+    if (make_kv_map(&k, p.c.k, p.c, kChunk, whole_heads(p) ? DP / 64 : 1) != GGUF_OK || make_kv_map(&v, p.c.v, p.c, kChunk, whole_heads(p) ? DP / 64 : 1) != GGUF_OK)
         return GGUF_ERR_UNSUPPORTED;
     const LineSpace ws = line_space(p, plan, workspace);
-    auto f = attn_few_line_kernel<DP, BF16>;
+    auto f = attn_few_line_kernel<DP, BF16, W>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<DP>::SMEM) != cudaSuccess ||
         launch_pdl(f, dim3(plan.blocks), dim3(kThreads), FewCfg<DP>::SMEM, s, pdl, k, v, p, ws) != cudaSuccess)
         return GGUF_ERR_CUDA;
@@ -723,15 +890,16 @@ int launch_line(const AttnParams& p, const AttnPlan& plan, void* workspace, int 
     while (per < 16 && per * 4 < cuts) per *= 2;
     const int threads = cuts >= 64 ? kJoin : (int)ceil_div(db / 4 * per, 32) * 32;
     return launch_pdl(attn_line_join_kernel<BF16>, dim3(p.c.kv_heads * plan.tiles, p.b.n_seq, ceil_div(ws.rows, rb) * (p.c.dim / db)),
-                      dim3(threads), 0, s, pdl, p, ws, plan.blocks * kWarps, rb, db) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
+                      dim3(threads), 0, s, pdl, p, ws, plan.blocks * kWarps, rb, db,
+                      W::ROWS) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
 }
 
-template <int DP, bool BF16>
+template <int DP, bool BF16, class W>
 int launch_cluster(const AttnParams& p, const AttnPlan& plan, int pdl, cudaStream_t s) {
     CUtensorMap k, v;
-    if (make_kv_map(&k, p.c.k, p.c, kChunk) != GGUF_OK || make_kv_map(&v, p.c.v, p.c, kChunk) != GGUF_OK)
+    if (make_kv_map(&k, p.c.k, p.c, kChunk, whole_heads(p) ? DP / 64 : 1) != GGUF_OK || make_kv_map(&v, p.c.v, p.c, kChunk, whole_heads(p) ? DP / 64 : 1) != GGUF_OK)
         return GGUF_ERR_UNSUPPORTED;
-    auto f = attn_few_cluster_kernel<DP, BF16>;
+    auto f = attn_few_cluster_kernel<DP, BF16, W>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<DP>::SMEM) != cudaSuccess ||
         cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return GGUF_ERR_CUDA;
@@ -761,7 +929,11 @@ size_t attn_line_bytes(const AttnParams& p, const AttnPlan& plan) {
 
 template <int DP, bool BF16>
 static int run(const AttnParams& p, const AttnPlan& plan, void* workspace, int pdl, cudaStream_t s) {
-    return plan.blocks ? launch_line<DP, BF16>(p, plan, workspace, pdl, s) : launch_cluster<DP, BF16>(p, plan, pdl, s);
+    if (plan.few == 8)
+        return plan.blocks ? launch_line<DP, BF16, Rows8<DP, BF16>>(p, plan, workspace, pdl, s)
+                           : launch_cluster<DP, BF16, Rows8<DP, BF16>>(p, plan, pdl, s);
+    return plan.blocks ? launch_line<DP, BF16, Rows16<DP, BF16>>(p, plan, workspace, pdl, s)
+                       : launch_cluster<DP, BF16, Rows16<DP, BF16>>(p, plan, pdl, s);
 }
 
 int attn_few_launch(const AttnParams& p, const AttnPlan& plan, void* workspace, int pdl, cudaStream_t s) {

@@ -554,8 +554,8 @@ int launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int 
     geo.box = std::min(kKeys, 1 << p.c.page_shift);
     geo.beside = plan.mixed;
     CUtensorMap q, k, v;
-    if (make_q_map(&q, p, p.group, tokens) != GGUF_OK || make_kv_map(&k, p.c.k, p.c, geo.box) != GGUF_OK ||
-        make_kv_map(&v, p.c.v, p.c, geo.box) != GGUF_OK)
+    if (make_q_map(&q, p, p.group, tokens) != GGUF_OK || make_kv_map(&k, p.c.k, p.c, geo.box, 1) != GGUF_OK ||
+        make_kv_map(&v, p.c.v, p.c, geo.box, 1) != GGUF_OK)
         return GGUF_ERR_UNSUPPORTED;
     auto f = attn_many_kernel<DP, BF16>;
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, ManyCfg<DP>::SMEM) != cudaSuccess)
