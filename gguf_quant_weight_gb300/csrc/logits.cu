@@ -7,10 +7,12 @@
 //
 // A block takes one slice of one row.  It counts the history's tokens that
 // fall into its slice with integer atomics in shared memory (their order does
-// not matter), marks the biased ones, and then passes over its logits once.
-// A biased token's list entries are added in the list's order, so the result
-// does not depend on timing either.  The logits' bytes bound it; each block
-// reads the row's whole history, from L2 after the first.
+// not matter), marks the biased ones, and then passes over its logits once,
+// which every thread has had on their way meanwhile.  A biased token's list
+// entries are added in the list's order, so the result does not depend on
+// timing either (an entry alone for its token, the usual case, is added without
+// going through the list).  The logits' bytes bound it; each block reads the row's whole
+// history, from L2 after the first.
 #include "serving.cuh"
 
 namespace gg {
@@ -18,7 +20,7 @@ namespace gg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSlice = 4096;   // tokens a block
+constexpr int kAtOnce = 4;       // of the history, read by a thread at once
 
 template <int DT> struct El;
 template <> struct El<GGUF_DT_F32> { using T = float; };
@@ -31,103 +33,173 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <int DT, int ODT>
-__global__ void __launch_bounds__(kThreads) logits_adjust_kernel(const LogitsParams p) {
+// E: tokens a thread (a slice is kThreads * E).  Groups of tokens start at
+// 16-byte boundaries of the row's inputs.
+template <int DT, int ODT, int E>
+__global__ void __launch_bounds__(kThreads, 5) logits_adjust_kernel(const LogitsParams p) {
     using X = typename El<DT>::T;
     using Y = typename El<ODT>::T;
-    __shared__ int s_count[kSlice + 4];
-    __shared__ uint32_t s_biased[kSlice / 32 + 1];
+    constexpr int SLICE = kThreads * E;
+    constexpr int G = 16 / (int)sizeof(X) < E ? 16 / (int)sizeof(X) : E;      // tokens of a group
+    struct alignas(G * sizeof(X)) In { X v[G]; };
+    __shared__ int s_count[SLICE];
+    __shared__ uint32_t s_biased[SLICE / 32];
+    __shared__ float s_bias[SLICE];              // of a biased token that is in the list once
+    __shared__ int s_twice;                      // whether one of the slice is there more often
     const int r = blockIdx.y, tid = threadIdx.x;
     const X* x = static_cast<const X*>(p.x) + r * p.ld;
     Y* y = static_cast<Y*>(p.y) + r * p.ldo;
-    // groups of four tokens start at 16-byte boundaries of the row's inputs
-    const int m = (int)(r * p.ld & 3);
-    const int64_t first = (int64_t)blockIdx.x * kSlice - m;       // token of s_count[0]
-    const int64_t vocab = p.vocab;
-    for (int i = tid; i < kSlice + 4; i += kThreads) s_count[i] = 0;
-    for (int i = tid; i < kSlice / 32 + 1; i += kThreads) s_biased[i] = 0;
+    const int m = (int)(r * p.ld & (G - 1));
+    const int first = blockIdx.x * SLICE - m;                      // token of s_count[0]
+    const int vocab = (int)p.vocab;
+    if (p.r.hist)
+        for (int i = tid; i < SLICE; i += kThreads) s_count[i] = 0;
+    if (p.r.bias_ids && tid < SLICE / 32) s_biased[tid] = 0;
+    if (tid == 0) s_twice = 0;
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    if (p.r.hist) {
-        const int e = p.r.hist_start[r + 1];
-        for (int i = p.r.hist_start[r] + tid; i < e; i += kThreads) {
-            const int id = p.r.hist[i];
-            const int64_t at = id - first;
-            if (id >= 0 && id < vocab && at >= 0 && at < kSlice) atomicAdd(&s_count[at], 1);
+
+    // everything that depends on nothing, on its way at once: the row's numbers,
+    // then the thread's groups tid, tid + kThreads, ...
+    int h0 = 0, h1 = 0, b0 = 0, nb = 0;
+    float repeat = 1.f, frequency = 0.f, presence = 0.f;
+    if (p.r.hist) h0 = p.r.hist_start[r], h1 = p.r.hist_start[r + 1];
+    if (p.r.bias_ids) b0 = p.r.bias_start[r], nb = p.r.bias_start[r + 1] - b0;
+    if (p.r.repeat) repeat = p.r.repeat[r];
+    if (p.r.frequency) frequency = p.r.frequency[r];
+    if (p.r.presence) presence = p.r.presence[r];
+    const uint32_t* allow = p.r.allow ? p.r.allow + r * p.r.allow_stride : nullptr;
+    In in[E / G];
+#pragma unroll
+    for (int k = 0; k < E / G; ++k) {
+        const int v0 = first + (tid + k * kThreads) * G;
+        if (v0 >= 0 && v0 + G <= vocab) in[k] = *reinterpret_cast<const In*>(x + v0);
+    }
+    // a group's bits of the mask: from one word, or the end of one and the start of the next
+    uint32_t bits[E / G];
+    if (allow) {
+#pragma unroll
+        for (int k = 0; k < E / G; ++k) {
+            const int v0 = first + (tid + k * kThreads) * G, w = v0 < 0 ? 0 : v0 >> 5;
+            if (v0 >= vocab) continue;
+            const int sh = v0 - 32 * w;
+            const uint32_t lo = allow[w], hi = sh + G > 32 && 32 * (w + 1) < vocab ? allow[w + 1] : 0u;
+            bits[k] = sh < 0 ? lo << -sh : __funnelshift_r(lo, hi, sh);
         }
     }
-    int b0 = 0, b1 = 0;
-    if (p.r.bias_ids) {
-        b0 = p.r.bias_start[r];
-        b1 = p.r.bias_start[r + 1];
-        for (int i = b0 + tid; i < b1; i += kThreads) {
-            const int id = p.r.bias_ids[i];
-            const int64_t at = id - first;
-            if (id >= 0 && id < vocab && at >= 0 && at < kSlice) atomicOr(&s_biased[at >> 5], 1u << (at & 31));
+    int b_id = -1;
+    float b_val = 0.f;
+    if (tid < nb) {
+        b_id = p.r.bias_ids[b0 + tid];
+        b_val = p.r.bias[b0 + tid];
+    }
+    for (int i0 = h0 + tid; i0 < h1; i0 += kAtOnce * kThreads) {
+        int id[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) id[j] = i0 + j * kThreads < h1 ? p.r.hist[i0 + j * kThreads] : -1;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const unsigned at = (unsigned)id[j] - (unsigned)first;
+            if (id[j] >= 0 && id[j] < vocab && at < SLICE) atomicAdd(&s_count[at], 1);
+        }
+    }
+    for (int i = tid; i < nb; i += kThreads) {
+        if (i != tid) {
+            b_id = p.r.bias_ids[b0 + i];
+            b_val = p.r.bias[b0 + i];
+        }
+        const unsigned at = (unsigned)b_id - (unsigned)first;
+        if (b_id >= 0 && b_id < vocab && at < SLICE) {
+            const uint32_t bit = 1u << (at & 31);
+            if (atomicOr(&s_biased[at >> 5], bit) & bit) s_twice = 1;
+            s_bias[at] = b_val;
         }
     }
     __syncthreads();
-    const float repeat = p.r.repeat ? p.r.repeat[r] : 1.f;
-    const float frequency = p.r.frequency ? p.r.frequency[r] : 0.f;
-    const float presence = p.r.presence ? p.r.presence[r] : 0.f;
-    const uint32_t* allow = p.r.allow ? p.r.allow + r * p.r.allow_stride : nullptr;
-    const bool out4 = ((r * p.ldo - m) & 3) == 0;                  // groups are aligned in the outputs too
-    for (int g = tid; g < kSlice / 4; g += kThreads) {
-        const int64_t v0 = first + 4 * g;
+    const bool out_wide = ((r * p.ldo - m) & (G - 1)) == 0;        // groups are aligned in the outputs too
+#pragma unroll
+    for (int k = 0; k < E / G; ++k) {
+        const int at = (tid + k * kThreads) * G;
+        const int v0 = first + at;
         if (v0 >= vocab) break;
-        const bool whole = v0 >= 0 && v0 + 4 <= vocab;
-        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        const bool whole = v0 >= 0 && v0 + G <= vocab;
+        float f[G];
         if (whole) {
-            struct alignas(4 * sizeof(X)) Pack { X v[4]; };
-            const Pack k = *reinterpret_cast<const Pack*>(x + v0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = to_f(k.v[i]);
+            for (int i = 0; i < G; ++i) f[i] = to_f(in[k].v[i]);
         } else {
-            for (int i = 0; i < 4; ++i)
-                if (v0 + i >= 0 && v0 + i < vocab) f[i] = to_f(x[v0 + i]);
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t v = v0 + i;
-            if (v < 0 || v >= vocab) continue;
-            const int c = s_count[4 * g + i];
-            if (c) f[i] = (f[i] > 0.f ? f[i] / repeat : f[i] * repeat) - fmaf((float)c, frequency, presence);
-            if (s_biased[(4 * g + i) >> 5] >> ((4 * g + i) & 31) & 1)
-                for (int j = b0; j < b1; ++j)
-                    if (p.r.bias_ids[j] == v) f[i] += p.r.bias[j];
-            if (allow && !(allow[v >> 5] >> (v & 31) & 1)) f[i] = -INFINITY;
+            for (int i = 0; i < G; ++i) f[i] = v0 + i >= 0 && v0 + i < vocab ? to_f(x[v0 + i]) : 0.f;
         }
-        if (whole && out4) {
-            struct alignas(4 * sizeof(Y)) Pack { Y v[4]; };
-            Pack k;
+        if (p.r.hist) {
+            int c[G];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) put(&k.v[i], f[i]);
-            *reinterpret_cast<Pack*>(y + v0) = k;
+            for (int i = 0; i < G; i += 4) *reinterpret_cast<int4*>(c + i) = *reinterpret_cast<const int4*>(s_count + at + i);
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (c[i]) f[i] = (f[i] > 0.f ? f[i] / repeat : f[i] * repeat) - fmaf((float)c[i], frequency, presence);
+        }
+        if (nb > 0) {
+            const uint32_t here = s_biased[at >> 5] >> (at & 31) & ((1u << G) - 1);      // a group lies in one word
+            if (here && !s_twice) {
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    if (here >> i & 1) f[i] += s_bias[at + i];
+            } else if (here) {
+                for (int j = 0; j < nb; ++j) {
+                    const unsigned i = (unsigned)p.r.bias_ids[b0 + j] - (unsigned)v0;
+                    const float b = p.r.bias[b0 + j];
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        if ((unsigned)g == i) f[g] += b;
+                }
+            }
+        }
+        if (allow) {
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (!(bits[k] >> i & 1)) f[i] = -INFINITY;
+        }
+        if (whole && out_wide) {
+            constexpr int N = 16 / (int)sizeof(Y) < G ? 16 / (int)sizeof(Y) : G;
+            struct alignas(N * sizeof(Y)) Out { Y v[N]; };
+#pragma unroll
+            for (int i = 0; i < G; i += N) {
+                Out o;
+#pragma unroll
+                for (int j = 0; j < N; ++j) put(&o.v[j], f[i + j]);
+                *reinterpret_cast<Out*>(y + v0 + i) = o;
+            }
         } else {
-            for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int i = 0; i < G; ++i)
                 if (v0 + i >= 0 && v0 + i < vocab) put(&y[v0 + i], f[i]);
         }
     }
 }
 
+template <int DT, int ODT>
+cudaError_t launch(const LogitsParams& p, int num_sms, int pdl, cudaStream_t s) {
+    // 4096 tokens a block; a quarter of it where that leaves SMs idle.  A row's
+    // groups may start up to seven tokens before it.
+    const bool small = ceil_div(p.vocab + 7, kThreads * 16) * p.rows < num_sms;
+    const dim3 grid((unsigned)ceil_div(p.vocab + 7, kThreads * (small ? 4 : 16)), (unsigned)p.rows);
+    return small ? launch_pdl(logits_adjust_kernel<DT, ODT, 4>, grid, dim3(kThreads), 0, s, pdl, p)
+                 : launch_pdl(logits_adjust_kernel<DT, ODT, 16>, grid, dim3(kThreads), 0, s, pdl, p);
+}
+
 template <int DT>
-cudaError_t launch(const LogitsParams& p, int pdl, cudaStream_t s) {
-    // a row's groups may start up to three tokens before it
-    const dim3 grid((unsigned)ceil_div(p.vocab + 3, kSlice), (unsigned)p.rows);
-    switch (p.odt) {
-        case GGUF_DT_F32: return launch_pdl(logits_adjust_kernel<DT, GGUF_DT_F32>, grid, dim3(kThreads), 0, s, pdl, p);
-        case GGUF_DT_F16: return launch_pdl(logits_adjust_kernel<DT, GGUF_DT_F16>, grid, dim3(kThreads), 0, s, pdl, p);
-        default: return launch_pdl(logits_adjust_kernel<DT, GGUF_DT_BF16>, grid, dim3(kThreads), 0, s, pdl, p);
-    }
+cudaError_t launch(const LogitsParams& p, int num_sms, int pdl, cudaStream_t s) {
+    if (p.odt == GGUF_DT_F32) return launch<DT, GGUF_DT_F32>(p, num_sms, pdl, s);
+    return p.odt == GGUF_DT_F16 ? launch<DT, GGUF_DT_F16>(p, num_sms, pdl, s) : launch<DT, GGUF_DT_BF16>(p, num_sms, pdl, s);
 }
 
 }  // namespace
 
 cudaError_t logits_adjust_launch(const LogitsParams& p, int num_sms, int pdl, cudaStream_t s) {
-    (void)num_sms;
-    if (p.dt == GGUF_DT_F32) return launch<GGUF_DT_F32>(p, pdl, s);
-    return p.dt == GGUF_DT_F16 ? launch<GGUF_DT_F16>(p, pdl, s) : launch<GGUF_DT_BF16>(p, pdl, s);
+    if (p.dt == GGUF_DT_F32) return launch<GGUF_DT_F32>(p, num_sms, pdl, s);
+    return p.dt == GGUF_DT_F16 ? launch<GGUF_DT_F16>(p, num_sms, pdl, s) : launch<GGUF_DT_BF16>(p, num_sms, pdl, s);
 }
 
 }  // namespace gg
