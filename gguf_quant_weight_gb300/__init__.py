@@ -198,9 +198,7 @@ def exported_symbols():
 
 
 def _p(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
     return t.data_ptr()
 
@@ -342,30 +340,33 @@ def gguf_mm_debug_timeout(spin_limit, stream=None):
 
 # --- serving operators --------------------------------------------------------
 
-def _ref(struct):
-    return None if struct is None else struct._ref
-
+# These run between products that take a few microseconds each, so the
+# marshalling is kept short: a call of one token is bound by the host.
 
 def gguf_kv_append(q, ldq, k, ldk, v, ldv, xdt, heads, rope, batch, cache, q_out, ldqo, stream=None):
-    return _check("gguf_kv_append", load_library().gguf_kv_append(
-        _p(q), ldq, _p(k), ldk, _p(v), ldv, xdt, heads, _ref(rope), _ref(batch), _ref(cache), _p(q_out), ldqo,
-        _s(stream)))
+    st = (_lib or load_library()).gguf_kv_append(
+        _p(q), ldq, _p(k), ldk, _p(v), ldv, xdt, heads, rope and rope._ref, batch and batch._ref, cache and cache._ref,
+        _p(q_out), ldqo, stream if stream.__class__ is int else _s(stream))
+    return _check("gguf_kv_append", st) if st else st
 
 
 def gguf_paged_attn(q, ldq, heads, batch, cache, scale, causal, window, out, ldo, lse=None, workspace=None, ws_bytes=0,
                     stream=None):
-    return _check("gguf_paged_attn", load_library().gguf_paged_attn(
-        _p(q), ldq, heads, _ref(batch), _ref(cache), scale, causal, window, _p(out), ldo, _p(lse), _p(workspace),
-        ws_bytes, _s(stream)))
+    st = (_lib or load_library()).gguf_paged_attn(
+        _p(q), ldq, heads, batch and batch._ref, cache and cache._ref, scale, causal, window, _p(out), ldo, _p(lse),
+        _p(workspace), ws_bytes, stream if stream.__class__ is int else _s(stream))
+    return _check("gguf_paged_attn", st) if st else st
 
 
 def gguf_paged_attn_workspace_size(batch, cache, heads) -> int:
-    return load_library().gguf_paged_attn_workspace_size(_ref(batch), _ref(cache), heads)
+    return load_library().gguf_paged_attn_workspace_size(batch and batch._ref, cache and cache._ref, heads)
 
 
 def gguf_logits_adjust(logits, dt, ld, rows, vocab, rules, out, odt, ldo, stream=None):
-    return _check("gguf_logits_adjust", load_library().gguf_logits_adjust(
-        _p(logits), dt, ld, rows, vocab, _ref(rules), _p(out), odt, ldo, _s(stream)))
+    st = (_lib or load_library()).gguf_logits_adjust(
+        _p(logits), dt, ld, rows, vocab, rules and rules._ref, _p(out), odt, ldo,
+        stream if stream.__class__ is int else _s(stream))
+    return _check("gguf_logits_adjust", st) if st else st
 
 
 # --- GGUF container reader (host only) ---------------------------------------

@@ -43,9 +43,9 @@ __global__ void __launch_bounds__(kThreads, 5) logits_adjust_kernel(const Logits
     constexpr int G = 16 / (int)sizeof(X) < E ? 16 / (int)sizeof(X) : E;      // tokens of a group
     struct alignas(G * sizeof(X)) In { X v[G]; };
     __shared__ int s_count[SLICE];
-    __shared__ uint32_t s_biased[SLICE / 32];
-    __shared__ float s_bias[SLICE];              // of a biased token that is in the list once
-    __shared__ int s_twice;                      // whether one of the slice is there more often
+    __shared__ uint32_t s_biased[SLICE / 32];    // in the list
+    __shared__ uint32_t s_again[SLICE / 32];     // more than once
+    __shared__ float s_bias[SLICE];              // the bias of one that is there once
     const int r = blockIdx.y, tid = threadIdx.x;
     const X* x = static_cast<const X*>(p.x) + r * p.ld;
     Y* y = static_cast<Y*>(p.y) + r * p.ldo;
@@ -54,8 +54,7 @@ __global__ void __launch_bounds__(kThreads, 5) logits_adjust_kernel(const Logits
     const int vocab = (int)p.vocab;
     if (p.r.hist)
         for (int i = tid; i < SLICE; i += kThreads) s_count[i] = 0;
-    if (p.r.bias_ids && tid < SLICE / 32) s_biased[tid] = 0;
-    if (tid == 0) s_twice = 0;
+    if (p.r.bias_ids && tid < SLICE / 32) s_biased[tid] = s_again[tid] = 0;
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
@@ -112,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 5) logits_adjust_kernel(const Logits
         const unsigned at = (unsigned)b_id - (unsigned)first;
         if (b_id >= 0 && b_id < vocab && at < SLICE) {
             const uint32_t bit = 1u << (at & 31);
-            if (atomicOr(&s_biased[at >> 5], bit) & bit) s_twice = 1;
+            if (atomicOr(&s_biased[at >> 5], bit) & bit) atomicOr(&s_again[at >> 5], bit);
             s_bias[at] = b_val;
         }
     }
@@ -141,18 +140,19 @@ __global__ void __launch_bounds__(kThreads, 5) logits_adjust_kernel(const Logits
                 if (c[i]) f[i] = (f[i] > 0.f ? f[i] / repeat : f[i] * repeat) - fmaf((float)c[i], frequency, presence);
         }
         if (nb > 0) {
-            const uint32_t here = s_biased[at >> 5] >> (at & 31) & ((1u << G) - 1);      // a group lies in one word
-            if (here && !s_twice) {
+            const int sh = at & 31;                                                // a group lies in one word
+            const uint32_t again = s_again[at >> 5] >> sh & ((1u << G) - 1), once = s_biased[at >> 5] >> sh & ~again;
 #pragma unroll
-                for (int i = 0; i < G; ++i)
-                    if (here >> i & 1) f[i] += s_bias[at + i];
-            } else if (here) {
+            for (int i = 0; i < G; ++i)
+                if (once >> i & 1) f[i] += s_bias[at + i];
+            if (again) {
+#pragma unroll 8
                 for (int j = 0; j < nb; ++j) {
                     const unsigned i = (unsigned)p.r.bias_ids[b0 + j] - (unsigned)v0;
                     const float b = p.r.bias[b0 + j];
 #pragma unroll
                     for (int g = 0; g < G; ++g)
-                        if ((unsigned)g == i) f[g] += b;
+                        if ((unsigned)g == i && (again >> g & 1)) f[g] += b;
                 }
             }
         }

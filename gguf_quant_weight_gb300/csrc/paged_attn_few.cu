@@ -879,7 +879,8 @@ int launch_line(const AttnParams& p, const AttnPlan& plan, void* workspace, int 
         return GGUF_ERR_UNSUPPORTED;
     const LineSpace ws = line_space(p, plan, workspace);
     auto f = attn_few_line_kernel<DP, BF16, W>;
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<DP>::SMEM) != cudaSuccess ||
+    static std::atomic<uint64_t> ready{0};
+    if (set_once(f, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<DP>::SMEM, ready) != cudaSuccess ||
         launch_pdl(f, dim3(plan.blocks), dim3(kThreads), FewCfg<DP>::SMEM, s, pdl, k, v, p, ws) != cudaSuccess)
         return GGUF_ERR_CUDA;
     // a block to a row of an item, with threads for four shares each; where few
@@ -900,8 +901,9 @@ int launch_cluster(const AttnParams& p, const AttnPlan& plan, int pdl, cudaStrea
     if (make_kv_map(&k, p.c.k, p.c, kChunk, whole_heads(p) ? DP / 64 : 1) != GGUF_OK || make_kv_map(&v, p.c.v, p.c, kChunk, whole_heads(p) ? DP / 64 : 1) != GGUF_OK)
         return GGUF_ERR_UNSUPPORTED;
     auto f = attn_few_cluster_kernel<DP, BF16, W>;
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<DP>::SMEM) != cudaSuccess ||
-        cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    static std::atomic<uint64_t> ready{0}, wide{0};
+    if (set_once(f, cudaFuncAttributeMaxDynamicSharedMemorySize, FewCfg<DP>::SMEM, ready) != cudaSuccess ||
+        set_once(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, wide) != cudaSuccess)
         return GGUF_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     const int tiles = plan.mixed ? plan.few_tiles : plan.tiles;

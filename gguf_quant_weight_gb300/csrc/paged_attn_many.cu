@@ -558,7 +558,8 @@ int launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int 
         make_kv_map(&v, p.c.v, p.c, geo.box, 1) != GGUF_OK)
         return GGUF_ERR_UNSUPPORTED;
     auto f = attn_many_kernel<DP, BF16>;
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, ManyCfg<DP>::SMEM) != cudaSuccess)
+    static std::atomic<uint64_t> ready{0};
+    if (set_once(f, cudaFuncAttributeMaxDynamicSharedMemorySize, ManyCfg<DP>::SMEM, ready) != cudaSuccess)
         return GGUF_ERR_CUDA;
     const dim3 grid(p.c.kv_heads * plan.splits, plan.tiles, p.b.n_seq);
     return launch_pdl(f, grid, dim3(kThreads), ManyCfg<DP>::SMEM, s, pdl, q, k, v, p, part, geo) == cudaSuccess

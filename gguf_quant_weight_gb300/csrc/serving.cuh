@@ -2,6 +2,8 @@
 // paged_attn.cu, logits.cu); the C entry points and their checks are in
 // serving.cu.
 #pragma once
+#include <atomic>
+
 #include "common.cuh"
 
 namespace gg {
@@ -68,6 +70,20 @@ cudaError_t kv_append_launch(const AppendParams& p, int num_sms, int pdl, cudaSt
 size_t paged_attn_workspace_bytes(const AttnParams& p, int num_sms);
 int paged_attn_launch(const AttnParams& p, void* workspace, int num_sms, int pdl, cudaStream_t stream);
 cudaError_t logits_adjust_launch(const LogitsParams& p, int num_sms, int pdl, cudaStream_t stream);
+
+// Sets a kernel's attribute on each device once: `done` is the kernel's own
+// set of devices that have it.
+template <class F>
+cudaError_t set_once(F* kernel, cudaFuncAttribute what, int value, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, what, value);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Launches kernel<<<grid, block, smem, stream>>>(args...), as a programmatic
 // dependent of the kernel before it on the stream where pdl is set (the kernel
