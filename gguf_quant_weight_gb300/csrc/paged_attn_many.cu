@@ -34,8 +34,8 @@ constexpr float kRaise = 8.f;       // log2 of how far scores may pass the maxim
 template <int DP> struct ManyCfg {
     static constexpr int HALF = 128 * 128;                 // bytes of 128 rows x 64 values
     static constexpr int TILE = DP / 64 * HALF;            // 128 rows x DP values
-    static constexpr int STAGES = DP == 128 ? 5 : 8;
-    static constexpr int SMEM = (2 + STAGES) * TILE;       // 224 KB at 128 values; the static part has 3 KB
+    static constexpr int STAGES = DP == 128 ? 4 : 6;
+    static constexpr int SMEM = (2 + STAGES) * TILE;       // 192 KB at 128 values
 };
 
 template <bool BF16> struct Elem { using T = __half; };
@@ -54,6 +54,20 @@ __device__ __forceinline__ void store32(void* to, const uint32_t* v) {   // 32 b
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
+}
+
+// Whether x holds for any thread of two warps that share barrier `id`.
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)x), "r"(id)
+        : "memory");
+    return any != 0;
 }
 
 struct Geometry {
@@ -438,12 +452,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 64; j += 2)
                     top[j >> 1 & 3] = max3_nan(top[j >> 1 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
                 float mx = max3_nan(max3_nan(top[0], top[1], top[2]), top[3], top[3]);
-                // (and both have their scores: weights may replace them.  The next value
-                // follows products that needed both threads' weights: this one is read.)
-                const float other = exchange(mx);
-                mx = max3_nan(mx, other, other);
-                const bool raise = !(mx <= m) && !((mx - m) * c2 <= kRaise);
-                if (__any_sync(0xffffffffu, raise)) {
+                // Whether any row of the two warps has to raise its maximum: mostly none has.
+                // (Past this barrier both threads have their scores, and weights may replace
+                // them; and what was exchanged before has been read, since products that
+                // needed both threads' weights came between.)
+                if (pair_any(pair, !(mx <= m) && !((mx - m) * c2 <= kRaise))) {
+                    const float other = exchange(mx);
+                    mx = max3_nan(mx, other, other);
+                    const bool raise = !(mx <= m) && !((mx - m) * c2 <= kRaise);
                     const float f = raise ? exp2_fast((m - mx) * c2) : 1.f;
                     if (raise) m = mx < INFINITY ? mx : NAN;     // the row has no finite sum: all of it is NaN
                     l *= f;
