@@ -13,6 +13,10 @@
 // timing either (an entry alone for its token, the usual case, is added without
 // going through the list).  The logits' bytes bound it; each block reads the row's whole
 // history, from L2 after the first.
+// Measured on GB300: 256 x 131072 f32 in and out in 53 us (5.0 of the 6.8 TB/s
+// of a copy; the reads of a block wait for its history, and five blocks to an SM
+// do not quite cover it -- with four it takes 57 us, with six registers spill),
+// one row of 32003 in 2.7 us.
 #include "serving.cuh"
 
 namespace gg {

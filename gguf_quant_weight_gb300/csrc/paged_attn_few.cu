@@ -1,17 +1,17 @@
-// Attention of few rows over a paged cache: single tokens, and short chunks.
+// Attention of few rows over a paged cache: single tokens, and chunks of up to
+// 16 rows (tokens x query heads of a key head).
 //
-// Each key and value is read once for the query heads that share it, and is
-// used for at most 16 rows, so the cache's bytes bound this: 512 bytes a key
-// and key head at 128 values, against 16 rows x 512 operations that legacy
-// tensor instructions do in a tenth of the time the bytes take.  The work is
-// therefore arranged around loads in flight:
-//   * a warp is a worker of its own: it takes every fourth chunk of 16 keys of
-//     its block, which a tensor copy brings into the warp's ring of slots
-//     (swizzled, zeros past head_dim), and keeps kStages chunks in flight.  No
-//     warp waits for another until the end.
-//   * scores S = Q K^T with the queries in registers as the first operand; the
-//     accumulator's layout of S is the layout that the weights need as first
-//     operand of P V, so they never leave the registers.
+// Each key and value is read once for the query heads that share it, so the
+// cache's bytes bound this: 512 bytes a key and key head at 128 values, against
+// 16 rows x 512 operations, a tenth of the time even on the legacy tensor
+// instructions, whose operands can stay in registers.  The work is therefore
+// arranged around loads in flight:
+//   * a warp is a worker of its own: tensor copies bring chunks of 16 keys into
+//     its ring of slots (swizzled, zeros past head_dim), STAGES of them ahead.
+//     No warp waits for another until the end.
+//   * scores and weights stay in registers: an accumulator of S has the layout
+//     that the weights need as first operand of P V (or, for up to 8 rows and
+//     with the products turned around, a transpose of 8 x 8 away from it).
 //   * small calls split the keys of a (sequence, key head) over the blocks of a
 //     cluster; the warps' results are joined in shared memory, the blocks'
 //     through distributed shared memory, in one launch.
@@ -20,6 +20,12 @@
 //     pause and the sequences' lengths do not matter.  A second kernel joins
 //     what was cut.
 // Partial results are always joined in the same order.
+//
+// Measured on GB300, 32 heads on 8 of 128, bf16: one token over 1021 keys 6.2 us;
+// 64 tokens over 100..8000 keys, 570 MB, 104 us (5.5 of the 6.8 TB/s of a copy;
+// the copies alone take 87 us, joining about 5); one token over 131071 keys of 4
+// heads, 268 MB, 51 us.  Two blocks of four warps with three chunks ahead each
+// take 104 us of the batch; three blocks with two ahead 124, one with six 135.
 #include "attn.cuh"
 
 namespace gg {

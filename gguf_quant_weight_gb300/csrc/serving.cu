@@ -144,6 +144,7 @@ int gguf_paged_attn(const void* q, int64_t ldq, int64_t heads, const gguf_kv_bat
     p.lse = lse;
     p.heads = (int)heads;
     p.group = p.heads / p.c.kv_heads;
+    if ((int64_t)p.b.max_q * p.group > (1 << 30)) return GGUF_ERR_UNSUPPORTED;   // rows are counted in 32 bits
     p.scale = scale;
     p.causal = causal;
     // a window that reaches back past any position hides nothing
