@@ -120,12 +120,15 @@ struct Partials {
 struct AttnPlan {
     int few;        // few rows: of a tile (8 or 16); 0: all sequences in the many-rows form
     int mixed;      // sequences of few rows in the few-rows form, the others in the many-rows form
-    int tiles;      // row tiles of a sequence and key head (or pairs of tiles of up to 128 rows)
+    int tiles;      // row tiles of a sequence and key head (or of 128 rows, or of two of these)
     int few_tiles;  // mixed: row tiles of the sequences of few rows
     int cluster;    // few rows, small calls: blocks of a cluster that split the keys
     int blocks;     // few rows, large calls: blocks among whose warps all keys are dealt out; else 0
     int splits;     // many rows: shares of the keys, joined through the workspace where there are several
 };
+
+// Row tiles that a block of the many-rows form takes.
+inline int many_tiles(const AttnParams& p) { return p.c.dim > 64 ? 2 : 1; }
 
 size_t attn_line_bytes(const AttnParams& p, const AttnPlan& plan);
 int attn_few_launch(const AttnParams& p, const AttnPlan& plan, void* workspace, int pdl, cudaStream_t s);

@@ -40,7 +40,7 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 // E: tokens a thread (a slice is kThreads * E).  Groups of tokens start at
 // 16-byte boundaries of the row's inputs.
 template <int DT, int ODT, int E>
-__global__ void __launch_bounds__(kThreads, 5) logits_adjust_kernel(const LogitsParams p) {
+__global__ void __launch_bounds__(kThreads, E == 32 ? 4 : 5) logits_adjust_kernel(const LogitsParams p) {
     using X = typename El<DT>::T;
     using Y = typename El<ODT>::T;
     constexpr int SLICE = kThreads * E;
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, 5) logits_adjust_kernel(const Logits
     __shared__ int s_count[SLICE];
     __shared__ uint32_t s_biased[SLICE / 32];    // in the list
     __shared__ uint32_t s_again[SLICE / 32];     // more than once
-    __shared__ float s_bias[SLICE];              // the bias of one that is there once
+    __shared__ uint16_t s_entry[SLICE];          // where, of one that is there once
     const int r = blockIdx.y, tid = threadIdx.x;
     const X* x = static_cast<const X*>(p.x) + r * p.ld;
     Y* y = static_cast<Y*>(p.y) + r * p.ldo;
@@ -91,12 +91,7 @@ __global__ void __launch_bounds__(kThreads, 5) logits_adjust_kernel(const Logits
             bits[k] = sh < 0 ? lo << -sh : __funnelshift_r(lo, hi, sh);
         }
     }
-    int b_id = -1;
-    float b_val = 0.f;
-    if (tid < nb) {
-        b_id = p.r.bias_ids[b0 + tid];
-        b_val = p.r.bias[b0 + tid];
-    }
+    int b_id = tid < nb ? p.r.bias_ids[b0 + tid] : -1;
     for (int i0 = h0 + tid; i0 < h1; i0 += kAtOnce * kThreads) {
         int id[kAtOnce];
 #pragma unroll
@@ -108,15 +103,12 @@ __global__ void __launch_bounds__(kThreads, 5) logits_adjust_kernel(const Logits
         }
     }
     for (int i = tid; i < nb; i += kThreads) {
-        if (i != tid) {
-            b_id = p.r.bias_ids[b0 + i];
-            b_val = p.r.bias[b0 + i];
-        }
+        if (i != tid) b_id = p.r.bias_ids[b0 + i];
         const unsigned at = (unsigned)b_id - (unsigned)first;
         if (b_id >= 0 && b_id < vocab && at < SLICE) {
             const uint32_t bit = 1u << (at & 31);
-            if (atomicOr(&s_biased[at >> 5], bit) & bit) atomicOr(&s_again[at >> 5], bit);
-            s_bias[at] = b_val;
+            if ((atomicOr(&s_biased[at >> 5], bit) & bit) || i > 0xffff) atomicOr(&s_again[at >> 5], bit);
+            s_entry[at] = (uint16_t)i;
         }
     }
     __syncthreads();
@@ -148,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 5) logits_adjust_kernel(const Logits
             const uint32_t again = s_again[at >> 5] >> sh & ((1u << G) - 1), once = s_biased[at >> 5] >> sh & ~again;
 #pragma unroll
             for (int i = 0; i < G; ++i)
-                if (once >> i & 1) f[i] += s_bias[at + i];
+                if (once >> i & 1) f[i] += p.r.bias[b0 + s_entry[at + i]];
             if (again) {
 #pragma unroll 8
                 for (int j = 0; j < nb; ++j) {
@@ -185,12 +177,14 @@ __global__ void __launch_bounds__(kThreads, 5) logits_adjust_kernel(const Logits
 
 template <int DT, int ODT>
 cudaError_t launch(const LogitsParams& p, int num_sms, int pdl, cudaStream_t s) {
-    // 4096 tokens a block; a quarter of it where that leaves SMs idle.  A row's
-    // groups may start up to seven tokens before it.
-    const bool small = ceil_div(p.vocab + 7, kThreads * 16) * p.rows < num_sms;
-    const dim3 grid((unsigned)ceil_div(p.vocab + 7, kThreads * (small ? 4 : 16)), (unsigned)p.rows);
+    // 64 bytes of a row a thread, so 4096 or 8192 tokens a block: fewer blocks read
+    // the row's history; 1024 where that leaves SMs idle.  A row's groups may
+    // start up to seven tokens before it.
+    constexpr int E = DT == GGUF_DT_F32 ? 16 : 32;
+    const bool small = ceil_div(p.vocab + 7, kThreads * E) * p.rows < num_sms;
+    const dim3 grid((unsigned)ceil_div(p.vocab + 7, kThreads * (small ? 4 : E)), (unsigned)p.rows);
     return small ? launch_pdl(logits_adjust_kernel<DT, ODT, 4>, grid, dim3(kThreads), 0, s, pdl, p)
-                 : launch_pdl(logits_adjust_kernel<DT, ODT, 16>, grid, dim3(kThreads), 0, s, pdl, p);
+                 : launch_pdl(logits_adjust_kernel<DT, ODT, E>, grid, dim3(kThreads), 0, s, pdl, p);
 }
 
 template <int DT>

@@ -90,10 +90,10 @@ AttnPlan make_plan(const AttnParams& p, int num_sms) {
             while (a.cluster < 16 && a.cluster < want) a.cluster *= 2;
         }
     } else {
-        a.tiles = (int)ceil_div(p.b.max_q, 2 * (128 / p.group));
+        a.tiles = (int)ceil_div(p.b.max_q, many_tiles(p) * (128 / p.group));
         // the keys are split where the tiles alone leave SMs idle
         const int64_t units = std::max<int64_t>(1, ceil_div(span, 128)), pairs = (int64_t)p.b.n_seq * p.c.kv_heads * a.tiles;
-        a.splits = (int)std::min(units, std::max<int64_t>(1, num_sms / pairs));
+        a.splits = (int)std::min(units, std::max<int64_t>(1, (3 - many_tiles(p)) * num_sms / pairs));
         // among several sequences some may have few rows
         a.mixed = p.b.n_seq > 1 && a.splits == 1 && p.group <= kFewRows;
         if (a.mixed) {

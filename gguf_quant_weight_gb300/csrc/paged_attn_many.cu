@@ -3,7 +3,9 @@
 //
 // A block takes two tiles of up to 128 rows of a (sequence, key head) -- the
 // query heads of the group, token by token -- through their keys, 128 at a
-// time.  Per tile of keys
+// time; for heads of up to 64 values one tile, with two blocks to an SM (short
+// sequences then leave no half of a block idle: 24 ragged chunks 26.6 us instead
+// of 29.6; heads of 128 values have no room for two blocks' keys).  Per tile of keys
 //   S = Q K^T   both operands from shared memory, 128 x 128 sums in TMEM
 //   P = exp2(c S - c m), c = scale log2 e: two threads to a row, 64 scores each
 //               in registers; the weights, in 16 bits, replace the scores in TMEM
@@ -14,7 +16,7 @@
 // pass it by 2^8: below that the weights and sums stay far from overflow and
 // equally precise, and O keeps its scale; so O is rescaled a few times in all.
 //
-// Warps 0-7 and 8-15: the two tiles' rows; warp 16 issues copies, warp 17 products.
+// Eight warps to a tile of rows, then one that issues copies and one for products.
 // A block that is done takes over one that has not begun (its index comes from
 // the launch's own queue), so its copies and products of the next tiles start
 // while the last rows are written; blocks stand in the order of their work, the
@@ -26,7 +28,7 @@
 // of a pair of tiles take 2048 cycles, work 70 % of the time.  Measured on GB300:
 // 8111-token prompt, 32 heads on 8 of 128, bf16, 330 us, 1630 TFLOP/s (a plain
 // bf16 product reaches 1860); heads of 64 values have half the products for the
-// same weights, and reach 600.  Short items (a window of 1000 keys: 10 tiles)
+// same weights, and reach 660 to 930.  Short items (a window of 1000 keys: 10 tiles)
 // spend a quarter of their time on the first tile and on writing their rows.
 #include "attn.cuh"
 
@@ -34,15 +36,17 @@ namespace gg {
 
 namespace {
 
-constexpr int kThreads = 576;
 constexpr int kKeys = 128;          // keys of a tile
 constexpr float kRaise = 8.f;       // log2 of how far scores may pass the maximum in use
 
-template <int DP> struct ManyCfg {
+template <int DP, int TILES> struct ManyCfg {
     static constexpr int HALF = 128 * 128;                 // bytes of 128 rows x 64 values
     static constexpr int TILE = DP / 64 * HALF;            // 128 rows x DP values
-    static constexpr int STAGES = DP == 128 ? 4 : 6;
-    static constexpr int SMEM = (2 + STAGES) * TILE;       // 192 KB at 128 values
+    static constexpr int STAGES = TILES == 2 ? 4 : 5;
+    static constexpr int SMEM = (TILES + STAGES) * TILE;   // 192 KB for two tiles of 128 values, 96 KB for one of 64
+    static constexpr int COPIES = 8 * TILES, PRODUCTS = COPIES + 1;           // warps
+    static constexpr int THREADS = 32 * (PRODUCTS + 1);
+    static constexpr int COLUMNS = 256 * TILES;            // of TMEM: scores of the tiles, then sums, 128 each
 };
 
 template <bool BF16> struct Elem { using T = __half; };
@@ -94,12 +98,13 @@ struct Item {
     int more;           // 1: an item with rows, 0: one without, -1: the end
 };
 
+template <int TILES>
 __device__ __forceinline__ bool find_item(const AttnParams& p, int splits, const Geometry& geo, uint3 at, Item& w, bool tell) {
     w.kvh = at.x / splits;
     w.split = at.x - w.kvh * splits;
-    w.r0 = (gridDim.y - 1 - at.y) * 2 * geo.rows;
+    w.r0 = (gridDim.y - 1 - at.y) * TILES * geo.rows;
     w.n = w.tiles[0] = w.tiles[1] = 0;
-    if (!row_span(p, at.z, w.r0, 2 * geo.rows, w.s, tell) || is_few(p, w.s.n)) return false;
+    if (!row_span(p, at.z, w.r0, TILES * geo.rows, w.s, tell) || is_few(p, w.s.n)) return false;
     const RowSpan& s = w.s;
     const int lo = s.lo / kKeys, all = s.hi > s.lo ? (s.hi + kKeys - 1) / kKeys - lo : 0;
     w.k0 = lo;
@@ -109,7 +114,7 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int splits, const
         k1 = lo + (int)((int64_t)all * (w.split + 1) / splits);
     }
     w.tiles[0] = k1 - w.k0;
-    if (w.r0 + geo.rows < s.n * p.group) {
+    if (TILES == 2 && w.r0 + geo.rows < s.n * p.group) {
         w.tiles[1] = w.tiles[0];
         if (p.causal) {          // the first tile's last token sees up to here
             const int hi = min(s.len, s.len - s.n + (w.r0 + geo.rows) / p.group);
@@ -145,11 +150,11 @@ __device__ __forceinline__ bool taken_block(const uint4* from, uint3& at) {
     return got != 0;
 }
 
-template <int DP, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int DP, bool BF16, int TILES>
+__global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
     attn_many_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const AttnParams p, const Partials part, const Geometry geo) {
-    using C = ManyCfg<DP>;
+    using C = ManyCfg<DP, TILES>;
     using T = typename Elem<BF16>::T;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // copies of K and V; Q; scores, weights (halves) and sums of a tile; the next block's index
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ float s_pair[2][2][128];          // two threads of a row
     __shared__ uint32_t s_tmem;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t sq = smem_u32(smem_raw), ring = sq + 2 * C::TILE;
+    const uint32_t sq = smem_u32(smem_raw), ring = sq + TILES * C::TILE;
 
     if (sq & 1023) {            // the swizzle's unit; the alignment asked for gives it
         if (threadIdx.x == 0) report(p.status, GGUF_ERR_CUDA);
@@ -182,24 +187,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s_weight[i][1], 4);
             mbar_init(&s_sum[i], 1);
             mbar_init(&s_item[i], 1);
-            mbar_init(&s_read[i], 17);                               // warps that read it
+            mbar_init(&s_read[i], C::COPIES + 1);                               // warps that read it
         }
         mbar_init(&s_next, 1);
         fence_mbar_init();
     }
-    if (warp == 17) tmem_alloc(&s_tmem, 512);
+    if (warp == C::PRODUCTS) tmem_alloc(&s_tmem, C::COLUMNS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // all 512 columns, so the address is 0: S of the two tiles at 0 and 128, O at 256 and 384
-    constexpr uint32_t tmem = 0;
+    // S of tile t at column 128 t, O at 128 (TILES + t).  (All 512 columns begin at 0.)
+    const uint32_t tmem = TILES == 2 ? 0 : __shfl_sync(0xffffffffu, s_tmem, 0);
     // Beside the few-rows kernel of the same call, which has waited for what came
     // before, this one waits at its end, so that what comes after waits for both.
     if (!geo.beside) pdl_wait();
     pdl_launch_dependents();
 
     bool ok = true;
-    // the k-th item of this block, as warp 16 found it
+    // the k-th item of this block, as the copying warp found it
     auto next_item = [&](int k) -> const Item& {
         ok = mbar_wait(&s_item[k & 1], k >> 1 & 1, p.status);
         ok = __all_sync(0xffffffffu, ok);
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&s_read[k & 1]);
     };
 
-    if (warp == 16) {
+    if (warp == C::COPIES) {
         // ---- copies: Q, then K and V of each tile of keys through the ring
         const int nbox = kKeys / geo.box;    // boxes of a tile: a page each, or half of one
         int st = 0, quse[2] = {0, 0};        // the ring's next stage; copies of Q so far
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (w.more == 0) {
                 if (lane == 0) take_block(&s_answer, &s_next);
-                w.more = find_item(p, part.splits, geo, at, w, lane == 0) ? 1 : 0;
+                w.more = find_item<TILES>(p, part.splits, geo, at, w, lane == 0) ? 1 : 0;
             }
             if (k >= 2) ok = ok && mbar_wait(&s_read[k & 1], (k >> 1) - 1 & 1, p.status);
             ok = __all_sync(0xffffffffu, ok);
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (w.more < 0) break;
             if (w.more == 0) continue;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < TILES; ++t) {
                 if (w.tiles[t] == 0) continue;
                 if (quse[t] > 0) ok = ok && mbar_wait(&s_qfree[t], quse[t] - 1 & 1, p.status);
                 ++quse[t];
@@ -293,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (quse[t] > 0) mbar_wait(&s_q[t], quse[t] - 1 & 1, p.status);
             if (!ok) mbar_wait(&s_next, 0, p.status), mbar_wait(&s_next, 1, p.status);
         }
-    } else if (warp == 17) {
+    } else if (warp == C::PRODUCTS) {
         // ---- products.  The warp's own instructions are what the tensor cores
         // wait for between products: it goes through them together, descriptors
         // advance by additions, and nothing is divided.
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // in halves of 64 keys, as their weights come
         auto sums = [&](int t, int from, bool first) {
             const uint32_t b = __shfl_sync(0xffffffffu, v_lo + from * (C::TILE >> 4), 0);
-            const uint32_t a = tmem + 128 * t, d = tmem + 256 + 128 * t;
+            const uint32_t a = tmem + 128 * t, d = tmem + 128 * (TILES + t);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 wait(&s_weight[t][h], weights >> t & 1);
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more == 0 || n == 0) continue;
             const int first = next();
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < TILES; ++t)
                 if (tiles[t] > 0) {
                     wait(&s_q[t], quse >> t & 1);
                     quse ^= 1u << t;
@@ -371,10 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i < tiles[0]) sums(0, v_st, i == 0);
                 if (more_keys) k_st = next();
                 if (i + 1 < tiles[0]) scores(0, k_st, i + 2 == tiles[0]);
-                if (i < tiles[1]) sums(1, v_st, i == 0);
+                if (TILES == 2 && i < tiles[1]) sums(1, v_st, i == 0);
                 umma_commit_warp(&s_empty[v_st]);
                 if (more_keys) v_next = next();
-                if (i + 1 < tiles[1]) scores(1, k_st, i + 2 == tiles[1]);
+                if (TILES == 2 && i + 1 < tiles[1]) scores(1, k_st, i + 2 == tiles[1]);
                 if (more_keys) umma_commit_warp(&s_empty[k_st]);
                 v_st = v_next;
             }
@@ -385,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (in, half) has the row's scores 64 half .. 64 half + 63
         const int t = warp >> 3, half = warp >> 2 & 1, in = 32 * (warp & 3) + lane, pair = 1 + t * 4 + (warp & 3);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 128 * t + lanes;
+        const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 128 * (TILES + t) + lanes;
         const float c2 = p.scale * kLog2e;
         int stage0 = 1;             // the ring's stage of the item's first V, and its parity
         uint32_t turn0 = 0;
@@ -566,11 +571,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 17) tmem_dealloc(tmem, 512);
+    if (warp == C::PRODUCTS) tmem_dealloc(tmem, C::COLUMNS);
 }
 
-template <int DP, bool BF16>
+template <int DP, bool BF16, int TILES>
 int launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int pdl, cudaStream_t s) {
+    using C = ManyCfg<DP, TILES>;
     Geometry geo;
     const int tokens = 128 / p.group;
     geo.rows = tokens * p.group;
@@ -580,20 +586,18 @@ int launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int 
     if (make_q_map(&q, p, p.group, tokens) != GGUF_OK || make_kv_map(&k, p.c.k, p.c, geo.box, 1) != GGUF_OK ||
         make_kv_map(&v, p.c.v, p.c, geo.box, 1) != GGUF_OK)
         return GGUF_ERR_UNSUPPORTED;
-    auto f = attn_many_kernel<DP, BF16>;
+    auto f = attn_many_kernel<DP, BF16, TILES>;
     static std::atomic<uint64_t> ready{0};
-    if (set_once(f, cudaFuncAttributeMaxDynamicSharedMemorySize, ManyCfg<DP>::SMEM, ready) != cudaSuccess)
-        return GGUF_ERR_CUDA;
+    if (set_once(f, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM, ready) != cudaSuccess) return GGUF_ERR_CUDA;
     const dim3 grid(p.c.kv_heads * plan.splits, plan.tiles, p.b.n_seq);
-    return launch_pdl(f, grid, dim3(kThreads), ManyCfg<DP>::SMEM, s, pdl, q, k, v, p, part, geo) == cudaSuccess
-               ? GGUF_OK : GGUF_ERR_CUDA;
+    return launch_pdl(f, grid, dim3(C::THREADS), C::SMEM, s, pdl, q, k, v, p, part, geo) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
 }
 
 }  // namespace
 
 int attn_many_launch(const AttnParams& p, const AttnPlan& plan, const Partials& part, int pdl, cudaStream_t s) {
-    if (p.c.dim > 64) return p.c.bf16 ? launch<128, true>(p, plan, part, pdl, s) : launch<128, false>(p, plan, part, pdl, s);
-    return p.c.bf16 ? launch<64, true>(p, plan, part, pdl, s) : launch<64, false>(p, plan, part, pdl, s);
+    if (many_tiles(p) == 2) return p.c.bf16 ? launch<128, true, 2>(p, plan, part, pdl, s) : launch<128, false, 2>(p, plan, part, pdl, s);
+    return p.c.bf16 ? launch<64, true, 1>(p, plan, part, pdl, s) : launch<64, false, 1>(p, plan, part, pdl, s);
 }
 
 }  // namespace gg
