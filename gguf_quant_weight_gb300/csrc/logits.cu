@@ -13,10 +13,10 @@
 // timing either (an entry alone for its token, the usual case, is added without
 // going through the list).  The logits' bytes bound it; each block reads the row's whole
 // history, from L2 after the first.
-// Measured on GB300: 256 x 131072 f32 in and out in 53 us (5.0 of the 6.8 TB/s
-// of a copy; the reads of a block wait for its history, and five blocks to an SM
-// do not quite cover it -- with four it takes 57 us, with six registers spill),
-// one row of 32003 in 2.7 us.
+// Measured on GB300: 256 x 131072 f32 in and out, histories of 1..2048, in 50 us
+// (5.4 of the 6.8 TB/s of a copy; without histories 40 us: a block's stores wait
+// for its row's, and six blocks to an SM do not quite cover it, four take 57 us),
+// 37 x 128259 from bf16 with every rule in 10 us, one row of 32003 in 2.4 us.
 #include "serving.cuh"
 
 namespace gg {
@@ -40,7 +40,7 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 // E: tokens a thread (a slice is kThreads * E).  Groups of tokens start at
 // 16-byte boundaries of the row's inputs.
 template <int DT, int ODT, int E>
-__global__ void __launch_bounds__(kThreads, E == 32 ? 4 : 5) logits_adjust_kernel(const LogitsParams p) {
+__global__ void __launch_bounds__(kThreads, E == 32 ? 4 : 6) logits_adjust_kernel(const LogitsParams p) {
     using X = typename El<DT>::T;
     using Y = typename El<ODT>::T;
     constexpr int SLICE = kThreads * E;
@@ -92,26 +92,35 @@ __global__ void __launch_bounds__(kThreads, E == 32 ? 4 : 5) logits_adjust_kerne
         }
     }
     int b_id = tid < nb ? p.r.bias_ids[b0 + tid] : -1;
+    // An id counts where its distance from the slice's first token, modulo 2^32, is
+    // inside the slice; what is counted there before the row's first token or past
+    // its last is never looked at, so ids outside the vocabulary need no test.
     for (int i0 = h0 + tid; i0 < h1; i0 += kAtOnce * kThreads) {
-        int id[kAtOnce];
+        unsigned at[kAtOnce];
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) id[j] = i0 + j * kThreads < h1 ? p.r.hist[i0 + j * kThreads] : -1;
+        for (int j = 0; j < kAtOnce; ++j)
+            at[j] = i0 + j * kThreads < h1 ? (unsigned)p.r.hist[i0 + j * kThreads] - (unsigned)first : 0xffffffffu;
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            const unsigned at = (unsigned)id[j] - (unsigned)first;
-            if (id[j] >= 0 && id[j] < vocab && at < SLICE) atomicAdd(&s_count[at], 1);
-        }
+        for (int j = 0; j < kAtOnce; ++j)
+            if (at[j] < SLICE) atomicAdd(&s_count[at[j]], 1);
     }
     for (int i = tid; i < nb; i += kThreads) {
         if (i != tid) b_id = p.r.bias_ids[b0 + i];
         const unsigned at = (unsigned)b_id - (unsigned)first;
-        if (b_id >= 0 && b_id < vocab && at < SLICE) {
+        if (at < SLICE) {
             const uint32_t bit = 1u << (at & 31);
             if ((atomicOr(&s_biased[at >> 5], bit) & bit) || i > 0xffff) atomicOr(&s_again[at >> 5], bit);
             s_entry[at] = (uint16_t)i;
         }
     }
     __syncthreads();
+    // x / repeat as a product with 1 / repeat, which is within a unit of it: a
+    // division at every token's place in the unrolled code costs more than the rest
+    // of the pass, in instructions to fetch
+    const float inv = 1.f / repeat;
+    auto penalised = [&](float v, int c) {
+        return c ? v * (v > 0.f ? inv : repeat) - fmaf((float)c, frequency, presence) : v;
+    };
     const bool out_wide = ((r * p.ldo - m) & (G - 1)) == 0;        // groups are aligned in the outputs too
 #pragma unroll
     for (int k = 0; k < E / G; ++k) {
@@ -128,12 +137,15 @@ __global__ void __launch_bounds__(kThreads, E == 32 ? 4 : 5) logits_adjust_kerne
             for (int i = 0; i < G; ++i) f[i] = v0 + i >= 0 && v0 + i < vocab ? to_f(x[v0 + i]) : 0.f;
         }
         if (p.r.hist) {
-            int c[G];
 #pragma unroll
-            for (int i = 0; i < G; i += 4) *reinterpret_cast<int4*>(c + i) = *reinterpret_cast<const int4*>(s_count + at + i);
-#pragma unroll
-            for (int i = 0; i < G; ++i)
-                if (c[i]) f[i] = (f[i] > 0.f ? f[i] / repeat : f[i] * repeat) - fmaf((float)c[i], frequency, presence);
+            for (int i = 0; i < G; i += 4) {
+                const int4 c = *reinterpret_cast<const int4*>(s_count + at + i);
+                if ((c.x | c.y | c.z | c.w) == 0) continue;
+                f[i] = penalised(f[i], c.x);
+                f[i + 1] = penalised(f[i + 1], c.y);
+                f[i + 2] = penalised(f[i + 2], c.z);
+                f[i + 3] = penalised(f[i + 3], c.w);
+            }
         }
         if (nb > 0) {
             const int sh = at & 31;                                                // a group lies in one word
@@ -178,11 +190,13 @@ __global__ void __launch_bounds__(kThreads, E == 32 ? 4 : 5) logits_adjust_kerne
 template <int DT, int ODT>
 cudaError_t launch(const LogitsParams& p, int num_sms, int pdl, cudaStream_t s) {
     // 64 bytes of a row a thread, so 4096 or 8192 tokens a block: fewer blocks read
-    // the row's history; 1024 where that leaves SMs idle.  A row's groups may
-    // start up to seven tokens before it.
+    // the row's history; 1024 where that leaves SMs idle.  Where rows
+    // begin inside a group, the groups start up to seven tokens before them.
     constexpr int E = DT == GGUF_DT_F32 ? 16 : 32;
-    const bool small = ceil_div(p.vocab + 7, kThreads * E) * p.rows < num_sms;
-    const dim3 grid((unsigned)ceil_div(p.vocab + 7, kThreads * (small ? 4 : E)), (unsigned)p.rows);
+    constexpr int G = DT == GGUF_DT_F32 ? 4 : 8;
+    const int64_t span = p.vocab + (p.ld % G && p.rows > 1 ? G - 1 : 0);
+    const bool small = ceil_div(span, kThreads * E) * p.rows < num_sms;
+    const dim3 grid((unsigned)ceil_div(span, kThreads * (small ? 4 : E)), (unsigned)p.rows);
     return small ? launch_pdl(logits_adjust_kernel<DT, ODT, 4>, grid, dim3(kThreads), 0, s, pdl, p)
                  : launch_pdl(logits_adjust_kernel<DT, ODT, E>, grid, dim3(kThreads), 0, s, pdl, p);
 }

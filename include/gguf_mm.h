@@ -425,7 +425,8 @@ typedef struct {
  * writes out (row r at out + r * ldo).  For a token v that comes c times in the
  * row's history, x its logit in f32:
  *   c > 0:  x = (x > 0 ? x / repeat[r] : x * repeat[r]) - (c * frequency[r] + presence[r])
- * then the biases of v are added in the order of the list, and a token that
+ * (the quotient to within a unit), then the biases of v are added in the order
+ * of the list, and a token that
  * `allow` leaves out becomes -inf.  dt and odt: F32, F16 or BF16; out may be
  * logits itself when the types and strides agree.  logits and out 16-byte
  * aligned (rows may start anywhere).  The result does not depend on timing.
