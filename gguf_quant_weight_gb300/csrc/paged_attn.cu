@@ -68,7 +68,7 @@ constexpr int kFewRows = 16;
 // Chunks of 16 keys from which a call deals its keys out to all warps and joins in
 // a second kernel: 16 rows over 4000 keys (2008 chunks) take 11.7 us in clusters
 // and 24 dealt out, over 8 x 4000 keys (16064 chunks) 37.7 dealt out.
-constexpr int64_t kLineChunks = 4096;
+constexpr int64_t kLineChunks = 8192;
 
 // The form and the split of a call, from its sizes alone.
 AttnPlan make_plan(const AttnParams& p, int num_sms) {
@@ -85,9 +85,9 @@ AttnPlan make_plan(const AttnParams& p, int num_sms) {
         if (pairs * chunks > kLineChunks) {
             a.blocks = 2 * num_sms;
         } else {
-            // blocks enough for two to an SM, with a chunk to each warp
-            const int64_t want = std::min(ceil_div(2 * num_sms, pairs), ceil_div(chunks, 4));
-            while (a.cluster < 16 && a.cluster < want) a.cluster *= 2;
+            // as many blocks as two to an SM can be at once, with a chunk to each warp
+            const int64_t most = 2 * num_sms / pairs;
+            while (a.cluster < 16 && 2 * a.cluster <= most && 4 * a.cluster < chunks) a.cluster *= 2;
         }
     } else {
         a.tiles = (int)ceil_div(p.b.max_q, many_tiles(p) * (128 / p.group));

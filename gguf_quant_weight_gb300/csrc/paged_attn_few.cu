@@ -400,7 +400,7 @@ __device__ __forceinline__ void load_chunk(uint32_t at, const CUtensorMap* tmK, 
 template <int DP, bool BF16, class W>
 __global__ void __launch_bounds__(kThreads)
     attn_few_cluster_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                            const AttnParams p, int tiles) {
+                            const AttnParams p, int tiles, int stages) {
     using C = FewCfg<DP>;
     using T = typename Elem<BF16>::T;
     extern __shared__ uint8_t smem_raw[];
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads)
             prefetch_tmap(&tmK);
             prefetch_tmap(&tmV);
         }
-        for (int i = 0; i < C::STAGES; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
         fence_mbar_init();
     }
     __syncwarp();
@@ -433,12 +433,15 @@ __global__ void __launch_bounds__(kThreads)
     const int mine = c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;   // chunks c0 + warp + 4 i
     const int32_t* pages = p.b.pages + s.seq * p.b.pages_stride;
     const int per_page = p.c.page_shift - 4;                         // log2 of the chunks in a page
-    const uint32_t slots = smem_u32(ring) + warp * C::STAGES * C::SLOT;
+    const uint32_t slots = smem_u32(ring) + warp * stages * C::SLOT;
 
     int page_of = 0;          // lane i: the page of the warp's chunk 32 j + i
     uint32_t have = 0;        // bit i % 32: chunk i was loaded
+    int st_get = 0;
     auto issue = [&](int i) {
         if (i >= mine) return;
+        const int to = st_get;
+        st_get = to + 1 == stages ? 0 : to + 1;
         if ((i & 31) == 0) {
             page_of = -1;
             if (i + lane < mine) {
@@ -453,21 +456,20 @@ __global__ void __launch_bounds__(kThreads)
         const uint32_t bit = 1u << (i & 31);
         have = page >= 0 ? have | bit : have & ~bit;
         if (page < 0 || lane != 0) return;
-        const int st = i % C::STAGES;
-        load_chunk<DP>(slots + st * C::SLOT, &tmK, &tmV, whole_heads(p), ((c0 + warp + kWarps * i) & ((1 << per_page) - 1)) * kChunk, kvh,
-                       page, &full[st]);
+        load_chunk<DP>(slots + to * C::SLOT, &tmK, &tmV, whole_heads(p), ((c0 + warp + kWarps * i) & ((1 << per_page) - 1)) * kChunk, kvh,
+                       page, &full[to]);
     };
 #pragma unroll 1
-    for (int i = 0; i < C::STAGES; ++i) issue(i);
+    for (int i = 0; i < stages; ++i) issue(i);
 
     W w;
     w.begin(p, s, kvh, r0, lane);
     const float c2 = p.scale * kLog2e;
     uint32_t phase = 0;                                              // bit st: the parity that slot st waits for
     bool ok = true;
+    int st = 0;
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
-        const int st = i % C::STAGES;
         if (have >> (i & 31) & 1) {
             if (!mbar_wait(&full[st], phase >> st & 1, p.status)) {
                 ok = false;
@@ -477,11 +479,12 @@ __global__ void __launch_bounds__(kThreads)
             w.take(s, slots + st * C::SLOT, (c0 + warp + kWarps * i) * kChunk, c2, lane);
             __syncwarp();
         }
-        issue(i + C::STAGES);
+        st = st + 1 == stages ? 0 : st + 1;
+        issue(i + stages);
     }
     if (!ok) {
         // let the copies in flight land before the ring is used for anything else
-        for (int i = 0; i < C::STAGES; ++i) mbar_wait(&full[i], phase >> i & 1, p.status, 1 << 12);
+        for (int i = 0; i < stages; ++i) mbar_wait(&full[i], phase >> i & 1, p.status, 1 << 12);
     }
 
     // join the block's warps: the sums at the largest maximum, in the ring's place
@@ -913,9 +916,14 @@ int launch_cluster(const AttnParams& p, const AttnPlan& plan, int pdl, cudaStrea
         return GGUF_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     const int tiles = plan.mixed ? plan.few_tiles : plan.tiles;
+    // no more slots to a warp than chunks: blocks of short sequences are small, and
+    // more of them are on the GPU at once
+    using C = FewCfg<DP>;
+    const int64_t chunks = ceil_div(ceil_div(p.b.max_kv, kChunk) + 1, plan.cluster * kWarps);
+    const int stages = (int)std::min<int64_t>(C::STAGES, std::max<int64_t>(1, chunks));
     cfg.gridDim = dim3(plan.cluster, p.c.kv_heads * tiles, p.b.n_seq);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = FewCfg<DP>::SMEM;
+    cfg.dynamicSmemBytes = std::max(kWarps * stages * C::SLOT, kWarps * W::ROWS * (DP + 4) * 4) + 1024;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -925,7 +933,7 @@ int launch_cluster(const AttnParams& p, const AttnPlan& plan, int pdl, cudaStrea
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, f, k, v, p, tiles) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, f, k, v, p, tiles, stages) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
 }
 
 }  // namespace
