@@ -66,9 +66,11 @@ __global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(const AttnParams
 // tokens (4 rows) of 64 sequences 104 / 221, over 131071 keys 51 / 56.
 constexpr int kFewRows = 16;
 // Chunks of 16 keys from which a call deals its keys out to all warps and joins in
-// a second kernel: 16 rows over 4000 keys (2008 chunks) take 11.7 us in clusters
-// and 24 dealt out, over 8 x 4000 keys (16064 chunks) 37.7 dealt out.
-constexpr int64_t kLineChunks = 8192;
+// a second kernel.  Clusters / dealt out, us: 16 sequences of 2000 keys (16128
+// chunks) 26.8 / 32.3, 32 of 50..1000 20.2 / 23.4, 36 of 400 16.1 / 23.3, 2 of
+// 16000 (16016) 39.2 / 35.0; dealt out, 64 of 100..8000 take 104 (up to 256512
+// chunks), and 156 in clusters.
+constexpr int64_t kLineChunks = 16384;
 
 // The form and the split of a call, from its sizes alone.
 AttnPlan make_plan(const AttnParams& p, int num_sms) {

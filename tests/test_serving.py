@@ -278,6 +278,14 @@ def test_attn_keys_dealt_out(dt, dim, causal, window, seqs, group):
     check_attn(Case(seqs, 2, dim, dt, page=16, seed=dim + window, wide=LARGE_WIDE), group, causal, window, **LARGE)
 
 
+@pytest.mark.parametrize("dt,dim", [("bf16", 128), ("f16", 64), ("bf16", 96)])
+@pytest.mark.parametrize("seqs,group,window", [([(1, 9000)], 4, 0), ([(2, 3000)], 8, 0), ([(1, 5000)], 1, 700),
+                                               ([(1, 3)], 16, 0), ([(3, 2500), (0, 10), (1, 1)], 5, 0)])
+def test_attn_few_items_in_many_shares(dt, dim, seqs, group, window):
+    # hundreds of shares of one item are joined, and as many warps have nothing where keys are few
+    check_attn(Case(seqs, 2, dim, dt, page=16, seed=dim + group, wide=20000), group, 1, window, max_kv_len=16 * 20000)
+
+
 @pytest.mark.parametrize("group", [1, 2, 3, 5, 7, 8, 16, 20])
 @pytest.mark.parametrize("seqs", [[(1, 300), (1, 77)], [(6, 70), (1, 1)], [(150, 200)]])
 def test_attn_groups(group, seqs):
