@@ -489,6 +489,11 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
                             tmem_st16(to + c, y);
                         }
                         tmem_st_wait();
+                        // The products of a tile's first 64 keys wait for the first half's
+                        // weights alone and add to every column of O, so neither warp may
+                        // deliver weights before both have rescaled their columns.
+                        tc_fence_before();
+                        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
                     }
                 }
                 const float mb = m == -INFINITY ? 0.f : -m * c2;
