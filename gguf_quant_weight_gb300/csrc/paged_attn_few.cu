@@ -81,6 +81,11 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
     return v;
 }
 
+// A wait that a warp's lanes give up together, if at all: what follows is for whole warps.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* status) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+}
+
 // The workspace of a call in equal shares: sums and statistics in places of
 // `rows` rows, two to a worker, and where each sequence begins in the line.
 struct LineSpace {
@@ -471,7 +476,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
         if (have >> (i & 31) & 1) {
-            if (!mbar_wait(&full[st], phase >> st & 1, p.status)) {
+            if (!wait_warp(&full[st], phase >> st & 1, p.status)) {
                 ok = false;
                 break;
             }
@@ -763,7 +768,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll 1
     while (left > 0) {
         if (have >> st & 1) {
-            if (!mbar_wait(&full[st], phase >> st & 1, p.status)) break;
+            if (!wait_warp(&full[st], phase >> st & 1, p.status)) break;
             phase ^= 1u << st;
             w.take(use.s, slots + st * C::SLOT, (use.s.lo / kChunk + use.c) * kChunk, c2, lane);
             __syncwarp();

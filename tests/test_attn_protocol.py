@@ -152,3 +152,27 @@ def test_all_come_to_their_end_when_waits_run_out(raising):
 def test_the_check_sees_a_warp_that_leaves_alone():
     with pytest.raises(AssertionError, match="left waiting"):
         explore([rows(0, 2, (1,), together=False), rows(1, 2, (1,), together=False), products(2)], expiry=True)
+
+
+# ------------------------------------------------------------------ the few-rows kernels: lanes of one warp
+
+def lane(chunks, together):
+    """A lane that waits for each chunk's copy and then joins the warp's matrix instructions on it."""
+    code = []
+    for i in range(chunks):
+        code += [("wait", "score", i + 1), ("both ok", "wait %d" % i) if together else ("leave alone",), ("meet", "products %d" % i)]
+    return code
+
+
+def copies(chunks):
+    return [("add", "score")] * chunks
+
+
+def test_lanes_of_a_warp_give_up_together():
+    good, bad = explore([lane(3, True), lane(3, True), copies(3)], expiry=True)
+    assert good == 1 and bad > 0
+
+
+def test_the_check_sees_a_lane_that_leaves_alone():
+    with pytest.raises(AssertionError, match="left waiting"):
+        explore([lane(2, False), lane(2, False), copies(2)], expiry=True)
