@@ -19,7 +19,9 @@
 //     that the GPU holds, across sequences, so that a warp's copies never
 //     pause and the sequences' lengths do not matter.  A second kernel joins
 //     what was cut.
-// Partial results are always joined in the same order.
+// Partial results are always joined in the same order.  One has seen nothing
+// where its sum of weights is 0; its maximum does not tell, since maxima pass
+// over NaN: scores of NaN alone leave -inf there, and NaN in the sums.
 //
 // Measured on GB300, 32 heads on 8 of 128, bf16: one token over 1021 keys 6.2 us;
 // 64 tokens over 100..8000 keys, 570 MB, 104 us (5.5 of the 6.8 TB/s of a copy;
@@ -510,11 +512,11 @@ __global__ void __launch_bounds__(kThreads)
         float top = -INFINITY;
 #pragma unroll
         for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_m[v][row]);
-        f[x] = w.m[x] == -INFINITY ? 0.f : exp2_fast(w.m[x] - top);
+        f[x] = w.l[x] == 0.f ? 0.f : exp2_fast(w.m[x] - top);
         if (warp == 0 && W::speaks(lane)) {
             float sum = 0.f;
 #pragma unroll
-            for (int v = 0; v < kWarps; ++v) sum += s_m[v][row] == -INFINITY ? 0.f : s_l[v][row] * exp2_fast(s_m[v][row] - top);
+            for (int v = 0; v < kWarps; ++v) sum += s_l[v][row] == 0.f ? 0.f : s_l[v][row] * exp2_fast(s_m[v][row] - top);
             s_ml[row] = make_float2(top, sum);
         }
     }
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(kThreads)
             for (int c = 0; c < kCluster; ++c) top = fmaxf(top, mc[c]);
 #pragma unroll
             for (int c = 0; c < kCluster; ++c) {
-                const float f = mc[c] == -INFINITY ? 0.f : exp2_fast(mc[c] - top);
+                const float f = lc[c] == 0.f ? 0.f : exp2_fast(mc[c] - top);
                 sum += f * lc[c];
                 v += f * vc[c];
             }
@@ -846,7 +848,7 @@ __global__ void __launch_bounds__(kJoin) attn_line_join_kernel(const AttnParams 
     float top = -INFINITY, sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float2 ml, float4 o) {
-        if (ml.x == -INFINITY) return;
+        if (ml.y == 0.f) return;
         const float t = fmaxf(top, ml.x), a = exp2_fast(top - t), b = exp2_fast(ml.x - t);
         top = t;
         sum = sum * a + ml.y * b;
