@@ -395,21 +395,23 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
         int stage0 = 1;             // the ring's stage of the item's first V, and its parity
         uint32_t turn0 = 0;
         uint32_t par = 0;           // parity of the tile's next scores, weights and sums
-        // Two warps that share a barrier never leave each other there: one whose
-        // wait has run out goes on to the next meeting, and both leave together.
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status));
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status)) != 0;
         };
-        auto both_ok = [&]() { return ok = !pair_any(pair, !ok); };
-        // the row's two threads' values, to both
-        auto exchange = [&](float x) {
+        // Two warps that share a barrier never leave each other there: one whose wait
+        // has run out goes on to the meetings that the other has before it learns of
+        // it, and both leave from the same one.
+        // The row's two threads' values, to both; false where a warp gives up.
+        auto exchange = [&](float x, bool good, float& other) {
             s_pair[t][half][in] = x;
-            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-            return s_pair[t][half ^ 1][in];
+            const bool both = !pair_any(pair, !good);
+            other = s_pair[t][half ^ 1][in];
+            return both;
         };
         for (int k = 0;; ++k) {
             const Item& w = next_item(k);
-            if (!both_ok() || w.more < 0) break;
+            ok = !pair_any(pair, !ok);      // (also: what was exchanged before has been read)
+            if (!ok || w.more < 0) break;
             if (w.more == 0) {
                 item_done(k);
                 continue;
@@ -429,7 +431,17 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
 #pragma unroll 1
             for (int i = 0; i < mine; ++i) {
                 const int j0 = (k0 + i) * kKeys;
-                wait(&s_score[t], par);
+                // without the scores: the two meetings up to the exchange, then away
+                auto give_up = [&]() {
+                    float none;
+                    pair_any(pair, true);
+                    exchange(0.f, false, none);
+                    ok = false;
+                };
+                if (!wait(&s_score[t], par)) {
+                    give_up();
+                    break;
+                }
                 tc_fence_after();
                 uint32_t v[64];
                 tmem_ld32(ts + 64 * half, v);
@@ -451,9 +463,12 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
                     // not reach the sums.  The products of the first tile of rows come
                     // first, and those of 64 keys wait for the warps that clear them here.
                     if ((j0 < w.s.lo || j0 + kKeys > w.s.hi) && (t == 0 || i >= w.tiles[0])) {
-                        wait(&s_full[v_st], v_turn);
+                        if (!wait(&s_full[v_st], v_turn)) {
+                            give_up();
+                            break;
+                        }
                         const int row = 64 * half + (in >> 1);
-                        if (ok && (j0 + row < w.s.lo || j0 + row >= w.s.hi))
+                        if (j0 + row < w.s.lo || j0 + row >= w.s.hi)
 #pragma unroll 1
                             for (int e = in & 1; e < DP / 8; e += 2)
                                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
@@ -468,23 +483,24 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
                 for (int j = 0; j < 64; j += 2)
                     top[j >> 1 & 3] = max3_nan(top[j >> 1 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
                 float mx = max3_nan(max3_nan(top[0], top[1], top[2]), top[3], top[3]);
-                // Whether any row of the two warps has to raise its maximum, or a wait has run
-                // out: mostly neither.  (Past this barrier both threads have their scores, and
+                // Whether any row of the two warps has to raise its maximum (or a warp gives
+                // up): mostly none has.  (Past this barrier both threads have their scores, and
                 // weights may replace them; and what was exchanged before has been read, since
                 // products that needed both threads' weights came between.)
-                if (pair_any(pair, !ok || (!(mx <= m) && !((mx - m) * c2 <= kRaise)))) {
-                    if (!both_ok()) break;
-                    const float other = exchange(mx);
+                if (pair_any(pair, !(mx <= m) && !((mx - m) * c2 <= kRaise))) {
+                    float other;
+                    ok = exchange(mx, true, other);
+                    if (!ok) break;
                     mx = max3_nan(mx, other, other);
                     const bool raise = !(mx <= m) && !((mx - m) * c2 <= kRaise);
                     const float f = raise ? exp2_fast((m - mx) * c2) : 1.f;
                     if (raise) m = mx < INFINITY ? mx : NAN;     // the row has no finite sum: all of it is NaN
                     l *= f;
                     if (i > 0) {
-                        wait(&s_sum[t], par ^ 1);
+                        const bool good = wait(&s_sum[t], par ^ 1);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 16 * half; ok && c < DP; c += 32) {
+                        for (int c = 16 * half; good && c < DP; c += 32) {
                             uint32_t y[16];
                             tmem_ld16(to + c, y);
                             tmem_ld_wait();
@@ -498,7 +514,8 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
                         // weights alone and add to every column of O, so neither warp may
                         // deliver weights before both have rescaled their columns.
                         tc_fence_before();
-                        if (!both_ok()) break;
+                        ok = !pair_any(pair, !good);
+                        if (!ok) break;
                     }
                 }
                 const float mb = m == -INFINITY ? 0.f : -m * c2;
@@ -527,9 +544,11 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
             stage0 += 2 * w.n;
             turn0 ^= stage0 / C::STAGES & 1;
             stage0 %= C::STAGES;
-            if (mine > 0 && ok) wait(&s_sum[t], par ^ 1);
-            if (!both_ok()) break;      // (also: what was exchanged before has been read)
-            l += exchange(l);
+            if (!ok) break;
+            float other;
+            ok = exchange(l, mine == 0 || wait(&s_sum[t], par ^ 1), other);
+            if (!ok) break;
+            l += other;
             tc_fence_after();
             const int D = p.c.dim, head = w.kvh * p.group + r % p.group;
             const int64_t row = (int64_t)(w.s.t0 + tok) * p.heads + head;

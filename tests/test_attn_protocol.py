@@ -39,9 +39,7 @@ def rows(half, tiles, raising, joined=True, together=True):
     for i in range(tiles):
         wait("score", i + 1)
         code.append(("vote", "tile %d" % i, i in raising))       # its end: the next "deliver" unless any has voted
-        if together:
-            meet("any %d" % i)
-        code.append(("meet", "exchange %d" % i))
+        meet("exchange %d" % i)
         if i > 0:
             code.append(("wait", "sum", i))
             code.append(("act", "rescale", half, i))
