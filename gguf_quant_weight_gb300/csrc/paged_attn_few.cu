@@ -106,8 +106,12 @@ LineSpace line_space(const AttnParams& p, const AttnPlan& plan, void* base) {
     return ws;
 }
 
-template <bool BF16> struct Elem { using T = __half; };
-template <> struct Elem<true> { using T = __nv_bfloat16; };
+// LIFT: what a weight, at most 1, is multiplied by as operand of P V.  An f16 would
+// lose digits below 2^-14 and be 0 below 2^-25, and 10^5 such keys beside a dominant
+// one are a visible part of a row; lifted they keep their digits down to 2^-29 and
+// vanish below 2^-40.
+template <bool BF16> struct Elem { using T = __half; static constexpr float LIFT = 32768.f; };
+template <> struct Elem<true> { using T = __nv_bfloat16; static constexpr float LIFT = 1.f; };
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
@@ -237,7 +241,7 @@ struct Rows16 {
             for (int n = 0; n < 2; ++n) {
                 const float a = exp2_fast(sc[n][2 * x] - base), b = exp2_fast(sc[n][2 * x + 1] - base);
                 l[x] += a + b;
-                w[2 * n + x] = pack2<BF16>(a, b);
+                w[2 * n + x] = pack2<BF16>(a * Elem<BF16>::LIFT, b * Elem<BF16>::LIFT);
             }
         }
         const int vr = (lane & 7) + (lane >> 3 & 1) * 8, vc = lane >> 4;
@@ -250,8 +254,13 @@ struct Rows16 {
         }
     }
 
-    // The lanes' shares of the rows' sums of weights, together.
+    // The lanes' shares of the rows' sums of weights, together; the sums as they are without the lift.
     __device__ __forceinline__ void end() {
+        if (!BF16)
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i][j] *= 1.f / Elem<BF16>::LIFT;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
@@ -365,7 +374,8 @@ struct Rows8 {
             e[2 + x] = exp2_fast(e[2 + x] - base);
             l[x] += e[x] + e[2 + x];
         }
-        const uint32_t w0 = transpose8(pack2<BF16>(e[0], e[1])), w1 = transpose8(pack2<BF16>(e[2], e[3]));
+        constexpr float up = Elem<BF16>::LIFT;
+        const uint32_t w0 = transpose8(pack2<BF16>(e[0] * up, e[1] * up)), w1 = transpose8(pack2<BF16>(e[2] * up, e[3] * up));
         const int vr = (lane & 7) + (lane >> 4) * 8, vc = lane >> 3 & 1;
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i) {
@@ -376,6 +386,11 @@ struct Rows8 {
     }
 
     __device__ __forceinline__ void end() {
+        if (!BF16)
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[i][j] *= 1.f / Elem<BF16>::LIFT;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll

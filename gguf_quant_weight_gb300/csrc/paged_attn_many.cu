@@ -38,6 +38,10 @@ namespace {
 
 constexpr int kKeys = 128;          // keys of a tile
 constexpr float kRaise = 8.f;       // log2 of how far scores may pass the maximum in use
+// log2 of what the weights of an f16 call are lifted by, with kRaise at most to 2^15: an
+// f16 loses digits below 2^-14 and is 0 below 2^-25, and 10^5 keys of such weights are a
+// visible part of a row.  Sums of weights and of values carry it alike.
+constexpr float kLift = 7.f;
 
 template <int DP, int TILES> struct ManyCfg {
     static constexpr int HALF = 128 * 128;                 // bytes of 128 rows x 64 values
@@ -49,8 +53,9 @@ template <int DP, int TILES> struct ManyCfg {
     static constexpr int COLUMNS = 256 * TILES;            // of TMEM: scores of the tiles, then sums, 128 each
 };
 
-template <bool BF16> struct Elem { using T = __half; };
-template <> struct Elem<true> { using T = __nv_bfloat16; };
+// LIFT: log2 of the weights' factor; DROP: what takes it out of a sum.
+template <bool BF16> struct Elem { using T = __half; static constexpr float LIFT = kLift, DROP = 1.f / 128.f; };
+template <> struct Elem<true> { using T = __nv_bfloat16; static constexpr float LIFT = 0.f, DROP = 1.f; };
 
 __device__ __forceinline__ void tma_load_q(uint32_t smem_dst, const CUtensorMap* map, int d, int head, int token,
                                            uint64_t* bar) {
@@ -518,7 +523,7 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
                         if (!ok) break;
                     }
                 }
-                const float mb = m == -INFINITY ? 0.f : -m * c2;
+                const float mb = m == -INFINITY ? 0.f : fmaf(-m, c2, Elem<BF16>::LIFT);
                 const f32x2 cc = {c2, c2}, bb = {mb, mb};
                 f32x2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
@@ -571,6 +576,9 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
                 if (!is) continue;
                 if (part.splits > 1) {
 #pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (!BF16) y[j] = __float_as_uint(__uint_as_float(y[j]) * Elem<BF16>::DROP);
+#pragma unroll
                     for (int j = 0; j < 16; j += 4)
                         *reinterpret_cast<uint4*>(po + c + j) = make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]);
                     continue;
@@ -587,9 +595,9 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
             }
             if (!is || half != 0) {
             } else if (part.splits > 1)
-                part.ml[(int64_t)w.split * p.b.n_tokens * p.heads + row] = make_float2(l == 0.f ? -INFINITY : m * c2, l);
+                part.ml[(int64_t)w.split * p.b.n_tokens * p.heads + row] = make_float2(l == 0.f ? -INFINITY : m * c2, l * Elem<BF16>::DROP);
             else if (p.lse)
-                p.lse[row] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+                p.lse[row] = l == 0.f ? -INFINITY : m * p.scale + logf(l * Elem<BF16>::DROP);
             tc_fence_before();
             item_done(k);
         }

@@ -96,3 +96,66 @@ def test_nan_key_makes_the_rows_that_see_it_nan(dt, dim, form, group, n, length,
             assert torch.isnan(out[j, :group]).all() and torch.isnan(lse[j, :group]).all()
             out[j, :group], lse[j, :group] = clean[j, :group], clean_lse[j, :group]
     assert torch.equal(out.nan_to_num(7.0), clean.nan_to_num(7.0)) and torch.equal(lse, clean_lse), "another row changed"
+
+
+# ------------------------------------------------------------------ weights of every size
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("form,group,n", [("cluster", 4, 1), ("cluster", 8, 2), ("dealt", 2, 1), ("dealt", 16, 1), ("many", 20, 1),
+                                          ("many", 1, 40)])
+@pytest.mark.parametrize("first", [True, False])
+def test_many_small_weights_beside_one_dominant_key(dt, form, group, n, first):
+    # One key at weight 1 (the first, or the last before the new tokens) and 131072 at 2^-23 .. 2^-28, which are
+    # together a few thousandths of the row: all of the output is theirs, and all of it of one sign.  Bounds:
+    #   * a weight is rounded to within u of itself, which moves the output by u times itself; an f16 below what
+    #     the lifted type holds whole, by 2^-25 of the lift instead: 2^-40 a key (2^-32 with many rows);
+    #   * a weight's own error is e as in tests/test_serving.py, so the output's is 2 e of it;
+    #   * a lane adds the weights of at most 512 keys to its sum, one after the other, each to within 2^-24 of it.
+    N = 131073 + n
+    c = Case([(n, N)], 1, 64, dt, page=64, seed=group, wide=16 * LARGE // 64 if form == "dealt" else None)
+    q = c.values((n, group, 64))
+    q[..., 0] = 8.0
+    low = torch.tensor(c.rs.uniform(-19.4, -16.0, N), dtype=torch.float32)
+    low[0 if first else N - n - 1] = 0.0
+    pages = torch.tensor(c.pages[0, :-(-N // 64)].astype(np.int64), device=DEV)
+    flat = torch.zeros((len(pages) * 64, 64), device=DEV)
+    flat[:N, 0] = low.to(DEV)
+    values = torch.ones_like(flat) + 0.5 * torch.rand(flat.shape, device=DEV)
+    values[0 if first else N - n - 1] = 0.0
+    for cache, x in ((c.k, flat), (c.v, values)):
+        cache[pages, 0] = x.reshape(len(pages), 64, 64).to(cache.dtype)
+    out, lse = run_in(c, form, group, q=q)
+    ref, rlse, vmax, smax = S.attention(U.host64(q), U.host64(c.k), U.host64(c.v), c.q_start, c.kv_len, c.pages, 0.125, 1, 0)
+    u = 2.0 ** -8 if dt == "bf16" else 2.0 ** -11
+    e = 2.0 ** -23 * 16 * smax + 2.0 ** -20
+    assert 1e-3 < np.abs(ref).max() < 1e-1
+    sums = 512 * 2.0 ** -24
+    small = 0.0 if dt == "bf16" else N * (2.0 ** -32 if form == "many" else 2.0 ** -40)
+    near(U.host64(out), ref, dt, (u + 2 * e + sums)[..., None] * np.abs(ref) + small * vmax[..., None], "out")
+    near(lse.cpu().numpy(), rlse, "f32", e + sums, "lse")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_small_weights_in_rows_of_one_share(dt):
+    # the same in the many-rows form with its keys in one piece, as so many heads leave them: fewer keys, larger values
+    N, n, KV = 2001, 40, 160
+    c = Case([(n, N)], KV, 64, dt, page=32, seed=30)
+    q = c.values((n, KV, 64))
+    q[..., 0] = 8.0
+    c.k.zero_()
+    low = torch.tensor(c.rs.uniform(-19.4, -16.0, N), dtype=torch.float32)
+    low[0] = 0.0
+    c.v.copy_(100.0 + 50.0 * torch.rand(c.v.shape, device=DEV))
+    t = np.arange(N)
+    pages, slots = (torch.tensor(x.astype(np.int64), device=DEV) for x in (c.pages[0, t // 32], t % 32))
+    c.k[pages, :, slots, 0] = low.to(DEV, c.k.dtype)[:, None]
+    c.v[int(c.pages[0, 0]), :, 0] = 0.0
+    out, lse = run_in(c, "many", 1, q=q)
+    assert g.gguf_paged_attn_workspace_size(c.batch(), g.gguf_kv_cache(c.k, c.v), KV) == 0, "the keys were split"
+    ref, rlse, vmax, smax = S.attention(U.host64(q), U.host64(c.k), U.host64(c.v), c.q_start, c.kv_len, c.pages, 0.125, 1, 0)
+    u = 2.0 ** -8 if dt == "bf16" else 2.0 ** -11
+    e = 2.0 ** -23 * 16 * smax + 2.0 ** -20
+    sums = 32 * 2.0 ** -24         # two chains of 32 weights to a tile, and a tile at a time
+    small = 0.0 if dt == "bf16" else N * 2.0 ** -32
+    near(U.host64(out), ref, dt, (u + 2 * e + sums)[..., None] * np.abs(ref) + small * vmax[..., None], "out")
+    near(lse.cpu().numpy(), rlse, "f32", e + sums, "lse")
