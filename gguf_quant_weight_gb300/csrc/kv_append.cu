@@ -5,9 +5,9 @@
 //   (a, b) -> scale * (a cos - b sin, a sin + b cos).
 // The angle matters modulo one turn only, and p * freqs[i] reaches 10^5 and
 // more, where an f32 product has lost the digits that cos and sin depend on:
-// the product of a 24-bit and a 32-bit number fits a double, so the turns
-// p * freqs[i] / 2 pi are taken in double, their whole part dropped, and the
-// rest goes to sincospif in f32.  That is rot/2 angles to a token, shared by
+// the turns p * freqs[i] / 2 pi are taken in double (a position of 31 bits
+// leaves 22 and more after the point), their whole part dropped, and the rest
+// goes to sincospif in f32.  That is rot/2 angles to a token, shared by
 // all its heads through shared memory.
 //
 // The bytes bound it: every value of q, k and v is read once and written once.
@@ -64,11 +64,11 @@ __device__ __forceinline__ void store_v(T* p, const float (&f)[V]) {
 // depend on it.
 template <class X, class C, int V, bool NEOX>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams p) {
-    __shared__ int s_found, s_pos;
+    __shared__ int s_found, s_disorder, s_pos;
     __shared__ int64_t s_slot;                    // element offset of the token in the cache, -1: not stored
     __shared__ float s_cos[64], s_sin[64];
     const int t = blockIdx.x, tid = threadIdx.x;
-    if (tid == 0) s_found = 0;
+    if (tid == 0) s_found = s_disorder = 0;
 
     // a head's work: with halves, rot / 2V units that turn two vectors and the
     // rest that copy one; with neighbours, one vector each
@@ -109,16 +109,21 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
         if (u0 + j * step < n) find(u0 + j * step, ws[j]);           // of a row past the last sequence in vain
+    const int64_t room = p.b.pages_stride << p.c.page_shift;
     for (int i = tid; i < p.b.n_seq; i += kThreads) {
         const int from = p.b.q_start[i], to = p.b.q_start[i + 1], len = p.b.kv_len[i];
-        if (from <= t && t < to) {
-            const int pos = len - to + t;
+        const bool off = from < 0 || to < from || to > p.b.n_tokens || to - from > p.b.max_q || len > room || len > p.b.max_kv;
+        if (to < from) s_disorder = 1;          // a token may be in two sequences: none is touched
+        if (off) {
+            if (t == 0 && blockIdx.y == 0) report(p.status, GGUF_ERR_INVALID_ARG);
+        } else if (from <= t && t < to) {
+            const int pos = (int)max((int64_t)INT32_MIN, (int64_t)len - to + t);
             s_pos = pos;
             s_found = 1;
             int64_t slot = -1;
             if (pos >= 0) {
                 const int64_t col = pos >> p.c.page_shift;
-                const int page = col < p.b.pages_stride ? p.b.pages[i * p.b.pages_stride + col] : -1;
+                const int page = p.b.pages[i * p.b.pages_stride + col];
                 if ((unsigned)page < (unsigned)p.c.n_pages)
                     slot = page * p.c.page_stride + (pos & ((1 << p.c.page_shift) - 1)) * p.c.token_stride;
                 else
@@ -129,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
     }
     __syncthreads();
     pdl_launch_dependents();
-    if (!s_found) return;
+    if (!s_found || s_disorder) return;
     if (tid < half) {
         const int at = p.positions ? p.positions[t] : s_pos;
         const double turns = (double)at * (double)p.freqs[tid] * 0.15915494309189533577;  // 1 / (2 pi)

@@ -298,9 +298,11 @@ int gguf_dense_gemm_noalloc(const void* wdense, int wdt, int64_t ld, int64_t N, 
  * kept past the call.
  *
  * An index that leads outside the caller's buffers is never followed: a page
- * id outside [0, n_pages) where a key is read or written, a position past the
- * page table's row, q_start out of order or past n_tokens.  Such a token's or
- * sequence's results are undefined, and gguf_mm_check_errors() reports
+ * id outside [0, n_pages) where a key is read or written, a sequence's q_start
+ * out of order or outside [0, n_tokens], its kv_len past the page table's row,
+ * more new tokens or keys than max_q_len and max_kv_len.  Such a
+ * token's or sequence's results are undefined (it appends nothing; where
+ * q_start falls, none of the batch does), and gguf_mm_check_errors() reports
  * GGUF_ERR_INVALID_ARG.
  * ------------------------------------------------------------------------- */
 
@@ -326,7 +328,7 @@ typedef struct {
 /* A batch of sequences.  Rows of the packed inputs at and after q_start[n_seq]
  * are left alone, so n_tokens may be an upper bound (a captured graph's).
  *   q_start  [n_seq + 1] int32, non-decreasing, q_start[0] >= 0, q_start[n_seq] <= n_tokens
- *   kv_len   [n_seq] int32 (0: no keys at all)
+ *   kv_len   [n_seq] int32 (0 or less: no keys at all)
  *   pages    [n_seq][pages_stride] int32; entries past a sequence's last page
  *            are not read (attention under a window also reads none before it)
  *   max_q_len, max_kv_len  bounds on the sequences' new tokens and keys, known
@@ -343,7 +345,7 @@ typedef struct {
 /* Rotary positions: pair i of a head, i < rot_dim / 2, turns by the angle
  * p * freqs[i] (radians, freqs f32 [rot_dim / 2]; base, scaling and per-channel
  * factors are in them) and is multiplied by `scale` (1 without scaling).
- * The product p * freqs[i] is taken in 64 bits, so far positions keep their digits.
+ * The product p * freqs[i] is taken in f64, so far positions keep their digits.
  *   style      GGUF_ROPE_NORM: pair i is values 2i, 2i+1;
  *              GGUF_ROPE_NEOX: values i, i + rot_dim / 2
  *   rot_dim    even, 2 .. head_dim; the values from rot_dim on are copied

@@ -1,0 +1,44 @@
+"""What the serving operators refuse, report and leave alone: the C entries'
+refusals and the binding's own checks (CPU), and the device's reports (GPU)."""
+import numpy as np
+import pytest
+
+import gguf_quant_weight_gb300 as g
+
+INV = g.GGUF_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ indexes on the device
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what,start,length,kw,good", [
+    ("falling q_start", [0, 5, 3, 8], [9, 9, 9], {}, []),
+    ("a falling pair of other sequences", [0, 2, 7, 6], [9, 9, 9], {}, []),
+    ("negative q_start", [-2, 3, 4, 8], [9, 9, 9], {}, [1, 2]),
+    ("q_start past the tokens", [0, 3, 4, 9], [9, 9, 9], {}, [0, 1]),
+    ("more new tokens than stated", [0, 2, 3, 8], [9, 9, 9], dict(max_q_len=4), [0, 1]),
+    ("more keys than stated", [0, 3, 4, 8], [9, 31, 9], dict(max_kv_len=30), [0, 2]),
+    ("more keys than pages", [0, 3, 4, 8], [9, 33, 9], {}, [0, 2])])
+def test_append_reports_arrays_out_of_range(what, start, length, kw, good):
+    torch = pytest.importorskip("torch")
+    from tests import gpu_util as U
+    U.require_gpu()
+    T, H, KV, D, page = 8, 2, 2, 64, 16
+    rs = np.random.default_rng(1)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    kc, vc = (U.guarded((6, KV, page, D), torch.bfloat16, 3.0) for _ in range(2))
+    q, k, v = (torch.tensor(rs.standard_normal((T, h, D)), dtype=torch.bfloat16, device="cuda") for h in (H, KV, KV))
+    out = U.guarded((T, H, D), torch.bfloat16, 3.0)
+    pages = i32([[0, 1], [2, 3], [4, 5]])
+    b = g.gguf_kv_batch(i32(start), i32(length), pages, T, kw.get("max_q_len", T), kw.get("max_kv_len", 32))
+    g.gguf_kv_append(q, H * D, k, KV * D, v, KV * D, g.GGUF_DT_BF16, H, None, b, g.gguf_kv_cache(kc.t, vc.t), out.t, H * D)
+    assert g.gguf_mm_check_errors() == INV, what
+    assert g.gguf_mm_check_errors() == 0
+    ko, vo, qo = (torch.full_like(x.t, 3.0) for x in (kc, vc, out))
+    for s in good:
+        for t in range(start[s], start[s + 1]):
+            p = length[s] - start[s + 1] + t
+            ko[int(pages[s, p // page]), :, p % page], vo[int(pages[s, p // page]), :, p % page], qo[t] = k[t], v[t], q[t]
+    for got, want in ((kc, ko), (vc, vo), (out, qo)):
+        got.check(what)
+        assert torch.equal(got.t, want), what
