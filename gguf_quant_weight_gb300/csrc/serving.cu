@@ -95,6 +95,8 @@ int gguf_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const
     if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || ldk % per16 || ldv % per16 ||
         (q && (ldq % per16 || ldqo % 8)))
         return GGUF_ERR_MISALIGNED;
+    // in place a row may only overwrite itself
+    if (q && q == q_out && (xdt != cache->dtype || (ldq != ldqo && p.b.n_tokens > 1))) return GGUF_ERR_INVALID_ARG;
     int sms = 0;
     if ((st = current_device_launch_facts(&sms, &p.status)) != GGUF_OK) return st;
     p.q = q;

@@ -365,7 +365,8 @@ typedef struct {
  * [head_dim] of xdt (F32, F16 or BF16); token t's heads start at q + t * ldq
  * (k + t * ldk, v + t * ldv; elements), so the three may be the columns of one
  * fused projection.  q_out [n_tokens][heads][head_dim] of the cache's dtype,
- * token t at q_out + t * ldqo; it may be q itself when the types agree.  The
+ * token t at q_out + t * ldqo; it may be q itself when xdt is the cache's dtype
+ * and ldqo = ldq, and may not overlap q, k or v otherwise.  The
  * rotation is computed in f32 and each value rounded once.
  *   rope  NULL: nothing is rotated (values are converted and stored)
  *   q     NULL (with q_out NULL): keys and values only

@@ -1,11 +1,31 @@
 """What the serving operators refuse, report and leave alone: the C entries'
 refusals and the binding's own checks (CPU), and the device's reports (GPU)."""
+import ctypes
+
 import numpy as np
 import pytest
 
 import gguf_quant_weight_gb300 as g
+from tests.test_serving_abi import batch, cache, lib  # noqa: F401
 
 INV = g.GGUF_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ in place
+
+def test_append_in_place_wants_the_same_type_and_rows(lib):  # noqa: F811
+    r = ctypes.byref
+    c = cache()
+
+    def call(q_out=1024, ldo=256, ldq=256, xdt=2, **kw):
+        return lib.gguf_kv_append(1024, ldq, 4096, 128, 8192, 128, xdt, 4, None, r(batch(**kw)), r(c), q_out, ldo, None)
+
+    fine = call()
+    assert fine != INV
+    assert call(xdt=0) == INV and call(xdt=1) == INV          # f32 or f16 rows under bf16 ones
+    assert call(ldo=264) == INV and call(ldq=264) == INV      # rows that overlap their neighbours
+    assert call(ldo=264, n_tokens=1, max_q_len=1) == fine
+    assert call(q_out=1 << 20, xdt=0, ldo=264) == fine
 
 
 # ------------------------------------------------------------------ indexes on the device
