@@ -97,6 +97,16 @@ _SIGS = {
 GGUF_ROPE_NORM, GGUF_ROPE_NEOX = 0, 1
 
 
+def _array(name, t, *dtypes):
+    """t as an array that the kernels read element after element: of one of the types, without gaps (None and a device
+    address pass)."""
+    if t is None or isinstance(t, int):
+        return t
+    if str(t.dtype).rsplit(".", 1)[-1] not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name} is a contiguous array of {' or '.join(dtypes)}, not {t.dtype} of strides {tuple(t.stride())}")
+    return t
+
+
 def _dt_of(t):
     import torch
     return {torch.float32: GGUF_DT_F32, torch.float16: GGUF_DT_F16, torch.bfloat16: GGUF_DT_BF16}[t.dtype]
@@ -123,11 +133,12 @@ class gguf_kv_batch(ctypes.Structure):
                 ("pages_stride", _c_i64), ("max_q_len", _c_i64), ("max_kv_len", _c_i64)]
 
     def __init__(self, q_start, kv_len, pages, n_tokens, max_q_len, max_kv_len):
-        if q_start.numel() != kv_len.numel() + 1 or pages.shape[0] != kv_len.numel() or pages.stride(1) != 1:
+        if q_start.numel() != kv_len.numel() + 1 or pages.shape[0] != kv_len.numel() or \
+                (pages.shape[1] > 1 and pages.stride(1) != 1):
             raise ValueError("q_start has one entry more than kv_len, and pages a row of stride 1 for each sequence")
-        for t in (q_start, kv_len, pages):
-            if "int32" not in str(t.dtype):
-                raise ValueError("q_start, kv_len and pages are int32")
+        if str(pages.dtype) != "torch.int32":
+            raise ValueError("q_start, kv_len and pages are int32")
+        _array("q_start", q_start, "int32"), _array("kv_len", kv_len, "int32")
         stride = pages.stride(0) if pages.shape[0] > 1 else pages.shape[1]
         super().__init__(_p(q_start), _p(kv_len), _p(pages), kv_len.numel(), n_tokens, stride, max_q_len, max_kv_len)
         self._keep = (q_start, kv_len, pages)
@@ -140,6 +151,9 @@ class gguf_rope(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
     def __init__(self, freqs, rot_dim, style=GGUF_ROPE_NORM, scale=1.0, positions=None):
+        _array("freqs", freqs, "float32"), _array("positions", positions, "int32")
+        if not (freqs is None or isinstance(freqs, int)) and 2 * freqs.numel() < rot_dim:
+            raise ValueError(f"freqs has {freqs.numel()} entries for {rot_dim // 2} pairs")
         super().__init__(_p(freqs), _p(positions), rot_dim, style, scale)
         self._keep = (freqs, positions)
         self._ref = ctypes.addressof(self)
@@ -152,6 +166,13 @@ class gguf_logit_rules(ctypes.Structure):
 
     def __init__(self, hist=None, hist_start=None, repeat=None, frequency=None, presence=None, bias_ids=None, bias=None,
                  bias_start=None, allow=None):
+        for name, t in (("hist", hist), ("hist_start", hist_start), ("bias_ids", bias_ids), ("bias_start", bias_start)):
+            _array(name, t, "int32")
+        for name, t in (("repeat", repeat), ("frequency", frequency), ("presence", presence), ("bias", bias)):
+            _array(name, t, "float32")
+        if allow is not None and (str(allow.dtype) not in ("torch.int32", "torch.uint32") or allow.dim() != 2 or
+                                  (allow.shape[1] > 1 and allow.stride(1) != 1)):
+            raise ValueError("allow is a matrix of 32-bit words whose rows are dense")
         stride = 0 if allow is None else allow.stride(0) if allow.shape[0] > 1 else allow.shape[1]
         super().__init__(*(_p(t) for t in (hist, hist_start, repeat, frequency, presence, bias_ids, bias, bias_start,
                                            allow)), stride)

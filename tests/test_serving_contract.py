@@ -62,3 +62,51 @@ def test_append_reports_arrays_out_of_range(what, start, length, kw, good):
     for got, want in ((kc, ko), (vc, vo), (out, qo)):
         got.check(what)
         assert torch.equal(got.t, want), what
+
+
+# ------------------------------------------------------------------ the binding's structs
+
+def test_batch_refuses_arrays_with_gaps():
+    torch = pytest.importorskip("torch")
+    i, pages = torch.zeros(6, dtype=torch.int32), torch.zeros((2, 4), dtype=torch.int32)
+    g.gguf_kv_batch(i[:3], i[:2], pages, 3, 1, 1)
+    for a in ((i[::2], i[:2], pages), (i[:3], i[:4:2], pages), (i[:3].long(), i[:2], pages), (i[:3], i[:2].to(torch.uint8), pages),
+              (i[:3], i[:2], pages.to(torch.int16)), (i[:3], i[:2], pages.T[:2])):
+        with pytest.raises(ValueError):
+            g.gguf_kv_batch(*a, 3, 1, 1)
+    column = torch.zeros((1, 2), dtype=torch.int32).T        # one page a sequence: its stride says nothing
+    assert g.gguf_kv_batch(i[:3], i[:2], column, 3, 1, 1).pages_stride == 1
+
+
+def test_rope_refuses_other_types_and_gaps():
+    torch = pytest.importorskip("torch")
+    f = torch.zeros(64)
+    p = torch.zeros(8, dtype=torch.int32)
+    g.gguf_rope(f[:32], 64, positions=p)
+    g.gguf_rope(f, 64)
+    assert g.gguf_rope(16, 64).freqs == 16                    # a device address
+    for a, kw in (((f.double(), 64), {}), ((f.half(), 64), {}), ((f[::2], 64), {}), ((f[:31], 64), {}),
+                  ((f, 64), dict(positions=p.long())), ((f, 64), dict(positions=p[::2]))):
+        with pytest.raises(ValueError):
+            g.gguf_rope(*a, **kw)
+
+
+def test_rules_refuse_other_types_and_gaps():
+    torch = pytest.importorskip("torch")
+    i, f, words = torch.zeros(8, dtype=torch.int32), torch.ones(8), torch.zeros((2, 8), dtype=torch.int32)
+    good = dict(hist=i, hist_start=i[:3], repeat=f[:2], frequency=f[:2], presence=f[:2], bias_ids=i, bias=f, bias_start=i[:3],
+                allow=words)
+    assert g.gguf_logit_rules(**good).allow_stride == 8
+    assert g.gguf_logit_rules(allow=words[:, :5]).allow_stride == 8
+    g.gguf_logit_rules()
+    for name in ("hist", "hist_start", "bias_ids", "bias_start"):
+        for bad in (i.long(), torch.zeros(16, dtype=torch.int32)[::2], f):
+            with pytest.raises(ValueError, match=name):
+                g.gguf_logit_rules(**dict(good, **{name: bad}))
+    for name in ("repeat", "frequency", "presence", "bias"):
+        for bad in (f.double(), torch.ones(4)[::2], torch.ones(1).expand(2), f.bfloat16(), i):
+            with pytest.raises(ValueError, match=name):
+                g.gguf_logit_rules(**dict(good, **{name: bad}))
+    for bad in (words.long(), words.T, words[0], words.bool()):
+        with pytest.raises(ValueError, match="allow"):
+            g.gguf_logit_rules(**dict(good, allow=bad))
