@@ -136,9 +136,9 @@ class gguf_kv_batch(ctypes.Structure):
         if q_start.numel() != kv_len.numel() + 1 or pages.shape[0] != kv_len.numel() or \
                 (pages.shape[1] > 1 and pages.stride(1) != 1):
             raise ValueError("q_start has one entry more than kv_len, and pages a row of stride 1 for each sequence")
-        if str(pages.dtype) != "torch.int32":
+        if str(pages.dtype) not in ("torch.int32", "torch.uint32"):
             raise ValueError("q_start, kv_len and pages are int32")
-        _array("q_start", q_start, "int32"), _array("kv_len", kv_len, "int32")
+        _array("q_start", q_start, "int32", "uint32"), _array("kv_len", kv_len, "int32", "uint32")
         stride = pages.stride(0) if pages.shape[0] > 1 else pages.shape[1]
         super().__init__(_p(q_start), _p(kv_len), _p(pages), kv_len.numel(), n_tokens, stride, max_q_len, max_kv_len)
         self._keep = (q_start, kv_len, pages)
@@ -151,7 +151,7 @@ class gguf_rope(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
     def __init__(self, freqs, rot_dim, style=GGUF_ROPE_NORM, scale=1.0, positions=None):
-        _array("freqs", freqs, "float32"), _array("positions", positions, "int32")
+        _array("freqs", freqs, "float32"), _array("positions", positions, "int32", "uint32")
         if not (freqs is None or isinstance(freqs, int)) and 2 * freqs.numel() < rot_dim:
             raise ValueError(f"freqs has {freqs.numel()} entries for {rot_dim // 2} pairs")
         super().__init__(_p(freqs), _p(positions), rot_dim, style, scale)
@@ -167,7 +167,7 @@ class gguf_logit_rules(ctypes.Structure):
     def __init__(self, hist=None, hist_start=None, repeat=None, frequency=None, presence=None, bias_ids=None, bias=None,
                  bias_start=None, allow=None):
         for name, t in (("hist", hist), ("hist_start", hist_start), ("bias_ids", bias_ids), ("bias_start", bias_start)):
-            _array(name, t, "int32")
+            _array(name, t, "int32", "uint32")
         for name, t in (("repeat", repeat), ("frequency", frequency), ("presence", presence), ("bias", bias)):
             _array(name, t, "float32")
         if allow is not None and (str(allow.dtype) not in ("torch.int32", "torch.uint32") or allow.dim() != 2 or
