@@ -219,7 +219,7 @@ def exported_symbols():
 
 
 def _p(t):
-    if t is None or t.__class__ is int:
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 

@@ -110,3 +110,14 @@ def test_rules_refuse_other_types_and_gaps():
     for bad in (words.long(), words.T, words[0], words.bool()):
         with pytest.raises(ValueError, match="allow"):
             g.gguf_logit_rules(**dict(good, allow=bad))
+
+
+def test_an_address_may_be_any_integer(lib):  # noqa: F811
+    class Address(int):
+        pass
+
+    x = Address(4096)
+    for call in (lambda: g.gguf_mm_gemv(x, 99, 0, 32, 32, x, 2, 1, None, x, 2, stream=Address(0)),
+                 lambda: g.gguf_logits_adjust(x, 9, 8, 1, 8, g.gguf_logit_rules(repeat=x), x, 0, 8, Address(0))):
+        with pytest.raises(g.GGUFError):
+            call()
