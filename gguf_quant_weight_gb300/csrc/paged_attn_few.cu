@@ -614,8 +614,8 @@ __device__ __forceinline__ int tile_chunks(const RowSpan& s) {
     return s.hi > s.lo ? (s.hi + kChunk - 1) / kChunk - s.lo / kChunk : 1;
 }
 template <int ROWS>
-__device__ __forceinline__ int seq_chunks(const AttnParams& p, int seq) {
-    int n = 0;
+__device__ __forceinline__ int64_t seq_chunks(const AttnParams& p, int seq) {
+    int64_t n = 0;
     RowSpan s;
     for (int r0 = 0; row_span(p, seq, r0, ROWS, s, false); r0 += ROWS) n += tile_chunks(s);
     return n * p.c.kv_heads;

@@ -159,3 +159,31 @@ def test_small_weights_in_rows_of_one_share(dt):
     small = 0.0 if dt == "bf16" else N * 2.0 ** -32
     near(U.host64(out), ref, dt, (u + 2 * e + sums)[..., None] * np.abs(ref) + small * vmax[..., None], "out")
     near(lse.cpu().numpy(), rlse, "f32", e + sums, "lse")
+
+
+# ------------------------------------------------------------------ counts that pass 32 bits
+
+def test_a_sequence_of_more_chunks_than_31_bits():
+    # 2^26 + 16 keys (a table that names three pages over and over) of 512 key heads: 2^31 + 512 chunks of 16 keys.
+    # All scores are 0 and the values 0 or 1, so that the sums are whole numbers: a worker's stay below 2^24, and
+    # what joins rounds a few of them to f32.
+    KV, D, page, N = 512, 16, 256, (1 << 26) + 16
+    rs = np.random.default_rng(31)
+    k = torch.tensor(rs.standard_normal((3, KV, page, D)), dtype=torch.bfloat16, device=DEV)
+    v = torch.tensor(rs.integers(0, 2, (3, KV, page, D)), dtype=torch.bfloat16, device=DEV)
+    table = rs.integers(0, 3, -(-N // page)).astype(np.int32)
+    i32 = lambda a: torch.tensor(np.asarray(a, np.int32), device=DEV)  # noqa: E731
+    batch, cache = g.gguf_kv_batch(i32([0, 1]), i32([N]), i32(table[None]), 1, 1, N), g.gguf_kv_cache(k, v)
+    n = g.gguf_paged_attn_workspace_size(batch, cache, KV)
+    q, ws = torch.zeros((1, KV, D), dtype=torch.bfloat16, device=DEV), U.workspace(n, 0xFF)
+    out, lse = U.guarded((1, KV, D), torch.bfloat16, 3.0), U.guarded((1, KV), torch.float32, 3.0)
+    g.gguf_paged_attn(q, KV * D, KV, batch, cache, 0.25, 1, 0, out.t, KV * D, lse.t, ws.t, n)
+    torch.cuda.synchronize()
+    for b in (out, lse, ws):
+        b.check("attention")
+    assert g.gguf_mm_check_errors() == 0
+    times = np.bincount(table[:-1], minlength=3).astype(np.float64)
+    v64 = U.host64(v)
+    ref = (times[:, None, None] * v64.sum(2)).sum(0) + v64[table[-1], :, :N % page].sum(1)
+    near(U.host64(out.t)[0], ref / N, "bf16", 2.0 ** -20, "out")
+    near(lse.t.cpu().numpy()[0], np.full(KV, math.log(N)), "f32", 2.0 ** -19, "lse")
