@@ -134,6 +134,35 @@ __device__ __forceinline__ void clear_unseen(const RowSpan& s, uint32_t vb, int 
     __syncwarp();
 }
 
+// Whether any of the 16 keys' values is NaN or infinite.
+template <int DP, bool BF16>
+__device__ __forceinline__ bool any_not_finite(uint32_t vb, int lane) {
+    using C = FewCfg<DP>;
+    constexpr uint32_t M = BF16 ? 0x7f807f80u : 0x7c007c00u;
+    bool bad = false;
+#pragma unroll 1
+    for (int e = lane; e < kChunk * 8 * (DP / 64); e += 32) {
+        uint32_t v[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(vb + e / (8 * kChunk) * C::BOX + e % (8 * kChunk) * 16)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bad |= __vcmpeq2(v[i] & M, M) != 0;
+    }
+    return __any_sync(0xffffffffu, bad);
+}
+// Value d of key j of a chunk's values.
+template <int DP, bool BF16>
+__device__ __forceinline__ float value_at(uint32_t vb, int j, int d) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];"
+                 : "=h"(v)
+                 : "r"(vb + d / 64 * FewCfg<DP>::BOX + j * 128 + (((d % 64 / 8) ^ (j & 7)) << 4) + d % 8 * 2)
+                 : "memory");
+    return BF16 ? __bfloat162float(__ushort_as_bfloat16(v)) : __half2float(__ushort_as_half(v));
+}
+
 // One warp's work on 16 rows: the queries as first operand (rows lane / 4 and
 // lane / 4 + 8), the sums, and the rows' statistics (m in units of ln 2).
 template <int DP, bool BF16>
@@ -146,6 +175,12 @@ struct Rows16 {
     float m[2], l[2];
     int lo[2], hi[2];
     int all_lo, all_hi;          // keys that every row sees
+
+    // Whether some of the rows see a key of the chunk from j0 that others do not.  Then
+    // values that are not finite must not meet the others' weights of 0.
+    __device__ __forceinline__ bool some_see(const RowSpan& s, int j0) const {
+        return max(j0, s.lo) < all_lo || min(j0 + kChunk, s.hi) > all_hi;
+    }
 
     static __device__ __forceinline__ int row(int x, int lane) { return lane / 4 + 8 * x; }
     // Whether this lane speaks for its rows' statistics.
@@ -239,10 +274,32 @@ struct Rows16 {
             const float base = m[x] == -INFINITY ? 0.f : m[x];       // a row that has seen nothing yet
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                const float a = exp2_fast(sc[n][2 * x] - base), b = exp2_fast(sc[n][2 * x + 1] - base);
+                float &a = sc[n][2 * x], &b = sc[n][2 * x + 1];
+                a = exp2_fast(a - base), b = exp2_fast(b - base);
                 l[x] += a + b;
                 w[2 * n + x] = pack2<BF16>(a * Elem<BF16>::LIFT, b * Elem<BF16>::LIFT);
             }
+        }
+        if (edge && some_see(s, j0) && any_not_finite<DP, BF16>(vb, lane)) {
+            // each row adds the keys that it sees, key by key
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int j = 8 * n + 2 * c + y;
+                            const float f = __shfl_sync(0xffffffffu, sc[n][2 * x + y], (lane & ~3) | c) * Elem<BF16>::LIFT;
+                            if (j0 + j < lo[x] || j0 + j >= hi[x]) continue;
+#pragma unroll
+                            for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+                                for (int z = 0; z < 2; ++z)
+                                    o[d][2 * x + z] += f * value_at<DP, BF16>(vb, j, 8 * d + lane % 4 * 2 + z);
+                        }
+            return;
         }
         const int vr = (lane & 7) + (lane >> 3 & 1) * 8, vc = lane >> 4;
 #pragma unroll
@@ -284,6 +341,10 @@ struct Rows8 {
     float m[2], l[2];
     int lo[2], hi[2];
     int all_lo, all_hi;
+
+    __device__ __forceinline__ bool some_see(const RowSpan& s, int j0) const {
+        return max(j0, s.lo) < all_lo || min(j0 + kChunk, s.hi) > all_hi;
+    }
 
     static __device__ __forceinline__ int row(int x, int lane) { return lane % 4 * 2 + x; }
     static __device__ __forceinline__ bool speaks(int lane) { return lane < 4; }
@@ -375,6 +436,24 @@ struct Rows8 {
             l[x] += e[x] + e[2 + x];
         }
         constexpr float up = Elem<BF16>::LIFT;
+        if (edge && some_see(s, j0) && any_not_finite<DP, BF16>(vb, lane)) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int j = 8 * y + c;
+                        const float f = __shfl_sync(0xffffffffu, e[2 * y + x], 4 * c + lane % 4) * up;
+                        if (j0 + j < lo[x] || j0 + j >= hi[x]) continue;
+#pragma unroll
+                        for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+                            for (int z = 0; z < 2; ++z)
+                                o[i][2 * z + x] += f * value_at<DP, BF16>(vb, j, 16 * i + lane / 4 + 8 * z);
+                    }
+            return;
+        }
         const uint32_t w0 = transpose8(pack2<BF16>(e[0] * up, e[1] * up)), w1 = transpose8(pack2<BF16>(e[2] * up, e[3] * up));
         const int vr = (lane & 7) + (lane >> 4) * 8, vc = lane >> 3 & 1;
 #pragma unroll

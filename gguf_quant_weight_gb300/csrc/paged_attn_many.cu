@@ -155,10 +155,62 @@ __device__ __forceinline__ bool taken_block(const uint4* from, uint3& at) {
     return got != 0;
 }
 
+// A row's weight of 0 for a key that only others of its tile see, times a value that
+// is not finite, has spoilt sums of the row.  Half of the row's columns, from c0 and
+// every other 16, again: those in which a key of [a, b) outside [lo, hi) holds such
+// a value, from the keys of [a, b) inside.  (Cold, so its own function.)
+struct Redo {
+    int a, b, lo, hi;
+    int kvh, c0;
+    const int32_t* pages;
+    const void* q;      // the row's query
+    float c2, base;     // weight = exp2(c2 s + base)
+    float factor;       // of a sum in what is stored: as f32 at `part`, else in 16 bits at `out`
+    float* part;
+    void* out;
+};
+template <bool BF16>
+__device__ __noinline__ void redo_row(const AttnParams& p, const Redo& r) {
+    using T = typename Elem<BF16>::T;
+    auto row_of = [&](const void* cache, int j) -> const T* {
+        const int page = r.pages[j >> p.c.page_shift];
+        if ((unsigned)page >= (unsigned)p.c.n_pages) return nullptr;
+        return static_cast<const T*>(cache) + page * p.c.page_stride + r.kvh * p.c.head_stride +
+               (j & ((1 << p.c.page_shift) - 1)) * p.c.token_stride;
+    };
+    for (int c = r.c0; c < p.c.dim; c += 32) {
+        uint32_t spoilt = 0;
+        for (int j = r.a; j < r.b; ++j) {
+            if (j == max(r.a, r.lo)) j = max(j, min(r.b, r.hi));         // past the keys that the row sees
+            const T* v = j < r.b ? row_of(p.c.v, j) : nullptr;
+            for (int d = 0; v && d < 16; ++d)
+                if (!isfinite((float)v[c + d])) spoilt |= 1u << d;
+        }
+        if (!spoilt) continue;
+        float sum[16] = {};
+        for (int j = max(r.a, r.lo); j < min(r.b, r.hi); ++j) {
+            const T *k = row_of(p.c.k, j), *v = row_of(p.c.v, j), *q = static_cast<const T*>(r.q);
+            if (!k) continue;
+            float s = 0.f;
+            for (int d = 0; d < p.c.dim; ++d) s = fmaf((float)q[d], (float)k[d], s);
+            const float w = exp2_fast(fmaf(s, r.c2, r.base));
+#pragma unroll
+            for (int d = 0; d < 16; ++d) sum[d] = fmaf(w, (float)v[c + d], sum[d]);
+        }
+#pragma unroll
+        for (int d = 0; d < 16; ++d) {
+            if (!(spoilt >> d & 1)) continue;
+            if (r.part) r.part[c + d] = sum[d] * r.factor;
+            else static_cast<T*>(r.out)[c + d] = T(sum[d] * r.factor);
+        }
+    }
+}
+
 template <int DP, bool BF16, int TILES>
 __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
     attn_many_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const AttnParams p, const Partials part, const Geometry geo) {
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnParams p, const Partials part,
+                     const Geometry geo) {
     using C = ManyCfg<DP, TILES>;
     using T = typename Elem<BF16>::T;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -421,10 +473,11 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
                 item_done(k);
                 continue;
             }
-            const int r = w.r0 + t * geo.rows + in, tok = r / p.group;
-            const bool is = in < geo.rows && tok < w.s.n;
             int lo = 0, hi = INT32_MAX;     // a row that is none: any scores, never stored
-            if (is) row_keys(p, w.s, w.s.len - w.s.n + tok, lo, hi);
+            {
+                const int tok = (w.r0 + t * geo.rows + in) / p.group;
+                if (in < geo.rows && tok < w.s.n) row_keys(p, w.s, w.s.len - w.s.n + tok, lo, hi);
+            }
             // the keys that all the warp's rows see need no mask (a warp without rows
             // still has its part in clearing V's edge)
             const int all_lo = max(w.s.lo, __reduce_max_sync(0xffffffffu, lo));
@@ -551,10 +604,13 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
             stage0 %= C::STAGES;
             if (!ok) break;
             float other;
-            ok = exchange(l, mine == 0 || wait(&s_sum[t], par ^ 1), other);
+            ok = exchange(l, w.tiles[t] == 0 || wait(&s_sum[t], par ^ 1), other);
             if (!ok) break;
             l += other;
             tc_fence_after();
+            // (again, rather than in registers through the loop)
+            const int r = w.r0 + t * geo.rows + in, tok = r / p.group;
+            const bool is = in < geo.rows && tok < w.s.n;
             const int D = p.c.dim, head = w.kvh * p.group + r % p.group;
             const int64_t row = (int64_t)(w.s.t0 + tok) * p.heads + head;
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
@@ -562,10 +618,11 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
             T* out = static_cast<T*>(p.out) + (int64_t)(w.s.t0 + tok) * p.ldo + head * D;
             float* po = part.o + ((int64_t)w.split * p.b.n_tokens * p.heads + row) * D;
             const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)p.ldo * 2) & 31) == 0;
+            float zero = 0.f;        // NaN where a sum is not finite
 #pragma unroll 1
             for (int c = 16 * half; c < D; c += 32) {
                 uint32_t y[16];
-                if (mine > 0) {
+                if (w.tiles[t] > 0) {
                     tmem_ld16(to + c, y);
                     tmem_ld_wait();
                     tmem_ld_regs(y);
@@ -574,6 +631,8 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
                     for (int j = 0; j < 16; ++j) y[j] = 0u;
                 }
                 if (!is) continue;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) zero = fmaf(__uint_as_float(y[j]), 0.f, zero);
                 if (part.splits > 1) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -593,6 +652,23 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
                     *reinterpret_cast<uint4*>(out + c + 8) = make_uint4(y[4], y[5], y[6], y[7]);
                 }
             }
+            if (zero != 0.f && l < INFINITY) {
+                Redo r;
+                r.a = max(w.s.lo, w.k0 * kKeys);
+                r.b = min(w.s.hi, (w.k0 + w.tiles[t]) * kKeys);
+                row_keys(p, w.s, w.s.len - w.s.n + tok, r.lo, r.hi);
+                r.kvh = w.kvh;
+                r.c0 = 16 * half;
+                r.pages = p.b.pages + w.s.seq * p.b.pages_stride;
+                r.q = static_cast<const T*>(p.q) + (int64_t)(w.s.t0 + tok) * p.ldq + head * D;
+                r.c2 = c2;
+                r.base = m == -INFINITY ? 0.f : fmaf(-m, c2, Elem<BF16>::LIFT);
+                r.factor = part.splits > 1 ? Elem<BF16>::DROP : inv;
+                r.part = part.splits > 1 ? po : nullptr;
+                r.out = out;
+                redo_row<BF16>(p, r);
+            }
+            __syncwarp();
             if (!is || half != 0) {
             } else if (part.splits > 1)
                 part.ml[(int64_t)w.split * p.b.n_tokens * p.heads + row] = make_float2(l == 0.f ? -INFINITY : m * c2, l * Elem<BF16>::DROP);

@@ -381,8 +381,9 @@ int gguf_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const
  *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K[j][h']) V[j][h'],  h' = h * kv_heads / heads,
  * over the keys 0 <= j < kv_len[b] with, where `causal` is set, j <= p, and
  * where window > 0, j > p - window.  A row that sees no key gives zeros.  What
- * the cache holds in slots that no row of the sequence sees, and in pages
- * before the window, has no influence (NaN and infinities included).
+ * the cache holds at keys that a row does not see has no influence on it (NaN
+ * and infinities included); pages that no row of a sequence sees are not read.
+ * A NaN or +inf among a row's scores makes all of the row NaN, its lse too.
  *   q, out  [n_tokens][heads][head_dim] of the cache's dtype, token t at
  *           t * ldq (ldo) elements; out may not overlap q
  *   heads   a multiple of kv_heads, at most 128 query heads to a key head

@@ -187,3 +187,40 @@ def test_a_sequence_of_more_chunks_than_31_bits():
     ref = (times[:, None, None] * v64.sum(2)).sum(0) + v64[table[-1], :, :N % page].sum(1)
     near(U.host64(out.t)[0], ref / N, "bf16", 2.0 ** -20, "out")
     near(lse.t.cpu().numpy()[0], np.full(KV, math.log(N)), "f32", 2.0 ** -19, "lse")
+
+
+# ------------------------------------------------------------------ values of keys that only some rows see
+
+@pytest.mark.parametrize("dt,dim", [("bf16", 128), ("f16", 64), ("bf16", 80)])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+@pytest.mark.parametrize("form,group,n,length,window", [
+    ("cluster", 4, 3, 40, 0), ("cluster", 1, 7, 300, 0), ("cluster", 1, 16, 16, 5), ("cluster", 2, 8, 70, 20),
+    ("dealt", 4, 4, 900, 0), ("dealt", 1, 8, 500, 0), ("many", 1, 40, 40, 0), ("many", 3, 300, 300, 0),
+    ("many", 2, 200, 2000, 0), ("many", 5, 150, 700, 100), ("many", 40, 30, 1000, 7)])
+def test_a_value_that_is_not_finite_reaches_only_rows_that_see_its_key(dt, dim, what, form, group, n, length, window):
+    # Rows share their tiles of keys: a row's weight of 0 for a key that only others see must not meet what stands there.
+    c = Case([(n, length), (1, 20)], 2, dim, dt, page=16, seed=n + dim, wide=LARGE if form == "dealt" else None)
+    c.poison()
+    q = c.values((c.n_tokens, 2 * group, dim))
+    clean, clean_lse = run_in(c, form, group, 1, window, q)
+    ref, _, vmax, smax = S.attention(U.host64(q), U.host64(c.k), U.host64(c.v), c.q_start, c.kv_len, c.pages, dim ** -0.5, 1, window)
+    u = 2.0 ** -8 if dt == "bf16" else 2.0 ** -11
+    e = 2.0 ** -23 * max(1, dim / 4) * smax + 2.0 ** -20
+    p = np.arange(length - n, length)
+    for at, d in ((length - 1, 5), (length - 1 - n // 2, dim - 1), (length - n + 1, slice(None)), (length - n - 3, 17)):
+        if at < 0:
+            continue
+        where = int(c.pages[0, at // 16]), 1, at % 16, d
+        keep = c.v[where].clone()
+        c.v[where] = what
+        out, lse = run_in(c, form, group, 1, window, q)
+        c.v[where] = keep
+        assert torch.equal(lse, clean_lse)
+        assert torch.equal(out[n:], clean[n:]) and torch.equal(out[:n, :group], clean[:n, :group]), "another head or sequence"
+        sees = (p >= at) & (not window or at > p - window)
+        got = U.host64(out)[:n, group:]
+        assert not np.isfinite(got[sees][..., d]).any(), at
+        near(got[~sees], ref[:n, group:][~sees], dt, ((u + 2 * e) * vmax)[:n, group:][~sees][..., None], "rows that do not see it")
+        others = np.ones(dim, bool)
+        others[d] = False
+        near(got[sees][..., others], ref[:n, group:][sees][..., others], dt, ((u + 2 * e) * vmax)[:n, group:][sees][..., None], "others")
