@@ -172,6 +172,8 @@ int gguf_logits_adjust(const void* logits, int dt, int64_t ld, int64_t rows, int
                           (const void*)r.presence, (const void*)r.bias_ids, (const void*)r.bias, (const void*)r.bias_start,
                           (const void*)r.allow})
         if (!aligned4(a)) return GGUF_ERR_MISALIGNED;
+    // in place a row may only overwrite itself
+    if (logits == out && (dt != odt || (ld != ldo && rows > 1))) return GGUF_ERR_INVALID_ARG;
     // a history without a penalty changes nothing
     if (!r.repeat && !r.frequency && !r.presence) r.hist = nullptr;
     int sms = 0, *status = nullptr;

@@ -121,3 +121,15 @@ def test_an_address_may_be_any_integer(lib):  # noqa: F811
                  lambda: g.gguf_logits_adjust(x, 9, 8, 1, 8, g.gguf_logit_rules(repeat=x), x, 0, 8, Address(0))):
         with pytest.raises(g.GGUFError):
             call()
+
+
+def test_logits_in_place_want_the_same_type_and_rows(lib):  # noqa: F811
+    rules = g.gguf_logit_rules()
+
+    def call(dt=0, odt=0, ld=104, ldo=104, rows=2, out=4096):
+        return lib.gguf_logits_adjust(4096, dt, ld, rows, 100, ctypes.byref(rules), out, odt, ldo, None)
+
+    fine = call()
+    assert fine != INV
+    assert call(dt=2) == INV and call(odt=1) == INV and call(ldo=100) == INV and call(ld=112) == INV
+    assert call(ldo=100, rows=1) == fine and call(dt=2, ldo=100, out=1 << 20) == fine
