@@ -17,15 +17,28 @@ def test_append_in_place_wants_the_same_type_and_rows(lib):  # noqa: F811
     r = ctypes.byref
     c = cache()
 
-    def call(q_out=1024, ldo=256, ldq=256, xdt=2, **kw):
-        return lib.gguf_kv_append(1024, ldq, 4096, 128, 8192, 128, xdt, 4, None, r(batch(**kw)), r(c), q_out, ldo, None)
+    def call(ldo=256, ldq=256, xdt=2):
+        return lib.gguf_kv_append(1024, ldq, 4096, 128, 8192, 128, xdt, 4, None, r(batch()), r(c), 1024, ldo, None)
 
-    fine = call()
-    assert fine != INV
     assert call(xdt=0) == INV and call(xdt=1) == INV          # f32 or f16 rows under bf16 ones
     assert call(ldo=264) == INV and call(ldq=264) == INV      # rows that overlap their neighbours
-    assert call(ldo=264, n_tokens=1, max_q_len=1) == fine
-    assert call(q_out=1 << 20, xdt=0, ldo=264) == fine
+
+
+@pytest.mark.gpu
+def test_one_row_in_place_may_name_any_stride():
+    torch = pytest.importorskip("torch")
+    from tests import gpu_util as U
+    U.require_gpu()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    x = torch.randn((1, 2, 64), device="cuda").bfloat16()
+    keep, cache16 = x.clone(), torch.zeros((1, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    b = g.gguf_kv_batch(i32([0, 1]), i32([1]), i32([[0]]), 1, 1, 1)
+    g.gguf_kv_append(x, 128, x, 128, x, 128, g.GGUF_DT_BF16, 2, None, b, g.gguf_kv_cache(cache16, torch.zeros_like(cache16)), x, 256)
+    y = torch.randn((1, 100), device="cuda")
+    was = y.clone()
+    g.gguf_logits_adjust(y, g.GGUF_DT_F32, 104, 1, 100, g.gguf_logit_rules(), y, g.GGUF_DT_F32, 100)
+    assert g.gguf_mm_check_errors() == 0
+    assert torch.equal(x, keep) and torch.equal(cache16[0, :, 0], keep[0]) and torch.equal(y, was)
 
 
 # ------------------------------------------------------------------ indexes on the device
@@ -126,10 +139,7 @@ def test_an_address_may_be_any_integer(lib):  # noqa: F811
 def test_logits_in_place_want_the_same_type_and_rows(lib):  # noqa: F811
     rules = g.gguf_logit_rules()
 
-    def call(dt=0, odt=0, ld=104, ldo=104, rows=2, out=4096):
-        return lib.gguf_logits_adjust(4096, dt, ld, rows, 100, ctypes.byref(rules), out, odt, ldo, None)
+    def call(dt=0, odt=0, ld=104, ldo=104):
+        return lib.gguf_logits_adjust(4096, dt, ld, 2, 100, ctypes.byref(rules), 4096, odt, ldo, None)
 
-    fine = call()
-    assert fine != INV
     assert call(dt=2) == INV and call(odt=1) == INV and call(ldo=100) == INV and call(ld=112) == INV
-    assert call(ldo=100, rows=1) == fine and call(dt=2, ldo=100, out=1 << 20) == fine
