@@ -161,6 +161,102 @@ def test_small_weights_in_rows_of_one_share(dt):
     near(lse.cpu().numpy(), rlse, "f32", e + sums, "lse")
 
 
+# ------------------------------------------------------------------ each form at the shapes that it has most to do with
+
+def poison(c):
+    """NaN and infinities in every slot that holds no key (as Case.poison, at once)."""
+    held = np.zeros((c.n_pages, c.page), bool)
+    for b, length in enumerate(c.kv_len):
+        t = np.arange(length)
+        page = c.pages[b, t // c.page]
+        held[page[page >= 0], (t % c.page)[page >= 0]] = True
+    junk = torch.tensor([math.nan, math.inf, -math.inf, 6e4] * (c.dim // 4), device=DEV)
+    keep = torch.tensor(held, device=DEV)[:, None, :, None]
+    for x in (c.k, c.v):
+        x.copy_(torch.where(keep, x.float(), junk).to(x.dtype))
+
+
+def check_form(c, form, group, causal=1, window=0, q=None):
+    """check_attn on bounds as they are, in the form that is meant: "cluster", "dealt", "many", "split" (many rows with
+    split keys) or "mixed" (sequences of few rows beside others).  Dealt-out keys leave the line's beginnings in the
+    workspace, and split ones their partial rows; the other forms ask for none.  (A window can make a call a small one
+    whatever its workspace, so what was written is looked at.)"""
+    H, D = group * c.kv_heads, c.dim
+    batch, cache = c.batch(), g.gguf_kv_cache(c.k, c.v)
+    rows = c.max_q * group
+    assert (rows > 16) == (form in ("many", "split", "mixed"))
+    if form == "mixed":
+        n = np.diff(c.q_start)
+        assert group <= 16 and len(n) > 1 and ((n > 0) & (n * group <= 16)).any()
+    q = c.values((c.n_tokens, H, D)) if q is None else q
+    poison(c)
+    n = g.gguf_paged_attn_workspace_size(batch, cache, H)
+    ws, out, lse = U.workspace(n, 0xFF), U.guarded((c.n_tokens, H, D), U.TORCH_DT[c.dt], 3.0), U.guarded((c.n_tokens, H), torch.float32, 3.0)
+    g.gguf_paged_attn(q, q.stride(0), H, batch, cache, D ** -0.5, causal, window, out.t, H * D, lse.t, ws.t, n)
+    torch.cuda.synchronize()
+    for b in (out, lse, ws):
+        b.check("attention")
+    assert g.gguf_mm_check_errors() == 0
+    assert bool((ws.t != 0xFF).any()) == (form in ("dealt", "split")), "another form than the test means to run"
+    ref, rlse, vmax, smax = S.attention(U.host64(q)[:c.rows], U.host64(c.k), U.host64(c.v), c.q_start, c.kv_len, c.pages, D ** -0.5,
+                                        causal, window)
+    u = 2.0 ** -8 if c.dt == "bf16" else 2.0 ** -11
+    e = 2.0 ** -23 * max(1, D / 4) * smax + 2.0 ** -20
+    got = U.host64(out.t)
+    near(got[:c.rows], ref, c.dt, ((u + 2 * e) * vmax)[..., None], "out")
+    assert np.all(got[c.rows:] == 3.0), "rows of no sequence were written"
+    near(lse.t.cpu().numpy()[:c.rows], rlse, "f32", e, "lse")
+
+
+def window_batch(n, window):
+    """Sequences shorter and longer than the window, `n` new tokens in most; the pages before some windows are gone."""
+    seqs = [(n if i % 7 else 1, 1 + 211 * i % 1900) for i in range(300)]
+    seqs[5], seqs[8] = (0, 40), (n, 0)
+    gone = [max(0, (b - a - window + 1) // 16) if i % 3 else 0 for i, (a, b) in enumerate(seqs)]
+    return seqs, gone
+
+
+@pytest.mark.parametrize("dt,dim", [("bf16", 64), ("f16", 128), ("bf16", 48)])
+@pytest.mark.parametrize("group,n,window", [(1, 1, 700), (4, 1, 501), (3, 5, 640), (16, 1, 700), (2, 8, 513)])
+def test_keys_dealt_out_under_a_causal_window(dt, dim, group, n, window):
+    # 300 sequences of two key heads whose windows hold 32 to 44 chunks of 16 keys: over 19000 chunks, where every
+    # item begins at its own first key
+    seqs, gone = window_batch(n, window)
+    check_form(Case(seqs, 2, dim, dt, page=16, seed=window + n, first_page=gone, extra_rows=2), "dealt", group, 1, window)
+
+
+@pytest.mark.parametrize("window", [1, 16, 100])
+def test_a_small_window_takes_clusters_whatever_the_lengths(window):
+    seqs, gone = window_batch(2, window)
+    check_form(Case(seqs, 2, 64, "bf16", page=16, seed=window, first_page=gone), "cluster", 4, 1, window)
+
+
+@pytest.mark.parametrize("dt,dim", [("bf16", 32), ("f16", 48), ("bf16", 112), ("f16", 128)])
+@pytest.mark.parametrize("form,group,seqs,window", [
+    ("dealt", 4, [(1, 3000 + 97 * i) for i in range(48)], 0), ("dealt", 8, [(2, 2900 + 61 * i) for i in range(50)], 0),
+    ("dealt", 4, [(1, 3000 + 97 * i) for i in range(60)], 2400), ("cluster", 5, [(3, 17 * i) for i in range(20)], 0),
+    ("many", 3, [(90, 100 + i) for i in range(80)], 0), ("mixed", 3, [(90 if i % 2 else 4, 100 + i) for i in range(80)], 50)])
+def test_head_sizes(dt, dim, form, group, seqs, window):
+    check_form(Case(seqs, 2, dim, dt, page=32, seed=dim), form, group, 1, window)
+
+
+@pytest.mark.parametrize("dt,dim", [("bf16", 128), ("f16", 64), ("bf16", 80)])
+@pytest.mark.parametrize("group,seqs,window", [
+    (20, [(1, 9000)], 0), (32, [(1, 5000), (1, 70)], 0), (128, [(1, 3333)], 0), (64, [(2, 2000), (0, 3), (1, 0)], 1111),
+    (24, [(1, 4000), (3, 4001)], 600), (9, [(2, 6000)], 0)])
+def test_many_heads_to_a_key_head_over_long_histories(dt, dim, group, seqs, window):
+    check_form(Case(seqs, 1, dim, dt, page=64, seed=group), "split", group, 1, window)
+
+
+@pytest.mark.parametrize("dt,dim", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("window", [0, 4500])
+def test_single_tokens_with_long_histories_beside_chunks(dt, dim, window):
+    # the few-rows sequences' keys are split over clusters of several blocks; 160 pieces of the chunks leave none of
+    # their keys to be split
+    seqs = [(200, 6000), (1, 9000), (1, 5000), (2, 100), (1, 1), (8, 7001), (9, 4100)]
+    check_form(Case(seqs, 8, dim, dt, page=64, seed=dim + window), "mixed", 2, 1, window)
+
+
 # ------------------------------------------------------------------ counts that pass 32 bits
 
 def test_a_sequence_of_more_chunks_than_31_bits():

@@ -33,7 +33,7 @@ def test_one_row_in_place_may_name_any_stride():
     x = torch.randn((1, 2, 64), device="cuda").bfloat16()
     keep, cache16 = x.clone(), torch.zeros((1, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
     b = g.gguf_kv_batch(i32([0, 1]), i32([1]), i32([[0]]), 1, 1, 1)
-    g.gguf_kv_append(x, 128, x, 128, x, 128, g.GGUF_DT_BF16, 2, None, b, g.gguf_kv_cache(cache16, torch.zeros_like(cache16)), x, 256)
+    g.gguf_kv_append(x, 128, keep, 128, keep, 128, g.GGUF_DT_BF16, 2, None, b, g.gguf_kv_cache(cache16, torch.zeros_like(cache16)), x, 256)
     y = torch.randn((1, 100), device="cuda")
     was = y.clone()
     g.gguf_logits_adjust(y, g.GGUF_DT_F32, 104, 1, 100, g.gguf_logit_rules(), y, g.GGUF_DT_F32, 100)
