@@ -118,10 +118,9 @@ struct Partials {
 };
 
 struct AttnPlan {
-    int few;        // few rows: of a tile (8 or 16); 0: all sequences in the many-rows form
+    int few;        // few rows: at most 8 or 16 of a sequence and key head; 0: all sequences in the many-rows form
     int mixed;      // sequences of few rows in the few-rows form, the others in the many-rows form
-    int tiles;      // row tiles of a sequence and key head (or of 128 rows, or of two of these)
-    int few_tiles;  // mixed: row tiles of the sequences of few rows
+    int tiles;      // many rows: tiles of 128 rows, or pairs of these, of a sequence and key head
     int cluster;    // few rows, small calls: blocks of a cluster that split the keys
     int blocks;     // few rows, large calls: blocks among whose warps all keys are dealt out; else 0
     int splits;     // many rows: shares of the keys, joined through the workspace where there are several

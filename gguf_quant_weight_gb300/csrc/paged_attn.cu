@@ -82,8 +82,7 @@ AttnPlan make_plan(const AttnParams& p, int num_sms) {
     a.cluster = a.splits = 1;
     if (rows <= kFewRows) {
         a.few = rows <= 8 ? 8 : 16;
-        a.tiles = (int)ceil_div(rows, a.few);
-        const int64_t pairs = (int64_t)p.b.n_seq * p.c.kv_heads * a.tiles;
+        const int64_t pairs = (int64_t)p.b.n_seq * p.c.kv_heads;
         if (pairs * chunks > kLineChunks) {
             a.blocks = 2 * num_sms;
         } else {
@@ -100,7 +99,6 @@ AttnPlan make_plan(const AttnParams& p, int num_sms) {
         a.mixed = p.b.n_seq > 1 && a.splits == 1 && p.group <= kFewRows;
         if (a.mixed) {
             a.few = 16;
-            a.few_tiles = (int)ceil_div((int64_t)(kFewRows / p.group) * p.group, a.few);
             while (a.cluster < 8 && 256 * a.cluster < chunks) a.cluster *= 2;     // about four thousand keys a block
         }
     }
@@ -135,7 +133,7 @@ size_t paged_attn_workspace_bytes(const AttnParams& p, int num_sms) {
 int paged_attn_launch(const AttnParams& call, void* workspace, int num_sms, int pdl, cudaStream_t s) {
     AttnParams p = call;
     const AttnPlan a = make_plan(p, num_sms);
-    if (a.tiles * (a.few && !a.mixed ? (int64_t)p.c.kv_heads : 1) > 65535 || a.few_tiles * p.c.kv_heads > 65535) return GGUF_ERR_UNSUPPORTED;   // a grid's limit
+    if (a.tiles > 65535) return GGUF_ERR_UNSUPPORTED;   // a grid's limit
     p.few_rows = a.mixed ? kFewRows : a.few ? INT32_MAX : 0;
     if (a.few && !a.mixed) return attn_few_launch(p, a, workspace, pdl, s);
     const int64_t rows = (int64_t)p.b.n_tokens * p.heads;

@@ -197,11 +197,11 @@ struct Rows16 {
             }
     }
 
-    __device__ __forceinline__ void begin(const AttnParams& p, const RowSpan& s, int kvh, int r0, int lane) {
+    __device__ __forceinline__ void begin(const AttnParams& p, const RowSpan& s, int kvh, int lane) {
         const int D = p.c.dim, steps = D / 16;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int r = r0 + row(x, lane), tok = r / p.group;
+            const int r = row(x, lane), tok = r / p.group;
             const bool is = tok < s.n;
             lo[x] = 0;
             hi[x] = INT32_MAX;           // a row that is none: zeros as queries, never stored
@@ -359,11 +359,11 @@ struct Rows8 {
             }
     }
 
-    __device__ __forceinline__ void begin(const AttnParams& p, const RowSpan& s, int kvh, int r0, int lane) {
+    __device__ __forceinline__ void begin(const AttnParams& p, const RowSpan& s, int kvh, int lane) {
         const int D = p.c.dim, steps = D / 16;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int tok = (r0 + row(x, lane)) / p.group;
+            const int tok = row(x, lane) / p.group;
             lo[x] = 0;
             hi[x] = INT32_MAX;
             if (tok < s.n) row_keys(p, s, s.len - s.n + tok, lo[x], hi[x]);
@@ -373,7 +373,7 @@ struct Rows8 {
         all_lo = max(s.lo, __reduce_max_sync(0xffffffffu, max(lo[0], lo[1])));
         all_hi = min(s.hi, __reduce_min_sync(0xffffffffu, min(hi[0], hi[1])));
         // as second operand: query lane / 4, values lane % 4 * 2 and 8 further
-        const int r = r0 + lane / 4, tok = r / p.group;
+        const int r = lane / 4, tok = r / p.group;
         const bool is = tok < s.n;
         const T* src = static_cast<const T*>(p.q) + (int64_t)(s.t0 + tok) * p.ldq + (kvh * p.group + r % p.group) * D +
                        lane % 4 * 2;
@@ -497,11 +497,11 @@ __device__ __forceinline__ void load_chunk(uint32_t at, const CUtensorMap* tmK, 
 
 // ------------------------------------------------------------------ keys split over a cluster
 
-// Block (x, y, z): the x-th block of the cluster, key head and row tile y, sequence z.
+// Block (x, y, z): the x-th block of the cluster, key head y, sequence z.
 template <int DP, bool BF16, class W>
 __global__ void __launch_bounds__(kThreads)
     attn_few_cluster_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                            const AttnParams p, int tiles, int stages) {
+                            const AttnParams p, int stages) {
     using C = FewCfg<DP>;
     using T = typename Elem<BF16>::T;
     extern __shared__ uint8_t smem_raw[];
@@ -523,10 +523,10 @@ __global__ void __launch_bounds__(kThreads)
     pdl_wait();
     pdl_launch_dependents();
 
-    const int kvh = blockIdx.y / tiles, r0 = (blockIdx.y % tiles) * W::ROWS;
+    const int kvh = blockIdx.y;
     RowSpan s;
     // the whole cluster alike
-    if (!row_span(p, blockIdx.z, r0, W::ROWS, s, threadIdx.x == 0) || !is_few(p, s.n)) return;
+    if (!row_span(p, blockIdx.z, 0, W::ROWS, s, threadIdx.x == 0) || !is_few(p, s.n)) return;
 
     // this block's chunks of 16 keys, in equal shares; the warps take them in turn
     const int c_lo = s.lo / kChunk, c_n = s.hi > s.lo ? (s.hi + kChunk - 1) / kChunk - c_lo : 0;
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < stages; ++i) issue(i);
 
     W w;
-    w.begin(p, s, kvh, r0, lane);
+    w.begin(p, s, kvh, lane);
     const float c2 = p.scale * kLog2e;
     uint32_t phase = 0;                                              // bit st: the parity that slot st waits for
     bool ok = true;
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     w.each(lane, [&](int x, int d, float v) { so[(warp * W::ROWS + W::row(x, lane)) * LD + d] = v * f[x]; });
     __syncthreads();
-    const int rows = min(W::ROWS, s.n * p.group - r0);
+    const int rows = s.n * p.group;
     for (int e = threadIdx.x; e < rows * LD; e += kThreads) {
         float v = so[e];
 #pragma unroll
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kThreads)
             sum = s_ml[row].y;
             v = so[row * LD + d];
         }
-        const int r = r0 + row, tok = s.t0 + r / p.group, head = kvh * p.group + r % p.group;
+        const int tok = s.t0 + row / p.group, head = kvh * p.group + row % p.group;
         put(static_cast<T*>(p.out) + (int64_t)tok * p.ldo + head * D + d, sum > 0.f ? v / sum : (sum == 0.f ? 0.f : sum));
         if (p.lse && d == 0) p.lse[(int64_t)tok * p.heads + head] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
     }
@@ -673,14 +673,13 @@ __global__ void __launch_bounds__(kThreads)
 
 // ------------------------------------------------------------------ keys in equal shares to every warp
 //
-// All chunks of the batch stand in one line: sequence by sequence, row tile by
-// row tile, key head by key head.  Of `total` chunks worker w of W, as many as
-// there are warps or chunks, takes [total w / W, total (w + 1) / W), whatever
-// sequences they belong to.  A
-// (sequence, tile, head) whose chunks one worker has alone is written at once;
-// of the others each worker leaves its sums in the workspace -- in place 2 w
-// where its share begins inside the item, 2 w + 1 where the item begins in its
-// share -- and the joining kernel adds them in the line's order.
+// All chunks of the batch stand in one line: sequence by sequence, key head by key
+// head.  Of `total` chunks worker w of W, as many as there are warps or chunks,
+// takes [total w / W, total (w + 1) / W), whatever sequences they belong to.  An
+// item (a sequence's key head) whose chunks one worker has alone is written at
+// once; of the others each worker leaves its sums in the workspace -- in place
+// 2 w where its share begins inside the item, 2 w + 1 where the item begins in
+// its share -- and the joining kernel adds them in the line's order.
 
 __device__ __forceinline__ int64_t share_begin(int64_t total, int w, int workers) { return total * w / workers; }
 // The worker that has chunk x.
@@ -688,42 +687,38 @@ __device__ __forceinline__ int share_of(int64_t total, int64_t x, int workers) {
     return (int)(((x + 1) * workers + total - 1) / total) - 1;
 }
 
-// (ROWS: rows of a tile.)  Chunks of one row tile of a sequence; a tile that sees no key has one, empty.
-__device__ __forceinline__ int tile_chunks(const RowSpan& s) {
+// Chunks of a sequence; one that sees no key has one, empty.
+__device__ __forceinline__ int seq_chunks(const RowSpan& s) {
     return s.hi > s.lo ? (s.hi + kChunk - 1) / kChunk - s.lo / kChunk : 1;
 }
+// Chunks that it takes of the line, with all key heads.
 template <int ROWS>
-__device__ __forceinline__ int64_t seq_chunks(const AttnParams& p, int seq) {
-    int64_t n = 0;
+__device__ __forceinline__ int64_t line_chunks(const AttnParams& p, int seq) {
     RowSpan s;
-    for (int r0 = 0; row_span(p, seq, r0, ROWS, s, false); r0 += ROWS) n += tile_chunks(s);
-    return n * p.c.kv_heads;
+    return row_span(p, seq, 0, ROWS, s, false) ? (int64_t)seq_chunks(s) * p.c.kv_heads : 0;
 }
 
 // A place in the line.
 struct Cursor {
     RowSpan s;
-    int r0, kvh;
+    int kvh;
     int c, n;          // chunk of the item, and how many it has
 };
 
-// The first item with rows at or after (seq, r0) -- false at the end.
+// The first item of a sequence with rows from `seq` on (past the end: none is asked for).
 template <int ROWS>
-__device__ __forceinline__ bool settle(const AttnParams& p, Cursor& k, int seq, int r0) {
-    for (; seq < p.b.n_seq; ++seq, r0 = 0)
-        if (row_span(p, seq, r0, ROWS, k.s, false)) {
-            k.r0 = r0;
-            k.n = tile_chunks(k.s);
+__device__ __forceinline__ void settle(const AttnParams& p, Cursor& k, int seq) {
+    for (; seq < p.b.n_seq; ++seq)
+        if (row_span(p, seq, 0, ROWS, k.s, false)) {
+            k.n = seq_chunks(k.s);
             k.kvh = k.c = 0;
-            return true;
+            return;
         }
-    return false;
 }
 template <int ROWS>
-__device__ __forceinline__ bool next_item(const AttnParams& p, Cursor& k) {
+__device__ __forceinline__ void next_item(const AttnParams& p, Cursor& k) {
     k.c = 0;
-    if (++k.kvh < p.c.kv_heads) return true;
-    return settle<ROWS>(p, k, k.s.seq, k.r0 + ROWS);
+    if (++k.kvh == p.c.kv_heads) settle<ROWS>(p, k, k.s.seq + 1);
 }
 
 template <int DP, bool BF16, class W>
@@ -757,7 +752,7 @@ __global__ void __launch_bounds__(kThreads)
     int workers = 0;
     auto scan = [&](int b0) {
         const int b = b0 + threadIdx.x;
-        own = b < p.b.n_seq ? seq_chunks<W::ROWS>(p, b) : 0;
+        own = b < p.b.n_seq ? line_chunks<W::ROWS>(p, b) : 0;
         int64_t sum = own;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -808,16 +803,9 @@ __global__ void __launch_bounds__(kThreads)
 
     // two places in the line: what is consumed, and what is loaded, STAGES chunks on
     Cursor use;
-    {
-        int64_t at = s_at[warp];
-        settle<W::ROWS>(p, use, s_seq[warp], 0);
-        while (at >= (int64_t)use.n * p.c.kv_heads) {
-            at -= (int64_t)use.n * p.c.kv_heads;
-            settle<W::ROWS>(p, use, use.s.seq, use.r0 + W::ROWS);
-        }
-        use.kvh = (int)(at / use.n);
-        use.c = (int)(at - (int64_t)use.kvh * use.n);
-    }
+    settle<W::ROWS>(p, use, s_seq[warp]);
+    use.kvh = (int)(s_at[warp] / use.n);
+    use.c = (int)(s_at[warp] - (int64_t)use.kvh * use.n);
     Cursor get = use;
     int to_get = left;
     const int per_page = p.c.page_shift - 4;
@@ -860,7 +848,7 @@ __global__ void __launch_bounds__(kThreads)
     int st = 0;
     bool inside = use.c > 0;                                         // the share begins inside an item
     W w;
-    w.begin(p, use.s, use.kvh, use.r0, lane);
+    w.begin(p, use.s, use.kvh, lane);
 #pragma unroll 1
     while (left > 0) {
         if (have >> st & 1) {
@@ -882,10 +870,10 @@ __global__ void __launch_bounds__(kThreads)
         float inv[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int row = W::row(x, lane), r = use.r0 + row, tok = use.s.t0 + r / p.group, head = use.kvh * p.group + r % p.group;
+            const int row = W::row(x, lane), tok = use.s.t0 + row / p.group, head = use.kvh * p.group + row % p.group;
             to[x] = -1;
             inv[x] = w.l[x] > 0.f ? 1.f / w.l[x] : (w.l[x] == 0.f ? 0.f : w.l[x]);
-            if (r >= use.s.n * p.group) continue;
+            if (row >= use.s.n * p.group) continue;
             to[x] = whole ? (int64_t)tok * p.ldo + head * D : (place * ws.rows + row) * D;
             if (!W::speaks(lane)) continue;
             if (!whole) ws.ml[place * ws.rows + row] = make_float2(w.m[x], w.l[x]);
@@ -896,49 +884,38 @@ __global__ void __launch_bounds__(kThreads)
         if (left > 0) {
             next_item<W::ROWS>(p, use);
             inside = false;
-            w.begin(p, use.s, use.kvh, use.r0, lane);
+            w.begin(p, use.s, use.kvh, lane);
         }
     }
     if (left > 0)        // a wait ran out: let the copies in flight land
         for (int i = 0; i < C::STAGES; ++i) mbar_wait(&full[i], phase >> i & 1, p.status, 1 << 12);
 }
 
-// Joins the items that several workers had: block (x, y, z) key head and row
-// tile x of sequence y, of it rows [rb (z / parts), + rb) and the z % parts-th
-// `db` values.  Each thread adds four values of a row over every per-th worker;
-// then the sums are added in pairs.
+// Joins the items that several workers had: block (x, y, z) key head x of sequence
+// y, of it row z / parts and the z % parts-th `db` values.  Each thread adds four
+// values over every per-th worker; then the sums are added in pairs.
 constexpr int kJoin = 512;
 template <bool BF16>
 __global__ void __launch_bounds__(kJoin) attn_line_join_kernel(const AttnParams p, const LineSpace ws, int workers /* warps of the grid */,
-                                                               int rb, int db, int ROWS) {
+                                                               int db, int ROWS) {
     using T = typename Elem<BF16>::T;
     __shared__ float4 s_v[kJoin];
     __shared__ float2 s_ml[kJoin];
     // what the batch's arrays say stands since before the kernel this one follows
-    const int tile = blockIdx.x / p.c.kv_heads, kvh = blockIdx.x % p.c.kv_heads, seq = blockIdx.y, D = p.c.dim;
+    const int kvh = blockIdx.x, seq = blockIdx.y, D = p.c.dim, parts = D / db, row = blockIdx.z / parts;
     RowSpan s;
-    const bool is = row_span(p, seq, tile * ROWS, ROWS, s, false);
-    int64_t x = 0;
-    for (int t = 0; is && t < tile; ++t) {
-        RowSpan u;
-        row_span(p, seq, t * ROWS, ROWS, u, false);
-        x += (int64_t)tile_chunks(u) * p.c.kv_heads;
-    }
+    const bool is = row_span(p, seq, 0, ROWS, s, false) && row < s.n * p.group;
     pdl_wait();
     pdl_launch_dependents();
     if (!is) return;
-    const int n = tile_chunks(s);
-    x += ws.begin[seq] + (int64_t)n * kvh;
+    const int n = seq_chunks(s);
+    const int64_t x = ws.begin[seq] + (int64_t)n * kvh;
     const int64_t total = ws.begin[p.b.n_seq];
     workers = (int)min((int64_t)workers, total);
     const int w0 = share_of(total, x, workers), w1 = share_of(total, x + n - 1, workers);
     if (w0 == w1) return;                                            // one worker had it and wrote it
-    const int parts = D / db, row0 = blockIdx.z / parts * rb;
-    const int rows = min(min(ROWS, s.n * p.group - tile * ROWS) - row0, rb);
-    if (rows <= 0) return;
-    const int work = rb * db / 4, per = blockDim.x / work;
-    const int g = threadIdx.x / work, e = threadIdx.x - g * work, in = e / (db / 4), row = row0 + in;
-    const int d = blockIdx.z % parts * db + (e - in * (db / 4)) * 4;
+    const int work = db / 4, per = blockDim.x / work, g = threadIdx.x / work;
+    const int d = blockIdx.z % parts * db + (threadIdx.x - g * work) * 4;
     float top = -INFINITY, sum = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float2 ml, float4 o) {
@@ -948,7 +925,7 @@ __global__ void __launch_bounds__(kJoin) attn_line_join_kernel(const AttnParams 
         sum = sum * a + ml.y * b;
         v = make_float4(v.x * a + o.x * b, v.y * a + o.y * b, v.z * a + o.z * b, v.w * a + o.w * b);
     };
-    if (g < per && in < rows) {
+    if (g < per) {
         for (int w = w0 + g; w <= w1; w += 4 * per) {
             float2 ml[4];
             float4 o[4];
@@ -974,8 +951,8 @@ __global__ void __launch_bounds__(kJoin) attn_line_join_kernel(const AttnParams 
         if (g + to < h) add(s_ml[threadIdx.x + to * work], s_v[threadIdx.x + to * work]);
         h = to;
     }
-    if (g != 0 || in >= rows) return;
-    const int r = tile * ROWS + row, tok = s.t0 + r / p.group, head = kvh * p.group + r % p.group;
+    if (g != 0) return;
+    const int tok = s.t0 + row / p.group, head = kvh * p.group + row % p.group;
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
     T* out = static_cast<T*>(p.out) + (int64_t)tok * p.ldo + head * D + d;
     *reinterpret_cast<uint2*>(out) = make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
@@ -995,14 +972,13 @@ int launch_line(const AttnParams& p, const AttnPlan& plan, void* workspace, int 
         return GGUF_ERR_CUDA;
     // a block to a row of an item, with threads for four shares each; where few
     // items are cut into a great many, a block to 16 values of a row
-    const int64_t cuts = plan.blocks * kWarps / ((int64_t)p.b.n_seq * p.c.kv_heads * plan.tiles) + 1;
-    const int rb = 1, db = cuts >= 64 ? 16 : p.c.dim;
+    const int64_t cuts = plan.blocks * kWarps / ((int64_t)p.b.n_seq * p.c.kv_heads) + 1;
+    const int db = cuts >= 64 ? 16 : p.c.dim;
     int per = 1;
     while (per < 16 && per * 4 < cuts) per *= 2;
     const int threads = cuts >= 64 ? kJoin : (int)ceil_div(db / 4 * per, 32) * 32;
-    return launch_pdl(attn_line_join_kernel<BF16>, dim3(p.c.kv_heads * plan.tiles, p.b.n_seq, ceil_div(ws.rows, rb) * (p.c.dim / db)),
-                      dim3(threads), 0, s, pdl, p, ws, plan.blocks * kWarps, rb, db,
-                      W::ROWS) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
+    return launch_pdl(attn_line_join_kernel<BF16>, dim3(p.c.kv_heads, p.b.n_seq, ws.rows * (p.c.dim / db)),
+                      dim3(threads), 0, s, pdl, p, ws, plan.blocks * kWarps, db, W::ROWS) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
 }
 
 template <int DP, bool BF16, class W>
@@ -1016,13 +992,12 @@ int launch_cluster(const AttnParams& p, const AttnPlan& plan, int pdl, cudaStrea
         set_once(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, wide) != cudaSuccess)
         return GGUF_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    const int tiles = plan.mixed ? plan.few_tiles : plan.tiles;
     // no more slots to a warp than chunks: blocks of short sequences are small, and
     // more of them are on the GPU at once
     using C = FewCfg<DP>;
     const int64_t chunks = ceil_div(ceil_div(p.b.max_kv, kChunk) + 1, plan.cluster * kWarps);
     const int stages = (int)std::min<int64_t>(C::STAGES, std::max<int64_t>(1, chunks));
-    cfg.gridDim = dim3(plan.cluster, p.c.kv_heads * tiles, p.b.n_seq);
+    cfg.gridDim = dim3(plan.cluster, p.c.kv_heads, p.b.n_seq);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = std::max(kWarps * stages * C::SLOT, kWarps * W::ROWS * (DP + 4) * 4) + 1024;
     cfg.stream = s;
@@ -1034,7 +1009,7 @@ int launch_cluster(const AttnParams& p, const AttnPlan& plan, int pdl, cudaStrea
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, f, k, v, p, tiles, stages) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, f, k, v, p, stages) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
 }
 
 }  // namespace

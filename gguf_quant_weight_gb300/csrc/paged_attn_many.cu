@@ -361,7 +361,10 @@ __global__ void __launch_bounds__(ManyCfg<DP, TILES>::THREADS, 3 - TILES)
         // advance by additions, and nothing is divided.
         const int steps = p.c.dim / 16;
         const uint32_t id_s = idesc_f16(128, 128, BF16), id_o = idesc_f16(128, p.c.dim, BF16) | kIdescBMajorMn;
-        constexpr uint32_t kHi = (1024 >> 4) | 1u << 14 | 2u << 29;          // both layouts' upper words are the same
+        // Q and K are K-major.  V's rows in the cache are its keys, the products' K: as B it is
+        // MN-major, eight keys to an atom of 1024 bytes, the next 64 values (the leading byte
+        // offset) a HALF further.  The upper words (atoms 1024 apart, 128-byte swizzle) agree.
+        constexpr uint32_t kHi = (1024 >> 4) | 1u << 14 | 2u << 29;
         const uint32_t q_lo = sq >> 4 | 1u << 16, k_lo = ring >> 4 | 1u << 16, v_lo = ring >> 4 | (C::HALF >> 4) << 16;
         int st = 0;                          // the ring's next stage, and its parity
         uint32_t turn = 0, quse = 0, weights = 0;   // bit t: parity of the next Q, and of the next weights

@@ -42,20 +42,6 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr) {
     return d;
 }
 
-// The same swizzled layout read with its rows as K (the operand is "MN-major"):
-// 128-byte rows hold 64 consecutive M/N values of one k, eight rows to an atom,
-// atoms 1024 bytes apart along K; the next 64 M/N values are `mn_stride` bytes
-// further.  `addr` is the address of the first of the 16 rows of a K step.
-__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t addr, uint32_t mn_stride) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(mn_stride >> 4) << 16;           // leading byte offset: next 64 values along M/N
-    d |= (uint64_t)(1024 >> 4) << 32;                // stride byte offset: next 8 rows along K
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
-
 // Instruction descriptor, kind::f16: D f32, A/B f16 (ab_bf16 = 0) or bf16
 // (ab_bf16 = 1), both K-major, shape M x N (M = 128, N % 16 == 0, 16..256).
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int ab_bf16) {
