@@ -12,7 +12,7 @@
 //
 // The bytes bound it: every value of q, k and v is read once and written once.
 // Measured on GB300 (32 + 2 x 8 heads of 128): 7.6k tokens from f32 rows in 44 us,
-// 6.2 of the 6.8 TB/s that a copy reaches; one token in 2.7 us, of which the
+// 6.2 of the 6.7 TB/s that a copy reaches; one token in 2.5 us, of which the
 // launch is most.  Blocks of 128 threads with two vectors ahead: with 256 threads
 // the prompts take 45.5 us, with three vectors ahead 49 us (fewer blocks fit).
 #include "serving.cuh"

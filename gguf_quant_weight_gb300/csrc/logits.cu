@@ -14,8 +14,9 @@
 // going through the list).  The logits' bytes bound it; each block reads the row's whole
 // history, from L2 after the first.
 // Measured on GB300: 256 x 131072 f32 in and out, histories of 1..2048, in 50 us
-// (5.4 of the 6.8 TB/s of a copy; without histories 40 us: a block's stores wait
-// for its row's, and six blocks to an SM do not quite cover it, four take 57 us),
+// (5.4 of the 6.7 TB/s of a copy; without histories 40 us: a block's stores wait
+// for its row's, and six blocks to an SM do not quite cover it; four take 57 us,
+// although six leave f32's 16 tokens a thread 40 registers, 60 bytes too few),
 // 37 x 128259 from bf16 with every rule in 10 us, one row of 32003 in 2.4 us.
 #include "serving.cuh"
 
@@ -114,7 +115,8 @@ __global__ void __launch_bounds__(kThreads, E == 32 ? 4 : 6) logits_adjust_kerne
         }
     }
     __syncthreads();
-    // x / repeat as a product with 1 / repeat, which is within a unit of it: a
+    // x / repeat as a product with 1 / repeat, which is within two units of it (for any
+    // repeat from 2^-126 to 2^126): a
     // division at every token's place in the unrolled code costs more than the rest
     // of the pass, in instructions to fetch
     const float inv = 1.f / repeat;

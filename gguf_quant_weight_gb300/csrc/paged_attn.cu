@@ -63,13 +63,14 @@ __global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(const AttnParams
 // Rows of a sequence up to which the few-rows form takes it.  Measured with 8 key
 // heads of 128 (few rows / many rows, us): 16 rows over 500, 4000, 30000 keys 7.2 /
 // 10.0, 11.8 / 15.4, 45 / 33; 32 rows 8.2 / 10.1, 21.8 / 15.9, 65 / 34.  Single
-// tokens (4 rows) of 64 sequences 104 / 221, over 131071 keys 51 / 56.
+// tokens (4 rows) of 64 sequences 105 / 221, over 131071 keys 52 / 56.  The rule
+// looks at rows alone, and is the wrong side for 16 rows over the longest histories.
 constexpr int kFewRows = 16;
 // Chunks of 16 keys from which a call deals its keys out to all warps and joins in
 // a second kernel.  Clusters / dealt out, us: 16 sequences of 2000 keys (16128
 // chunks) 26.8 / 32.3, 32 of 50..1000 20.2 / 23.4, 36 of 400 16.1 / 23.3, 2 of
-// 16000 (16016) 39.2 / 35.0; dealt out, 64 of 100..8000 take 104 (up to 256512
-// chunks), and 156 in clusters.
+// 16000 (16016) 39.2 / 35.0; dealt out, 64 of 100..8000 take 105 (up to 256512
+// chunks), and 156 in clusters.  Few long sequences would change sides earlier.
 constexpr int64_t kLineChunks = 16384;
 
 // The form and the split of a call, from its sizes alone.
@@ -99,7 +100,12 @@ AttnPlan make_plan(const AttnParams& p, int num_sms) {
         a.mixed = p.b.n_seq > 1 && a.splits == 1 && p.group <= kFewRows;
         if (a.mixed) {
             a.few = 16;
-            while (a.cluster < 8 && 256 * a.cluster < chunks) a.cluster *= 2;     // about four thousand keys a block
+            // About four thousand keys a block.  As the rule has it / 1 / 2 / 4 / 8 blocks,
+            // us: 24 sequences of 1..500 tokens over 100..8000 keys 132 / 137 / 132 / 142 /
+            // 133, over up to 1000 keys 50 / 50 / 52 / 54 / 61, 64 of 1..20 tokens over
+            // 100..8000 keys 169 / 168 / 168 / 174 / 205; only 16 of 1..100 tokens over
+            // 12000..16000 keys are served worse: 404 / 327 / 340 / 415 / 416.
+            while (a.cluster < 8 && 256 * a.cluster < chunks) a.cluster *= 2;
         }
     }
     return a;

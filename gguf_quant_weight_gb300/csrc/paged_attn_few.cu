@@ -9,8 +9,8 @@
 //   * a warp is a worker of its own: tensor copies bring chunks of 16 keys into
 //     its ring of slots (swizzled, zeros past head_dim), STAGES of them ahead.
 //     No warp waits for another until the end.
-//   * scores and weights stay in registers: an accumulator of S has the layout
-//     that the weights need as first operand of P V (or, for up to 8 rows and
+//   * scores and weights stay in registers, the weights rounded to 16 bits: an
+//     accumulator of S has the layout that they need as first operand of P V (or, for up to 8 rows and
 //     with the products turned around, a transpose of 8 x 8 away from it).
 //   * small calls split the keys of a (sequence, key head) over the blocks of a
 //     cluster; the warps' results are joined in shared memory, the blocks'
@@ -24,10 +24,10 @@
 // over NaN: scores of NaN alone leave -inf there, and NaN in the sums.
 //
 // Measured on GB300, 32 heads on 8 of 128, bf16: one token over 1021 keys 6.2 us;
-// 64 tokens over 100..8000 keys, 570 MB, 104 us (5.5 of the 6.8 TB/s of a copy;
+// 64 tokens over 100..8000 keys, 570 MB, 105 us (5.4 of the 6.7 TB/s of a copy;
 // the copies alone take 87 us, joining about 5); one token over 131071 keys of 4
-// heads, 268 MB, 51 us.  Two blocks of four warps with three chunks ahead each
-// take 104 us of the batch; three blocks with two ahead 124, one with six 135.
+// heads, 268 MB, 52 us.  Two blocks of four warps with three chunks ahead each
+// take 105 us of the batch; three blocks with two ahead 124, one with six 135.
 #include "attn.cuh"
 
 namespace gg {

@@ -4,11 +4,13 @@
 // A block takes two tiles of up to 128 rows of a (sequence, key head) -- the
 // query heads of the group, token by token -- through their keys, 128 at a
 // time; for heads of up to 64 values one tile, with two blocks to an SM (short
-// sequences then leave no half of a block idle: 24 ragged chunks 26.6 us instead
-// of 29.6; heads of 128 values have no room for two blocks' keys).  Per tile of keys
+// sequences then leave no half of a block idle: 24 ragged chunks take a tenth
+// less; heads of 128 values have no room for two blocks' keys).  Per tile of keys
 //   S = Q K^T   both operands from shared memory, 128 x 128 sums in TMEM
 //   P = exp2(c S - c m), c = scale log2 e: two threads to a row, 64 scores each
-//               in registers; the weights, in 16 bits, replace the scores in TMEM
+//               in registers; the weights, in 16 bits (as the tensor cores take
+//               them: each moves a row by at most its half unit of |V|), replace the
+//               scores in TMEM
 //   O += P V    P from TMEM, V from shared memory as it lies in the cache
 //               (its rows are the keys: an MN-major operand), sums in TMEM.
 // While one tile's threads take exponentials, the tensor cores work on the
@@ -26,10 +28,19 @@
 // values), its rows' threads (about 1300, of them 900 for the weights) and sums
 // (512), two of which run side by side; so the tensor cores, which the products
 // of a pair of tiles take 2048 cycles, work 70 % of the time.  Measured on GB300:
-// 8111-token prompt, 32 heads on 8 of 128, bf16, 330 us, 1630 TFLOP/s (a plain
-// bf16 product reaches 1860); heads of 64 values have half the products for the
-// same weights, and reach 660 to 930.  Short items (a window of 1000 keys: 10 tiles)
-// spend a quarter of their time on the first tile and on writing their rows.
+// 8111-token prompt, 32 heads on 8 of 128, bf16, 333 us in a burst of calls, 1618
+// TFLOP/s, and 357 us, 1510, after a second of them, when the power limit lowers the
+// clock (a plain bf16 product reaches 1931 and 1740); heads of 64 values have half
+// the products for the same weights, and reach 660 to 930.  Short items (a window
+// of 1000 keys: 10 tiles) spend a quarter of their time on the first tile and on
+// writing their rows.  The row threads' 96 registers, all that 18 to 20 warps leave
+// them, are 20 bytes short at 128 values and 52 to 68 at 64.
+//
+// A row's two warps meet at barriers of their own: where any row raises its maximum,
+// after they have rescaled the sums (the products add to all columns of O once the
+// first half's weights are there), and where an item begins and ends.  A bounded
+// wait that has run out in one of them is made known at these, so that both leave.
+// The meetings cost a tenth of the window's 64 us and 1 % of the prompt.
 #include "attn.cuh"
 
 namespace gg {

@@ -429,10 +429,10 @@ typedef struct {
  * writes out (row r at out + r * ldo).  For a token v that comes c times in the
  * row's history, x its logit in f32:
  *   c > 0:  x = (x > 0 ? x / repeat[r] : x * repeat[r]) - (c * frequency[r] + presence[r])
- * (the quotient to within a unit), then the biases of v are added in the order
- * of the list, and a token that
- * `allow` leaves out becomes -inf.  dt and odt: F32, F16 or BF16; out may be
- * logits itself when the types and strides agree.  logits and out 16-byte
+ * (the quotient to within two units in the last place, for |repeat| from 2^-126
+ * to 2^126), then the biases of v are added in the order of the list, and a
+ * token that `allow` leaves out becomes -inf.  dt and odt: F32, F16 or BF16; out
+ * may be logits itself when the types and strides agree.  logits and out 16-byte
  * aligned (rows may start anywhere).  The result does not depend on timing.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, NO_DEVICE, CUDA. */
 int gguf_logits_adjust(const void* logits, int dt, int64_t ld, int64_t rows, int64_t vocab,
