@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(const AttnParams
         }
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
-            if (ml[j].x == -INFINITY) continue;
+            if (ml[j].y == 0.f) continue;                      // saw nothing (the maximum does not tell: it may pass over NaN)
             const float f = exp2_fast(ml[j].x - top);
             sum += f * ml[j].y;
 #pragma unroll

@@ -22,6 +22,19 @@ def _gpu():
     U.require_gpu()
 
 
+def poison(c):
+    """NaN and infinities in every slot that holds no key (as Case.poison, at once)."""
+    held = np.zeros((c.n_pages, c.page), bool)
+    for b, length in enumerate(c.kv_len):
+        t = np.arange(length)
+        page = c.pages[b, t // c.page]
+        held[page[page >= 0], (t % c.page)[page >= 0]] = True
+    junk = torch.tensor([math.nan, math.inf, -math.inf, 6e4] * (c.dim // 4), device=DEV)
+    keep = torch.tensor(held, device=DEV)[:, None, :, None]
+    for x in (c.k, c.v):
+        x.copy_(torch.where(keep, x.float(), junk).to(x.dtype))
+
+
 @pytest.mark.parametrize("dt,dim", [("bf16", 128), ("f16", 128), ("bf16", 64), ("f16", 48)])
 @pytest.mark.parametrize("seqs,group", [([(700, 700)], 2), ([(130, 900), (300, 301)], 5), ([(40, 1500)], 1)])
 def test_maximum_rises_with_every_tile(dt, dim, seqs, group):
@@ -98,6 +111,29 @@ def test_nan_key_makes_the_rows_that_see_it_nan(dt, dim, form, group, n, length,
     assert torch.equal(out.nan_to_num(7.0), clean.nan_to_num(7.0)) and torch.equal(lse, clean_lse), "another row changed"
 
 
+@pytest.mark.parametrize("dt,dim", [("bf16", 64), ("f16", 128)])
+@pytest.mark.parametrize("group,n,length", [(16, 62, 1908), (3, 100, 6000), (1, 300, 7000), (7, 90, 2700)])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_bad_key_before_keys_that_a_row_does_not_see(dt, dim, group, n, length, what):
+    # Split keys: a share whose first tile of keys makes a row NaN and whose next holds keys of later tokens alone.
+    KV = 8
+    c = Case([(n, length)], KV, dim, dt, page=64, seed=group)
+    poison(c)
+    q = c.values((n, KV * group, dim)).abs() + 0.5          # so that a key of infinities scores infinity
+    clean, clean_lse = run_in(c, "many", group, q=q)
+    splits = g.gguf_paged_attn_workspace_size(c.batch(), g.gguf_kv_cache(c.k, c.v), KV * group) / (n * KV * group * (4 * dim + 8))
+    assert 2 <= splits <= length / 128 / 1.9, "shares of at least two tiles are meant"
+    for at in list(range(length - n - 3, length, 9)) + [length // 128 * 128 - 1, length - 1, 0]:
+        where = int(c.pages[0, at // 64]), slice(None), at % 64
+        keep = c.k[where].clone()
+        c.k[where] = what
+        out, lse = run_in(c, "many", group, q=q)
+        c.k[where] = keep
+        sees = torch.arange(length - n, length, device=DEV) >= at
+        assert torch.isnan(out[sees]).all() and torch.isnan(lse[sees]).all(), at
+        assert torch.equal(out[~sees], clean[~sees]) and torch.equal(lse[~sees], clean_lse[~sees]), at
+
+
 # ------------------------------------------------------------------ weights of every size
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -162,19 +198,6 @@ def test_small_weights_in_rows_of_one_share(dt):
 
 
 # ------------------------------------------------------------------ each form at the shapes that it has most to do with
-
-def poison(c):
-    """NaN and infinities in every slot that holds no key (as Case.poison, at once)."""
-    held = np.zeros((c.n_pages, c.page), bool)
-    for b, length in enumerate(c.kv_len):
-        t = np.arange(length)
-        page = c.pages[b, t // c.page]
-        held[page[page >= 0], (t % c.page)[page >= 0]] = True
-    junk = torch.tensor([math.nan, math.inf, -math.inf, 6e4] * (c.dim // 4), device=DEV)
-    keep = torch.tensor(held, device=DEV)[:, None, :, None]
-    for x in (c.k, c.v):
-        x.copy_(torch.where(keep, x.float(), junk).to(x.dtype))
-
 
 def check_form(c, form, group, causal=1, window=0, q=None):
     """check_attn on bounds as they are, in the form that is meant: "cluster", "dealt", "many", "split" (many rows with
