@@ -180,7 +180,73 @@ class gguf_logit_rules(ctypes.Structure):
         self._ref = ctypes.addressof(self)
 
 
+class gguf_head_norm(ctypes.Structure):
+    """Norms of the query and key heads: weights f32 [head_dim] (None: those heads are not normed) and eps."""
+    _fields_ = [("q", _c_vp), ("k", _c_vp), ("eps", ctypes.c_float)]
+
+    def __init__(self, q, k, eps=1e-6):
+        _array("q", q, "float32"), _array("k", k, "float32")
+        super().__init__(_p(q), _p(k), eps)
+        self._keep = (q, k)
+        self._ref = ctypes.addressof(self)
+
+
+GGUF_SCORE_SOFTMAX, GGUF_SCORE_SIGMOID = 0, 1
+GGUF_ACT_SILU, GGUF_ACT_GELU = 0, 1
+
+
+class gguf_router(ctypes.Structure):
+    """A router: w [n_expert, K] of f32, f16 or bf16 without gaps, bias f32 [n_expert] or None."""
+    _fields_ = [("w", _c_vp), ("bias", _c_vp), ("wdt", ctypes.c_int32), ("n_expert", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("score", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+    def __init__(self, w, top_k, score=GGUF_SCORE_SOFTMAX, bias=None, renormalize=True, scale=1.0):
+        _array("w", w, "float32", "float16", "bfloat16"), _array("bias", bias, "float32")
+        if w.dim() != 2 or not (bias is None or isinstance(bias, int)) and bias.numel() != w.shape[0]:
+            raise ValueError("w is [n_expert, K], and bias has one entry for each expert")
+        super().__init__(_p(w), _p(bias), _dt_of(w), w.shape[0], top_k, score, int(renormalize), scale)
+        self._keep = (w, bias)
+        self._ref = ctypes.addressof(self)
+
+
+class gguf_moe_weights(ctypes.Structure):
+    """Experts' gate and up [n_expert][F, K] and down [n_expert][K, F] as GGUF blocks back to back (uint8 tensors without
+    gaps, or device addresses)."""
+    _fields_ = [("gate", _c_vp), ("up", _c_vp), ("down", _c_vp), ("gate_type", ctypes.c_int32), ("up_type", ctypes.c_int32),
+                ("down_type", ctypes.c_int32), ("act", ctypes.c_int32), ("n_expert", _c_i64), ("K", _c_i64), ("F", _c_i64)]
+
+    def __init__(self, gate, up, down, gate_type, up_type, down_type, K, F, n_expert, act=GGUF_ACT_SILU):
+        for name, t, qt, n, k in (("gate", gate, gate_type, F, K), ("up", up, up_type, F, K), ("down", down, down_type, K, F)):
+            _array(name, t, "uint8")
+            if qt in BLOCK_VALUES and not (t is None or isinstance(t, int)) and \
+                    t.numel() != n_expert * n * (k // BLOCK_VALUES[qt]) * BLOCK_BYTES[qt]:
+                raise ValueError(f"{name} has {t.numel()} bytes, not those of {n_expert} tensors [{n}, {k}]")
+        super().__init__(_p(gate), _p(up), _p(down), gate_type, up_type, down_type, act, n_expert, K, F)
+        self._keep = (gate, up, down)
+        self._ref = ctypes.addressof(self)
+
+
+class gguf_sampler(ctypes.Structure):
+    """What each row is drawn by: temperature, top_p, min_p f32 [rows], top_k int32 [rows]; what is None is not used."""
+    _fields_ = [("temperature", _c_vp), ("top_k", _c_vp), ("top_p", _c_vp), ("min_p", _c_vp)]
+
+    def __init__(self, temperature=None, top_k=None, top_p=None, min_p=None):
+        _array("top_k", top_k, "int32")
+        for name, t in (("temperature", temperature), ("top_p", top_p), ("min_p", min_p)):
+            _array(name, t, "float32")
+        super().__init__(_p(temperature), _p(top_k), _p(top_p), _p(min_p))
+        self._keep = (temperature, top_k, top_p, min_p)
+        self._ref = ctypes.addressof(self)
+
+
 _SIGS.update({
+    "gguf_kv_append_norm": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp,
+                                     _c_vp, _c_i64, _c_vp]),
+    "gguf_moe_router": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp]),
+    "gguf_moe_ffn": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp, _c_int, _c_vp, _c_sz, _c_vp]),
+    "gguf_moe_ffn_workspace_size": (_c_sz, [_c_i64, _c_i64, _c_i64]),
+    "gguf_sample": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
     "gguf_kv_append": (_c_int, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_int, _c_i64, _c_vp, _c_vp, _c_vp,
                                 _c_vp, _c_i64, _c_vp]),
     "gguf_paged_attn": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_vp, ctypes.c_float, _c_int, _c_i64, _c_vp, _c_i64,
@@ -388,6 +454,37 @@ def gguf_logits_adjust(logits, dt, ld, rows, vocab, rules, out, odt, ldo, stream
         _p(logits), dt, ld, rows, vocab, rules and rules._ref, _p(out), odt, ldo,
         stream if stream.__class__ is int else _s(stream))
     return _check("gguf_logits_adjust", st) if st else st
+
+
+def gguf_kv_append_norm(q, ldq, k, ldk, v, ldv, xdt, heads, norm, rope, batch, cache, q_out, ldqo, stream=None):
+    st = (_lib or load_library()).gguf_kv_append_norm(
+        _p(q), ldq, _p(k), ldk, _p(v), ldv, xdt, heads, norm and norm._ref, rope and rope._ref, batch and batch._ref,
+        cache and cache._ref, _p(q_out), ldqo, stream if stream.__class__ is int else _s(stream))
+    return _check("gguf_kv_append_norm", st) if st else st
+
+
+def gguf_moe_router(x, xdt, T, K, router, ids, weights, stream=None):
+    st = (_lib or load_library()).gguf_moe_router(
+        _p(x), xdt, T, K, router and router._ref, _p(ids), _p(weights), stream if stream.__class__ is int else _s(stream))
+    return _check("gguf_moe_router", st) if st else st
+
+
+def gguf_moe_ffn(experts, x, xdt, T, ids, weights, top_k, residual, y, ydt, workspace=None, ws_bytes=0, stream=None):
+    st = (_lib or load_library()).gguf_moe_ffn(
+        experts and experts._ref, _p(x), xdt, T, _p(ids), _p(weights), top_k, _p(residual), _p(y), ydt, _p(workspace), ws_bytes,
+        stream if stream.__class__ is int else _s(stream))
+    return _check("gguf_moe_ffn", st) if st else st
+
+
+def gguf_moe_ffn_workspace_size(F, T, top_k) -> int:
+    return load_library().gguf_moe_ffn_workspace_size(F, T, top_k)
+
+
+def gguf_sample(logits, dt, ld, rows, vocab, sampler, u, token, logprob=None, stream=None):
+    st = (_lib or load_library()).gguf_sample(
+        _p(logits), dt, ld, rows, vocab, sampler and sampler._ref, _p(u), _p(token), _p(logprob),
+        stream if stream.__class__ is int else _s(stream))
+    return _check("gguf_sample", st) if st else st
 
 
 # --- GGUF container reader (host only) ---------------------------------------

@@ -54,6 +54,47 @@ __device__ __forceinline__ void store_v(T* p, const float (&f)[V]) {
     *reinterpret_cast<Pack*>(p) = k;
 }
 
+// Where a block's token belongs, found by all of its threads together.
+struct Place {
+    int found, disorder, pos;
+    int64_t slot;                                 // element offset of the token in the cache, -1: not stored
+};
+
+__device__ __forceinline__ void search(const AppendParams& p, int t, Place& at) {
+    const int64_t room = p.b.pages_stride << p.c.page_shift;
+    for (int i = threadIdx.x; i < p.b.n_seq; i += kThreads) {
+        const int from = p.b.q_start[i], to = p.b.q_start[i + 1], len = p.b.kv_len[i];
+        const bool off = from < 0 || to < from || to > p.b.n_tokens || to - from > p.b.max_q || len > room || len > p.b.max_kv;
+        if (to < from) at.disorder = 1;          // a token may be in two sequences: none is touched
+        if (off) {
+            if (t == 0 && blockIdx.y == 0) report(p.status, GGUF_ERR_INVALID_ARG);
+        } else if (from <= t && t < to) {
+            const int pos = (int)max((int64_t)INT32_MIN, (int64_t)len - to + t);
+            at.pos = pos;
+            at.found = 1;
+            int64_t slot = -1;
+            if (pos >= 0) {
+                const int64_t col = pos >> p.c.page_shift;
+                const int page = p.b.pages[i * p.b.pages_stride + col];
+                if ((unsigned)page < (unsigned)p.c.n_pages)
+                    slot = page * p.c.page_stride + (pos & ((1 << p.c.page_shift) - 1)) * p.c.token_stride;
+                else
+                    report(p.status, GGUF_ERR_INVALID_ARG);
+            }
+            at.slot = slot;
+        }
+    }
+}
+
+__device__ __forceinline__ void angle(const AppendParams& p, int t, int pos, int i, float& cos, float& sin) {
+    const int at = p.positions ? p.positions[t] : pos;
+    const double turns = (double)at * (double)p.freqs[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    float sn, cs;
+    sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cs);
+    cos = cs * p.rope_scale;
+    sin = sn * p.rope_scale;
+}
+
 // X: input type, C: cache type, V: values a thread moves at a time.  Block
 // (x, y) takes token x and the y-th of gridDim.y shares of its values.
 //
@@ -64,11 +105,10 @@ __device__ __forceinline__ void store_v(T* p, const float (&f)[V]) {
 // depend on it.
 template <class X, class C, int V, bool NEOX>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams p) {
-    __shared__ int s_found, s_disorder, s_pos;
-    __shared__ int64_t s_slot;                    // element offset of the token in the cache, -1: not stored
+    __shared__ Place at;
     __shared__ float s_cos[64], s_sin[64];
     const int t = blockIdx.x, tid = threadIdx.x;
-    if (tid == 0) s_found = s_disorder = 0;
+    if (tid == 0) at.found = at.disorder = 0;
 
     // a head's work: with halves, rot / 2V units that turn two vectors and the
     // rest that copy one; with neighbours, one vector each
@@ -109,42 +149,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
         if (u0 + j * step < n) find(u0 + j * step, ws[j]);           // of a row past the last sequence in vain
-    const int64_t room = p.b.pages_stride << p.c.page_shift;
-    for (int i = tid; i < p.b.n_seq; i += kThreads) {
-        const int from = p.b.q_start[i], to = p.b.q_start[i + 1], len = p.b.kv_len[i];
-        const bool off = from < 0 || to < from || to > p.b.n_tokens || to - from > p.b.max_q || len > room || len > p.b.max_kv;
-        if (to < from) s_disorder = 1;          // a token may be in two sequences: none is touched
-        if (off) {
-            if (t == 0 && blockIdx.y == 0) report(p.status, GGUF_ERR_INVALID_ARG);
-        } else if (from <= t && t < to) {
-            const int pos = (int)max((int64_t)INT32_MIN, (int64_t)len - to + t);
-            s_pos = pos;
-            s_found = 1;
-            int64_t slot = -1;
-            if (pos >= 0) {
-                const int64_t col = pos >> p.c.page_shift;
-                const int page = p.b.pages[i * p.b.pages_stride + col];
-                if ((unsigned)page < (unsigned)p.c.n_pages)
-                    slot = page * p.c.page_stride + (pos & ((1 << p.c.page_shift) - 1)) * p.c.token_stride;
-                else
-                    report(p.status, GGUF_ERR_INVALID_ARG);
-            }
-            s_slot = slot;
-        }
-    }
+    search(p, t, at);
     __syncthreads();
     pdl_launch_dependents();
-    if (!s_found || s_disorder) return;
-    if (tid < half) {
-        const int at = p.positions ? p.positions[t] : s_pos;
-        const double turns = (double)at * (double)p.freqs[tid] * 0.15915494309189533577;  // 1 / (2 pi)
-        float sn, cs;
-        sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cs);
-        s_cos[tid] = cs * p.rope_scale;
-        s_sin[tid] = sn * p.rope_scale;
-    }
+    if (!at.found || at.disorder) return;
+    if (tid < half) angle(p, t, at.pos, tid, s_cos[tid], s_sin[tid]);
     __syncthreads();
-    const int64_t slot = s_slot;
+    const int64_t slot = at.slot;
     auto write = [&](const Unit& w) {
         if (w.h < p.heads || slot >= 0) {
             C* dst = w.h < p.heads ? static_cast<C*>(p.q_out) + t * p.ldqo + w.h * D
@@ -189,8 +200,142 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
     }
 }
 
+// The same with the heads of q and k normed on the way:
+//   x -> x / sqrt(mean(x^2) + eps) * weight, then turned.
+// A head is held by a group of `lanes` lanes (a power of two, its last ones
+// idle where the head's units are fewer), so that the sum of squares takes a
+// few shuffles and each value is still read once; a lane takes U units of the
+// head, more than one only where the rotated part's edges keep vectors below
+// four values.  Values are copied by the same groups.
+template <class X, class C, int V, bool NEOX>
+__global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendParams p, int lanes) {
+    constexpr int U = V >= 4 ? 1 : V == 2 ? 2 : 4;
+    __shared__ Place at;
+    __shared__ float s_cos[64], s_sin[64];
+    __shared__ __align__(16) float s_wq[128], s_wk[128];
+    const int t = blockIdx.x, tid = threadIdx.x;
+    if (tid == 0) at.found = at.disorder = 0;
+    const int half = p.rot >> 1;
+    const int D = p.c.dim, HK = p.heads + p.c.kv_heads, n = HK + p.c.kv_heads;
+    const int turn = NEOX ? half / V : p.rot / V;
+    const int units = turn + (D - p.rot) / V;
+    const int groups = kThreads / lanes, step = gridDim.y * groups, me = tid & (lanes - 1);
+    struct Head {
+        Raw<V, X> a[U], b[NEOX ? U : 1];
+    };
+    // unit u of a head starts at value `first` and, in a turned pair of halves, at half + first
+    auto first = [&](int u) { return u < turn ? u * V : p.rot + (u - turn) * V; };
+    auto fetch = [&](int h, Head& w) {
+        const X* src = h < p.heads ? static_cast<const X*>(p.q) + t * p.ldq + h * D
+                       : h < HK    ? static_cast<const X*>(p.k) + t * p.ldk + (h - p.heads) * D
+                                   : static_cast<const X*>(p.v) + t * p.ldv + (h - HK) * D;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int u = me + i * lanes;
+            if (u >= units) continue;
+            w.a[i].load(src + first(u));
+            if (NEOX && u < turn) w.b[i].load(src + half + first(u));
+        }
+    };
+    __syncthreads();
+    pdl_wait();
+    int h0 = blockIdx.y * groups + tid / lanes;
+    Head ws[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+        if (h0 + j * step < n) fetch(h0 + j * step, ws[j]);
+    if (tid < D) {
+        if (p.q_norm) s_wq[tid] = p.q_norm[tid];
+        if (p.k_norm) s_wk[tid] = p.k_norm[tid];
+    }
+    search(p, t, at);
+    __syncthreads();
+    pdl_launch_dependents();
+    if (!at.found || at.disorder) return;
+    if (tid < half) angle(p, t, at.pos, tid, s_cos[tid], s_sin[tid]);
+    __syncthreads();
+    const int64_t slot = at.slot;
+    // the whole warp comes here for as many heads as any of its groups has
+    auto write = [&](int h, const Head& w) {
+        const bool on = h < n;
+        float a[U][V], b[U][V], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int u = me + i * lanes;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                a[i][k] = on && u < units ? w.a[i][k] : 0.f;
+                b[i][k] = NEOX && on && u < turn ? w.b[NEOX ? i : 0][k] : 0.f;
+                sum = fmaf(a[i][k], a[i][k], fmaf(b[i][k], b[i][k], sum));
+            }
+        }
+        for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (!on || !(h < p.heads || slot >= 0)) return;
+        const float* weight = h < p.heads ? (p.q_norm ? s_wq : nullptr) : h < HK && p.k_norm ? s_wk : nullptr;
+        const float inv = 1.f / sqrtf(sum / (float)D + p.eps);
+        C* dst = h < p.heads ? static_cast<C*>(p.q_out) + t * p.ldqo + h * D
+                 : h < HK    ? static_cast<C*>(p.c.k) + slot + (h - p.heads) * p.c.head_stride
+                             : static_cast<C*>(p.c.v) + slot + (h - HK) * p.c.head_stride;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int u = me + i * lanes;
+            if (u >= units) continue;
+            const int d = first(u);
+            if (weight) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    a[i][k] = a[i][k] * inv * weight[d + k];
+                    if (NEOX && u < turn) b[i][k] = b[i][k] * inv * weight[half + d + k];
+                }
+            }
+            if (h < HK && u < turn) {
+                if (NEOX) {
+                    float y[V], z[V];
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        const float cs = s_cos[d + k], sn = s_sin[d + k];
+                        y[k] = a[i][k] * cs - b[i][k] * sn;
+                        z[k] = a[i][k] * sn + b[i][k] * cs;
+                    }
+                    store_v<V>(dst + d, y);
+                    store_v<V>(dst + half + d, z);
+                } else {
+                    float y[V];
+#pragma unroll
+                    for (int k = 0; k < V / 2; ++k) {
+                        const float cs = s_cos[d / 2 + k], sn = s_sin[d / 2 + k];
+                        y[2 * k] = a[i][2 * k] * cs - a[i][2 * k + 1] * sn;
+                        y[2 * k + 1] = a[i][2 * k] * sn + a[i][2 * k + 1] * cs;
+                    }
+                    store_v<V>(dst + d, y);
+                }
+            } else {
+                store_v<V>(dst + d, a[i]);
+                if (NEOX && u < turn) store_v<V>(dst + half + d, b[i]);
+            }
+        }
+    };
+    // a warp's groups hold neighbouring heads, so the first of them says when it is done
+    for (int w0 = h0 - (tid & 31) / lanes; w0 < n; w0 += kAhead * step, h0 += kAhead * step) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (w0 + j * step < n) write(h0 + j * step, ws[j]);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (h0 + (kAhead + j) * step < n) fetch(h0 + (kAhead + j) * step, ws[j]);
+    }
+}
+
 template <class X, class C, int V, bool NEOX>
 cudaError_t launch(const AppendParams& p, int num_sms, int pdl, cudaStream_t s) {
+    if (p.q_norm || p.k_norm) {
+        const int half = p.rot / 2, units = (NEOX ? half / V : p.rot / V) + (p.c.dim - p.rot) / V;
+        int lanes = 1;
+        while (lanes < 32 && lanes < units) lanes *= 2;
+        const int64_t heads = p.heads + 2 * p.c.kv_heads;
+        const int64_t share = std::max<int64_t>(1, std::min(ceil_div(heads, kThreads / lanes), ceil_div(4 * num_sms, p.b.n_tokens)));
+        return launch_pdl(kv_append_norm_kernel<X, C, V, NEOX>, dim3(p.b.n_tokens, (unsigned)share), dim3(kThreads), 0, s, pdl, p, lanes);
+    }
     const int64_t per_token = (int64_t)(p.heads + 2 * p.c.kv_heads) * p.c.dim / V;
     // enough blocks to occupy the SMs when there are few tokens
     const int64_t share = std::max<int64_t>(1, std::min(ceil_div(per_token, kThreads), ceil_div(4 * num_sms, p.b.n_tokens)));

@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdlib>
 
+#include "formats.cuh"
 #include "gemm.cuh"
 #include "serving.cuh"
 
@@ -63,15 +64,17 @@ int check_heads(int64_t heads, const CacheParams& c) {
     return heads / c.kv_heads > 128 || heads > (1 << 14) ? GGUF_ERR_UNSUPPORTED : GGUF_OK;
 }
 
+bool valid_qtype(int qt) {
+    return qt == GGUF_Q4_0 || qt == GGUF_Q4_1 || qt == GGUF_Q5_0 || qt == GGUF_Q5_1 || qt == GGUF_Q8_0 ||
+           (qt >= GGUF_Q2_K && qt <= GGUF_Q6_K);
+}
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA; }
 
-}  // namespace
-
-extern "C" {
-
-int gguf_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, int xdt,
-                   int64_t heads, const gguf_rope* rope, const gguf_kv_batch* batch, const gguf_kv_cache* cache,
-                   void* q_out, int64_t ldqo, gguf_stream_t stream) {
+// gguf_kv_append (norm NULL) and gguf_kv_append_norm
+int append(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, int xdt, int64_t heads,
+           const gguf_head_norm* norm, const gguf_rope* rope, const gguf_kv_batch* batch, const gguf_kv_cache* cache,
+           void* q_out, int64_t ldqo, gguf_stream_t stream) {
     AppendParams p{};
     if (!k || !v || (q == nullptr) != (q_out == nullptr)) return GGUF_ERR_INVALID_ARG;
     int st = check_cache(cache, &p.c);
@@ -90,6 +93,13 @@ int gguf_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const
         p.rope_scale = rope->scale;
         p.rot = rope->rot_dim;
         p.style = rope->style;
+    }
+    if (norm) {
+        if (!(norm->eps >= 0.f) || !std::isfinite(norm->eps)) return GGUF_ERR_INVALID_ARG;
+        if (!aligned4(norm->q) || !aligned4(norm->k)) return GGUF_ERR_MISALIGNED;
+        p.q_norm = q ? norm->q : nullptr;
+        p.k_norm = norm->k;
+        p.eps = norm->eps;
     }
     const int per16 = xdt == GGUF_DT_F32 ? 4 : 8;
     if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || ldk % per16 || ldv % per16 ||
@@ -110,6 +120,23 @@ int gguf_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const
     p.xdt = xdt;
     p.heads = q ? (int)heads : 0;
     return cuda_status(kv_append_launch(p, sms, pdl_on(), (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int gguf_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, int xdt,
+                   int64_t heads, const gguf_rope* rope, const gguf_kv_batch* batch, const gguf_kv_cache* cache,
+                   void* q_out, int64_t ldqo, gguf_stream_t stream) {
+    return append(q, ldq, k, ldk, v, ldv, xdt, heads, nullptr, rope, batch, cache, q_out, ldqo, stream);
+}
+
+int gguf_kv_append_norm(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, int xdt,
+                        int64_t heads, const gguf_head_norm* norm, const gguf_rope* rope, const gguf_kv_batch* batch,
+                        const gguf_kv_cache* cache, void* q_out, int64_t ldqo, gguf_stream_t stream) {
+    if (!norm) return GGUF_ERR_INVALID_ARG;
+    return append(q, ldq, k, ldk, v, ldv, xdt, heads, norm, rope, batch, cache, q_out, ldqo, stream);
 }
 
 size_t gguf_paged_attn_workspace_size(const gguf_kv_batch* batch, const gguf_kv_cache* cache, int64_t heads) {
@@ -180,6 +207,91 @@ int gguf_logits_adjust(const void* logits, int dt, int64_t ld, int64_t rows, int
     const int st = current_device_launch_facts(&sms, &status);
     if (st != GGUF_OK) return st;
     return cuda_status(logits_adjust_launch(p, sms, pdl_on(), (cudaStream_t)stream));
+}
+
+int gguf_sample(const void* logits, int dt, int64_t ld, int64_t rows, int64_t vocab, const gguf_sampler* sampler,
+                const float* u, int32_t* token, float* logprob, gguf_stream_t stream) {
+    if (!logits || !u || !token || rows <= 0 || vocab <= 0 || ld < vocab) return GGUF_ERR_INVALID_ARG;
+    if (!valid_dtype(dt) || rows > (1 << 16) - 1 || vocab > 400000 || ld > (int64_t(1) << 38)) return GGUF_ERR_UNSUPPORTED;
+    SampleParams p{logits, ld, (int)rows, (int)vocab, dt, sampler ? *sampler : gguf_sampler{}, u, token, logprob};
+    if (!aligned16(logits)) return GGUF_ERR_MISALIGNED;
+    for (const void* a : {(const void*)u, (const void*)token, (const void*)logprob, (const void*)p.s.temperature,
+                          (const void*)p.s.top_k, (const void*)p.s.top_p, (const void*)p.s.min_p})
+        if (!aligned4(a)) return GGUF_ERR_MISALIGNED;
+    int sms = 0, *status = nullptr;
+    const int st = current_device_launch_facts(&sms, &status);
+    if (st != GGUF_OK) return st;
+    return cuda_status(sample_launch(p, sms, pdl_on(), (cudaStream_t)stream));
+}
+
+int gguf_moe_router(const void* x, int xdt, int64_t T, int64_t K, const gguf_router* router, int32_t* ids,
+                    float* weights, gguf_stream_t stream) {
+    if (!x || !router || !router->w || !ids || !weights || T <= 0 || K <= 0) return GGUF_ERR_INVALID_ARG;
+    const gguf_router& r = *router;
+    if (r.n_expert <= 0 || r.top_k <= 0 || r.top_k > r.n_expert || !std::isfinite(r.scale)) return GGUF_ERR_INVALID_ARG;
+    if ((r.score != GGUF_SCORE_SOFTMAX && r.score != GGUF_SCORE_SIGMOID) || (r.renormalize != 0 && r.renormalize != 1))
+        return GGUF_ERR_INVALID_ARG;
+    if (!valid_dtype(xdt) || !valid_dtype(r.wdt) || r.n_expert > 1024 || r.top_k > 64) return GGUF_ERR_UNSUPPORTED;
+    if (K % 8 || K > (1 << 20) || T > kMaxTokens) return GGUF_ERR_UNSUPPORTED;
+    if (!aligned16(x) || !aligned16(r.w) || !aligned4(r.bias) || !aligned4(ids) || !aligned4(weights)) return GGUF_ERR_MISALIGNED;
+    int sms = 0, *status = nullptr;
+    const int st = current_device_launch_facts(&sms, &status);
+    if (st != GGUF_OK) return st;
+    const RouterParams p{x, r.w, r.bias, ids, weights, (int)T, (int)K, r.n_expert, r.top_k, xdt, r.wdt, r.score, r.renormalize, r.scale};
+    return cuda_status(moe_router_launch(p, sms, pdl_on(), (cudaStream_t)stream));
+}
+
+size_t gguf_moe_ffn_workspace_size(int64_t F, int64_t T, int64_t top_k) {
+    if (F <= 0 || F > (1 << 20) || T <= 0 || top_k <= 0 || T > kMoeFfnRows || top_k > kMoeFfnRows || T * top_k > kMoeFfnRows) return 0;
+    return (size_t)(T * top_k * F) * sizeof(float);
+}
+
+int gguf_moe_ffn(const gguf_moe_weights* experts, const void* x, int xdt, int64_t T, const int32_t* ids,
+                 const float* weights, int64_t top_k, const void* residual, void* y, int ydt, void* workspace,
+                 size_t ws_bytes, gguf_stream_t stream) {
+    if (!experts || !x || !ids || !weights || !y || T <= 0 || top_k <= 0) return GGUF_ERR_INVALID_ARG;
+    const gguf_moe_weights& m = *experts;
+    if (!m.gate || !m.up || !m.down || m.n_expert <= 0 || m.K <= 0 || m.F <= 0) return GGUF_ERR_INVALID_ARG;
+    if (m.act != GGUF_ACT_SILU && m.act != GGUF_ACT_GELU) return GGUF_ERR_INVALID_ARG;
+    if (!valid_qtype(m.gate_type) || !valid_qtype(m.up_type) || !valid_qtype(m.down_type)) return GGUF_ERR_UNSUPPORTED;
+    if (m.K % block_values(m.gate_type) || m.K % block_values(m.up_type) || m.F % block_values(m.down_type)) return GGUF_ERR_INVALID_ARG;
+    if (!valid_dtype(xdt) || !valid_dtype(ydt)) return GGUF_ERR_UNSUPPORTED;
+    if (m.n_expert > kMoeFfnExperts || m.K > (1 << 20) || m.F > (1 << 20) || T > kMoeFfnRows || top_k > kMoeFfnRows ||
+        T * top_k > kMoeFfnRows)
+        return GGUF_ERR_UNSUPPORTED;
+    if (!aligned16(m.gate) || !aligned16(m.up) || !aligned16(m.down) || !aligned16(x) || !aligned16(residual) || !aligned16(y) ||
+        !aligned16(workspace) || !aligned4(ids) || !aligned4(weights))
+        return GGUF_ERR_MISALIGNED;
+    if (!workspace || ws_bytes < gguf_moe_ffn_workspace_size(m.F, T, top_k)) return GGUF_ERR_WORKSPACE;
+    int sms = 0, *status = nullptr;
+    const int st = current_device_launch_facts(&sms, &status);
+    if (st != GGUF_OK) return st;
+    auto row_bytes = [](int qt, int64_t k) { return k / block_values(qt) * block_bytes(qt); };
+    MoeFfnParams p{};
+    p.gate = static_cast<const uint8_t*>(m.gate);
+    p.up = static_cast<const uint8_t*>(m.up);
+    p.down = static_cast<const uint8_t*>(m.down);
+    p.gate_rb = row_bytes(m.gate_type, m.K);
+    p.up_rb = row_bytes(m.up_type, m.K);
+    p.down_rb = row_bytes(m.down_type, m.F);
+    p.gate_type = m.gate_type;
+    p.up_type = m.up_type;
+    p.down_type = m.down_type;
+    p.act = m.act;
+    p.n_expert = (int)m.n_expert;
+    p.T = (int)T;
+    p.top_k = (int)top_k;
+    p.K = m.K;
+    p.F = m.F;
+    p.x = x;
+    p.xdt = xdt;
+    p.ydt = ydt;
+    p.ids = ids;
+    p.weights = weights;
+    p.residual = residual;
+    p.y = y;
+    p.h = static_cast<float*>(workspace);
+    return moe_ffn_launch(p, pdl_on(), (cudaStream_t)stream);
 }
 
 }  // extern "C"

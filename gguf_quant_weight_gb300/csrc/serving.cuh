@@ -1,5 +1,5 @@
 // Parameters and host entry points of the serving kernels (kv_append.cu,
-// paged_attn.cu, logits.cu); the C entry points and their checks are in
+// paged_attn.cu, logits.cu, moe_router.cu, moe_ffn.cu, sample.cu); the C entry points and their checks are in
 // serving.cu.
 #pragma once
 #include <atomic>
@@ -38,6 +38,8 @@ struct AppendParams {
     float rope_scale;
     int rot, style;
     int xdt, heads;          // heads = 0: no q
+    const float *q_norm, *k_norm;    // the heads' norms [dim], null: none
+    float eps;
     int* status;
 };
 
@@ -66,10 +68,54 @@ struct LogitsParams {
     gguf_logit_rules r;
 };
 
+struct RouterParams {
+    const void* x;
+    const void* w;
+    const float* bias;
+    int32_t* ids;
+    float* weights;
+    int T, K, n_expert, top_k;
+    int xdt, wdt, score, renormalize;
+    float scale;
+};
+
+constexpr int kMoeFfnRows = 512, kMoeFfnExperts = 1024;      // routed rows and experts at most
+
+struct MoeFfnParams {
+    const uint8_t *gate, *up, *down;
+    int64_t gate_rb, up_rb, down_rb;     // bytes of a row
+    int gate_type, up_type, down_type, act;
+    int n_expert, T, top_k;
+    int64_t K, F;
+    const void* x;
+    int xdt, ydt;
+    const int32_t* ids;
+    const float* weights;
+    const void* residual;
+    void* y;
+    float* h;                            // workspace [T * top_k][F]
+    // set by the launch: columns a row of x and of h takes, tiles of 8 columns at
+    // a time, the down kernel's warps and how many of them share an expert
+    int x_parts, h_parts, tiles, down_warps, splits;
+};
+
+struct SampleParams {
+    const void* x;
+    int64_t ld;
+    int rows, vocab, dt;
+    gguf_sampler s;
+    const float* u;
+    int32_t* token;
+    float* logprob;
+};
+
 cudaError_t kv_append_launch(const AppendParams& p, int num_sms, int pdl, cudaStream_t stream);
 size_t paged_attn_workspace_bytes(const AttnParams& p, int num_sms);
 int paged_attn_launch(const AttnParams& p, void* workspace, int num_sms, int pdl, cudaStream_t stream);
 cudaError_t logits_adjust_launch(const LogitsParams& p, int num_sms, int pdl, cudaStream_t stream);
+cudaError_t moe_router_launch(const RouterParams& p, int num_sms, int pdl, cudaStream_t stream);
+int moe_ffn_launch(MoeFfnParams p, int pdl, cudaStream_t stream);
+cudaError_t sample_launch(const SampleParams& p, int num_sms, int pdl, cudaStream_t stream);
 
 // Sets a kernel's attribute on each device once: `done` is the kernel's own
 // set of devices that have it.

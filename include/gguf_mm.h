@@ -377,6 +377,25 @@ int gguf_kv_append(const void* q, int64_t ldq, const void* k, int64_t ldk, const
                    int64_t heads, const gguf_rope* rope, const gguf_kv_batch* batch, const gguf_kv_cache* cache,
                    void* q_out, int64_t ldqo, gguf_stream_t stream);
 
+/* Norms of the heads, before they are rotated: each head x [head_dim] of the
+ * queries (keys) becomes x / sqrt(mean(x^2) + eps) * weight.
+ *   q, k  f32 [head_dim], the same for all heads; NULL: those heads are not normed
+ *   eps   not negative, finite */
+typedef struct {
+    const float* q;
+    const float* k;
+    float eps;
+} gguf_head_norm;
+
+/* gguf_kv_append with the heads of q and k normed first, in the same pass: the
+ * sum of squares, the norm and the rotation are computed in f32 and each value
+ * is rounded once.  All other arguments, the rules for tokens out of range and
+ * the errors as gguf_kv_append; norm may not be NULL (INVALID_ARG), and where q
+ * is NULL norm->q is not read. */
+int gguf_kv_append_norm(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, int xdt,
+                        int64_t heads, const gguf_head_norm* norm, const gguf_rope* rope, const gguf_kv_batch* batch,
+                        const gguf_kv_cache* cache, void* q_out, int64_t ldqo, gguf_stream_t stream);
+
 /* Attention of the new tokens over the paged cache (their own keys appended):
  *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K[j][h']) V[j][h'],  h' = h * kv_heads / heads,
  * over the keys 0 <= j < kv_len[b] with, where `causal` is set, j <= p, and
@@ -437,6 +456,118 @@ typedef struct {
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, NO_DEVICE, CUDA. */
 int gguf_logits_adjust(const void* logits, int dt, int64_t ld, int64_t rows, int64_t vocab,
                        const gguf_logit_rules* rules, void* out, int odt, int64_t ldo, gguf_stream_t stream);
+
+/* What each row of logits is drawn by; a NULL member is a filter that is not used.
+ *   temperature  f32 [rows]: logits are divided by it (NULL: 1); 0: the largest
+ *                logit is taken, whatever the other members say; below 0 or NaN:
+ *                the row has no distribution
+ *   top_k        int32 [rows]: only the top_k largest may be drawn (0 or less: all)
+ *   top_p        f32 [rows]: only the shortest run of the largest whose share of
+ *                what top_k leaves reaches top_p (at least one; 1 or more: all; below 0 counts as 0)
+ *   min_p        f32 [rows]: only those at least min_p times as likely as the
+ *                likeliest (0 or less: all; above 1 counts as 1)
+ * A NaN in top_p or min_p is a filter that is not used.  Among equal logits the
+ * lower index comes first.  A token has to pass all filters. */
+typedef struct {
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+} gguf_sampler;
+
+/* Draws token[r] from row r of logits [rows][vocab] (of dt, row r at logits +
+ * r * ld): with w_i = exp((x_i - max x) / temperature) for the tokens that pass
+ * the filters, the first i in the order of the vocabulary with
+ *   w_0 + ... + w_i > u[r] * (sum of all w),
+ * u [rows] f32 uniform in [0, 1) (below 0 and NaN count as 0; at 1 and above the
+ * last token that passes is taken).  The sums are exact to about 1e-11 of the whole,
+ * so that the token is the one that 64-bit arithmetic gives.
+ *   logprob  f32 [rows] or NULL: log(w_token / sum of all w), 0 where the
+ *            temperature is 0
+ * A row without a distribution (a NaN or +inf among its logits, nothing but
+ * -inf, its temperature) gives token -1 and logprob NaN.
+ * The result does not depend on timing, nor on the other rows.  logits 16-byte
+ * aligned (rows may start anywhere), the arrays 4-byte aligned.  vocab at most
+ * 400000.  sampler NULL: no filters, temperature 1.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, NO_DEVICE, CUDA. */
+int gguf_sample(const void* logits, int dt, int64_t ld, int64_t rows, int64_t vocab, const gguf_sampler* sampler,
+                const float* u, int32_t* token, float* logprob, gguf_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A mixture of experts around the products: which experts a token takes, and a
+ * few tokens through them in one call.  The ids that gguf_moe_router writes are
+ * what gguf_mm_id, gguf_mm_id_slots and gguf_moe_ffn read.
+ * ------------------------------------------------------------------------- */
+
+/* A router.  HOST memory, read during the call; w and bias are device memory.
+ *   w        [n_expert][K] of wdt (F32, F16 or BF16), as a file's ffn_gate_inp
+ *   bias     f32 [n_expert], added to what the experts are chosen by and not to
+ *            their weights, or NULL
+ *   n_expert at most 1024;  top_k at most 64 and n_expert
+ *   score    GGUF_SCORE_SOFTMAX: p = softmax of the scores over all experts;
+ *            GGUF_SCORE_SIGMOID: p = 1 / (1 + exp(-score))
+ *   renormalize  (0 or 1): the chosen experts' p are divided by their sum
+ *   scale    what the weights are multiplied by at last (finite) */
+enum { GGUF_SCORE_SOFTMAX = 0, GGUF_SCORE_SIGMOID = 1 };
+typedef struct {
+    const void* w;
+    const float* bias;
+    int32_t wdt;
+    int32_t n_expert;
+    int32_t top_k;
+    int32_t score;
+    int32_t renormalize;
+    float scale;
+} gguf_router;
+
+/* The experts of each token: scores x [T][K] (of xdt: F32, F16 or BF16) . w^T,
+ * the top_k of the largest p + bias in falling order, the lower index first among equals:
+ *   ids [T][top_k] int32,  weights [T][top_k] f32.
+ * The choice and its order are those of 64-bit arithmetic; weights are accurate
+ * to f32's rounding.  A token with a score that is not finite gets top_k
+ * different experts all the same, and weights that may be NaN.  K a multiple of
+ * 8; x and w 16-byte aligned, the other arrays 4-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, NO_DEVICE, CUDA. */
+int gguf_moe_router(const void* x, int xdt, int64_t T, int64_t K, const gguf_router* router, int32_t* ids,
+                    float* weights, gguf_stream_t stream);
+
+/* The experts' gated feed-forward.  HOST memory, read during the call.
+ *   gate, up  n_expert weight tensors [F][K] back to back, as gguf_mm_id takes them
+ *   down      n_expert weight tensors [K][F]
+ *   *_type    any of the ten formats, each its own
+ *   act       GGUF_ACT_SILU: a / (1 + exp(-a));
+ *             GGUF_ACT_GELU: a / 2 * (1 + tanh(sqrt(2 / pi) * (a + 0.044715 a^3)))
+ *   n_expert  at most 1024;  K, F multiples of their formats' blocks */
+enum { GGUF_ACT_SILU = 0, GGUF_ACT_GELU = 1 };
+typedef struct {
+    const void* gate;
+    const void* up;
+    const void* down;
+    int32_t gate_type, up_type, down_type;
+    int32_t act;
+    int64_t n_expert, K, F;
+} gguf_moe_weights;
+
+/* A few tokens through their experts:
+ *   y[t] = residual[t] + sum over s of weights[t][s] * Down_e(act(Gate_e x[t]) * Up_e x[t]),  e = ids[t][s]
+ *   x [T][K] of xdt, ids [T][top_k] int32, weights [T][top_k] f32, residual [T][K]
+ *   of ydt or NULL, y [T][K] of ydt (F32, F16 or BF16 each); y may be residual,
+ *   and may not overlap x.
+ * At most 512 routed rows (T * top_k): larger batches are gguf_mm_id's and
+ * gguf_mm_id_slots'.  An id outside [0, n_expert) adds nothing; one that comes
+ * twice in a token adds twice.  The activations are not rounded to int8 codes:
+ * products are those of the decoded weights with x, in f32, the
+ * hidden values rounded to f16 (scaled, so whatever their range) where y is BF16 and to 22 bits otherwise.
+ * Slots are added in their order; the result does not depend on timing.
+ * Pointers 16-byte aligned (ids, weights: 4).
+ * Workspace: gguf_moe_ffn_workspace_size() bytes.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, NO_DEVICE, CUDA. */
+int gguf_moe_ffn(const gguf_moe_weights* experts, const void* x, int xdt, int64_t T, const int32_t* ids,
+                 const float* weights, int64_t top_k, const void* residual, void* y, int ydt, void* workspace,
+                 size_t ws_bytes, gguf_stream_t stream);
+
+/* Bytes of workspace gguf_moe_ffn needs; 0 for invalid arguments. */
+size_t gguf_moe_ffn_workspace_size(int64_t F, int64_t T, int64_t top_k);
 
 /* Synchronises `stream`, then returns and clears the device status word of the
  * current device: GGUF_OK, GGUF_ERR_TIMEOUT (a bounded wait in a kernel expired;

@@ -105,3 +105,77 @@ def logits(x, hist, repeat, frequency, presence, biases, allow):
         if allow is not None:
             y[r, ~allow[r]] = -np.inf
     return y
+
+
+def head_norm(x, weight, eps):
+    """x [..., dim] divided by the root of its mean square and multiplied by weight [dim] (None: x itself)."""
+    x = np.array(x, np.float64)
+    if weight is None:
+        return x
+    return x / np.sqrt((x * x).mean(-1, keepdims=True) + float(eps)) * np.asarray(weight, np.float64)
+
+
+def router(x, w, bias, top_k, sigmoid, renormalize, scale):
+    """(ids, weights) of each token: the largest p + bias first, the lower index among equals."""
+    z = np.asarray(x, np.float64) @ np.asarray(w, np.float64).T
+    T, E = z.shape
+    ids, weights = np.zeros((T, top_k), np.int64), np.zeros((T, top_k))
+    for t in range(T):
+        if sigmoid:
+            p = 1.0 / (1.0 + np.exp(-z[t]))
+        else:
+            p = np.exp(z[t] - z[t].max())
+            p = p / p.sum()
+        # without a bias the scores have the order of p, also where p is too small to tell
+        rank = z[t] if bias is None else p + np.asarray(bias, np.float64)
+        ids[t] = sorted(range(E), key=lambda e: (-rank[e], e))[:top_k]
+        v = p[ids[t]]
+        weights[t] = (v / v.sum() if renormalize else v) * float(scale)
+    return ids, weights
+
+
+def activate(a, gelu):
+    a = np.asarray(a, np.float64)
+    if gelu:
+        return 0.5 * a * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (a + 0.044715 * a ** 3)))
+    return a / (1.0 + np.exp(-a))
+
+
+def moe_ffn(x, gate, up, down, ids, weights, gelu, residual):
+    """x [T, K]; gate, up [E, F, K], down [E, K, F] as values; ids outside the experts add nothing."""
+    y = np.zeros(x.shape) if residual is None else np.array(residual, np.float64)
+    for t in range(x.shape[0]):
+        for s, e in enumerate(ids[t]):
+            if 0 <= e < gate.shape[0]:
+                y[t] += weights[t, s] * (down[e] @ (activate(gate[e] @ x[t], gelu) * (up[e] @ x[t])))
+    return y
+
+
+def sample(x, temperature, top_k, top_p, min_p, u):
+    """(token, logprob, number kept) of one row of logits."""
+    x = np.array(x, np.float64) + 0.0
+    t, u = float(temperature), float(u)
+    u = u if u > 0 else 0.0
+    top = x.max() if x.size else -np.inf
+    if not t >= 0 or np.isnan(x).any() or not np.isfinite(top):
+        return -1, np.nan, 0
+    if t == 0:
+        return int(np.argmax(x)), 0.0, 1
+    order = [i for i in sorted(range(len(x)), key=lambda i: (-x[i], i)) if x[i] > -np.inf]
+    if top_k > 0:
+        order = order[:int(top_k)]
+    with np.errstate(over="ignore"):
+        w = np.exp((x[order] - top) / t)
+    n = len(order)
+    if top_p < 1:
+        n = min(n, 1 + int((np.cumsum(w) < max(float(top_p), 0.0) * w.sum()).sum()))
+    if min_p > 0:
+        least = top + t * math.log(min(float(min_p), 1.0)) if math.isfinite(t) else -np.inf
+        n = min(n, int((x[order] >= least).sum()))
+    kept = sorted(order[:n])
+    with np.errstate(over="ignore"):
+        w = np.exp((x[kept] - top) / t)
+    upto = np.cumsum(w)
+    past = np.flatnonzero(upto > u * upto[-1]) if u < 1 else []
+    at = int(past[0]) if len(past) else int(np.flatnonzero(w > 0)[-1])
+    return kept[at], float(np.log(w[at] / upto[-1])), len(kept)
