@@ -1,25 +1,34 @@
 // A few tokens through their experts' gated feed-forward, on the GGUF blocks:
 //   y[t] = residual[t] + sum_s w[t][s] * Down_e( act(Gate_e x[t]) * Up_e x[t] ),  e = ids[t][s],
-// in two kernels: gate, up and the activation; down, the weighted sum and the
-// residual.  Unlike the decode GEMV, activations are not rounded to int8: what
-// a routed row gives is accurate to f32's rounding (f32 and f16 outputs) or to
-// f16's (bf16 outputs).
+// in three kernels: gate, up and the activation; the hidden values made ready
+// for the tensor cores; down, the weighted sum and the residual.  Unlike the
+// decode GEMV, activations are not rounded to int8: what a routed row gives is
+// accurate to f32's rounding (f32 and f16 outputs) or to f16's (bf16 outputs).
 //
-// The weights' bytes bound it, so an expert's blocks are read once for all of
+// The weights' bytes bound it, and next to them the instructions that take
+// blocks apart, so an expert's blocks are read and taken apart once for all of
 // the batch's rows that it has: the tensor cores' m16n8k16 takes 16 weight rows
 // as A and up to 8 columns of activations as B.  A's values are the blocks'
-// integers, exact in f16: codes times their sub-block scale where the product
-// is (Q2_K .. Q5_K: at most 31 * 63), summed over a block before its d is
-// applied, codes alone otherwise (Q6_K, the 32-value types), summed over a
-// scale's values.  B's columns are the activations scaled by a power of two per
-// 256 of them; an f32 value takes two columns, its f16 rounding and what that
-// left, so 22 bits of it.  Which values of a sub-block a lane holds is free as long
-// as A and B agree: lane t of four has bytes 4t .. 4t+3 of each 16, and of
-// those the even and the odd ones make its two pairs, which is how masks of
-// 0x00ff00ff find them in a word of codes.
+// codes.  A code without an offset needs no conversion: an integer's bits are
+// the f16 number 2^-24 times it (a subnormal, which the tensor cores take), so a mask gives
+// two of them, and the high nibble stays where it is, 16 times as large.  Codes
+// with a zero point become 1024 + code by a byte permutation, less 1024 + zero
+// point.  The products of a sub-block are summed by the tensor cores, and its
+// scale is applied in f32.  B's columns are the activations scaled by a power of two
+// per 256 of them; an f32 value takes two columns, its f16 rounding and what
+// that left, so 22 bits of it.  Which values of a sub-block a lane holds is free as
+// long as A and B agree: lane t of four has bytes 4t .. 4t+3 of each 16, and of
+// those the even and the odd ones make its two pairs, which is how masks find
+// them in a word of codes.
 //
 // Mins: sum_j m_j * (sum of sub-block j's activations) is one more product, of
 // the mins (exact in f16) with the sums in two f16 parts.
+//
+// Each warp streams its own pieces of the weights, 16 rows x 256 values, through a ring of
+// asynchronous copies that runs on across the experts and row tiles of its block,
+// one block to an SM.  A row's piece is copied in whole 16-byte units from the boundary before it;
+// the rows lie an odd multiple of 16 bytes apart, so that the eight rows that a
+// load of the warp meets fall into different banks.
 #include <type_traits>
 
 #include "formats.cuh"
@@ -30,57 +39,82 @@ namespace gg {
 namespace {
 
 constexpr int kChunk = 256;                       // values of K a warp takes at a time
-constexpr int kTiles = 2;                         // of 8 columns, at a time
-constexpr int kColStride = 2 * kChunk + 64;       // bytes of a column in shared memory: 8 lanes' 16 bytes from 2 columns meet no bank twice
-constexpr int kTileBytes = 8 * kColStride + 8 * 64 + 8 * 4;   // columns, their sums' parts, their scales
-constexpr int kUpWarps = 8, kDownWarps = 24;      // kDownWarps: at most
-constexpr size_t kDownSmem = 221184;              // beside the routes
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kColStride = 2 * kChunk + 64;       // bytes of a column: f16 values, then the sums of its 16-value groups in two f16
+                                                  // parts; 8 lanes' 16 bytes from 2 columns meet no bank twice
+constexpr int kTileBytes = 8 * kColStride;
+constexpr int kTiles = 2;                         // of 8 columns, at most
+constexpr int kMaxStages = 3;                     // pieces of a warp on their way
+constexpr size_t kSmem = 232448 - 2048;           // of a block, beside its static part
 
 // ---------------------------------------------------------------- the experts' rows
 
-// What each block makes of the ids: the experts with rows, and the rows
-// (entries token * top_k + slot) of each.  The order of an expert's rows is
-// whatever the atomics give; a row's result does not depend on its column.
-struct Routes {
-    int n_active;
-    int start[kMoeFfnExperts + 1];     // first of expert e's rows in list
-    int cursor[kMoeFfnExperts];
-    uint16_t active[kMoeFfnRows];   // experts with rows, in order
-    uint16_t list[kMoeFfnRows];
+// A group is up to `at_once` rows of one expert: the columns of one pass over its weights.
+struct Group {
+    int16_t expert, n;
+    int16_t first;                  // of its rows (entries token * top_k + slot) in Routes::list
 };
 
-__device__ void make_routes(Routes& r, const int32_t* ids, int entries, int n_expert, int tid, int threads) {
-    for (int e = tid; e < n_expert; e += threads) r.cursor[e] = 0;
+// What each block makes of the ids, all blocks the same: an expert's rows are in
+// the order of the entries, since its groups may be different blocks' work.  In
+// dynamic shared memory, sized by `bytes`.
+struct Routes {
+    int* cursor;                    // [n_expert]
+    Group* group;                   // [entries]
+    uint16_t* list;                 // [entries], by expert
+    int16_t* id;                    // [entries], -1: none
+    __host__ __device__ static size_t bytes(int entries, int n_expert) {
+        return (size_t)ceil_div(4 * (int64_t)n_expert + 10 * (int64_t)entries, 16) * 16;
+    }
+    __device__ Routes(uint8_t* at, int entries, int n_expert)
+        : cursor(reinterpret_cast<int*>(at)), group(reinterpret_cast<Group*>(cursor + n_expert)),
+          list(reinterpret_cast<uint16_t*>(group + entries)), id(reinterpret_cast<int16_t*>(list + entries)) {}
+};
+
+// Returns the number of groups.
+__device__ int make_routes(const Routes& r, const int32_t* ids, int entries, int n_expert, int at_once, int tid) {
+    __shared__ int s_groups;
+    for (int e = tid; e < n_expert; e += kThreads) r.cursor[e] = 0;
     __syncthreads();
-    for (int i = tid; i < entries; i += threads) {
+    for (int i = tid; i < entries; i += kThreads) {
         const int e = ids[i];
-        if ((unsigned)e < (unsigned)n_expert) atomicAdd(&r.cursor[e], 1);
+        const bool in = (unsigned)e < (unsigned)n_expert;
+        r.id[i] = in ? (int16_t)e : -1;
+        if (in) atomicAdd(&r.cursor[e], 1);
     }
     __syncthreads();
     if (tid < 32) {
-        int rows = 0, act = 0;
+        int rows = 0, groups = 0;
         for (int b = 0; b < n_expert; b += 32) {
-            const int e = b + tid, c = e < n_expert ? r.cursor[e] : 0;
-            int sum = c;
+            const int e = b + tid, c = e < n_expert ? r.cursor[e] : 0, g = (c + at_once - 1) / at_once;
+            if (!__any_sync(0xffffffffu, c > 0)) continue;
+            int both = c | g << 16;             // at most 512 of each
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, sum, o);
-                if (tid >= o) sum += v;
+                const int v = __shfl_up_sync(0xffffffffu, both, o);
+                if (tid >= o) both += v;
             }
-            const unsigned on = __ballot_sync(0xffffffffu, c > 0);
-            if (e < n_expert) r.start[e] = r.cursor[e] = rows + sum - c;
-            if (c > 0) r.active[act + __popc(on & ((1u << tid) - 1))] = (uint16_t)e;
-            rows += __shfl_sync(0xffffffffu, sum, 31);
-            act += __popc(on);
+            const int c0 = rows + (both & 0xffff) - c, g0 = groups + (both >> 16) - g;
+            if (c > 0) r.cursor[e] = c0;
+            for (int k = 0; k < g; ++k)
+                r.group[g0 + k] = Group{(int16_t)e, (int16_t)min(at_once, c - k * at_once), (int16_t)(c0 + k * at_once)};
+            const int last = __shfl_sync(0xffffffffu, both, 31);
+            rows += last & 0xffff;
+            groups += last >> 16;
         }
-        if (tid == 0) r.n_active = act, r.start[n_expert] = rows;
+        if (tid == 0) s_groups = groups;
+        __syncwarp();
+        for (int b = 0; b < entries; b += 32) {
+            const int e = b + tid < entries ? r.id[b + tid] : -1;
+            const unsigned same = __match_any_sync(0xffffffffu, e), before = same & ((1u << tid) - 1);
+            if (e >= 0) r.list[r.cursor[e] + __popc(before)] = (uint16_t)(b + tid);
+            __syncwarp();
+            if (e >= 0 && !before) r.cursor[e] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
-    for (int i = tid; i < entries; i += threads) {
-        const int e = ids[i];
-        if ((unsigned)e < (unsigned)n_expert) r.list[atomicAdd(&r.cursor[e], 1)] = (uint16_t)i;
-    }
-    __syncthreads();
+    return s_groups;
 }
 
 // ---------------------------------------------------------------- B: the activations
@@ -108,10 +142,10 @@ __device__ __forceinline__ void load4(const void* p, int dt, int64_t i, float (&
     }
 }
 
-// One row's values [base, base + 32 * nsub) into column `col` of the warp's
-// tiles (and, with two parts, the column after it).  The whole warp calls it.
-__device__ __forceinline__ void stage_row(uint8_t* tiles, int col, int parts, const void* x, int dt, int64_t base, int nsub,
-                                          int lane) {
+// One row's values [base, base + 32 * nsub) of x as a column of kColStride bytes (and,
+// with two parts, the column after it).  Returns what the column's products are
+// multiplied by.  The whole warp calls it.
+__device__ __forceinline__ float make_column(uint8_t* col, int parts, const void* x, int dt, int64_t base, int nsub, int lane) {
     const int j = lane >> 2, t = lane & 3;
     float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
     if (j < nsub) {
@@ -136,49 +170,48 @@ __device__ __forceinline__ void stage_row(uint8_t* tiles, int col, int parts, co
         a[i] *= scale, b[i] *= scale;
         sa += a[i], sb += b[i];
     }
-    uint8_t* tile = tiles + (col >> 3) * kTileBytes;
-    const int c = col & 7;
     uint4 hi;
     hi.x = pack2(a[0], a[2]), hi.y = pack2(a[1], a[3]), hi.z = pack2(b[0], b[2]), hi.w = pack2(b[1], b[3]);
-    *reinterpret_cast<uint4*>(tile + c * kColStride + j * 64 + t * 16) = hi;
+    *reinterpret_cast<uint4*>(col + lane * 16) = hi;
     sa += __shfl_xor_sync(0xffffffffu, sa, 1), sb += __shfl_xor_sync(0xffffffffu, sb, 1);
     sa += __shfl_xor_sync(0xffffffffu, sa, 2), sb += __shfl_xor_sync(0xffffffffu, sb, 2);
-    __half* sums = reinterpret_cast<__half*>(tile + 8 * kColStride + c * 64);    // [hi 16][lo 16]
-    float* scales = reinterpret_cast<float*>(tile + 8 * kColStride + 8 * 64);
+    uint32_t* sums = reinterpret_cast<uint32_t*>(col + 2 * kChunk);      // [first parts 16][second parts 16] f16
     if (t == 0) {
         const uint32_t h = pack2(sa, sb);
         const float2 f = unpack2(h);
-        *reinterpret_cast<uint32_t*>(sums + 2 * j) = h;
-        *reinterpret_cast<uint32_t*>(sums + 16 + 2 * j) = pack2(sa - f.x, sb - f.y);
+        sums[j] = h;
+        sums[8 + j] = pack2(sa - f.x, sb - f.y);
     }
-    if (lane == 0) scales[c] = back;
     if (parts == 2) {
-        // a multiple of two columns to a tile: the next column is in the same one
         float2 f = unpack2(hi.x);
         uint4 lo;
         lo.x = pack2(a[0] - f.x, a[2] - f.y);
         f = unpack2(hi.y), lo.y = pack2(a[1] - f.x, a[3] - f.y);
         f = unpack2(hi.z), lo.z = pack2(b[0] - f.x, b[2] - f.y);
         f = unpack2(hi.w), lo.w = pack2(b[1] - f.x, b[3] - f.y);
-        *reinterpret_cast<uint4*>(tile + (c + 1) * kColStride + j * 64 + t * 16) = lo;
-        if (t == 0) {       // the first column has the whole sums
-            *reinterpret_cast<uint32_t*>(sums + 32 + 2 * j) = 0u;
-            *reinterpret_cast<uint32_t*>(sums + 48 + 2 * j) = 0u;
-        }
-        if (lane == 0) scales[c + 1] = back;
+        *reinterpret_cast<uint4*>(col + kColStride + lane * 16) = lo;
+        if (t == 0) sums[kColStride / 4 + j] = sums[kColStride / 4 + 8 + j] = 0u;       // the first column has the whole sums
     }
+    return back;
 }
 
 // ---------------------------------------------------------------- A: the blocks
 
-__device__ __forceinline__ uint32_t ld32(const uint8_t* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); }
-__device__ __forceinline__ uint32_t ld16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint16_t*>(p)); }
+// 256 values of a row: their bytes, and how far apart rows lie in shared memory
+// (the piece from the 16-byte boundary before it to the one after it, and an odd
+// multiple of 16)
+__host__ __device__ constexpr int piece_bytes(int qt) { return block32(qt) ? 8 * block_bytes(qt) : block_bytes(qt); }
+__host__ __device__ constexpr bool piece_aligned(int qt) { return qt == GGUF_Q4_K || qt == GGUF_Q5_K; }
+__host__ __device__ constexpr int piece_stride(int qt) {
+    const int slack = piece_aligned(qt) ? 0 : block_bytes(qt) % 4 ? 14 : 12;
+    return ((piece_bytes(qt) + slack + 15) / 16 | 1) * 16;
+}
+
+__device__ __forceinline__ uint32_t ld32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+__device__ __forceinline__ uint32_t ld16(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
 // a word at a 2-byte boundary
 __device__ __forceinline__ uint32_t ld32h(const uint8_t* p) { return ld16(p) | ld16(p + 2) << 16; }
 
-__host__ __device__ constexpr bool int_scaled(int qt) {
-    return qt == GGUF_Q2_K || qt == GGUF_Q3_K || qt == GGUF_Q4_K || qt == GGUF_Q5_K;
-}
 __host__ __device__ constexpr bool has_min(int qt) {
     return qt == GGUF_Q2_K || qt == GGUF_Q4_K || qt == GGUF_Q5_K || b32_has_min(qt);
 }
@@ -187,28 +220,25 @@ __host__ __device__ constexpr int zero_point(int qt) {
     return qt == GGUF_Q6_K ? 32 : qt == GGUF_Q3_K ? 4 : qt == GGUF_Q8_0 ? 128 : block32(qt) ? b32_zero_point(qt) : 0;
 }
 
-// 256 values of one weight row as lane t of four holds them.  load(): row, the
-// row's first byte; c, the chunk; nsub, how many of its 32-value groups exist
-// (fewer than 8 at the end of a row of 32-value blocks).
+// 256 values of one weight row as lane t of four holds them.  load(): from their
+// first byte; nsub, how many of their 32-value groups exist (fewer than 8 at the
+// end of a row of 32-value blocks).
 template <int QT> struct Raw;
 
 template <> struct Raw<GGUF_Q4_K> {
     uint32_t w[4][2];
     uint4 head;         // d, dmin, scales
-    __device__ __forceinline__ void load(const uint8_t* row, int64_t c, int, int t) {
-        const uint8_t* b = row + c * 144;
-        head = __ldg(reinterpret_cast<const uint4*>(b));
+    __device__ __forceinline__ void load(const uint8_t* b, int, int t) {
+        head = *reinterpret_cast<const uint4*>(b);
 #pragma unroll
         for (int p = 0; p < 4; ++p) w[p][0] = ld32(b + 16 + 32 * p + 4 * t), w[p][1] = ld32(b + 32 + 32 * p + 4 * t);
     }
-    __device__ __forceinline__ uint32_t codes(int j, int half, int) const { return (w[j >> 1][half] >> (4 * (j & 1))) & 0x0f0f0f0fu; }
 };
 template <> struct Raw<GGUF_Q5_K> {
     uint32_t w[4][2], h[2];
     uint4 head;
-    __device__ __forceinline__ void load(const uint8_t* row, int64_t c, int, int t) {
-        const uint8_t* b = row + c * 176;
-        head = __ldg(reinterpret_cast<const uint4*>(b));
+    __device__ __forceinline__ void load(const uint8_t* b, int, int t) {
+        head = *reinterpret_cast<const uint4*>(b);
         h[0] = ld32(b + 16 + 4 * t), h[1] = ld32(b + 32 + 4 * t);
 #pragma unroll
         for (int p = 0; p < 4; ++p) w[p][0] = ld32(b + 48 + 32 * p + 4 * t), w[p][1] = ld32(b + 64 + 32 * p + 4 * t);
@@ -220,8 +250,7 @@ template <> struct Raw<GGUF_Q5_K> {
 };
 template <> struct Raw<GGUF_Q6_K> {
     uint32_t ql[4][2], qh[2][2], sc[4], d;
-    __device__ __forceinline__ void load(const uint8_t* row, int64_t c, int, int t) {
-        const uint8_t* b = row + c * 210;
+    __device__ __forceinline__ void load(const uint8_t* b, int, int t) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) ql[p][0] = ld32h(b + 32 * p + 4 * t), ql[p][1] = ld32h(b + 32 * p + 16 + 4 * t);
 #pragma unroll
@@ -239,8 +268,7 @@ template <> struct Raw<GGUF_Q6_K> {
 };
 template <> struct Raw<GGUF_Q2_K> {
     uint32_t w[2][2], sc[4], dm;
-    __device__ __forceinline__ void load(const uint8_t* row, int64_t c, int, int t) {
-        const uint8_t* b = row + c * 84;
+    __device__ __forceinline__ void load(const uint8_t* b, int, int t) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) sc[p] = ld32(b + 4 * p);
 #pragma unroll
@@ -251,8 +279,7 @@ template <> struct Raw<GGUF_Q2_K> {
 };
 template <> struct Raw<GGUF_Q3_K> {
     uint32_t w[2][2], h[2], sc[3], d;
-    __device__ __forceinline__ void load(const uint8_t* row, int64_t c, int, int t) {
-        const uint8_t* b = row + c * 110;
+    __device__ __forceinline__ void load(const uint8_t* b, int, int t) {
         h[0] = ld32h(b + 4 * t), h[1] = ld32h(b + 16 + 4 * t);
 #pragma unroll
         for (int p = 0; p < 2; ++p) w[p][0] = ld32h(b + 32 + 32 * p + 4 * t), w[p][1] = ld32h(b + 48 + 32 * p + 4 * t);
@@ -274,10 +301,10 @@ template <> struct Raw<GGUF_Q3_K> {
 template <int QT> struct Raw {
     static constexpr int BB = block_bytes(QT), WORDS = QT == GGUF_Q8_0 ? 2 : 1;
     uint32_t w[8][WORDS], qh[b32_has_qh(QT) ? 8 : 1], d[8];      // d: d and, where there is one, m above it
-    __device__ __forceinline__ void load(const uint8_t* row, int64_t c, int nsub, int t) {
+    __device__ __forceinline__ void load(const uint8_t* row, int nsub, int t) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint8_t* b = row + (c * 8 + min(j, nsub - 1)) * BB;
+            const uint8_t* b = row + min(j, nsub - 1) * BB;
             if constexpr (QT == GGUF_Q8_0) {
                 w[j][0] = ld32h(b + 2 + 4 * t), w[j][1] = ld32h(b + 18 + 4 * t);
             } else if constexpr (BB % 4 == 0) {
@@ -305,22 +332,25 @@ template <int QT> struct Raw {
     }
 };
 
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
 __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
-// byte i of a word twice over, as the f16 numbers 1024 + byte
-__device__ __forceinline__ __half2 byte_h2(uint32_t w, int i) { return as_h2(__byte_perm(w, 0x64646464u, 0x4040 | i | i << 8)); }
 __device__ __forceinline__ float f16_low(uint32_t v) { return __half2float(__ushort_as_half((unsigned short)(v & 0xffffu))); }
 __device__ __forceinline__ float f16_high(uint32_t v) { return __half2float(__ushort_as_half((unsigned short)(v >> 16))); }
+// byte i of a word as a float, and (sixteenth) a sixteenth of it: the mantissa's last bits of 2^23 (2^19)
+__device__ __forceinline__ float byte_f(uint32_t w, int i, bool sixteenth = false) {
+    const uint32_t m = sixteenth ? 0x49000000u : 0x4b000000u;
+    return __uint_as_float(__byte_perm(w, m, 0x7650 | i)) - __uint_as_float(m);
+}
 
 // The 6-bit scales (lo, hi of four) and mins of Q4_K / Q5_K as words of bytes.
-__device__ __forceinline__ void six_bits(const uint4& head, uint32_t (&sc)[2], uint32_t (&mn)[2]) {
+__device__ __forceinline__ void six_bits(const uint4& head, uint32_t (&sc)[4], uint32_t (&mn)[4]) {
     sc[0] = head.y & 0x3f3f3f3fu;
     mn[0] = head.z & 0x3f3f3f3fu;
     sc[1] = (head.w & 0x0f0f0f0fu) | ((head.y >> 2) & 0x30303030u);
@@ -328,23 +358,23 @@ __device__ __forceinline__ void six_bits(const uint4& head, uint32_t (&sc)[2], u
 }
 
 // acc[tile] += (16 weight rows x 256 values) * (the tile's columns).  r[0], r[1]:
-// the rows lane / 4 and lane / 4 + 8.
-template <int QT>
-__device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const uint8_t* tiles, int n_tiles, int nsub, int lane,
-                                         float (&acc)[kTiles][4]) {
-    const int g = lane >> 2, t = lane & 3;
-    const uint8_t* col = tiles + g * kColStride + t * 16;
-    constexpr int Z = 1024 + zero_point(QT);
-    float total[kTiles][4] = {};
-    uint32_t sc[2][4], mn[2][4];        // by row: scales and mins as bytes
+// the rows lane / 4 and lane / 4 + 8.  B gives column lane / 4's values of 32-value group j
+// (values), its sums' parts (sums(tile, k): those of groups 8k + 2t, 2t + 1 of 16), and what columns 2t, 2t + 1 are
+// multiplied by (back).
+template <int QT, int TILES, class B>
+__device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, int n_tiles, int nsub, int lane, float (&acc)[TILES][4]) {
+    const int t = lane & 3;
+    constexpr bool plain = zero_point(QT) == 0;         // codes as they are, subnormals: 2^-24 of them
+    constexpr bool narrow = QT == GGUF_Q2_K || QT == GGUF_Q3_K || QT == GGUF_Q6_K;      // scales of 16 values
+    const __half2 zero = __float2half2_rn(-(float)(1024 + zero_point(QT)));
+    float total[TILES][4] = {};
+    uint32_t sc[2][4] = {}, mn[2][4] = {};      // by row: scales and mins as bytes
     float d[2], dmin[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         d[i] = 1.f, dmin[i] = 1.f;
         if constexpr (QT == GGUF_Q4_K || QT == GGUF_Q5_K) {
-            uint32_t s[2], m[2];
-            six_bits(r[i].head, s, m);
-            sc[i][0] = s[0], sc[i][1] = s[1], mn[i][0] = m[0], mn[i][1] = m[1];
+            six_bits(r[i].head, sc[i], mn[i]);
             d[i] = f16_low(r[i].head.x), dmin[i] = f16_high(r[i].head.x);
         } else if constexpr (QT == GGUF_Q2_K) {
 #pragma unroll
@@ -355,114 +385,100 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const uint8_t* t
             for (int p = 0; p < 4; ++p) sc[i][p] = r[i].scales(p);
             d[i] = f16_low(r[i].d);
         } else if constexpr (QT == GGUF_Q6_K) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) sc[i][p] = r[i].sc[p] ^ 0x80808080u;
             d[i] = f16_low(r[i].d);
         }
     }
+    // scale of 16-value group 2 j + half (of group j, where they have 32 values) of row i
+    auto scale = [&](int i, int j, int half) -> float {
+        if constexpr (block32(QT)) return f16_low(r[i].d[j]);
+        const int s = narrow ? 2 * j + half : j;
+        if constexpr (QT == GGUF_Q4_K) return byte_f(sc[i][s >> 2], s & 3, j & 1);        // its high nibbles are 16 times too large
+        const float v = byte_f(sc[i][s >> 2], s & 3);
+        return QT == GGUF_Q6_K ? v - 128.f : QT == GGUF_Q3_K ? v - 32.f : v;
+    };
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         if (block32(QT) && j >= nsub) break;
-        uint4 b[kTiles];
+        uint4 b[TILES];
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-            if (n < n_tiles) b[n] = *reinterpret_cast<const uint4*>(col + n * kTileBytes + j * 64);
-        float part[kTiles][4] = {};
+        for (int n = 0; n < TILES; ++n)
+            if (n < n_tiles) b[n] = col.values(n, j);
+        float part[TILES][4] = {};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             uint32_t a[4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t c = r[i].codes(j, half, t);
-                const __half2 even = as_h2((c & 0x00ff00ffu) | 0x64006400u), odd = as_h2(((c >> 8) & 0x00ff00ffu) | 0x64006400u);
-                if constexpr (int_scaled(QT)) {
-                    // (1024 + code) * scale - (1024 + zero point) * scale, one exact operation
-                    constexpr bool wide = QT == GGUF_Q4_K || QT == GGUF_Q5_K;
-                    const int s = wide ? j : 2 * j + half;
-                    constexpr int bias = QT == GGUF_Q3_K ? 1024 + 32 : 1024;
-                    const __half2 scale = __hsub2(byte_h2(sc[i][s >> 2], s & 3), __float2half2_rn((float)bias));
-                    // (1024 + 4) * scale leaves f16's exact integers for the 6-bit scales of Q3_K: its codes lose their 4 first
-                    if constexpr (QT == GGUF_Q3_K) {
-                        a[i] = as_u32(__hmul2(__hsub2(even, __float2half2_rn((float)Z)), scale));
-                        a[i + 2] = as_u32(__hmul2(__hsub2(odd, __float2half2_rn((float)Z)), scale));
+                if constexpr (QT == GGUF_Q4_K) {
+                    const uint32_t w = r[i].w[j >> 1][half], m = j & 1 ? 0x00f000f0u : 0x000f000fu;
+                    a[i] = w & m;
+                    a[i + 2] = (w >> 8) & m;
+                } else {
+                    const uint32_t c = r[i].codes(j, half, t);
+                    if constexpr (plain) {
+                        a[i] = __byte_perm(c, 0u, 0x4240);
+                        a[i + 2] = __byte_perm(c, 0u, 0x4341);
                     } else {
-                        const __half2 less = __hmul2(scale, __float2half2_rn(-1024.f));
-                        a[i] = as_u32(__hfma2(even, scale, less));
-                        a[i + 2] = as_u32(__hfma2(odd, scale, less));
+                        a[i] = as_u32(__hadd2(as_h2(__byte_perm(c, 0x64646464u, 0x4240)), zero));
+                        a[i + 2] = as_u32(__hadd2(as_h2(__byte_perm(c, 0x64646464u, 0x4341)), zero));
                     }
-                } else {
-                    a[i] = as_u32(__hsub2(even, __float2half2_rn((float)Z)));
-                    a[i + 2] = as_u32(__hsub2(odd, __float2half2_rn((float)Z)));
                 }
             }
+            if (narrow && half == 1) {
 #pragma unroll
-            for (int n = 0; n < kTiles; ++n) {
-                if (n >= n_tiles) continue;
-                const uint32_t b0 = half ? b[n].z : b[n].x, b1 = half ? b[n].w : b[n].y;
-                if constexpr (int_scaled(QT)) {
-                    mma(total[n], a, b0, b1);
-                } else if constexpr (QT == GGUF_Q6_K) {
-                    float one[4] = {};
-                    mma(one, a, b0, b1);
-                    const int s = 2 * j + half;
-                    const float s0 = (float)(int8_t)(r[0].sc[s >> 2] >> (8 * (s & 3))), s1 = (float)(int8_t)(r[1].sc[s >> 2] >> (8 * (s & 3)));
-                    total[n][0] = fmaf(one[0], s0, total[n][0]);
-                    total[n][1] = fmaf(one[1], s0, total[n][1]);
-                    total[n][2] = fmaf(one[2], s1, total[n][2]);
-                    total[n][3] = fmaf(one[3], s1, total[n][3]);
-                } else {
-                    mma(part[n], a, b0, b1);
-                }
+                for (int n = 0; n < TILES; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.f;
             }
-        }
-        if constexpr (block32(QT)) {
-            const float d0 = f16_low(r[0].d[j]), d1 = f16_low(r[1].d[j]);
 #pragma unroll
-            for (int n = 0; n < kTiles; ++n) {
-                total[n][0] = fmaf(part[n][0], d0, total[n][0]);
-                total[n][1] = fmaf(part[n][1], d0, total[n][1]);
-                total[n][2] = fmaf(part[n][2], d1, total[n][2]);
-                total[n][3] = fmaf(part[n][3], d1, total[n][3]);
+            for (int n = 0; n < TILES; ++n)
+                if (n < n_tiles) mma(part[n], a[0], a[1], a[2], a[3], half ? b[n].z : b[n].x, half ? b[n].w : b[n].y);
+            if (narrow || half == 1) {
+                const float s0 = scale(0, j, half), s1 = scale(1, j, half);
+#pragma unroll
+                for (int n = 0; n < TILES; ++n) {
+                    if (n >= n_tiles) continue;
+                    total[n][0] = fmaf(part[n][0], s0, total[n][0]);
+                    total[n][1] = fmaf(part[n][1], s0, total[n][1]);
+                    total[n][2] = fmaf(part[n][2], s1, total[n][2]);
+                    total[n][3] = fmaf(part[n][3], s1, total[n][3]);
+                }
             }
         }
     }
+    if constexpr (plain) d[0] *= 0x1p24f, d[1] *= 0x1p24f;
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
+    for (int n = 0; n < TILES; ++n) {
         if (n >= n_tiles) continue;
-        const uint8_t* tile = tiles + n * kTileBytes;
-        const float2 back = *reinterpret_cast<const float2*>(tile + 8 * kColStride + 8 * 64 + 8 * t);
+        const float2 back = col.back(n);
         if constexpr (has_min(QT)) {
-            // sums 2t, 2t + 1 of the first eight 16-value groups, then of the others
             float low[4] = {};
-            const uint8_t* sums = tile + 8 * kColStride + g * 64 + 4 * t;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                uint32_t a[4];
+                uint32_t a[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
+                    // mins are subnormals too, but those of the 32-value blocks, f16 numbers
                     if constexpr (QT == GGUF_Q2_K) {
-                        const uint32_t two = ((t < 2 ? mn[i][2 * k] : mn[i][2 * k + 1]) >> (16 * (t & 1))) & 0xffffu;
-                        a[i] = as_u32(__hsub2(as_h2((two & 0xffu) | (two & 0xff00u) << 8 | 0x64006400u), __float2half2_rn(1024.f)));
+                        const uint32_t two = (t < 2 ? mn[i][2 * k] : mn[i][2 * k + 1]) >> (16 * (t & 1));
+                        a[i] = (two & 0xffu) | (two & 0xff00u) << 8;
                     } else if constexpr (block32(QT)) {
                         // group 4k + t's m: no register is indexed by a lane
                         const uint32_t m = t < 2 ? (t ? r[i].d[4 * k + 1] : r[i].d[4 * k]) : (t == 2 ? r[i].d[4 * k + 2] : r[i].d[4 * k + 3]);
-                        const bool in = 4 * k + t < nsub;
-                        a[i] = in ? __byte_perm(m, 0u, 0x3232) : 0u;
+                        a[i] = 4 * k + t < nsub ? __byte_perm(m, 0u, 0x3232) : 0u;
                     } else {
-                        const uint32_t m = (mn[i][k] >> (8 * t)) & 0xffu;
-                        a[i] = as_u32(__hsub2(as_h2(m * 0x00010001u | 0x64006400u), __float2half2_rn(1024.f)));
+                        a[i] = ((mn[i][k] >> (8 * t)) & 0xffu) * 0x00010001u;
                     }
-                    a[i + 2] = a[i];        // with the sums' first part and their second
                 }
-                mma(low, a, *reinterpret_cast<const uint32_t*>(sums + 16 * k), *reinterpret_cast<const uint32_t*>(sums + 32 + 16 * k));
+                const uint2 s = col.sums(n, k);         // the same mins with the sums' first part and their second
+                mma(low, a[0], a[1], a[0], a[1], s.x, s.y);
             }
-            const float sign = block32(QT) ? 1.f : -1.f;    // Q4_1, Q5_1 add their m
-            total[n][0] = fmaf(sign * dmin[0], low[0], d[0] * total[n][0]);
-            total[n][1] = fmaf(sign * dmin[0], low[1], d[0] * total[n][1]);
-            total[n][2] = fmaf(sign * dmin[1], low[2], d[1] * total[n][2]);
-            total[n][3] = fmaf(sign * dmin[1], low[3], d[1] * total[n][3]);
-            acc[n][0] = fmaf(total[n][0], back.x, acc[n][0]);
-            acc[n][1] = fmaf(total[n][1], back.y, acc[n][1]);
-            acc[n][2] = fmaf(total[n][2], back.x, acc[n][2]);
-            acc[n][3] = fmaf(total[n][3], back.y, acc[n][3]);
+            // Q4_1, Q5_1 add their m
+            const float m0 = block32(QT) ? 1.f : -0x1p24f * dmin[0], m1 = block32(QT) ? 1.f : -0x1p24f * dmin[1];
+            acc[n][0] = fmaf(fmaf(m0, low[0], d[0] * total[n][0]), back.x, acc[n][0]);
+            acc[n][1] = fmaf(fmaf(m0, low[1], d[0] * total[n][1]), back.y, acc[n][1]);
+            acc[n][2] = fmaf(fmaf(m1, low[2], d[1] * total[n][2]), back.x, acc[n][2]);
+            acc[n][3] = fmaf(fmaf(m1, low[3], d[1] * total[n][3]), back.y, acc[n][3]);
         } else {
             acc[n][0] = fmaf(d[0] * total[n][0], back.x, acc[n][0]);
             acc[n][1] = fmaf(d[0] * total[n][1], back.y, acc[n][1]);
@@ -470,15 +486,6 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const uint8_t* t
             acc[n][3] = fmaf(d[1] * total[n][3], back.y, acc[n][3]);
         }
     }
-}
-
-// The rows at and after `n` of a matrix's last 16 stand for its last row (their results are dropped).
-template <int QT>
-__device__ __forceinline__ void load_rows(Raw<QT> (&r)[2], const uint8_t* w, int64_t row0, int64_t n, int64_t rb, int64_t c, int nsub,
-                                          int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    r[0].load(w + min(row0 + g, n - 1) * rb, c, nsub, t);
-    r[1].load(w + min(row0 + g + 8, n - 1) * rb, c, nsub, t);
 }
 
 // f(QT) for a type known at run time only
@@ -498,6 +505,62 @@ __device__ __forceinline__ void with_type(int qt, F&& f) {
     }
 }
 
+// ---------------------------------------------------------------- the weights' ring
+
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the last n groups of this thread's copies have arrived
+__device__ __forceinline__ void copies_wait(int n) {
+    if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
+
+// A matrix of one expert, as rows of pieces.  The rows at and after n of its last 16 stand for its last row (their results
+// are dropped).
+struct Matrix {
+    const uint8_t* w;
+    const uint8_t* end;             // of all experts' bytes: nothing is read past it
+    int64_t rb;                     // bytes of a row
+    int n;                          // rows
+};
+
+// Two lanes to a row, every other 16 bytes each.
+template <int QT>
+__device__ __forceinline__ void fetch_piece(uint32_t slot, const Matrix& m, int row0, int c, int lane) {
+    const int row = lane >> 1, half = lane & 1;
+    const uint8_t* src = m.w + (int64_t)min(row0 + row, m.n - 1) * m.rb + (int64_t)c * piece_bytes(QT) + 16 * half;
+    const uint32_t dst = slot + row * piece_stride(QT) + 16 * half;
+    if constexpr (piece_aligned(QT)) {
+#pragma unroll
+        for (int i = 0; i < piece_stride(QT) / 16; i += 2)
+            if (i + 1 < piece_stride(QT) / 16 || half == 0) copy16(dst + 16 * i, src + 16 * i, 16);
+    } else {
+        const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);
+        src -= off;
+        // bytes from the boundary on: the piece's, fewer at the end of a row of 32-value blocks
+        const int len = off + (int)min((int64_t)piece_bytes(QT), m.rb - (int64_t)c * piece_bytes(QT)) - 16 * half;
+        const int64_t left = m.end - src;
+#pragma unroll
+        for (int i = 0; i < piece_stride(QT) / 16; i += 2)
+            if (16 * i < len) copy16(dst + 16 * i, src + 16 * i, (int)min((int64_t)16, left - 16 * i));
+    }
+}
+
+template <int QT>
+__device__ __forceinline__ void read_piece(Raw<QT> (&r)[2], const uint8_t* slot, const Matrix& m, int row0, int c, int nsub, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int off = 0;
+        if constexpr (!piece_aligned(QT))
+            off = (int)(reinterpret_cast<uintptr_t>(m.w) + (uint32_t)min(row0 + g + 8 * i, m.n - 1) * (uint32_t)m.rb + (uint32_t)c * piece_bytes(QT)) & 15;
+        r[i].load(slot + (g + 8 * i) * piece_stride(QT) + off, nsub, t);
+    }
+}
+
 __device__ __forceinline__ float activate(float a, int act) {
     if (act == GGUF_ACT_SILU) return a / (1.f + expf(-a));
     // tanh form: 0.79788... = sqrt(2 / pi)
@@ -506,233 +569,363 @@ __device__ __forceinline__ float activate(float a, int act) {
 
 // ---------------------------------------------------------------- gate, up, activation
 
-// Block (x, y): rows 16 x .. of gate and up, of the y-th expert that has rows.
-// Its warps take the chunks of K in turn; their sums meet in shared memory.
+// A job is `rt` tiles of 16 rows of gate and up, for one group; a block takes a
+// run of jobs, so that it makes a group's columns once for many of them.  Of its warps, wp =
+// 8 / rt share a tile of one matrix, each taking every wp-th chunk of K; their
+// sums meet in shared memory.
 // QT: both matrices' type, or -1 where they differ.
-template <int QT>
-__global__ void __launch_bounds__(32 * kUpWarps, QT < 0 ? 2 : 3) moe_ffn_up_kernel(const MoeFfnParams p) {
-    extern __shared__ __align__(16) uint8_t s_tiles[];      // a warp's tiles, then its sums
-    __shared__ Routes s_routes;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_wait();
-    make_routes(s_routes, p.ids, p.T * p.top_k, p.n_expert, tid, 32 * kUpWarps);
-    if ((int)blockIdx.y >= s_routes.n_active) return;
-    const int e = s_routes.active[blockIdx.y], first = s_routes.start[e], rows = s_routes.start[e + 1] - first;
-    const int64_t row0 = 16 * (int64_t)blockIdx.x;
-    const uint8_t* gate = p.gate + e * p.F * p.gate_rb;
-    const uint8_t* up = p.up + e * p.F * p.up_rb;
-    const int parts = p.x_parts, chunks = (int)ceil_div(p.K, kChunk);
-    const int at_once = 8 * p.tiles / parts;                // rows
-    uint8_t* tiles = s_tiles + warp * p.tiles * kTileBytes;
-    float* sums = reinterpret_cast<float*>(s_tiles);        // [warp][matrix][16 rows][16 columns]
-    for (int r0 = 0; r0 < rows; r0 += at_once) {
-        const int n = min(at_once, rows - r0), n_tiles = (n * parts + 7) >> 3;
-        float a[2][kTiles][4] = {};
-        for (int c = warp; c < chunks; c += kUpWarps) {
-            const int nsub = (int)min((int64_t)8, (p.K - (int64_t)c * kChunk) / 32);
-            auto stage = [&] {
-                __syncwarp();
-                for (int i = 0; i < n; ++i) {
-                    const int token = s_routes.list[first + r0 + i] / p.top_k;
-                    stage_row(tiles, i * parts, parts, p.x, p.xdt, token * p.K + (int64_t)c * kChunk, nsub, lane);
-                }
-                __syncwarp();
-            };
-            if constexpr (QT >= 0) {
-                Raw<QT> rg[2], ru[2];
-                load_rows<QT>(rg, gate, row0, p.F, p.gate_rb, c, nsub, lane);
-                load_rows<QT>(ru, up, row0, p.F, p.up_rb, c, nsub, lane);
-                stage();
-                multiply<QT>(rg, tiles, n_tiles, nsub, lane, a[0]);
-                multiply<QT>(ru, tiles, n_tiles, nsub, lane, a[1]);
-            } else {
-                stage();
-                with_type(p.gate_type, [&](auto q) {
-                    Raw<decltype(q)::value> r[2];
-                    load_rows<decltype(q)::value>(r, gate, row0, p.F, p.gate_rb, c, nsub, lane);
-                    multiply<decltype(q)::value>(r, tiles, n_tiles, nsub, lane, a[0]);
-                });
-                with_type(p.up_type, [&](auto q) {
-                    Raw<decltype(q)::value> r[2];
-                    load_rows<decltype(q)::value>(r, up, row0, p.F, p.up_rb, c, nsub, lane);
-                    multiply<decltype(q)::value>(r, tiles, n_tiles, nsub, lane, a[1]);
-                });
-            }
-        }
-        __syncthreads();            // the tiles are read
-        const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int k = 0; k < kTiles; ++k) {
-                if (k >= n_tiles) continue;
-                float* to = sums + ((warp * 2 + m) * 16) * 16 + k * 8 + 2 * t;
-                *reinterpret_cast<float2*>(to + g * 16) = make_float2(a[m][k][0], a[m][k][1]);
-                *reinterpret_cast<float2*>(to + (g + 8) * 16) = make_float2(a[m][k][2], a[m][k][3]);
-            }
-        __syncthreads();
-        for (int i = tid; i < n * 16; i += 32 * kUpWarps) {
-            const int r = i & 15, k = i >> 4;
-            if (row0 + r >= p.F) continue;
-            float v[2] = {0.f, 0.f};
-#pragma unroll
-            for (int w = 0; w < kUpWarps; ++w)
-                for (int q = 0; q < parts; ++q) {
-                    const float* from = sums + (w * 2 * 16 + r) * 16 + k * parts + q;
-                    v[0] += from[0];
-                    v[1] += from[16 * 16];
-                }
-            p.h[(int64_t)s_routes.list[first + r0 + k] * p.F + row0 + r] = activate(v[0], p.act) * v[1];
-        }
-        __syncthreads();
+struct ColumnsInShared {
+    const uint8_t* at;              // the chunk's tiles, at this lane's column and 16 bytes
+    const float* scales;            // the chunk's, at 2t
+    int t;
+    __device__ __forceinline__ uint4 values(int n, int j) const { return *reinterpret_cast<const uint4*>(at + n * kTileBytes + j * 64); }
+    __device__ __forceinline__ uint2 sums(int n, int k) const {
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(at + n * kTileBytes + 2 * kChunk - 16 * t);
+        return make_uint2(s[4 * k + t], s[8 + 4 * k + t]);
     }
+    __device__ __forceinline__ float2 back(int n) const { return *reinterpret_cast<const float2*>(scales + 8 * n); }
+};
+
+template <int QT>
+__global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnParams p) {
+    extern __shared__ __align__(16) uint8_t s_dyn[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int entries = p.T * p.top_k, tiles = p.up_tiles, chunks = (int)ceil_div(p.K, kChunk), parts = p.x_parts;
+    const Routes routes(s_dyn, entries, p.n_expert);
+    // a group's columns: of all chunks, or, where K is too long, of the one that each warp is at
+    const int held = p.up_resident ? chunks : kWarps;
+    uint8_t* const columns = s_dyn + Routes::bytes(entries, p.n_expert);                    // [held][tile]
+    float* const scales = reinterpret_cast<float*>(columns + (size_t)held * tiles * kTileBytes);        // [held][8 * tiles]
+    float* const sums = scales + held * 8 * tiles;                                          // [2][warp][16 rows][8 * tiles]
+    uint8_t* const ring = reinterpret_cast<uint8_t*>(sums + 2 * kWarps * 128 * tiles) + (size_t)warp * p.up_stages * p.up_slot;
+    const uint32_t ring_at = smem_u32(ring);
+    pdl_wait();
+    pdl_launch_dependents();        // all blocks of this kernel are running
+    const int groups = make_routes(routes, p.ids, entries, p.n_expert, 8 * tiles / parts, tid);
+    const int rt = p.up_rt, wp = 8 / rt;
+    const int64_t per_group = ceil_div(p.F, 16 * rt), jobs = per_group * groups;
+    const int64_t job0 = jobs * blockIdx.x / gridDim.x, job1 = jobs * (blockIdx.x + 1) / gridDim.x;
+    // this warp's part of a job
+    const int my_tile = warp / (2 * wp), mat = (warp / wp) & 1, c0 = warp % wp;
+    const int qt = mat ? p.up_type : p.gate_type;
+    auto place = [&](int64_t job, Matrix& m, int& row0) {
+        const int e = routes.group[job / per_group].expert;
+        const uint8_t* w = mat ? p.up : p.gate;
+        m.rb = mat ? p.up_rb : p.gate_rb;
+        m.n = (int)p.F;
+        m.w = w + e * p.F * m.rb;
+        m.end = w + p.n_expert * p.F * m.rb;
+        row0 = ((int)(job % per_group) * rt + my_tile) * 16;
+    };
+    // the ring's next piece to fetch
+    int64_t fjob = job0;
+    int fc = c0, fslot = 0, slot = 0;
+    Matrix fm{};
+    int frow = 0;
+    if (fjob < job1) place(fjob, fm, frow);
+    auto fetch = [&] {
+        if (fjob < job1 && fc < chunks) {
+            if constexpr (QT >= 0) fetch_piece<QT>(ring_at + fslot * p.up_slot, fm, frow, fc, lane);
+            else with_type(qt, [&](auto q) { fetch_piece<decltype(q)::value>(ring_at + fslot * p.up_slot, fm, frow, fc, lane); });
+            fslot = fslot + 1 == p.up_stages ? 0 : fslot + 1;
+            fc += wp;
+            if (fc >= chunks && ++fjob < job1) fc = c0, place(fjob, fm, frow);
+        }
+        copies_commit();
+    };
+    for (int i = 0; i < p.up_stages; ++i) fetch();
+
+    int made = -1, buffer = 0;
+    Group g{};
+    auto make = [&](int k, int c, int at) {         // the columns of the group's row k, chunk c
+        const int col = k * parts, token = routes.list[g.first + k] / p.top_k;
+        const int nsub = (int)min((int64_t)8, (p.K - (int64_t)c * kChunk) / 32);
+        const float back = make_column(columns + (size_t)(at * tiles * 8 + col) * kColStride, parts, p.x, p.xdt,
+                                       token * p.K + (int64_t)c * kChunk, nsub, lane);
+        if (lane < parts) scales[at * 8 * tiles + col + lane] = back;
+    };
+    for (int64_t job = job0; job < job1; ++job, buffer ^= 1) {
+        if ((int)(job / per_group) != made) {
+            made = (int)(job / per_group);
+            g = routes.group[made];
+            // every warp has passed the barrier of the job before, so nothing reads the old columns
+            if (p.up_resident)
+                for (int i = warp; i < g.n * chunks; i += kWarps) make(i % g.n, i / g.n, i / g.n);
+            __syncthreads();
+        }
+        const int n_tiles = (g.n * parts + 7) >> 3;
+        Matrix m;
+        int row0;
+        place(job, m, row0);
+        float acc[kTiles][4] = {};
+        for (int c = c0; c < chunks; c += wp) {
+            const int at = p.up_resident ? c : warp;
+            if (!p.up_resident)
+                for (int k = 0; k < g.n; ++k) make(k, c, at);
+            copies_wait(p.up_stages - 1);
+            __syncwarp();
+            const int nsub = (int)min((int64_t)8, (p.K - (int64_t)c * kChunk) / 32), t = lane & 3;
+            const ColumnsInShared col{columns + (size_t)at * tiles * kTileBytes + (lane >> 2) * kColStride + t * 16, scales + at * 8 * tiles + 2 * t, t};
+            auto unit = [&](auto q) {
+                constexpr int Q = decltype(q)::value;
+                Raw<Q> r[2];
+                read_piece<Q>(r, ring + slot * p.up_slot, m, row0, c, nsub, lane);
+                __syncwarp();       // the piece is read: its place may be filled
+                fetch();
+                multiply<Q, kTiles>(r, col, n_tiles, nsub, lane, acc);
+            };
+            if constexpr (QT >= 0) unit(std::integral_constant<int, QT>{});
+            else with_type(qt, unit);
+            slot = slot + 1 == p.up_stages ? 0 : slot + 1;
+            if (!p.up_resident) __syncwarp();       // the columns are read
+        }
+        float* const to = sums + (size_t)(buffer * kWarps + warp) * 128 * tiles;
+#pragma unroll
+        for (int k = 0; k < kTiles; ++k) {
+            if (k >= n_tiles) continue;
+            float* at = to + (lane >> 2) * 8 * tiles + 8 * k + 2 * (lane & 3);
+            *reinterpret_cast<float2*>(at) = make_float2(acc[k][0], acc[k][1]);
+            *reinterpret_cast<float2*>(at + 64 * tiles) = make_float2(acc[k][2], acc[k][3]);
+        }
+        __syncthreads();
+        // the sums of two jobs have places of their own, so the warps go on meanwhile
+        const int used = min(wp, chunks);
+        for (int i = tid; i < rt * g.n * 16; i += kThreads) {
+            const int r = i & 15, k = (i >> 4) % g.n, tile = (i >> 4) / g.n;
+            const int64_t row = (job % per_group * rt + tile) * 16 + r;
+            if (row >= p.F) continue;
+            float v[2] = {0.f, 0.f};
+            const float* from = sums + (size_t)(buffer * kWarps + tile * 2 * wp) * 128 * tiles + r * 8 * tiles + k * parts;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                for (int w = 0; w < used; ++w) {
+                    const float* f = from + (size_t)(q * wp + w) * 128 * tiles;
+                    v[q] += parts == 2 ? f[0] + f[1] : f[0];
+                }
+            p.h[(int64_t)routes.list[g.first + k] * p.F + row] = activate(v[0], p.act) * v[1];
+        }
+    }
+}
+
+// ---------------------------------------------------------------- the hidden values as columns
+
+// A warp a column: [entry][chunk][part] of kColStride bytes, and what its products are multiplied by [entry][chunk].
+__global__ void __launch_bounds__(256) moe_ffn_columns_kernel(const MoeFfnParams p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, chunks = (int)ceil_div(p.F, kChunk);
+    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (i >= (int64_t)p.T * p.top_k * chunks) return;
+    const int64_t entry = i / chunks, c = i % chunks;
+    const int nsub = (int)min((int64_t)8, (p.F - c * kChunk) / 32);
+    const float back = make_column(p.columns + i * p.h_parts * kColStride, p.h_parts, p.h, GGUF_DT_F32, entry * p.F + c * kChunk, nsub, lane);
+    if (lane == 0) p.column_scales[i] = back;
 }
 
 // ---------------------------------------------------------------- down, weights, residual
 
-// Block x: rows 16 x .. of down, every expert's.  `splits` warps share an
-// expert's chunks of F; each routed row's sums of each of them have their own
-// place in shared memory and are added up in one order.
+// Block x: rows 16 x .. of down, every group's.  `splits` warps share a group's
+// chunks of F; each routed row's sums of each of them have their own place in
+// shared memory and are added up in one order.
+struct ColumnsInRegisters {
+    uint4 v[8];
+    uint2 s[2];
+    float2 f;
+    __device__ __forceinline__ uint4 values(int, int j) const { return v[j]; }
+    __device__ __forceinline__ uint2 sums(int, int k) const { return s[k]; }
+    __device__ __forceinline__ float2 back(int) const { return f; }
+};
+
 template <int QT>
-__global__ void __launch_bounds__(32 * kDownWarps, 1) moe_ffn_down_kernel(const MoeFfnParams p) {
-    extern __shared__ __align__(16) uint8_t s_dyn[];        // warps' tiles, then the rows' sums [split][entry][16]
-    __shared__ Routes s_routes;
+__global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnParams p) {
+    extern __shared__ __align__(16) uint8_t s_dyn[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int entries = p.T * p.top_k, parts = p.h_parts, splits = p.splits;
-    float* sums = reinterpret_cast<float*>(s_dyn + p.down_warps * p.tiles * kTileBytes);
-    uint8_t* tiles = s_dyn + warp * p.tiles * kTileBytes;
+    const Routes routes(s_dyn, entries, p.n_expert);
+    float* const sums = reinterpret_cast<float*>(s_dyn + Routes::bytes(entries, p.n_expert));       // [split][entry][16]
+    constexpr int kSlot = 16 * piece_stride(QT);
+    uint8_t* const ring = reinterpret_cast<uint8_t*>(sums + (size_t)splits * entries * 16) + (size_t)warp * p.down_stages * kSlot;
+    const uint32_t ring_at = smem_u32(ring);
+    // The kernel before this one began when the one before that had ended, so the ids are there; the columns are
+    // waited for once the first weights are on their way.
+    const int items = make_routes(routes, p.ids, entries, p.n_expert, 8 / parts, tid) * splits;
+    const int row0 = 16 * blockIdx.x, chunks = (int)ceil_div(p.F, kChunk);
+    auto place = [&](int item, Matrix& m) {
+        m.rb = p.down_rb;
+        m.n = (int)p.K;
+        m.w = p.down + routes.group[item / splits].expert * p.K * p.down_rb;
+        m.end = p.down + p.n_expert * p.K * p.down_rb;
+    };
+    int fitem = warp, fc = warp % splits, fslot = 0, slot = 0;
+    Matrix fm{};
+    if (fitem < items) place(fitem, fm);
+    auto fetch = [&] {
+        if (fitem < items) {
+            fetch_piece<QT>(ring_at + fslot * kSlot, fm, row0, fc, lane);
+            fslot = fslot + 1 == p.down_stages ? 0 : fslot + 1;
+            fc += splits;
+            if (fc >= chunks && (fitem += kWarps) < items) fc = fitem % splits, place(fitem, fm);
+        }
+        copies_commit();
+    };
+    for (int i = 0; i < p.down_stages; ++i) fetch();
     pdl_wait();
-    make_routes(s_routes, p.ids, entries, p.n_expert, tid, 32 * p.down_warps);
-    const int64_t row0 = 16 * (int64_t)blockIdx.x;
-    const int chunks = (int)ceil_div(p.F, kChunk), at_once = 8 * p.tiles / parts;
-    const int items = s_routes.n_active * splits;
-    for (int item = warp; item < items; item += p.down_warps) {
-        const int e = s_routes.active[item / splits], split = item % splits;
-        const int first = s_routes.start[e], rows = s_routes.start[e + 1] - first;
-        const uint8_t* down = p.down + e * p.K * p.down_rb;
-        for (int r0 = 0; r0 < rows; r0 += at_once) {
-            const int n = min(at_once, rows - r0), n_tiles = (n * parts + 7) >> 3;
-            float a[kTiles][4] = {};
-            for (int c = split; c < chunks; c += splits) {
-                const int nsub = (int)min((int64_t)8, (p.F - (int64_t)c * kChunk) / 32);
-                Raw<QT> r[2];
-                load_rows<QT>(r, down, row0, p.K, p.down_rb, c, nsub, lane);
-                __syncwarp();
-                for (int i = 0; i < n; ++i)
-                    stage_row(tiles, i * parts, parts, p.h, GGUF_DT_F32,
-                              (int64_t)s_routes.list[first + r0 + i] * p.F + (int64_t)c * kChunk, nsub, lane);
-                __syncwarp();
-                multiply<QT>(r, tiles, n_tiles, nsub, lane, a);
+    const int g = lane >> 2, t = lane & 3;
+    for (int item = warp; item < items; item += kWarps) {
+        const Group group = routes.group[item / splits];
+        Matrix m;
+        place(item, m);
+        float acc[1][4] = {};
+        // this lane's column, and columns 2t, 2t + 1, of the group's rows
+        auto entry_of = [&](int col) { return (int64_t)routes.list[group.first + min(col / parts, group.n - 1)]; };
+        const int64_t mine = entry_of(g) * chunks, first = entry_of(2 * t) * chunks, second = entry_of(2 * t + 1) * chunks;
+        for (int c = item % splits; c < chunks; c += splits) {
+            ColumnsInRegisters col;
+            const uint8_t* at = p.columns + ((mine + c) * parts + g % parts) * kColStride;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) col.v[j] = __ldg(reinterpret_cast<const uint4*>(at + j * 64 + t * 16));
+            if constexpr (has_min(QT)) {
+                const uint32_t* s = reinterpret_cast<const uint32_t*>(at + 2 * kChunk);
+                col.s[0] = make_uint2(__ldg(s + t), __ldg(s + 8 + t)), col.s[1] = make_uint2(__ldg(s + 4 + t), __ldg(s + 12 + t));
             }
-            const int g = lane >> 2, t = lane & 3;
+            col.f = make_float2(__ldg(p.column_scales + first + c), __ldg(p.column_scales + second + c));
+            copies_wait(p.down_stages - 1);
+            __syncwarp();
+            const int nsub = (int)min((int64_t)8, (p.F - (int64_t)c * kChunk) / 32);
+            Raw<QT> r[2];
+            read_piece<QT>(r, ring + slot * kSlot, m, row0, c, nsub, lane);
+            slot = slot + 1 == p.down_stages ? 0 : slot + 1;
+            __syncwarp();           // the piece is read: its place may be filled
+            fetch();
+            multiply<QT, 1>(r, col, 1, nsub, lane, acc);
+        }
+        // columns 2t, 2t + 1: the two parts of one row, or two rows
+        float* const to = sums + (size_t)(item % splits) * entries * 16;
+        if (parts == 2) {
+            if (t < group.n) {
+                float* at = to + routes.list[group.first + t] * 16;
+                at[g] = acc[0][0] + acc[0][1];
+                at[g + 8] = acc[0][2] + acc[0][3];
+            }
+        } else {
 #pragma unroll
-            for (int k = 0; k < kTiles; ++k) {
-                if (k >= n_tiles) continue;
-                // columns 2t, 2t + 1: the two parts of one row, or two rows
-                const int col = 8 * k + 2 * t;
-                if (parts == 2) {
-                    if (col / 2 < n) {
-                        float* to = sums + ((int64_t)split * entries + s_routes.list[first + r0 + col / 2]) * 16;
-                        to[g] = a[k][0] + a[k][1];
-                        to[g + 8] = a[k][2] + a[k][3];
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        if (col + q < n) {
-                            float* to = sums + ((int64_t)split * entries + s_routes.list[first + r0 + col + q]) * 16;
-                            to[g] = a[k][q];
-                            to[g + 8] = a[k][q + 2];
-                        }
+            for (int q = 0; q < 2; ++q)
+                if (2 * t + q < group.n) {
+                    float* at = to + routes.list[group.first + 2 * t + q] * 16;
+                    at[g] = acc[0][q];
+                    at[g + 8] = acc[0][q + 2];
                 }
-            }
         }
     }
     __syncthreads();
-    for (int i = tid; i < p.T * 16; i += 32 * p.down_warps) {
-        const int r = i & 15, t = i >> 4;
+    for (int i = tid; i < p.T * 16; i += kThreads) {
+        const int r = i & 15, token = i >> 4;
         if (row0 + r >= p.K) continue;
-        const int64_t o = t * p.K + row0 + r;
+        const int64_t o = token * p.K + row0 + r;
         float v = p.residual ? load_act(p.residual, p.ydt, o) : 0.f;
         for (int s = 0; s < p.top_k; ++s) {
-            const int at = t * p.top_k + s;
+            const int at = token * p.top_k + s;
             if ((unsigned)p.ids[at] >= (unsigned)p.n_expert) continue;
             float row = 0.f;
-            for (int q = 0; q < splits; ++q) row += sums[((int64_t)q * entries + at) * 16 + r];
+            for (int q = 0; q < splits; ++q) row += sums[((size_t)q * entries + at) * 16 + r];
             v = fmaf(p.weights[at], row, v);
         }
         store_out(p.y, p.ydt, o, v);
     }
 }
 
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA; }
+
 template <int QT>
-int launch_up(const MoeFfnParams& p, int pdl, cudaStream_t s) {
+int launch_up(const MoeFfnParams& p, int blocks, size_t smem, int pdl, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    // a warp's tiles, or the warps' sums
-    const size_t smem = std::max<size_t>((size_t)kUpWarps * p.tiles * kTileBytes, kUpWarps * 2 * 256 * sizeof(float));
-    if (set_once(moe_ffn_up_kernel<QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUpWarps * kTiles * kTileBytes, done) != cudaSuccess)
-        return GGUF_ERR_CUDA;
-    const dim3 grid((unsigned)ceil_div(p.F, 16), (unsigned)std::min(p.T * p.top_k, p.n_expert));
-    return launch_pdl(moe_ffn_up_kernel<QT>, grid, dim3(32 * kUpWarps), smem, s, pdl, p) == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
+    if (set_once(moe_ffn_up_kernel<QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem, done) != cudaSuccess) return GGUF_ERR_CUDA;
+    return cuda_status(launch_pdl(moe_ffn_up_kernel<QT>, dim3((unsigned)blocks), dim3(kThreads), smem, s, pdl, p));
 }
 
 template <int QT>
-int launch_down(const MoeFfnParams& p, int pdl, cudaStream_t s) {
+int launch_down(const MoeFfnParams& p, size_t smem, int pdl, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    if (set_once(moe_ffn_down_kernel<QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDownSmem, done) != cudaSuccess)
-        return GGUF_ERR_CUDA;
-    const size_t smem = (size_t)p.down_warps * p.tiles * kTileBytes + (size_t)p.splits * p.T * p.top_k * 16 * sizeof(float);
-    const cudaError_t e = launch_pdl(moe_ffn_down_kernel<QT>, dim3((unsigned)ceil_div(p.K, 16)), dim3(32 * p.down_warps), smem, s, pdl, p);
-    return e == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA;
+    if (set_once(moe_ffn_down_kernel<QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem, done) != cudaSuccess) return GGUF_ERR_CUDA;
+    return cuda_status(launch_pdl(moe_ffn_down_kernel<QT>, dim3((unsigned)ceil_div(p.K, 16)), dim3(kThreads), smem, s, pdl, p));
 }
 
-int dispatch_up(int qt, const MoeFfnParams& p, int pdl, cudaStream_t s) {
+int dispatch_up(int qt, const MoeFfnParams& p, int blocks, size_t smem, int pdl, cudaStream_t s) {
     switch (qt) {
-        case GGUF_Q4_0: return launch_up<GGUF_Q4_0>(p, pdl, s);
-        case GGUF_Q4_1: return launch_up<GGUF_Q4_1>(p, pdl, s);
-        case GGUF_Q5_0: return launch_up<GGUF_Q5_0>(p, pdl, s);
-        case GGUF_Q5_1: return launch_up<GGUF_Q5_1>(p, pdl, s);
-        case GGUF_Q8_0: return launch_up<GGUF_Q8_0>(p, pdl, s);
-        case GGUF_Q2_K: return launch_up<GGUF_Q2_K>(p, pdl, s);
-        case GGUF_Q3_K: return launch_up<GGUF_Q3_K>(p, pdl, s);
-        case GGUF_Q4_K: return launch_up<GGUF_Q4_K>(p, pdl, s);
-        case GGUF_Q5_K: return launch_up<GGUF_Q5_K>(p, pdl, s);
-        case GGUF_Q6_K: return launch_up<GGUF_Q6_K>(p, pdl, s);
-        default: return launch_up<-1>(p, pdl, s);
+#define GG_CASE(Q) case Q: return launch_up<Q>(p, blocks, smem, pdl, s);
+        GG_CASE(GGUF_Q4_0) GG_CASE(GGUF_Q4_1) GG_CASE(GGUF_Q5_0) GG_CASE(GGUF_Q5_1) GG_CASE(GGUF_Q8_0)
+        GG_CASE(GGUF_Q2_K) GG_CASE(GGUF_Q3_K) GG_CASE(GGUF_Q4_K) GG_CASE(GGUF_Q5_K) GG_CASE(GGUF_Q6_K)
+#undef GG_CASE
+        default: return launch_up<-1>(p, blocks, smem, pdl, s);
     }
 }
 
-int dispatch_down(int qt, const MoeFfnParams& p, int pdl, cudaStream_t s) {
-    switch (qt) {
-        case GGUF_Q4_0: return launch_down<GGUF_Q4_0>(p, pdl, s);
-        case GGUF_Q4_1: return launch_down<GGUF_Q4_1>(p, pdl, s);
-        case GGUF_Q5_0: return launch_down<GGUF_Q5_0>(p, pdl, s);
-        case GGUF_Q5_1: return launch_down<GGUF_Q5_1>(p, pdl, s);
-        case GGUF_Q8_0: return launch_down<GGUF_Q8_0>(p, pdl, s);
-        case GGUF_Q2_K: return launch_down<GGUF_Q2_K>(p, pdl, s);
-        case GGUF_Q3_K: return launch_down<GGUF_Q3_K>(p, pdl, s);
-        case GGUF_Q4_K: return launch_down<GGUF_Q4_K>(p, pdl, s);
-        case GGUF_Q5_K: return launch_down<GGUF_Q5_K>(p, pdl, s);
-        default: return launch_down<GGUF_Q6_K>(p, pdl, s);
+int dispatch_down(const MoeFfnParams& p, size_t smem, int pdl, cudaStream_t s) {
+    switch (p.down_type) {
+#define GG_CASE(Q) case Q: return launch_down<Q>(p, smem, pdl, s);
+        GG_CASE(GGUF_Q4_0) GG_CASE(GGUF_Q4_1) GG_CASE(GGUF_Q5_0) GG_CASE(GGUF_Q5_1) GG_CASE(GGUF_Q8_0)
+        GG_CASE(GGUF_Q2_K) GG_CASE(GGUF_Q3_K) GG_CASE(GGUF_Q4_K) GG_CASE(GGUF_Q5_K)
+#undef GG_CASE
+        default: return launch_down<GGUF_Q6_K>(p, smem, pdl, s);
     }
 }
+
+int slot_bytes(int qt) {
+    switch (qt) {
+#define GG_CASE(Q) case Q: return 16 * piece_stride(Q);
+        GG_CASE(GGUF_Q4_0) GG_CASE(GGUF_Q4_1) GG_CASE(GGUF_Q5_0) GG_CASE(GGUF_Q5_1) GG_CASE(GGUF_Q8_0)
+        GG_CASE(GGUF_Q2_K) GG_CASE(GGUF_Q3_K) GG_CASE(GGUF_Q4_K) GG_CASE(GGUF_Q5_K)
+#undef GG_CASE
+        default: return 16 * piece_stride(GGUF_Q6_K);
+    }
+}
+
+// hidden values, their columns, the columns' scales
+size_t hidden_bytes(int64_t entries, int64_t F) { return (size_t)ceil_div(entries * F * 4, 256) * 256; }
+size_t column_bytes(int64_t entries, int64_t F) { return (size_t)(entries * ceil_div(F, kChunk) * 2 * kColStride); }
 
 }  // namespace
 
-int moe_ffn_launch(MoeFfnParams p, int pdl, cudaStream_t s) {
+size_t moe_ffn_workspace_bytes(int64_t F, int64_t T, int64_t top_k) {
+    const int64_t entries = T * top_k;
+    return hidden_bytes(entries, F) + column_bytes(entries, F) + (size_t)(entries * ceil_div(F, kChunk) * 4);
+}
+
+int moe_ffn_launch(MoeFfnParams p, void* workspace, int num_sms, int pdl, cudaStream_t s) {
+    const int entries = p.T * p.top_k;
+    p.h = static_cast<float*>(workspace);
+    p.columns = static_cast<uint8_t*>(workspace) + hidden_bytes(entries, p.F);
+    p.column_scales = reinterpret_cast<float*>(p.columns + column_bytes(entries, p.F));
     p.x_parts = p.xdt == GGUF_DT_F32 ? 2 : 1;           // the 16-bit types' values are f16 numbers, scaled
     // the hidden values' rounding to f16 is below what a bf16 output rounds, and would not be below an f16 output's
     p.h_parts = p.ydt == GGUF_DT_BF16 ? 1 : 2;
-    p.tiles = p.T * p.x_parts <= 8 ? 1 : kTiles;
-    int st = dispatch_up(p.gate_type == p.up_type ? p.gate_type : -1, p, pdl, s);
+    const size_t routes = Routes::bytes(entries, p.n_expert);
+
+    // up: two tiles of columns where a group may need them and there is room for two pieces to a warp beside them
+    const int64_t chunks = ceil_div(p.K, kChunk);
+    p.up_slot = std::max(slot_bytes(p.gate_type), slot_bytes(p.up_type));
+    auto fixed = [&](int64_t held, int tiles) { return routes + (size_t)(held * tiles * (kTileBytes + 32) + 2 * kWarps * 128 * tiles * 4); };
+    auto stages = [&](size_t used, size_t slot) { return used > kSmem ? 0 : (int)std::min<size_t>(kMaxStages, (kSmem - used) / (kWarps * slot)); };
+    p.up_tiles = p.T * p.x_parts > 8 && stages(fixed(chunks, 2), p.up_slot) >= 2 ? 2 : 1;
+    p.up_resident = stages(fixed(chunks, p.up_tiles), p.up_slot) >= 1;
+    const size_t up_fixed = fixed(p.up_resident ? chunks : kWarps, p.up_tiles);
+    p.up_stages = stages(up_fixed, p.up_slot);
+    p.up_rt = chunks >= 8 ? 1 : chunks >= 4 ? 2 : chunks >= 2 ? 4 : 8;
+    const int64_t most = ceil_div(p.F, 16 * p.up_rt) * entries;
+    int st = dispatch_up(p.gate_type == p.up_type ? p.gate_type : -1, p, (int)std::min<int64_t>(num_sms, most),
+                         up_fixed + (size_t)kWarps * p.up_stages * p.up_slot, pdl, s);
     if (st != GGUF_OK) return st;
-    p.tiles = p.T * p.h_parts <= 8 ? 1 : kTiles;
-    p.down_warps = p.tiles == 1 ? kDownWarps : 16;
-    // with few experts, several warps share one's chunks, as far as there is room for their sums
-    const int64_t entries = p.T * p.top_k, experts = std::min<int64_t>(entries, p.n_expert);
-    const int64_t room = (kDownSmem - (size_t)p.down_warps * p.tiles * kTileBytes) / (entries * 16 * sizeof(float));
-    p.splits = (int)std::max<int64_t>(1, std::min({p.down_warps / experts, ceil_div(p.F, kChunk), room}));
-    return dispatch_down(p.down_type, p, pdl, s);
+
+    const int64_t fchunks = ceil_div(p.F, kChunk);
+    st = cuda_status(launch_pdl(moe_ffn_columns_kernel, dim3((unsigned)ceil_div(entries * fchunks, 8)), dim3(256), 0, s, pdl, p));
+    if (st != GGUF_OK) return st;
+
+    // down: with few experts, several warps share one's chunks, as far as there is room for their sums and two pieces to a warp
+    const size_t slot = slot_bytes(p.down_type), one = (size_t)entries * 16 * 4;
+    const int64_t room = ((int64_t)kSmem - (int64_t)routes - (int64_t)(kWarps * 2 * slot)) / (int64_t)one;
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({kWarps / std::min(entries, p.n_expert), fchunks, room}));
+    p.down_stages = stages(routes + p.splits * one, slot);
+    return dispatch_down(p, routes + p.splits * one + kWarps * p.down_stages * slot, pdl, s);
 }
 
 }  // namespace gg

@@ -243,7 +243,7 @@ int gguf_moe_router(const void* x, int xdt, int64_t T, int64_t K, const gguf_rou
 
 size_t gguf_moe_ffn_workspace_size(int64_t F, int64_t T, int64_t top_k) {
     if (F <= 0 || F > (1 << 20) || T <= 0 || top_k <= 0 || T > kMoeFfnRows || top_k > kMoeFfnRows || T * top_k > kMoeFfnRows) return 0;
-    return (size_t)(T * top_k * F) * sizeof(float);
+    return moe_ffn_workspace_bytes(F, T, top_k);
 }
 
 int gguf_moe_ffn(const gguf_moe_weights* experts, const void* x, int xdt, int64_t T, const int32_t* ids,
@@ -290,8 +290,7 @@ int gguf_moe_ffn(const gguf_moe_weights* experts, const void* x, int xdt, int64_
     p.weights = weights;
     p.residual = residual;
     p.y = y;
-    p.h = static_cast<float*>(workspace);
-    return moe_ffn_launch(p, pdl_on(), (cudaStream_t)stream);
+    return moe_ffn_launch(p, workspace, sms, pdl_on(), (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -93,10 +93,14 @@ struct MoeFfnParams {
     const float* weights;
     const void* residual;
     void* y;
-    float* h;                            // workspace [T * top_k][F]
-    // set by the launch: columns a row of x and of h takes, tiles of 8 columns at
-    // a time, the down kernel's warps and how many of them share an expert
-    int x_parts, h_parts, tiles, down_warps, splits;
+    // set by the launch.  In the workspace: hidden values [T * top_k][F], then as
+    // the down kernel's columns, and the columns' scales
+    float* h;
+    uint8_t* columns;
+    float* column_scales;
+    int x_parts, h_parts;                // columns that a row of x and of h takes
+    int up_tiles, up_rt, up_stages, up_slot, up_resident;
+    int down_stages, splits;
 };
 
 struct SampleParams {
@@ -114,7 +118,8 @@ size_t paged_attn_workspace_bytes(const AttnParams& p, int num_sms);
 int paged_attn_launch(const AttnParams& p, void* workspace, int num_sms, int pdl, cudaStream_t stream);
 cudaError_t logits_adjust_launch(const LogitsParams& p, int num_sms, int pdl, cudaStream_t stream);
 cudaError_t moe_router_launch(const RouterParams& p, int num_sms, int pdl, cudaStream_t stream);
-int moe_ffn_launch(MoeFfnParams p, int pdl, cudaStream_t stream);
+size_t moe_ffn_workspace_bytes(int64_t F, int64_t T, int64_t top_k);
+int moe_ffn_launch(MoeFfnParams p, void* workspace, int num_sms, int pdl, cudaStream_t stream);
 cudaError_t sample_launch(const SampleParams& p, int num_sms, int pdl, cudaStream_t stream);
 
 // Sets a kernel's attribute on each device once: `done` is the kernel's own
