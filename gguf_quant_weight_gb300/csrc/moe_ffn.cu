@@ -49,72 +49,79 @@ constexpr size_t kSmem = 232448 - 2048;           // of a block, beside its stat
 
 // ---------------------------------------------------------------- the experts' rows
 
-// A group is up to `at_once` rows of one expert: the columns of one pass over its weights.
+// A group is some rows of one expert, as many as one pass over its weights takes.
 struct Group {
     int16_t expert, n;
     int16_t first;                  // of its rows (entries token * top_k + slot) in Routes::list
+    int16_t wide;                   // of up: groups of two tiles before it
 };
 
-// What each block makes of the ids, all blocks the same: an expert's rows are in
-// the order of the entries, since its groups may be different blocks' work.  In
-// dynamic shared memory, sized by `bytes`.
+// The rows by expert and, within one, in the order of the entries; the groups for
+// up's passes and for down's.  Every block of up makes them for itself from the
+// ids (an expert's groups may be different blocks' work, so all have to agree),
+// and the first leaves them in the workspace for down.
 struct Routes {
-    int* cursor;                    // [n_expert]
-    Group* group;                   // [entries]
-    uint16_t* list;                 // [entries], by expert
-    int16_t* id;                    // [entries], -1: none
-    __host__ __device__ static size_t bytes(int entries, int n_expert) {
-        return (size_t)ceil_div(4 * (int64_t)n_expert + 10 * (int64_t)entries, 16) * 16;
-    }
-    __device__ Routes(uint8_t* at, int entries, int n_expert)
-        : cursor(reinterpret_cast<int*>(at)), group(reinterpret_cast<Group*>(cursor + n_expert)),
-          list(reinterpret_cast<uint16_t*>(group + entries)), id(reinterpret_cast<int16_t*>(list + entries)) {}
+    Group* up;                      // [entries]
+    Group* down;                    // [entries]
+    uint16_t* list;                 // [entries]
+    __host__ __device__ static size_t bytes(int entries) { return (size_t)ceil_div(18 * (int64_t)entries, 16) * 16; }
+    __device__ Routes(uint8_t* at, int entries)
+        : up(reinterpret_cast<Group*>(at)), down(up + entries), list(reinterpret_cast<uint16_t*>(down + entries)) {}
 };
+// What make_routes works in: a bit for each expert and entry, [entries / 32][n_expert], and the experts' first rows.
+__host__ __device__ inline size_t routes_scratch(int entries, int n_expert) { return (size_t)(ceil_div(entries, 32) + 1) * n_expert * 4; }
 
-// Returns the number of groups.
-__device__ int make_routes(const Routes& r, const int32_t* ids, int entries, int n_expert, int at_once, int tid) {
-    __shared__ int s_groups;
-    for (int e = tid; e < n_expert; e += kThreads) r.cursor[e] = 0;
+// Returns the groups of up (low half) and of down.
+__device__ int make_routes(const Routes& r, uint32_t* scratch, const int32_t* ids, int entries, int n_expert, int up_rows, int down_rows,
+                           int tid) {
+    __shared__ int s_warp[kWarps];
+    const int lane = tid & 31, warp = tid >> 5, words = (entries + 31) >> 5;
+    uint32_t* const first = scratch + words * n_expert;
+    const int id = tid < entries ? ids[tid] : -1;           // at most kThreads entries
+    for (int i = tid; i < words * n_expert; i += kThreads) scratch[i] = 0;
     __syncthreads();
-    for (int i = tid; i < entries; i += kThreads) {
-        const int e = ids[i];
-        const bool in = (unsigned)e < (unsigned)n_expert;
-        r.id[i] = in ? (int16_t)e : -1;
-        if (in) atomicAdd(&r.cursor[e], 1);
-    }
+    const bool in = (unsigned)id < (unsigned)n_expert;
+    if (in) atomicOr(&scratch[warp * n_expert + id], 1u << lane);
     __syncthreads();
-    if (tid < 32) {
-        int rows = 0, groups = 0;
-        for (int b = 0; b < n_expert; b += 32) {
-            const int e = b + tid, c = e < n_expert ? r.cursor[e] : 0, g = (c + at_once - 1) / at_once;
-            if (!__any_sync(0xffffffffu, c > 0)) continue;
-            int both = c | g << 16;             // at most 512 of each
+    int done = 0;                                           // rows, groups of up, groups of down: 10 bits each
+    for (int b = 0; b < n_expert; b += kThreads) {
+        const int e = b + tid;
+        int rows = 0;
+        if (e < n_expert)
+            for (int w = 0; w < words; ++w) rows += __popc(scratch[w * n_expert + e]);
+        const int ups = (rows + up_rows - 1) / up_rows, downs = (rows + down_rows - 1) / down_rows;
+        const int mine = rows | ups << 10 | downs << 20;
+        int upto = mine;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, both, o);
-                if (tid >= o) both += v;
-            }
-            const int c0 = rows + (both & 0xffff) - c, g0 = groups + (both >> 16) - g;
-            if (c > 0) r.cursor[e] = c0;
-            for (int k = 0; k < g; ++k)
-                r.group[g0 + k] = Group{(int16_t)e, (int16_t)min(at_once, c - k * at_once), (int16_t)(c0 + k * at_once)};
-            const int last = __shfl_sync(0xffffffffu, both, 31);
-            rows += last & 0xffff;
-            groups += last >> 16;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
         }
-        if (tid == 0) s_groups = groups;
-        __syncwarp();
-        for (int b = 0; b < entries; b += 32) {
-            const int e = b + tid < entries ? r.id[b + tid] : -1;
-            const unsigned same = __match_any_sync(0xffffffffu, e), before = same & ((1u << tid) - 1);
-            if (e >= 0) r.list[r.cursor[e] + __popc(before)] = (uint16_t)(b + tid);
-            __syncwarp();
-            if (e >= 0 && !before) r.cursor[e] += __popc(same);
-            __syncwarp();
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = upto;
+        __syncthreads();
+        int before = done + upto - mine;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += s_warp[w];
+            done += s_warp[w];
+        }
+        if (rows) {
+            const int at = before & 1023;
+            first[e] = at;
+            for (int k = 0; k < ups; ++k)
+                r.up[(before >> 10 & 1023) + k] = Group{(int16_t)e, (int16_t)min(up_rows, rows - k * up_rows), (int16_t)(at + k * up_rows), 0};
+            for (int k = 0; k < downs; ++k)
+                r.down[(before >> 20) + k] = Group{(int16_t)e, (int16_t)min(down_rows, rows - k * down_rows), (int16_t)(at + k * down_rows), 0};
         }
     }
     __syncthreads();
-    return s_groups;
+    if (in) {
+        int at = first[id] + __popc(scratch[warp * n_expert + id] & ((1u << lane) - 1));
+        for (int w = 0; w < warp; ++w) at += __popc(scratch[w * n_expert + id]);
+        r.list[at] = (uint16_t)tid;
+    }
+    __syncthreads();
+    return (done >> 10 & 1023) | (done >> 20) << 16;
 }
 
 // ---------------------------------------------------------------- B: the activations
@@ -362,7 +369,7 @@ __device__ __forceinline__ void six_bits(const uint4& head, uint32_t (&sc)[4], u
 // (values), its sums' parts (sums(tile, k): those of groups 8k + 2t, 2t + 1 of 16), and what columns 2t, 2t + 1 are
 // multiplied by (back).
 template <int QT, int TILES, class B>
-__device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, int n_tiles, int nsub, int lane, float (&acc)[TILES][4]) {
+__device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, int nsub, int lane, float (&acc)[TILES][4]) {
     const int t = lane & 3;
     constexpr bool plain = zero_point(QT) == 0;         // codes as they are, subnormals: 2^-24 of them
     constexpr bool narrow = QT == GGUF_Q2_K || QT == GGUF_Q3_K || QT == GGUF_Q6_K;      // scales of 16 values
@@ -404,7 +411,7 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
         uint4 b[TILES];
 #pragma unroll
         for (int n = 0; n < TILES; ++n)
-            if (n < n_tiles) b[n] = col.values(n, j);
+            b[n] = col.values(n, j);
         float part[TILES][4] = {};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -432,12 +439,11 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
             }
 #pragma unroll
             for (int n = 0; n < TILES; ++n)
-                if (n < n_tiles) mma(part[n], a[0], a[1], a[2], a[3], half ? b[n].z : b[n].x, half ? b[n].w : b[n].y);
+                mma(part[n], a[0], a[1], a[2], a[3], half ? b[n].z : b[n].x, half ? b[n].w : b[n].y);
             if (narrow || half == 1) {
                 const float s0 = scale(0, j, half), s1 = scale(1, j, half);
 #pragma unroll
                 for (int n = 0; n < TILES; ++n) {
-                    if (n >= n_tiles) continue;
                     total[n][0] = fmaf(part[n][0], s0, total[n][0]);
                     total[n][1] = fmaf(part[n][1], s0, total[n][1]);
                     total[n][2] = fmaf(part[n][2], s1, total[n][2]);
@@ -449,7 +455,6 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
     if constexpr (plain) d[0] *= 0x1p24f, d[1] *= 0x1p24f;
 #pragma unroll
     for (int n = 0; n < TILES; ++n) {
-        if (n >= n_tiles) continue;
         const float2 back = col.back(n);
         if constexpr (has_min(QT)) {
             float low[4] = {};
@@ -527,25 +532,29 @@ struct Matrix {
     int n;                          // rows
 };
 
-// Two lanes to a row, every other 16 bytes each.
+// The warp's lanes take the 16 bytes units of the rows one after the other: a
+// copy instruction costs a cycle for each line of memory that it meets.
 template <int QT>
 __device__ __forceinline__ void fetch_piece(uint32_t slot, const Matrix& m, int row0, int c, int lane) {
-    const int row = lane >> 1, half = lane & 1;
-    const uint8_t* src = m.w + (int64_t)min(row0 + row, m.n - 1) * m.rb + (int64_t)c * piece_bytes(QT) + 16 * half;
-    const uint32_t dst = slot + row * piece_stride(QT) + 16 * half;
-    if constexpr (piece_aligned(QT)) {
+    constexpr int UNITS = piece_stride(QT) / 16;            // of a row
+    row0 = min(row0, m.n - 1);                              // a tile past the last row
+    const uint8_t* const base = m.w + (int64_t)row0 * m.rb + (int64_t)c * piece_bytes(QT);
+    const int bytes = (int)min((int64_t)piece_bytes(QT), m.rb - (int64_t)c * piece_bytes(QT));   // fewer at the end of a row of 32-value blocks
+    const int last = m.n - 1 - row0, low = (int)(reinterpret_cast<uintptr_t>(base) & 15);
+    const uint32_t rb = (uint32_t)m.rb;                     // 16 rows are below 2^32 bytes
+    const bool inside = m.end - base > 16 * m.rb;           // no copy reaches the end of the experts
 #pragma unroll
-        for (int i = 0; i < piece_stride(QT) / 16; i += 2)
-            if (i + 1 < piece_stride(QT) / 16 || half == 0) copy16(dst + 16 * i, src + 16 * i, 16);
-    } else {
-        const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);
-        src -= off;
-        // bytes from the boundary on: the piece's, fewer at the end of a row of 32-value blocks
-        const int len = off + (int)min((int64_t)piece_bytes(QT), m.rb - (int64_t)c * piece_bytes(QT)) - 16 * half;
-        const int64_t left = m.end - src;
-#pragma unroll
-        for (int i = 0; i < piece_stride(QT) / 16; i += 2)
-            if (16 * i < len) copy16(dst + 16 * i, src + 16 * i, (int)min((int64_t)16, left - 16 * i));
+    for (int i = 0; i < (16 * UNITS + 31) / 32; ++i) {
+        const int u = 32 * i + lane, row = u / UNITS, at = 16 * (u - row * UNITS);
+        if (16 * UNITS % 32 && u >= 16 * UNITS) break;
+        const uint32_t from = (uint32_t)min(row, last) * rb;
+        if constexpr (piece_aligned(QT)) {
+            copy16(slot + 16 * u, base + from + at, 16);
+        } else {
+            const int off = (low + (int)from) & 15;
+            const uint8_t* src = base + from + (at - off);
+            if (at < off + bytes) copy16(slot + 16 * u, src, inside ? 16 : (int)min((int64_t)16, (int64_t)(m.end - src)));
+        }
     }
 }
 
@@ -591,45 +600,77 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
     extern __shared__ __align__(16) uint8_t s_dyn[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int entries = p.T * p.top_k, tiles = p.up_tiles, chunks = (int)ceil_div(p.K, kChunk), parts = p.x_parts;
-    const Routes routes(s_dyn, entries, p.n_expert);
+    const Routes routes(s_dyn, entries);
     // a group's columns: of all chunks, or, where K is too long, of the one that each warp is at
     const int held = p.up_resident ? chunks : kWarps;
-    uint8_t* const columns = s_dyn + Routes::bytes(entries, p.n_expert);                    // [held][tile]
+    uint8_t* const columns = s_dyn + Routes::bytes(entries);                                // [held][tile]
     float* const scales = reinterpret_cast<float*>(columns + (size_t)held * tiles * kTileBytes);        // [held][8 * tiles]
     float* const sums = scales + held * 8 * tiles;                                          // [2][warp][16 rows][8 * tiles]
     uint8_t* const ring = reinterpret_cast<uint8_t*>(sums + 2 * kWarps * 128 * tiles) + (size_t)warp * p.up_stages * p.up_slot;
     const uint32_t ring_at = smem_u32(ring);
     pdl_wait();
     pdl_launch_dependents();        // all blocks of this kernel are running
-    const int groups = make_routes(routes, p.ids, entries, p.n_expert, 8 * tiles / parts, tid);
+    const int both = make_routes(routes, reinterpret_cast<uint32_t*>(columns), p.ids, entries, p.n_expert, 8 * tiles / parts, 8 / p.h_parts, tid);
+    const int groups = both & 0xffff;
+    if (blockIdx.x == 0) {
+        const uint4* from = reinterpret_cast<const uint4*>(s_dyn);
+        uint4* to = reinterpret_cast<uint4*>(p.routes);
+        for (int i = tid; i < (int)(Routes::bytes(entries) / 16); i += kThreads) to[i + 1] = from[i];
+        if (tid == 0) to[0] = make_uint4(both >> 16, 0, 0, 0);
+    }
     const int rt = p.up_rt, wp = 8 / rt;
-    const int64_t per_group = ceil_div(p.F, 16 * rt), jobs = per_group * groups;
-    const int64_t job0 = jobs * blockIdx.x / gridDim.x, job1 = jobs * (blockIdx.x + 1) / gridDim.x;
+    const int K = (int)p.K, F = (int)p.F, per_group = (F + 16 * rt - 1) / (16 * rt), jobs = per_group * groups;
+    // The blocks' shares of the jobs, where a job of two tiles counts 4 and one of one tile 3 (the blocks
+    // are taken apart once either way).
+    __shared__ int s_from[2], s_wide;
+    if (tid < 2) s_from[tid] = jobs;
+    if (warp == 0) {
+        int wide = 0;
+        for (int b = 0; b < groups; b += 32) {
+            const bool two = b + lane < groups && routes.up[b + lane].n * parts > 8;
+            const unsigned on = __ballot_sync(0xffffffffu, two);
+            if (b + lane < groups) routes.up[b + lane].wide = (int16_t)(wide + __popc(on & ((1u << lane) - 1)));
+            wide += __popc(on);
+        }
+        if (lane == 0) s_wide = wide;
+    }
+    __syncthreads();
+    const int64_t whole = (int64_t)per_group * (3 * groups + s_wide);
+    if (tid < groups) {
+        const int cost = routes.up[tid].n * parts > 8 ? 4 : 3;
+        const int64_t lo = (int64_t)per_group * (3 * tid + routes.up[tid].wide);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int64_t at = whole * (blockIdx.x + k) / gridDim.x - lo;
+            if (at >= 0 && at < (int64_t)per_group * cost) s_from[k] = tid * per_group + (int)at / cost;
+        }
+    }
+    __syncthreads();
+    const int job0 = s_from[0], job1 = s_from[1];
     // this warp's part of a job
     const int my_tile = warp / (2 * wp), mat = (warp / wp) & 1, c0 = warp % wp;
     const int qt = mat ? p.up_type : p.gate_type;
-    auto place = [&](int64_t job, Matrix& m, int& row0) {
-        const int e = routes.group[job / per_group].expert;
-        const uint8_t* w = mat ? p.up : p.gate;
-        m.rb = mat ? p.up_rb : p.gate_rb;
-        m.n = (int)p.F;
-        m.w = w + e * p.F * m.rb;
-        m.end = w + p.n_expert * p.F * m.rb;
-        row0 = ((int)(job % per_group) * rt + my_tile) * 16;
-    };
-    // the ring's next piece to fetch
-    int64_t fjob = job0;
-    int fc = c0, fslot = 0, slot = 0;
-    Matrix fm{};
-    int frow = 0;
-    if (fjob < job1) place(fjob, fm, frow);
+    Matrix m;
+    m.rb = mat ? p.up_rb : p.gate_rb;
+    m.n = F;
+    m.end = (mat ? p.up : p.gate) + p.n_expert * p.F * m.rb;
+    auto matrix_of = [&](int group) { return (mat ? p.up : p.gate) + routes.up[group].expert * p.F * m.rb; };
+    // a job is a group and a step through its rows; the ring's next piece to fetch runs ahead
+    int group = job0 / per_group, step = job0 - group * per_group;
+    int fjob = job0, fgroup = group, fstep = step, fc = c0, fslot = 0, slot = 0;
+    Matrix fm = m;
+    if (fjob < job1) fm.w = matrix_of(fgroup);
     auto fetch = [&] {
         if (fjob < job1 && fc < chunks) {
-            if constexpr (QT >= 0) fetch_piece<QT>(ring_at + fslot * p.up_slot, fm, frow, fc, lane);
-            else with_type(qt, [&](auto q) { fetch_piece<decltype(q)::value>(ring_at + fslot * p.up_slot, fm, frow, fc, lane); });
+            const int row0 = (fstep * rt + my_tile) * 16;
+            if constexpr (QT >= 0) fetch_piece<QT>(ring_at + fslot * p.up_slot, fm, row0, fc, lane);
+            else with_type(qt, [&](auto q) { fetch_piece<decltype(q)::value>(ring_at + fslot * p.up_slot, fm, row0, fc, lane); });
             fslot = fslot + 1 == p.up_stages ? 0 : fslot + 1;
             fc += wp;
-            if (fc >= chunks && ++fjob < job1) fc = c0, place(fjob, fm, frow);
+            if (fc >= chunks && ++fjob < job1) {
+                fc = c0;
+                if (++fstep == per_group) fstep = 0, fm.w = matrix_of(++fgroup);
+            }
         }
         copies_commit();
     };
@@ -639,24 +680,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
     Group g{};
     auto make = [&](int k, int c, int at) {         // the columns of the group's row k, chunk c
         const int col = k * parts, token = routes.list[g.first + k] / p.top_k;
-        const int nsub = (int)min((int64_t)8, (p.K - (int64_t)c * kChunk) / 32);
+        const int nsub = min(8, (K - c * kChunk) / 32);
         const float back = make_column(columns + (size_t)(at * tiles * 8 + col) * kColStride, parts, p.x, p.xdt,
-                                       token * p.K + (int64_t)c * kChunk, nsub, lane);
+                                       token * p.K + c * kChunk, nsub, lane);
         if (lane < parts) scales[at * 8 * tiles + col + lane] = back;
     };
-    for (int64_t job = job0; job < job1; ++job, buffer ^= 1) {
-        if ((int)(job / per_group) != made) {
-            made = (int)(job / per_group);
-            g = routes.group[made];
+    for (int job = job0; job < job1; ++job, buffer ^= 1) {
+        if (group != made) {
+            made = group;
+            g = routes.up[group];
+            m.w = matrix_of(group);
             // every warp has passed the barrier of the job before, so nothing reads the old columns
             if (p.up_resident)
                 for (int i = warp; i < g.n * chunks; i += kWarps) make(i % g.n, i / g.n, i / g.n);
             __syncthreads();
         }
         const int n_tiles = (g.n * parts + 7) >> 3;
-        Matrix m;
-        int row0;
-        place(job, m, row0);
+        const int row0 = (step * rt + my_tile) * 16;
         float acc[kTiles][4] = {};
         for (int c = c0; c < chunks; c += wp) {
             const int at = p.up_resident ? c : warp;
@@ -664,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
                 for (int k = 0; k < g.n; ++k) make(k, c, at);
             copies_wait(p.up_stages - 1);
             __syncwarp();
-            const int nsub = (int)min((int64_t)8, (p.K - (int64_t)c * kChunk) / 32), t = lane & 3;
+            const int nsub = min(8, (K - c * kChunk) / 32), t = lane & 3;
             const ColumnsInShared col{columns + (size_t)at * tiles * kTileBytes + (lane >> 2) * kColStride + t * 16, scales + at * 8 * tiles + 2 * t, t};
             auto unit = [&](auto q) {
                 constexpr int Q = decltype(q)::value;
@@ -672,7 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
                 read_piece<Q>(r, ring + slot * p.up_slot, m, row0, c, nsub, lane);
                 __syncwarp();       // the piece is read: its place may be filled
                 fetch();
-                multiply<Q, kTiles>(r, col, n_tiles, nsub, lane, acc);
+                // (an instruction that a predicate turns off still takes its turn)
+                if (n_tiles == 1) multiply<Q, 1>(r, col, nsub, lane, reinterpret_cast<float(&)[1][4]>(acc));
+                else multiply<Q, kTiles>(r, col, nsub, lane, acc);
             };
             if constexpr (QT >= 0) unit(std::integral_constant<int, QT>{});
             else with_type(qt, unit);
@@ -690,10 +732,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
         __syncthreads();
         // the sums of two jobs have places of their own, so the warps go on meanwhile
         const int used = min(wp, chunks);
-        for (int i = tid; i < rt * g.n * 16; i += kThreads) {
-            const int r = i & 15, k = (i >> 4) % g.n, tile = (i >> 4) / g.n;
-            const int64_t row = (job % per_group * rt + tile) * 16 + r;
-            if (row >= p.F) continue;
+        for (int i = tid; i < rt * 16 * 8 * tiles; i += kThreads) {
+            const int r = i & 15, k = (i >> 4) & (8 * tiles - 1), tile = i / (128 * tiles);
+            const int row = (step * rt + tile) * 16 + r;
+            if (k >= g.n || row >= F) continue;
             float v[2] = {0.f, 0.f};
             const float* from = sums + (size_t)(buffer * kWarps + tile * 2 * wp) * 128 * tiles + r * 8 * tiles + k * parts;
 #pragma unroll
@@ -704,6 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
                 }
             p.h[(int64_t)routes.list[g.first + k] * p.F + row] = activate(v[0], p.act) * v[1];
         }
+        if (++step == per_group) step = 0, ++group;
     }
 }
 
@@ -714,11 +757,11 @@ __global__ void __launch_bounds__(256) moe_ffn_columns_kernel(const MoeFfnParams
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, chunks = (int)ceil_div(p.F, kChunk);
-    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i >= (int64_t)p.T * p.top_k * chunks) return;
-    const int64_t entry = i / chunks, c = i % chunks;
-    const int nsub = (int)min((int64_t)8, (p.F - c * kChunk) / 32);
-    const float back = make_column(p.columns + i * p.h_parts * kColStride, p.h_parts, p.h, GGUF_DT_F32, entry * p.F + c * kChunk, nsub, lane);
+    const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (i >= p.T * p.top_k * chunks) return;
+    const int entry = i / chunks, c = i - entry * chunks;
+    const int nsub = min(8, ((int)p.F - c * kChunk) / 32);
+    const float back = make_column(p.columns + (int64_t)i * p.h_parts * kColStride, p.h_parts, p.h, GGUF_DT_F32, entry * p.F + c * kChunk, nsub, lane);
     if (lane == 0) p.column_scales[i] = back;
 }
 
@@ -741,40 +784,45 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnP
     extern __shared__ __align__(16) uint8_t s_dyn[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int entries = p.T * p.top_k, parts = p.h_parts, splits = p.splits;
-    const Routes routes(s_dyn, entries, p.n_expert);
-    float* const sums = reinterpret_cast<float*>(s_dyn + Routes::bytes(entries, p.n_expert));       // [split][entry][16]
+    const Routes routes(s_dyn, entries);
+    float* const weights = reinterpret_cast<float*>(s_dyn + Routes::bytes(entries));                // [entry]
+    float* const sums = weights + (entries + 3) / 4 * 4;                                            // [split][entry][16]
     constexpr int kSlot = 16 * piece_stride(QT);
     uint8_t* const ring = reinterpret_cast<uint8_t*>(sums + (size_t)splits * entries * 16) + (size_t)warp * p.down_stages * kSlot;
     const uint32_t ring_at = smem_u32(ring);
-    // The kernel before this one began when the one before that had ended, so the ids are there; the columns are
-    // waited for once the first weights are on their way.
-    const int items = make_routes(routes, p.ids, entries, p.n_expert, 8 / parts, tid) * splits;
-    const int row0 = 16 * blockIdx.x, chunks = (int)ceil_div(p.F, kChunk);
-    auto place = [&](int item, Matrix& m) {
-        m.rb = p.down_rb;
-        m.n = (int)p.K;
-        m.w = p.down + routes.group[item / splits].expert * p.K * p.down_rb;
-        m.end = p.down + p.n_expert * p.K * p.down_rb;
-    };
+    // The kernel before this one let it begin when up had ended, so the routes are
+    // there; the columns are waited for once the first weights are on their way.
+    for (int i = tid; i < (int)(Routes::bytes(entries) / 16); i += kThreads)
+        reinterpret_cast<uint4*>(s_dyn)[i] = reinterpret_cast<const uint4*>(p.routes)[i + 1];
+    const int items = *reinterpret_cast<const int*>(p.routes) * splits;
+    if (tid < entries) weights[tid] = (unsigned)p.ids[tid] < (unsigned)p.n_expert ? p.weights[tid] : 0.f;
+    // an id of no expert adds 0 * 0
+    for (int i = tid; i < splits * entries * 4; i += kThreads) reinterpret_cast<float4*>(sums)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    const int row0 = 16 * blockIdx.x, F = (int)p.F, chunks = (F + kChunk - 1) / kChunk;
+    Matrix m{nullptr, p.down + p.n_expert * p.K * p.down_rb, p.down_rb, (int)p.K};
+    auto matrix_of = [&](int item) { return p.down + routes.down[item / splits].expert * p.K * p.down_rb; };
     int fitem = warp, fc = warp % splits, fslot = 0, slot = 0;
-    Matrix fm{};
-    if (fitem < items) place(fitem, fm);
+    Matrix fm = m;
+    if (fitem < items) fm.w = matrix_of(fitem);
     auto fetch = [&] {
         if (fitem < items) {
             fetch_piece<QT>(ring_at + fslot * kSlot, fm, row0, fc, lane);
             fslot = fslot + 1 == p.down_stages ? 0 : fslot + 1;
             fc += splits;
-            if (fc >= chunks && (fitem += kWarps) < items) fc = fitem % splits, place(fitem, fm);
+            if (fc >= chunks && (fitem += kWarps) < items) fc = fitem % splits, fm.w = matrix_of(fitem);
         }
         copies_commit();
     };
     for (int i = 0; i < p.down_stages; ++i) fetch();
+    float residual = 0.f;           // of this thread's first output
+    if (p.residual && tid < p.T * 16 && row0 + (tid & 15) < p.K)
+        residual = load_act(p.residual, p.ydt, (tid >> 4) * p.K + row0 + (tid & 15));
     pdl_wait();
     const int g = lane >> 2, t = lane & 3;
     for (int item = warp; item < items; item += kWarps) {
-        const Group group = routes.group[item / splits];
-        Matrix m;
-        place(item, m);
+        const Group group = routes.down[item / splits];
+        m.w = matrix_of(item);
         float acc[1][4] = {};
         // this lane's column, and columns 2t, 2t + 1, of the group's rows
         auto entry_of = [&](int col) { return (int64_t)routes.list[group.first + min(col / parts, group.n - 1)]; };
@@ -791,13 +839,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnP
             col.f = make_float2(__ldg(p.column_scales + first + c), __ldg(p.column_scales + second + c));
             copies_wait(p.down_stages - 1);
             __syncwarp();
-            const int nsub = (int)min((int64_t)8, (p.F - (int64_t)c * kChunk) / 32);
+            const int nsub = min(8, (F - c * kChunk) / 32);
             Raw<QT> r[2];
             read_piece<QT>(r, ring + slot * kSlot, m, row0, c, nsub, lane);
             slot = slot + 1 == p.down_stages ? 0 : slot + 1;
             __syncwarp();           // the piece is read: its place may be filled
             fetch();
-            multiply<QT, 1>(r, col, 1, nsub, lane, acc);
+            multiply<QT, 1>(r, col, nsub, lane, acc);
         }
         // columns 2t, 2t + 1: the two parts of one row, or two rows
         float* const to = sums + (size_t)(item % splits) * entries * 16;
@@ -822,13 +870,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnP
         const int r = i & 15, token = i >> 4;
         if (row0 + r >= p.K) continue;
         const int64_t o = token * p.K + row0 + r;
-        float v = p.residual ? load_act(p.residual, p.ydt, o) : 0.f;
+        float v = i == tid ? residual : p.residual ? load_act(p.residual, p.ydt, o) : 0.f;
         for (int s = 0; s < p.top_k; ++s) {
             const int at = token * p.top_k + s;
-            if ((unsigned)p.ids[at] >= (unsigned)p.n_expert) continue;
             float row = 0.f;
             for (int q = 0; q < splits; ++q) row += sums[((size_t)q * entries + at) * 16 + r];
-            v = fmaf(p.weights[at], row, v);
+            v = fmaf(weights[at], row, v);
         }
         store_out(p.y, p.ydt, o, v);
     }
@@ -880,15 +927,16 @@ int slot_bytes(int qt) {
     }
 }
 
-// hidden values, their columns, the columns' scales
+// hidden values, their columns, the columns' scales, the routes and how many groups down has
 size_t hidden_bytes(int64_t entries, int64_t F) { return (size_t)ceil_div(entries * F * 4, 256) * 256; }
 size_t column_bytes(int64_t entries, int64_t F) { return (size_t)(entries * ceil_div(F, kChunk) * 2 * kColStride); }
+size_t scale_bytes(int64_t entries, int64_t F) { return (size_t)ceil_div(entries * ceil_div(F, kChunk) * 4, 16) * 16; }
 
 }  // namespace
 
 size_t moe_ffn_workspace_bytes(int64_t F, int64_t T, int64_t top_k) {
     const int64_t entries = T * top_k;
-    return hidden_bytes(entries, F) + column_bytes(entries, F) + (size_t)(entries * ceil_div(F, kChunk) * 4);
+    return hidden_bytes(entries, F) + column_bytes(entries, F) + scale_bytes(entries, F) + 16 + Routes::bytes((int)entries);
 }
 
 int moe_ffn_launch(MoeFfnParams p, void* workspace, int num_sms, int pdl, cudaStream_t s) {
@@ -896,10 +944,11 @@ int moe_ffn_launch(MoeFfnParams p, void* workspace, int num_sms, int pdl, cudaSt
     p.h = static_cast<float*>(workspace);
     p.columns = static_cast<uint8_t*>(workspace) + hidden_bytes(entries, p.F);
     p.column_scales = reinterpret_cast<float*>(p.columns + column_bytes(entries, p.F));
+    p.routes = reinterpret_cast<uint8_t*>(p.column_scales) + scale_bytes(entries, p.F);
     p.x_parts = p.xdt == GGUF_DT_F32 ? 2 : 1;           // the 16-bit types' values are f16 numbers, scaled
     // the hidden values' rounding to f16 is below what a bf16 output rounds, and would not be below an f16 output's
     p.h_parts = p.ydt == GGUF_DT_BF16 ? 1 : 2;
-    const size_t routes = Routes::bytes(entries, p.n_expert);
+    const size_t routes = Routes::bytes(entries);
 
     // up: two tiles of columns where a group may need them and there is room for two pieces to a warp beside them
     const int64_t chunks = ceil_div(p.K, kChunk);
@@ -910,10 +959,12 @@ int moe_ffn_launch(MoeFfnParams p, void* workspace, int num_sms, int pdl, cudaSt
     p.up_resident = stages(fixed(chunks, p.up_tiles), p.up_slot) >= 1;
     const size_t up_fixed = fixed(p.up_resident ? chunks : kWarps, p.up_tiles);
     p.up_stages = stages(up_fixed, p.up_slot);
+    // what making the routes takes is shared with the columns and the ring
+    const size_t up_smem = std::max(up_fixed + (size_t)kWarps * p.up_stages * p.up_slot, routes + routes_scratch(entries, p.n_expert));
     p.up_rt = chunks >= 8 ? 1 : chunks >= 4 ? 2 : chunks >= 2 ? 4 : 8;
     const int64_t most = ceil_div(p.F, 16 * p.up_rt) * entries;
     int st = dispatch_up(p.gate_type == p.up_type ? p.gate_type : -1, p, (int)std::min<int64_t>(num_sms, most),
-                         up_fixed + (size_t)kWarps * p.up_stages * p.up_slot, pdl, s);
+                         up_smem, pdl, s);
     if (st != GGUF_OK) return st;
 
     const int64_t fchunks = ceil_div(p.F, kChunk);
@@ -921,11 +972,11 @@ int moe_ffn_launch(MoeFfnParams p, void* workspace, int num_sms, int pdl, cudaSt
     if (st != GGUF_OK) return st;
 
     // down: with few experts, several warps share one's chunks, as far as there is room for their sums and two pieces to a warp
-    const size_t slot = slot_bytes(p.down_type), one = (size_t)entries * 16 * 4;
-    const int64_t room = ((int64_t)kSmem - (int64_t)routes - (int64_t)(kWarps * 2 * slot)) / (int64_t)one;
+    const size_t slot = slot_bytes(p.down_type), one = (size_t)entries * 16 * 4, down_fixed = routes + (entries + 3) / 4 * 16;
+    const int64_t room = ((int64_t)kSmem - (int64_t)down_fixed - (int64_t)(kWarps * 2 * slot)) / (int64_t)one;
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({kWarps / std::min(entries, p.n_expert), fchunks, room}));
-    p.down_stages = stages(routes + p.splits * one, slot);
-    return dispatch_down(p, routes + p.splits * one + kWarps * p.down_stages * slot, pdl, s);
+    p.down_stages = stages(down_fixed + p.splits * one, slot);
+    return dispatch_down(p, down_fixed + p.splits * one + kWarps * p.down_stages * slot, pdl, s);
 }
 
 }  // namespace gg

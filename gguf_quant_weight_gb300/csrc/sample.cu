@@ -1,5 +1,5 @@
 // Draws a token from each row of logits, from given random numbers, after
-// temperature, top-k, top-p and min-p, in one kernel that reads the logits once.
+// temperature, top-k, top-p and min-p, in one kernel.
 //
 // All three filters keep a run of the tokens in falling order (of equal logits
 // the lower index first), so together they keep the tokens before or at some (logit K,
@@ -8,18 +8,24 @@
 //
 // Which token that is must not hang on rounding: among 10^5 kept tokens a sum
 // that is off by 10^-7 meets the wrong one once in a hundred rows.  So a
-// weight 2^-z, z = (max - x) / temperature * log2 e, is taken to about 1e-10 of
-// itself (z in two floats; a table of 2^-(j + 1/2)/256 and three terms of the
+// weight 2^-z, z = (max - x) / temperature * log2 e, is taken to about 1e-9 of
+// itself, without a bias (z in two floats; a table of 2^-(j + 1/2)/32 and four terms of the
 // series for the rest, as in Tang's table-driven exponential, ACM TOMS 1989) and
 // becomes an integer of 46 bits.  Sums of integers do not depend on their order:
 // the result is the same however the row is cut, and atomics add them up.
 //
-// A cluster of up to 8 blocks holds a row in its shared memory.  Where a
-// filter's run ends is found by histograms: of z in sixteenths at first, then of
-// ranges of the logits' bits, until the bin in which it ends has at most kCap
+// A cluster of up to 8 blocks takes a row, a warp a run of its tokens.  The first
+// pass reads the logits for their maximum.  The second, out of L2, counts them by
+// their distance from it, in sixteenths of z: there top-k's last token is in a bin
+// that is known, and a bin's weights are known to 2.2 %, so that top-p's last
+// token lies before a bin that is known too.  The third lists the tokens up to
+// that bin (or min-p's bound) in shared memory; what follows looks at those
+// alone.  Where a run ends is found by histograms: of z again, with the exact
+// weights, then of ranges of the logits' bits, until the bin in which it ends has at most kCap
 // tokens, which are compared with each other.  Where that many tokens are all
 // that the filters can leave (the usual top-k or top-p), the first block draws
-// from them and the other passes are saved.
+// from them and the other passes are saved.  Lists that would overflow (flat
+// distributions) and rows without a filter are read from L2 again instead.
 #include <type_traits>
 
 #include "serving.cuh"
@@ -32,16 +38,16 @@ typedef unsigned long long u64;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2 * kThreads, kCap = 256;
-constexpr int kMaxSlice = 51200;                 // logits of a block: 200 KB
+constexpr int kList = 896;                       // tokens of a warp's list at most, a multiple of 128
 constexpr uint32_t kNone = 0x007fffffu;          // -inf's place in the order: every token above it is kept
 
-// 2^46 * 2^-(j + 1/2) / 256, j = 0 .. 255; that all weights are 2^(-1/512) too small changes nothing.
-// Running products in double: off by at most 256 * 2^-53.
+// 0.995 * 2^32 * 2^-(j + 1/2) / 32, j = 0 .. 31: all weights are too small by one factor, which changes
+// nothing, and stay below 2^32 with the series' up to 1.09 %.  Running products in double.
 struct Table {
-    u64 v[256];
+    uint32_t v[32];
     constexpr Table() : v() {
-        double t = 0x1p46 * 0.99864711289097017;         // 2^(-1/512)
-        for (int j = 0; j < 256; ++j, t *= 0.99729605608547013) v[j] = (u64)(t + 0.5);   // 2^(-1/256)
+        double t = 0.995 * 0x1p32 * 0.98922801319397548;     // 2^(-1/64)
+        for (int j = 0; j < 32; ++j, t *= 0.97857206208770009) v[j] = (uint32_t)(t + 0.5);   // 2^(-1/32)
     }
 };
 __device__ constexpr Table kTable;
@@ -54,9 +60,9 @@ __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// A float's bits in the order of its value, and back.
+// A float's bits in the order of its value (-0 as 0), and back.
 __device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t u = __float_as_uint(v);
+    const uint32_t u = __float_as_uint(v + 0.f);
     return (u >> 31) ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float float_of(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k); }
@@ -82,21 +88,52 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// the larger of the two, NaN if one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 struct Shared {
-    u64 table[256];
+    float value[kWarps * kList];                         // the warps' lists: logits, and where in the warp's run
+    uint16_t offset[kWarps * kList];
+    uint32_t table[32 * 32];                             // kTable, a copy for each lane's bank
     uint32_t count[kBins], low[kBins], high[kBins];      // of a histogram: tokens, and their weights' sums
     uint32_t cand_key[kCap], cand_idx[kCap], n_cand;
     u64 cand_w[kCap], kept_w[kCap];
     u64 warp_sum[kWarps];
     uint32_t warp_count[kWarps];
+    float warp_f[kWarps];
     // from each block of the cluster
-    uint32_t peer_max[8], peer_bad[8], peer_lo[8], peer_hi[8];
+    uint32_t peer_max[8], peer_bad[8], peer_lo[8], peer_hi[8], peer_listed[8];
+    float peer_tail[8];
     u64 peer_sum[3][8];
     // what one thread found, for all
     uint32_t bin, base_count, bin_count, all_count;
     u64 base_sum, all_sum;
-    uint32_t K, I, lo, hi, bad;
+    uint32_t K, I, lo, hi, bad, listed;
 };
+
+// f times W, exactly, rounded down or up; f in [0, 1)
+__device__ __forceinline__ u64 share_of(float f, u64 W, bool up) {
+    const uint32_t bits = __float_as_uint(f);
+    const int e = max(1, (int)(bits >> 23));
+    const uint32_t mant = (bits & 0x7fffffu) | (bits >> 23 ? 0x800000u : 0u);       // f = mant * 2^(e - 150)
+    const u64 lo = W * mant, hi = __umul64hi(W, (u64)mant);
+    const int sh = 150 - e;                                                         // 24 .. 149
+    u64 v, rest;
+    if (sh < 64) v = hi << (64 - sh) | lo >> sh, rest = lo << (64 - sh);
+    else if (sh == 64) v = hi, rest = lo;
+    else if (sh < 128) v = hi >> (sh - 64), rest = lo | hi << (128 - sh);
+    else v = 0, rest = lo | hi;
+    return v + (up && rest ? 1 : 0);
+}
 
 // logp of w of W, to f32's rounding also where it is near 0
 __device__ __forceinline__ float log_share(u64 w, u64 W) {
@@ -104,40 +141,42 @@ __device__ __forceinline__ float log_share(u64 w, u64 W) {
     return 2 * w > W ? log1pf(-((float)(W - w) / all)) : logf((float)w / all);
 }
 
-// seg: logits of a warp, a multiple of 128; block `rank` of a row's cluster holds
-// 16 seg of them, from index first + rank * 16 seg on.
+// seg: tokens of a warp, a multiple of 128; warp w of a row's cluster has those
+// from index first + w * seg on.
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p, int cluster, int seg) {
     using X = typename El<DT>::T;
-    extern __shared__ __align__(16) float s_x[];
-    __shared__ Shared s;
+    extern __shared__ __align__(16) uint8_t s_dyn[];
+    Shared& s = *reinterpret_cast<Shared*>(s_dyn);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int r = blockIdx.x / cluster;
     const X* x = static_cast<const X*>(p.x) + r * p.ld;
-    const int first = -(int)((r * p.ld) & 3) + rank * kWarps * seg;        // groups of four start at 8- or 16-byte boundaries
+    const int first = -(int)((r * p.ld) & 3) + (rank * kWarps + warp) * seg;        // groups of four start at 8- or 16-byte boundaries
     const int V = p.vocab;
     if (cluster > 1) cluster_arrive_relaxed();       // waited for before the first access to another block
-    if (tid < 256) s.table[tid] = kTable.v[tid];
+    for (int i = tid; i < 32 * 32; i += kThreads) s.table[i] = kTable.v[i >> 5];
     for (int i = tid; i < kBins; i += kThreads) s.count[i] = s.low[i] = s.high[i] = 0;
-    if (tid == 0) s.n_cand = 0, s.bad = 0, s.hi = 0, s.lo = 0xffffffffu;
+    if (tid == 0) s.n_cand = 0, s.bad = 0, s.hi = 0, s.lo = 0xffffffffu, s.listed = 0;
     pdl_wait();
     pdl_launch_dependents();
     const float T = p.s.temperature ? p.s.temperature[r] : 1.f;
     int k = p.s.top_k ? p.s.top_k[r] : 0;
     float top_p = p.s.top_p ? p.s.top_p[r] : 1.f, min_p = p.s.min_p ? p.s.min_p[r] : 0.f;
     const float u = p.u[r];
+    const bool greedy = T == 0.f;
+    if (greedy) k = 1, top_p = 1.f, min_p = 0.f;
+    const bool use_k = k > 0 && k < V, use_p = top_p < 1.f, use_m = min_p > 0.f;
+    // log2 e / temperature in two floats (no doubles here: an SM does two of them a cycle)
+    constexpr float kLog2eHigh = 1.44269502f, kLog2eLow = 1.92596299e-8f;
+    const float quotient = greedy ? 0.f : kLog2eHigh / T;
+    const bool two = T < INFINITY && quotient < 1e37f && !greedy;
+    const float ch = fminf(quotient, 1e37f), cl = two ? (fmaf(-ch, T, kLog2eHigh) + kLog2eLow) / T : 0.f;
 
-    // the row, and its maximum
-    float top = -INFINITY;
-    bool bad = !(T >= 0.f);
-    float* mine = s_x + warp * seg + 4 * lane;
-    const int at0 = first + warp * seg + 4 * lane;
+    // four tokens at `i` of the warp's run, -inf where the row has none
     struct alignas(4 * sizeof(X)) In { X v[4]; };
-#pragma unroll 8
-    for (int i = 0; i < seg; i += 128) {
-        const int v0 = at0 + i;
-        float f[4];
+    auto load = [&](int i, float (&f)[4]) {
+        const int v0 = first + i + 4 * lane;
         if (v0 >= 0 && v0 + 4 <= V) {
             const In in = *reinterpret_cast<const In*>(x + v0);
 #pragma unroll
@@ -146,34 +185,39 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = v0 + j >= 0 && v0 + j < V ? to_f(x[v0 + j]) : -INFINITY;
         }
+    };
+    constexpr int kAhead = 4;                        // of those, on their way at once
+    auto each_four = [&](auto&& f) {
+        for (int i = 0; i < seg; i += 128 * kAhead) {
+            float v[kAhead][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[j] += 0.f;                                 // -0 and 0 are equals
-            bad |= !(f[j] < INFINITY);
-            top = fmaxf(top, f[j]);
+            for (int j = 0; j < kAhead; ++j)
+                if (i + 128 * j < seg) load(i + 128 * j, v[j]);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (i + 128 * j < seg) f(v[j], i + 128 * j);
         }
-        *reinterpret_cast<float4*>(mine + i) = make_float4(f[0], f[1], f[2], f[3]);
-    }
+    };
+
+    // the maximum
+    float top = -INFINITY;
+    each_four([&](float (&f)[4], int) { top = max_nan(top, max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3]))); });
+    const bool bad = !(T >= 0.f) || !(top < INFINITY);       // or NaN
+    const uint32_t warp_key = __reduce_max_sync(0xffffffffu, bad ? kNone : key_of(top));
+    __syncthreads();                                 // s.bad, s.hi are 0
+    if (lane == 0) atomicMax(&s.hi, warp_key);
+    if (bad) s.bad = 1;
     __syncthreads();
-    {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, key_of(top));
-        if (lane == 0) atomicMax(&s.hi, m);
-        if (bad) s.bad = 1;
-    }
-    __syncthreads();
+    uint32_t max_key = s.hi, any_bad = s.bad;
     if (cluster > 1) {
         cluster_wait_acquire();
         if (tid < cluster) {
-            st_cluster(cluster_map(smem_u32(&s.peer_max[rank]), tid), s.hi);
-            st_cluster(cluster_map(smem_u32(&s.peer_bad[rank]), tid), s.bad);
+            st_cluster(cluster_map(smem_u32(&s.peer_max[rank]), tid), max_key);
+            st_cluster(cluster_map(smem_u32(&s.peer_bad[rank]), tid), any_bad);
         }
         cluster_sync_all();
-    } else {
-        if (tid == 0) s.peer_max[0] = s.hi, s.peer_bad[0] = s.bad;
-        __syncthreads();
+        for (int b = 0; b < cluster; ++b) max_key = max(max_key, s.peer_max[b]), any_bad |= s.peer_bad[b];
     }
-    uint32_t max_key = 0, any_bad = 0;
-    for (int c = 0; c < cluster; ++c) max_key = max(max_key, s.peer_max[c]), any_bad |= s.peer_bad[c];
     if (any_bad || max_key <= kNone) {
         if (rank == 0 && tid == 0) {
             p.token[r] = -1;
@@ -182,46 +226,164 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         return;
     }
     const float m = float_of(max_key);
-    const bool greedy = T == 0.f;
-    if (greedy) k = 1, top_p = 1.f, min_p = 0.f;
-    const double per = greedy ? 0.0 : 1.4426950408889634074 / (double)T;     // log2 e / temperature
-    const float ch = per < 1e38 ? (float)per : 1e38f, cl = per < 1e38 ? (float)(per - (double)ch) : 0.f;
-    const float bin_scale = 16.f * (greedy ? 1.4426950f : ch);
-    const int less = V > (1 << 18) ? 1 : 0;              // V weights below 2^46 stay below 2^64
+    const float bin_scale = 16.f * (greedy ? 1.4426950f : fminf(ch, 1e36f));
+    const int less = V > (1 << 18) ? 32 - __clz(V - 1) - 18 : 0;         // V weights below 2^46 stay below 2^64
 
     auto weight = [&](float v) -> u64 {
         const float dh = m - v, bb = dh - m, dl = (m - (dh - bb)) - (v + bb);          // m - v = dh + dl exactly
-        // not contracted: zl is what zh's own rounding left
-        const float zh = __fmul_rn(dh, ch), zl = __fadd_rn(__fmaf_rn(dh, ch, -zh), __fmaf_rn(dh, cl, __fmul_rn(dl, ch)));
-        if (!(zh < 62.f)) return 0;
-        const float grid = __fadd_rn(zh, 49152.f);       // 1.5 * 2^15: its last bit stands for 1 / 256
-        const float f = __fadd_rn(__fsub_rn(zh, __fsub_rn(grid, 49152.f)), zl);
-        const float g = f * -0.69314718f;
-        const float e = fmaf(g * g, fmaf(g, 0.16666667f, 0.5f), g);                    // 2^-f - 1
-        const uint32_t bits = __float_as_uint(grid);
-        const u64 t = s.table[bits & 255u];
-        const float t31 = __uint_as_float(((uint32_t)(t >> 22) & 0x7fffffu) | 0x4e800000u);   // the same as 2^31 ..
-        const int d = (int)(__float_as_uint(fmaf(t31, e, 12582912.f)) - 0x4b400000u);  // .. times e, to the nearest integer
-        return (u64)((long long)t + (long long)d * 32768) >> (((bits >> 8) & 63u) + less);
+        const float grid = __fmaf_rn(dh, ch, 393216.f);  // 1.5 * 2^18: its last bit stands for 1 / 32
+        if (!(grid < 393216.f + 45.f)) return 0;
+        const float f = __fmaf_rn(dl, ch, __fmaf_rn(dh, cl, __fmaf_rn(dh, ch, -__fsub_rn(grid, 393216.f))));
+        const float e = f * fmaf(f, fmaf(f, fmaf(f, 0.0096181291f, -0.055504109f), 0.24022651f), -0.69314718f);    // 2^-f - 1
+        const uint32_t bits = __float_as_uint(grid), t = s.table[(bits & 31u) * 32 + lane];
+        const float t28 = __uint_as_float(((t >> 8) & 0x7fffffu) | 0x4d000000u);       // t is 2^32 times the table's number: 2^28 ..
+        const uint32_t d = __float_as_uint(fmaf(t28, e, 12582912.f)) - 0x4b400000u;    // .. times e, to the nearest integer
+        return ((u64)(t + (d << 4)) << 32) >> (18u + ((bits >> 5) & 63u) + less);
     };
     auto bin_of = [&](float v) { return min(kBins - 1, (int)((m - v) * bin_scale)); };
+    auto sync = [&] {
+        if (cluster > 1) cluster_sync_all();
+        else __syncthreads();
+    };
+
+    // The bounds: a token with (m - x) * bin_scale at `limit` or more is not kept.
+    float limit = INFINITY;
+    const bool by_share = use_p && !use_k && top_p < 0.9999f;
+    if (greedy) {
+        limit = 1e-37f;
+    } else if (use_k || by_share) {
+        each_four([&](float (&f)[4], int) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float b = (m - f[j]) * bin_scale;
+                if (b < (float)(kBins - 1)) atomicAdd(&s.count[(int)b], 1u);
+            }
+        });
+        sync();
+        uint32_t n[2] = {0, 0};
+        for (int b = 0; b < cluster; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                n[j] += cluster > 1 ? ld_cluster(cluster_map(smem_u32(&s.count[2 * tid + j]), b)) : s.count[2 * tid + j];
+        // the weights in the middle of the bins stand for their tokens'
+        const float w0 = (float)n[0] * ex2(-(float)(2 * tid) * 0.0625f - 0.03125f), w1 = (float)n[1] * ex2(-(float)(2 * tid + 1) * 0.0625f - 0.03125f);
+        uint32_t upto = n[0] + n[1];
+        float mass = w0 + w1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            const float w = __shfl_up_sync(0xffffffffu, mass, o);
+            if (lane >= o) upto += v, mass += w;
+        }
+        if (lane == 31) s.warp_count[warp] = upto, s.warp_f[warp] = mass;
+        if (tid == 0) s.bin = kBins;
+        __syncthreads();
+        float all = 0.f;
+        for (int v = 0; v < kWarps; ++v) {
+            if (v < warp) upto += s.warp_count[v], mass += s.warp_f[v];
+            all += s.warp_f[v];
+        }
+        if (use_k) {
+            const uint32_t before = upto - n[0] - n[1];
+            if (before < (uint32_t)k && upto >= (uint32_t)k) s.bin = 2 * tid + (before + n[0] < (uint32_t)k ? 1 : 0);
+        } else {
+            // a share r of weights known to 2.2 % either way is off by at most 0.0434 r (1 - r)
+            const float share = fmaxf(top_p, 0.f), goal = (share + 0.0435f * share * (1.f - share)) * all, before = mass - w0 - w1;
+            if (before < goal && mass >= goal) s.bin = 2 * tid + (before + w0 < goal ? 1 : 0);
+        }
+        __syncthreads();
+        if (s.bin < kBins - 1) limit = (float)(s.bin + 1);
+    }
+    if (use_m && !(use_k && use_p)) limit = fminf(limit, 16.f * (0.01f - __log2f(fminf(min_p, 1.f))) + 1.f);
+
+    // the tokens above the bounds, listed by warp in the row's order; the others' weights, for top-p
+    bool listed = limit < INFINITY;
+    int chunks = seg >> 7;                           // of 128 tokens
+    float* const list = s.value + warp * kList;
+    uint16_t* const offs = s.offset + warp * kList;
+    u64 tail = 0;
+    if (listed) {
+        __syncthreads();                             // the warps' sums have been read
+        const bool want_tail = use_p && !use_k;
+        int n = 0;
+        float rest = 0.f;
+        each_four([&](float (&f)[4], int i) {
+            bool in[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) in[j] = (m - f[j]) * bin_scale < limit;
+            if (want_tail) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float dh = f[j] - m;
+                    rest += in[j] || !(f[j] > -INFINITY) ? 0.f : ex2(fmaf(dh, ch, dh * cl));
+                }
+            }
+            if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) return;
+            unsigned on[4];
+            const unsigned lt = (1u << lane) - 1;
+            int at = n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                on[j] = __ballot_sync(0xffffffffu, in[j]);
+                at += __popc(on[j] & lt);
+                n += __popc(on[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (in[j]) {
+                    if (at < kList) list[at] = f[j], offs[at] = (uint16_t)(i + 4 * lane + j);
+                    ++at;
+                }
+        });
+        if (n <= kList) {
+            chunks = (n + 127) >> 7;
+            for (int i = n + lane; i < 128 * chunks; i += 32) list[i] = -INFINITY, offs[i] = 0;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        if (lane == 0) s.warp_f[warp] = rest, atomicAdd(&s.listed, n <= kList ? (uint32_t)n : 1u << 24);
+        __syncthreads();
+        if (tid == 0) {
+            for (int w = 1; w < kWarps; ++w) s.warp_f[0] += s.warp_f[w];
+            if (cluster == 1) s.peer_listed[0] = s.listed, s.peer_tail[0] = s.warp_f[0];
+        }
+        __syncthreads();
+    }
     // tokens above or at (K, I)
     uint32_t K = kNone, I = 0;                           // I: one past the last index kept of K's
     auto kept = [&](uint32_t key, int i) { return key > K || (key == K && (uint32_t)i < I); };
+    auto four = [&](int i, float (&v)[4], int (&at)[4]) {
+        if (listed) {
+            const float4 a = *reinterpret_cast<const float4*>(list + i + 4 * lane);
+            const ushort4 o = *reinterpret_cast<const ushort4*>(offs + i + 4 * lane);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            at[0] = first + o.x, at[1] = first + o.y, at[2] = first + o.z, at[3] = first + o.w;
+        } else {
+            load(i, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) at[j] = first + i + 4 * lane + j;
+        }
+    };
     auto each = [&](auto&& f) {
-        for (int i = 0; i < seg; i += 128) {
-            const float4 v = *reinterpret_cast<const float4*>(mine + i);
-            f(v.x, at0 + i), f(v.y, at0 + i + 1), f(v.z, at0 + i + 2), f(v.w, at0 + i + 3);
+        if (listed) {
+            for (int i = 0; i < 128 * chunks; i += 128) {
+                float v[4];
+                int at[4];
+                four(i, v, at);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f(v[j], at[j]);
+            }
+        } else {
+            each_four([&](float (&v)[4], int i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f(v[j], first + i + 4 * lane + j);
+            });
         }
     };
     auto add_weight = [&](int b, u64 w) {
         const uint32_t lo = (uint32_t)w, old = atomicAdd(&s.low[b], lo);
         const uint32_t up = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
         if (up) atomicAdd(&s.high[b], up);
-    };
-    auto sync = [&] {
-        if (cluster > 1) cluster_sync_all();
-        else __syncthreads();
     };
     // the first bin at which the count (the sum) reaches the goal, from the histograms of all blocks;
     // goal_of(all_count, all_sum).  Leaves s.bin = kBins where it never does.
@@ -305,16 +467,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             }
         }
     };
-    // min-p as a key: x >= max + T ln(min_p), decided in double
-    uint32_t min_key = 0;
-    if (min_p > 0.f && T < INFINITY) {                   // at infinity all are equally likely
-        const double least = (double)m + (double)T * log((double)fminf(min_p, 1.f));
-        float f = (float)least;
-        if ((double)f < least) f = nextafterf(f, INFINITY);
-        min_key = key_of(f + 0.f);
-    }
-    const double uu = u > 0.f ? (double)u : 0.0;
-    auto target_of = [&](u64 W) { return u >= 1.f ? W - 1 : min(W - 1, (u64)(uu * (double)W)); };
+    const u64 least = !use_m ? 0 : min_p < 1.f ? share_of(min_p, weight(m), true) : weight(m);     // min-p's, of a weight
+    // the share of W that top-p keeps, the place in W that u asks for
+    auto goal_of_p = [&](u64 W) { return max((u64)1, share_of(fmaxf(top_p, 0.f), W, true)); };
+    auto target_of = [&](u64 W) { return u < 1.f ? share_of(u > 0.f ? u : 0.f, W, false) : u >= 1.f ? W - 1 : (u64)0; };
     auto emit = [&](int i, u64 w, u64 W) {
         p.token[r] = i;
         if (p.logprob) p.logprob[r] = log_share(w, W);
@@ -348,9 +504,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         const u64 goal = goal_of(W);
         if (!(goal >= before && goal - before < sum)) return;       // another warp's
-        for (int i = 0; i < seg; i += 128) {
-            const float4 v = *reinterpret_cast<const float4*>(mine + i);
-            const u64 w[4] = {f(v.x, at0 + i), f(v.y, at0 + i + 1), f(v.z, at0 + i + 2), f(v.w, at0 + i + 3)};
+        for (int i = 0; i < 128 * chunks; i += 128) {
+            float v[4];
+            int at[4];
+            four(i, v, at);
+            const u64 w[4] = {f(v[0], at[0]), f(v[1], at[1]), f(v[2], at[2]), f(v[3], at[3])};
             u64 upto = w[0] + w[1] + w[2] + w[3];
             const u64 own = upto;
 #pragma unroll
@@ -362,9 +520,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             if (past) {
                 if (lane == __ffs(past) - 1) {
                     u64 b = before + upto - own;
-                    int j = 0;
-                    while (b + w[j] <= goal) b += w[j++];
-                    found(at0 + i + j, w[j], W);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (b <= goal && b + w[j] > goal) found(at[j], w[j], W);
+                        b += w[j];
+                    }
                 }
                 return;
             }
@@ -372,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
     };
     // From the candidates, which are all that may be kept: the filters and the draw.  limit: top-k, where it is still to be
-    // applied; S: the sum that top-p takes its share of, or 0 for that of the top-k.
-    auto finish = [&](uint32_t limit, u64 S) {
+    // applied; S: the sum that top-p takes its share of, or 0 for that of the top-k and `rest`.
+    auto finish = [&](uint32_t limit, u64 S, u64 rest) {
         const int n = (int)s.n_cand;
         uint32_t key, idx;
         u64 w, upto;
@@ -386,12 +546,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 const uint32_t last = min(limit, (uint32_t)n) - 1;
                 if (tid < n && (uint32_t)pos == last) s.all_sum = upto;
                 __syncthreads();
-                S = s.all_sum;
+                S = s.all_sum + rest;
             }
-            const u64 goal = max((u64)1, (u64)ceil((double)fmaxf(top_p, 0.f) * (double)S));
+            const u64 goal = goal_of_p(S);
             keep = keep && upto - w < goal;
         }
-        keep = keep && key >= min_key;
+        keep = keep && w >= least;
         if (tid < n) s.kept_w[tid] = keep ? w : 0;
         __syncthreads();
         if (keep) {
@@ -407,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     };
 
     // Finds where the run ends that reaches the goal and puts (K, I) there; true where finish() has done the rest.
-    auto select = [&](bool by_sum, auto&& goal_of, uint32_t limit) -> bool {
+    auto select = [&](bool by_sum, auto&& goal_of, uint32_t limit, u64 rest) -> bool {
         each([&](float v, int i) {
             const uint32_t key = key_of(v);
             if (key > kNone && kept(key, i)) {
@@ -419,10 +579,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         u64 goal = border(by_sum, goal_of);
         const int b0 = (int)s.bin;
         if (b0 == kBins) return false;                   // the goal is past the row: all are kept
-        const u64 all_sum = by_sum ? s.all_sum : 0;
+        const u64 all_sum = by_sum ? s.all_sum + rest : 0;
         if (s.base_count + s.bin_count <= kCap) {
             gather([&](float v, uint32_t key, int i) { return kept(key, i) && bin_of(v) <= b0; });
-            if (rank == 0) finish(limit, all_sum);
+            if (rank == 0) finish(limit, all_sum, 0);
             return true;
         }
         uint32_t lo = 0, hi = 0xffffffffu;
@@ -513,38 +673,65 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         return false;
     };
 
-    bool histograms_used = false;
-    if (k > 0 && k < V) {
-        if (select(false, [&](uint32_t, u64) { return (u64)k; }, (uint32_t)k)) return;
-        histograms_used = K == kNone;
+    if (listed) {
+        if (cluster > 1) {
+            if (tid < cluster) {
+                st_cluster(cluster_map(smem_u32(&s.peer_listed[rank]), tid), s.listed);
+                st_cluster(cluster_map(smem_u32(&s.peer_tail[rank]), tid), __float_as_uint(s.warp_f[0]));
+            }
+            sync();
+        }
+        uint32_t n = 0;
+        float others = 0.f;
+        for (int b = 0; b < cluster; ++b) n += s.peer_listed[b], others += s.peer_tail[b];
+        tail = (u64)(others * (float)(0.995 * 0x1p46 * 0.98922801319397548)) >> less;        // weight()'s unit
+        if (n <= kCap) {
+            gather([&](float, uint32_t, int) { return true; });
+            if (rank == 0) finish(use_k ? (uint32_t)k : 0xffffffffu, 0, use_k ? 0 : tail);
+            return;
+        }
+        if (n >= 1u << 24) listed = false, chunks = seg >> 7, tail = 0;
+    } else if (use_k || by_share) {
+        sync();                                              // every block has read the counts
     }
-    if (top_p < 1.f) {
-        if (histograms_used) {       // top-k left all: its counts are cleared once every block has read them
+    if (use_k || by_share) {
+        for (int i = tid; i < kBins; i += kThreads) s.count[i] = 0;
+        __syncthreads();
+    }
+    if (use_k) {
+        if (select(false, [&](uint32_t, u64) { return (u64)k; }, (uint32_t)k, 0)) return;
+    }
+    if (use_p) {
+        if (use_k && K == kNone) {       // top-k left all: its counts are cleared once every block has read them
             sync();
             for (int i = tid; i < kBins; i += kThreads) s.count[i] = 0;
             __syncthreads();
         }
-        if (select(true, [&](uint32_t, u64 all) { return max((u64)1, (u64)ceil((double)fmaxf(top_p, 0.f) * (double)all)); }, 0xffffffffu)) return;
+        const u64 rest = use_k ? 0 : tail;
+        if (select(true, [&](uint32_t, u64 all) { return goal_of_p(all + rest); }, 0xffffffffu, rest)) return;
     }
-    if (min_key > K) K = min_key - 1, I = 0;             // everything at min_key and above, and nothing else
-    locate([&](float v, int i) -> u64 { return kept(key_of(v), i) ? weight(v) : 0; }, target_of, emit);
+    locate([&](float v, int i) -> u64 {
+        if (!kept(key_of(v), i)) return 0;
+        const u64 w = weight(v);
+        return w >= least ? w : 0;
+    }, target_of, emit);
 }
 
 template <int DT>
 cudaError_t launch(const SampleParams& p, int num_sms, int pdl, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = set_once(sample_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSlice * 4, done);
+    cudaError_t e = set_once(sample_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared), done);
     if (e != cudaSuccess) return e;
-    // blocks of 64 KB, so that two to an SM overlap their loads with their passes;
-    // more to a row where there are few rows
+    // up to 4350 tokens a warp, of which its list holds a fifth and more; more blocks
+    // to a row where there are few rows
     const int64_t span = p.vocab + 3;
     int cluster = 1;
-    while (cluster < 8 && (span > cluster * (int64_t)(16384) || (p.rows * cluster < num_sms && span > cluster * 2048))) cluster *= 2;
+    while (cluster < 8 && (span > cluster * (int64_t)(kWarps * 4350) || (p.rows * cluster < num_sms && span > cluster * 2048))) cluster *= 2;
     const int64_t seg = ceil_div(span, (int64_t)cluster * kWarps * 128) * 128;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.rows * cluster));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)seg * kWarps * sizeof(float);
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;

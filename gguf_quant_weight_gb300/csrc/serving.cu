@@ -212,7 +212,7 @@ int gguf_logits_adjust(const void* logits, int dt, int64_t ld, int64_t rows, int
 int gguf_sample(const void* logits, int dt, int64_t ld, int64_t rows, int64_t vocab, const gguf_sampler* sampler,
                 const float* u, int32_t* token, float* logprob, gguf_stream_t stream) {
     if (!logits || !u || !token || rows <= 0 || vocab <= 0 || ld < vocab) return GGUF_ERR_INVALID_ARG;
-    if (!valid_dtype(dt) || rows > (1 << 16) - 1 || vocab > 400000 || ld > (int64_t(1) << 38)) return GGUF_ERR_UNSUPPORTED;
+    if (!valid_dtype(dt) || rows > (1 << 16) - 1 || vocab > (1 << 22) || ld > (int64_t(1) << 38)) return GGUF_ERR_UNSUPPORTED;
     SampleParams p{logits, ld, (int)rows, (int)vocab, dt, sampler ? *sampler : gguf_sampler{}, u, token, logprob};
     if (!aligned16(logits)) return GGUF_ERR_MISALIGNED;
     for (const void* a : {(const void*)u, (const void*)token, (const void*)logprob, (const void*)p.s.temperature,

@@ -94,10 +94,11 @@ struct MoeFfnParams {
     const void* residual;
     void* y;
     // set by the launch.  In the workspace: hidden values [T * top_k][F], then as
-    // the down kernel's columns, and the columns' scales
+    // the down kernel's columns, the columns' scales, and what up makes of the ids
     float* h;
     uint8_t* columns;
     float* column_scales;
+    uint8_t* routes;
     int x_parts, h_parts;                // columns that a row of x and of h takes
     int up_tiles, up_rt, up_stages, up_slot, up_resident;
     int down_stages, splits;

@@ -480,15 +480,16 @@ typedef struct {
  * the filters, the first i in the order of the vocabulary with
  *   w_0 + ... + w_i > u[r] * (sum of all w),
  * u [rows] f32 uniform in [0, 1) (below 0 and NaN count as 0; at 1 and above the
- * last token that passes is taken).  The sums are exact to about 1e-11 of the whole,
- * so that the token is the one that 64-bit arithmetic gives.
+ * last token that passes is taken).  The weights are accurate to about 1e-9 of
+ * themselves and their sums exact, so that the token is the one that 64-bit
+ * arithmetic gives but where u or top_p falls that close to a border.
  *   logprob  f32 [rows] or NULL: log(w_token / sum of all w), 0 where the
  *            temperature is 0
  * A row without a distribution (a NaN or +inf among its logits, nothing but
  * -inf, its temperature) gives token -1 and logprob NaN.
  * The result does not depend on timing, nor on the other rows.  logits 16-byte
  * aligned (rows may start anywhere), the arrays 4-byte aligned.  vocab at most
- * 400000.  sampler NULL: no filters, temperature 1.
+ * 2^22.  sampler NULL: no filters, temperature 1.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, NO_DEVICE, CUDA. */
 int gguf_sample(const void* logits, int dt, int64_t ld, int64_t rows, int64_t vocab, const gguf_sampler* sampler,
                 const float* u, int32_t* token, float* logprob, gguf_stream_t stream);

@@ -99,7 +99,7 @@ def test_sample_refusals(lib):  # noqa: F811
 
     assert call(x=None) == INV and call(u=None) == INV and call(token=None) == INV and call(rows=0) == INV and call(vocab=0) == INV
     assert call(ld=99) == INV
-    assert call(dt=3) == UNS and call(rows=1 << 16) == UNS and call(vocab=400001, ld=400001) == UNS and call(ld=1 << 39) == UNS
+    assert call(dt=3) == UNS and call(rows=1 << 16) == UNS and call(vocab=(1 << 22) + 1, ld=1 << 23) == UNS and call(ld=1 << 39) == UNS
     assert call(x=24) == MIS and call(u=18) == MIS and call(token=18) == MIS and call(lp=17) == MIS
     for name in ("temperature", "top_k", "top_p", "min_p"):
         assert call(**{name: 18}) == MIS
