@@ -67,9 +67,9 @@ __device__ __forceinline__ uint32_t key_of(float v) {
 }
 __device__ __forceinline__ float float_of(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k); }
 
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+__device__ __forceinline__ uint2 ld_cluster2(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
     return v;
 }
 __device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
@@ -104,7 +104,7 @@ struct Shared {
     float value[kWarps * kList];                         // the warps' lists: logits, and where in the warp's run
     uint16_t offset[kWarps * kList];
     uint32_t table[32 * 32];                             // kTable, a copy for each lane's bank
-    uint32_t count[kBins], low[kBins], high[kBins];      // of a histogram: tokens, and their weights' sums
+    alignas(8) uint32_t count[kBins], low[kBins], high[kBins];      // of a histogram: tokens, and their weights' sums
     uint32_t cand_key[kCap], cand_idx[kCap], n_cand;
     u64 cand_w[kCap], kept_w[kCap];
     u64 warp_sum[kWarps];
@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
     const float m = float_of(max_key);
     const float bin_scale = 16.f * (greedy ? 1.4426950f : fminf(ch, 1e36f));
+    float fine_scale = bin_scale;                    // of the histograms: all bins for what is listed
     const int less = V > (1 << 18) ? 32 - __clz(V - 1) - 18 : 0;         // V weights below 2^46 stay below 2^64
 
     auto weight = [&](float v) -> u64 {
@@ -240,10 +241,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const uint32_t d = __float_as_uint(fmaf(t28, e, 12582912.f)) - 0x4b400000u;    // .. times e, to the nearest integer
         return ((u64)(t + (d << 4)) << 32) >> (18u + ((bits >> 5) & 63u) + less);
     };
-    auto bin_of = [&](float v) { return min(kBins - 1, (int)((m - v) * bin_scale)); };
+    auto bin_of = [&](float v) { return min(kBins - 1, (int)((m - v) * fine_scale)); };
     auto sync = [&] {
         if (cluster > 1) cluster_sync_all();
         else __syncthreads();
+    };
+
+    // counters 2 tid and 2 tid + 1 of all blocks, their loads on their way together
+    auto pair_of_all = [&](uint32_t* counters, uint32_t (&sum)[2]) {
+        uint2 v[8];
+        if (cluster == 1) v[0] = *reinterpret_cast<const uint2*>(counters + 2 * tid);
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+            if (cluster > 1 && b < cluster) v[b] = ld_cluster2(cluster_map(smem_u32(counters + 2 * tid), b));
+        sum[0] = v[0].x, sum[1] = v[0].y;
+#pragma unroll
+        for (int b = 1; b < 8; ++b)
+            if (b < cluster) sum[0] += v[b].x, sum[1] += v[b].y;
     };
 
     // The bounds: a token with (m - x) * bin_scale at `limit` or more is not kept.
@@ -260,11 +274,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             }
         });
         sync();
-        uint32_t n[2] = {0, 0};
-        for (int b = 0; b < cluster; ++b)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                n[j] += cluster > 1 ? ld_cluster(cluster_map(smem_u32(&s.count[2 * tid + j]), b)) : s.count[2 * tid + j];
+        uint32_t n[2];
+        pair_of_all(s.count, n);
         // the weights in the middle of the bins stand for their tokens'
         const float w0 = (float)n[0] * ex2(-(float)(2 * tid) * 0.0625f - 0.03125f), w1 = (float)n[1] * ex2(-(float)(2 * tid + 1) * 0.0625f - 0.03125f);
         uint32_t upto = n[0] + n[1];
@@ -307,15 +318,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const bool want_tail = use_p && !use_k;
         int n = 0;
         float rest = 0.f;
+        // the same bound for the logits themselves, a little below
+        const float above = fmaxf(m - limit / bin_scale - 1e-6f * (fabsf(m) + limit / bin_scale), -3.402823466e38f);
         each_four([&](float (&f)[4], int i) {
             bool in[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) in[j] = (m - f[j]) * bin_scale < limit;
-            if (want_tail) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float dh = f[j] - m;
-                    rest += in[j] || !(f[j] > -INFINITY) ? 0.f : ex2(fmaf(dh, ch, dh * cl));
+            for (int j = 0; j < 4; ++j) {
+                in[j] = f[j] >= above;
+                if (want_tail) {
+                    const float dh = fmaxf(f[j] - m, -1e30f);        // -inf times cl would be NaN
+                    const float w = ex2(fmaf(dh, ch, dh * cl));
+                    rest += in[j] ? 0.f : w;
                 }
             }
             if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) return;
@@ -389,20 +402,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     // goal_of(all_count, all_sum).  Leaves s.bin = kBins where it never does.
     auto border = [&](bool by_sum, auto&& goal_of) {
         sync();
-        uint32_t c[2] = {0, 0};
+        uint32_t c[2];
         u64 w[2] = {0, 0};
-        for (int b = 0; b < cluster; ++b) {
+        pair_of_all(s.count, c);
+        if (by_sum) {
+            const uint32_t* const low = s.low + 2 * tid;
+            uint2 v[8];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int at = 2 * tid + j;
-                if (cluster > 1) {
-                    c[j] += ld_cluster(cluster_map(smem_u32(&s.count[at]), b));
-                    if (by_sum) w[j] += (u64)ld_cluster(cluster_map(smem_u32(&s.low[at]), b)) + ((u64)ld_cluster(cluster_map(smem_u32(&s.high[at]), b)) << 32);
-                } else {
-                    c[j] += s.count[at];
-                    if (by_sum) w[j] += (u64)s.low[at] + ((u64)s.high[at] << 32);
-                }
-            }
+            for (int b = 0; b < 8; ++b)
+                if (b < cluster) v[b] = cluster > 1 ? ld_cluster2(cluster_map(smem_u32(low), b)) : *reinterpret_cast<const uint2*>(low);
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+                if (b < cluster) w[0] += v[b].x, w[1] += v[b].y;
+            uint32_t hi[2];
+            pair_of_all(s.high, hi);
+            w[0] += (u64)hi[0] << 32, w[1] += (u64)hi[1] << 32;
         }
         uint32_t ci = c[0] + c[1];
         u64 wi = w[0] + w[1];
@@ -459,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         __syncthreads();
         if (tid < n) {
+#pragma unroll 4
             for (int j = 0; j < n; ++j) {
                 const uint32_t kj = s.cand_key[j], ij = s.cand_idx[j];
                 const bool before = kj > key || (kj == key && ij < idx);
@@ -556,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         __syncthreads();
         if (keep) {
             u64 c = 0, W = 0;
+#pragma unroll 4
             for (int j = 0; j < n; ++j) {
                 const u64 wj = s.kept_w[j];
                 W += wj;
@@ -691,6 +707,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             return;
         }
         if (n >= 1u << 24) listed = false, chunks = seg >> 7, tail = 0;
+        else if (limit < (float)kBins) fine_scale = bin_scale * ((float)(kBins - 1) / limit);
     } else if (use_k || by_share) {
         sync();                                              // every block has read the counts
     }
@@ -722,11 +739,11 @@ cudaError_t launch(const SampleParams& p, int num_sms, int pdl, cudaStream_t s) 
     static std::atomic<uint64_t> done{0};
     cudaError_t e = set_once(sample_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared), done);
     if (e != cudaSuccess) return e;
-    // up to 4350 tokens a warp, of which its list holds a fifth and more; more blocks
+    // up to 2175 tokens a warp, of which its list holds two fifths; more blocks
     // to a row where there are few rows
     const int64_t span = p.vocab + 3;
     int cluster = 1;
-    while (cluster < 8 && (span > cluster * (int64_t)(kWarps * 4350) || (p.rows * cluster < num_sms && span > cluster * 2048))) cluster *= 2;
+    while (cluster < 8 && (span > cluster * (int64_t)(kWarps * 2175) || (p.rows * cluster < num_sms && span > cluster * 2048))) cluster *= 2;
     const int64_t seg = ceil_div(span, (int64_t)cluster * kWarps * 128) * 128;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.rows * cluster));
