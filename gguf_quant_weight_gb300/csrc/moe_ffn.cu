@@ -346,6 +346,14 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// the same, onto zeros
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
 __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 __device__ __forceinline__ float f16_low(uint32_t v) { return __half2float(__ushort_as_half((unsigned short)(v & 0xffffu))); }
@@ -412,7 +420,7 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
 #pragma unroll
         for (int n = 0; n < TILES; ++n)
             b[n] = col.values(n, j);
-        float part[TILES][4] = {};
+        float part[TILES][4];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             uint32_t a[4];
@@ -433,13 +441,12 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
                     }
                 }
             }
-            if (narrow && half == 1) {
 #pragma unroll
-                for (int n = 0; n < TILES; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.f;
+            for (int n = 0; n < TILES; ++n) {
+                if (half == 0) mma0(part[n], a[0], a[1], a[2], a[3], b[n].x, b[n].y);
+                else if (narrow) mma0(part[n], a[0], a[1], a[2], a[3], b[n].z, b[n].w);
+                else mma(part[n], a[0], a[1], a[2], a[3], b[n].z, b[n].w);
             }
-#pragma unroll
-            for (int n = 0; n < TILES; ++n)
-                mma(part[n], a[0], a[1], a[2], a[3], half ? b[n].z : b[n].x, half ? b[n].w : b[n].y);
             if (narrow || half == 1) {
                 const float s0 = scale(0, j, half), s1 = scale(1, j, half);
 #pragma unroll
@@ -457,7 +464,7 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
     for (int n = 0; n < TILES; ++n) {
         const float2 back = col.back(n);
         if constexpr (has_min(QT)) {
-            float low[4] = {};
+            float low[4];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 uint32_t a[2];
@@ -476,7 +483,8 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
                     }
                 }
                 const uint2 s = col.sums(n, k);         // the same mins with the sums' first part and their second
-                mma(low, a[0], a[1], a[0], a[1], s.x, s.y);
+                if (k == 0) mma0(low, a[0], a[1], a[0], a[1], s.x, s.y);
+                else mma(low, a[0], a[1], a[0], a[1], s.x, s.y);
             }
             // Q4_1, Q5_1 add their m
             const float m0 = block32(QT) ? 1.f : -0x1p24f * dmin[0], m1 = block32(QT) ? 1.f : -0x1p24f * dmin[1];
@@ -558,6 +566,36 @@ __device__ __forceinline__ void fetch_piece(uint32_t slot, const Matrix& m, int 
     }
 }
 
+// The same with what does not change from piece to piece kept in registers.
+template <int QT>
+struct Fetcher {
+    static constexpr int UNITS = piece_stride(QT) / 16, N = (16 * UNITS + 31) / 32;
+    uint32_t rel[N];                // where this lane's units lie from the tile's first row on
+    __device__ __forceinline__ void init(const Matrix& m, int lane) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = 32 * i + lane, row = u / UNITS;
+            rel[i] = (uint32_t)row * (uint32_t)m.rb + 16 * (u - row * UNITS);
+        }
+    }
+    __device__ __forceinline__ void fetch(uint32_t slot, const Matrix& m, int row0, int c, int lane) const {
+        const uint8_t* const base = m.w + (int64_t)row0 * m.rb + c * piece_bytes(QT);
+        if (row0 + 16 > m.n || (!piece_aligned(QT) && m.end - base <= 16 * m.rb)) return fetch_piece<QT>(slot, m, row0, c, lane);
+        const int low = (int)(reinterpret_cast<uintptr_t>(base) & 15), bytes = min(piece_bytes(QT), (int)m.rb - c * piece_bytes(QT));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = 32 * i + lane;
+            if (16 * UNITS % 32 && i == N - 1 && u >= 16 * UNITS) break;
+            if constexpr (piece_aligned(QT)) {
+                copy16(slot + 16 * u, base + rel[i], 16);
+            } else {
+                const int off = (low + (int)rel[i]) & 15, at = 16 * (u % UNITS);
+                if (at < off + bytes) copy16(slot + 16 * u, base + (int)(rel[i] - (uint32_t)off), 16);
+            }
+        }
+    }
+};
+
 template <int QT>
 __device__ __forceinline__ void read_piece(Raw<QT> (&r)[2], const uint8_t* slot, const Matrix& m, int row0, int c, int nsub, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -578,10 +616,11 @@ __device__ __forceinline__ float activate(float a, int act) {
 
 // ---------------------------------------------------------------- gate, up, activation
 
-// A job is `rt` tiles of 16 rows of gate and up, for one group; a block takes a
-// run of jobs, so that it makes a group's columns once for many of them.  Of its warps, wp =
-// 8 / rt share a tile of one matrix, each taking every wp-th chunk of K; their
-// sums meet in shared memory.
+// A job is 16 rows of gate and up, for one group; a block takes a run of jobs, so
+// that it makes a group's columns once for many of them.  Its warps work in teams of
+// 2 wp, each on its own job: of each matrix wp warps take every wp-th chunk of K, and
+// their sums meet in shared memory.  Small teams meet seldom for what they do in
+// between; larger ones are for calls that have too few jobs.
 // QT: both matrices' type, or -1 where they differ.
 struct ColumnsInShared {
     const uint8_t* at;              // the chunk's tiles, at this lane's column and 16 bytes
@@ -618,8 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
         for (int i = tid; i < (int)(Routes::bytes(entries) / 16); i += kThreads) to[i + 1] = from[i];
         if (tid == 0) to[0] = make_uint4(both >> 16, 0, 0, 0);
     }
-    const int rt = p.up_rt, wp = 8 / rt;
-    const int K = (int)p.K, F = (int)p.F, per_group = (F + 16 * rt - 1) / (16 * rt), jobs = per_group * groups;
+    const int K = (int)p.K, F = (int)p.F, per_group = (F + 15) / 16, jobs = per_group * groups;
     // The blocks' shares of the jobs, where a job of two tiles counts 4 and one of one tile 3 (the blocks
     // are taken apart once either way).
     __shared__ int s_from[2], s_wide;
@@ -648,35 +686,41 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
     __syncthreads();
     const int job0 = s_from[0], job1 = s_from[1];
     // this warp's part of a job
-    const int my_tile = warp / (2 * wp), mat = (warp / wp) & 1, c0 = warp % wp;
+    const int wp = p.up_wp, teams = kWarps / (2 * wp), team = warp / (2 * wp), mat = (warp / wp) & 1, c0 = warp % wp;
     const int qt = mat ? p.up_type : p.gate_type;
     Matrix m;
     m.rb = mat ? p.up_rb : p.gate_rb;
     m.n = F;
     m.end = (mat ? p.up : p.gate) + p.n_expert * p.F * m.rb;
     auto matrix_of = [&](int group) { return (mat ? p.up : p.gate) + routes.up[group].expert * p.F * m.rb; };
-    // a job is a group and a step through its rows; the ring's next piece to fetch runs ahead
-    int group = job0 / per_group, step = job0 - group * per_group;
-    int fjob = job0, fgroup = group, fstep = step, fc = c0, fslot = 0, slot = 0;
+    // A group's jobs [begin, end) go to the teams in turn.  The ring's next piece to fetch runs ahead.
+    int fgroup = job0 / per_group, fend = min(job1, (fgroup + 1) * per_group), fjob = job0 + team, fc = c0, fslot = 0, slot = 0;
     Matrix fm = m;
-    if (fjob < job1) fm.w = matrix_of(fgroup);
+    Fetcher<(QT < 0 ? GGUF_Q4_K : QT)> fetcher;
+    fetcher.init(m, lane);
+    auto settle = [&] {             // to a job that there is
+        while (fjob >= fend && fend < job1) fjob = fend + team, ++fgroup, fend = min(job1, fend + per_group);
+        if (fjob < fend) fm.w = matrix_of(fgroup);
+    };
+    settle();
     auto fetch = [&] {
-        if (fjob < job1 && fc < chunks) {
-            const int row0 = (fstep * rt + my_tile) * 16;
-            if constexpr (QT >= 0) fetch_piece<QT>(ring_at + fslot * p.up_slot, fm, row0, fc, lane);
+        if (fjob < fend) {
+            const int row0 = (fjob - fgroup * per_group) * 16;
+            if constexpr (QT >= 0) fetcher.fetch(ring_at + fslot * p.up_slot, fm, row0, fc, lane);
             else with_type(qt, [&](auto q) { fetch_piece<decltype(q)::value>(ring_at + fslot * p.up_slot, fm, row0, fc, lane); });
             fslot = fslot + 1 == p.up_stages ? 0 : fslot + 1;
             fc += wp;
-            if (fc >= chunks && ++fjob < job1) {
+            if (fc >= chunks) {
                 fc = c0;
-                if (++fstep == per_group) fstep = 0, fm.w = matrix_of(++fgroup);
+                fjob += teams;
+                if (fjob >= fend) settle();
             }
         }
         copies_commit();
     };
     for (int i = 0; i < p.up_stages; ++i) fetch();
 
-    int made = -1, buffer = 0;
+    int buffer = 0;
     Group g{};
     auto make = [&](int k, int c, int at) {         // the columns of the group's row k, chunk c
         const int col = k * parts, token = routes.list[g.first + k] / p.top_k;
@@ -685,18 +729,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
                                        token * p.K + c * kChunk, nsub, lane);
         if (lane < parts) scales[at * 8 * tiles + col + lane] = back;
     };
-    for (int job = job0; job < job1; ++job, buffer ^= 1) {
-        if (group != made) {
-            made = group;
-            g = routes.up[group];
-            m.w = matrix_of(group);
-            // every warp has passed the barrier of the job before, so nothing reads the old columns
-            if (p.up_resident)
-                for (int i = warp; i < g.n * chunks; i += kWarps) make(i % g.n, i / g.n, i / g.n);
-            __syncthreads();
-        }
-        const int n_tiles = (g.n * parts + 7) >> 3;
-        const int row0 = (step * rt + my_tile) * 16;
+    for (int group = job0 / per_group, begin = job0; begin < job1; ++group) {
+      const int end = min(job1, (group + 1) * per_group);
+      g = routes.up[group];
+      m.w = matrix_of(group);
+      if (p.up_resident) {
+          if (begin != job0) __syncthreads();       // the columns before are read
+          for (int i = warp; i < g.n * chunks; i += kWarps) make(i % g.n, i / g.n, i / g.n);
+          __syncthreads();
+      }
+      const int n_tiles = (g.n * parts + 7) >> 3;
+      for (int job = begin + team; job < end; job += teams, buffer ^= 1) {
+        const int row0 = (job - group * per_group) * 16;
         float acc[kTiles][4] = {};
         for (int c = c0; c < chunks; c += wp) {
             const int at = p.up_resident ? c : warp;
@@ -729,24 +773,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
             *reinterpret_cast<float2*>(at) = make_float2(acc[k][0], acc[k][1]);
             *reinterpret_cast<float2*>(at + 64 * tiles) = make_float2(acc[k][2], acc[k][3]);
         }
-        __syncthreads();
-        // the sums of two jobs have places of their own, so the warps go on meanwhile
-        const int used = min(wp, chunks);
-        for (int i = tid; i < rt * 16 * 8 * tiles; i += kThreads) {
-            const int r = i & 15, k = (i >> 4) & (8 * tiles - 1), tile = i / (128 * tiles);
-            const int row = (step * rt + tile) * 16 + r;
-            if (k >= g.n || row >= F) continue;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(64 * wp) : "memory");
+        // the sums of two jobs have places of their own, so the team goes on meanwhile
+        for (int i = tid - team * 64 * wp; i < 128 * tiles; i += 64 * wp) {
+            const int r = i & 15, k = i >> 4;
+            if (k >= g.n || row0 + r >= F) continue;
             float v[2] = {0.f, 0.f};
-            const float* from = sums + (size_t)(buffer * kWarps + tile * 2 * wp) * 128 * tiles + r * 8 * tiles + k * parts;
+            const float* from = sums + (size_t)(buffer * kWarps + team * 2 * wp) * 128 * tiles + r * 8 * tiles + k * parts;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                for (int w = 0; w < used; ++w) {
+                for (int w = 0; w < wp; ++w) {
                     const float* f = from + (size_t)(q * wp + w) * 128 * tiles;
                     v[q] += parts == 2 ? f[0] + f[1] : f[0];
                 }
-            p.h[(int64_t)routes.list[g.first + k] * p.F + row] = activate(v[0], p.act) * v[1];
+            p.h[(int64_t)routes.list[g.first + k] * p.F + row0 + r] = activate(v[0], p.act) * v[1];
         }
-        if (++step == per_group) step = 0, ++group;
+      }
+      begin = end;
     }
 }
 
@@ -804,10 +847,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnP
     auto matrix_of = [&](int item) { return p.down + routes.down[item / splits].expert * p.K * p.down_rb; };
     int fitem = warp, fc = warp % splits, fslot = 0, slot = 0;
     Matrix fm = m;
+    Fetcher<QT> fetcher;
+    fetcher.init(m, lane);
     if (fitem < items) fm.w = matrix_of(fitem);
     auto fetch = [&] {
         if (fitem < items) {
-            fetch_piece<QT>(ring_at + fslot * kSlot, fm, row0, fc, lane);
+            fetcher.fetch(ring_at + fslot * kSlot, fm, row0, fc, lane);
             fslot = fslot + 1 == p.down_stages ? 0 : fslot + 1;
             fc += splits;
             if (fc >= chunks && (fitem += kWarps) < items) fc = fitem % splits, fm.w = matrix_of(fitem);
@@ -961,8 +1006,10 @@ int moe_ffn_launch(MoeFfnParams p, void* workspace, int num_sms, int pdl, cudaSt
     p.up_stages = stages(up_fixed, p.up_slot);
     // what making the routes takes is shared with the columns and the ring
     const size_t up_smem = std::max(up_fixed + (size_t)kWarps * p.up_stages * p.up_slot, routes + routes_scratch(entries, p.n_expert));
-    p.up_rt = chunks >= 8 ? 1 : chunks >= 4 ? 2 : chunks >= 2 ? 4 : 8;
-    const int64_t most = ceil_div(p.F, 16 * p.up_rt) * entries;
+    const int64_t jobs = ceil_div(p.F, 16) * std::min(entries, p.n_expert);
+    p.up_wp = jobs <= num_sms ? 8 : jobs <= 2 * num_sms ? 4 : 2;
+    while (p.up_wp > chunks) p.up_wp /= 2;
+    const int64_t most = ceil_div(p.F, 16) * entries;
     int st = dispatch_up(p.gate_type == p.up_type ? p.gate_type : -1, p, (int)std::min<int64_t>(num_sms, most),
                          up_smem, pdl, s);
     if (st != GGUF_OK) return st;
@@ -971,10 +1018,11 @@ int moe_ffn_launch(MoeFfnParams p, void* workspace, int num_sms, int pdl, cudaSt
     st = cuda_status(launch_pdl(moe_ffn_columns_kernel, dim3((unsigned)ceil_div(entries * fchunks, 8)), dim3(256), 0, s, pdl, p));
     if (st != GGUF_OK) return st;
 
-    // down: with few experts, several warps share one's chunks, as far as there is room for their sums and two pieces to a warp
+    // down: with few experts, several warps share one's chunks, so that each warp has some three shares to take, as
+    // far as there is room for their sums and two pieces to a warp
     const size_t slot = slot_bytes(p.down_type), one = (size_t)entries * 16 * 4, down_fixed = routes + (entries + 3) / 4 * 16;
     const int64_t room = ((int64_t)kSmem - (int64_t)down_fixed - (int64_t)(kWarps * 2 * slot)) / (int64_t)one;
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({kWarps / std::min(entries, p.n_expert), fchunks, room}));
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(3 * kWarps, std::min(entries, p.n_expert)), fchunks, room}));
     p.down_stages = stages(down_fixed + p.splits * one, slot);
     return dispatch_down(p, down_fixed + p.splits * one + kWarps * p.down_stages * slot, pdl, s);
 }

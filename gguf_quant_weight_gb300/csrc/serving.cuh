@@ -100,7 +100,7 @@ struct MoeFfnParams {
     float* column_scales;
     uint8_t* routes;
     int x_parts, h_parts;                // columns that a row of x and of h takes
-    int up_tiles, up_rt, up_stages, up_slot, up_resident;
+    int up_tiles, up_wp, up_stages, up_slot, up_resident;
     int down_stages, splits;
 };
 
