@@ -24,11 +24,16 @@
 // Mins: sum_j m_j * (sum of sub-block j's activations) is one more product, of
 // the mins (exact in f16) with the sums in two f16 parts.
 //
-// Each warp streams its own pieces of the weights, 16 rows x 256 values, through a ring of
-// asynchronous copies that runs on across the experts and row tiles of its block,
-// one block to an SM.  A row's piece is copied in whole 16-byte units from the boundary before it;
-// the rows lie an odd multiple of 16 bytes apart, so that the eight rows that a
-// load of the warp meets fall into different banks.
+// Each warp streams its own pieces of the weights, 16 rows x 256 values, through a
+// ring of asynchronous copies that runs on across the experts and row tiles of its
+// block, one block to an SM.  A row's piece is copied from the 16-byte boundary
+// before it on; the rows lie an odd multiple of 16 bytes apart, so that the eight
+// rows that a load of the warp meets fall into different banks.  Where pieces start at such a
+// boundary (Q4_K, Q5_K) the lanes copy 16 bytes each; where they do not, which
+// costs the lanes the arithmetic of every row's offset, one bulk copy moves a row.
+// (A bulk copy of some 150 bytes holds its engine for about 19 cycles: with those
+// 64 tokens through Q4_K experts take 145 us and not 122, and without them three
+// tokens' Q6_K projection of 14336 takes 127 us and not 101.)
 #include <type_traits>
 
 #include "formats.cuh"
@@ -44,7 +49,7 @@ constexpr int kColStride = 2 * kChunk + 64;       // bytes of a column: f16 valu
                                                   // parts; 8 lanes' 16 bytes from 2 columns meet no bank twice
 constexpr int kTileBytes = 8 * kColStride;
 constexpr int kTiles = 2;                         // of 8 columns, at most
-constexpr int kMaxStages = 3;                     // pieces of a warp on their way
+constexpr int kMaxStages = 4;                     // pieces of a warp on their way
 constexpr size_t kSmem = 232448 - 2048;           // of a block, beside its static part
 
 // ---------------------------------------------------------------- the experts' rows
@@ -359,9 +364,9 @@ __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast
 __device__ __forceinline__ float f16_low(uint32_t v) { return __half2float(__ushort_as_half((unsigned short)(v & 0xffffu))); }
 __device__ __forceinline__ float f16_high(uint32_t v) { return __half2float(__ushort_as_half((unsigned short)(v >> 16))); }
 // byte i of a word as a float, and (sixteenth) a sixteenth of it: the mantissa's last bits of 2^23 (2^19)
-__device__ __forceinline__ float byte_f(uint32_t w, int i, bool sixteenth = false) {
+__device__ __forceinline__ float byte_f(uint32_t w, int i, bool sixteenth = false, float less = 0.f) {
     const uint32_t m = sixteenth ? 0x49000000u : 0x4b000000u;
-    return __uint_as_float(__byte_perm(w, m, 0x7650 | i)) - __uint_as_float(m);
+    return __uint_as_float(__byte_perm(w, m, 0x7650 | i)) - (__uint_as_float(m) + less);
 }
 
 // The 6-bit scales (lo, hi of four) and mins of Q4_K / Q5_K as words of bytes.
@@ -410,8 +415,7 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
         if constexpr (block32(QT)) return f16_low(r[i].d[j]);
         const int s = narrow ? 2 * j + half : j;
         if constexpr (QT == GGUF_Q4_K) return byte_f(sc[i][s >> 2], s & 3, j & 1);        // its high nibbles are 16 times too large
-        const float v = byte_f(sc[i][s >> 2], s & 3);
-        return QT == GGUF_Q6_K ? v - 128.f : QT == GGUF_Q3_K ? v - 32.f : v;
+        return byte_f(sc[i][s >> 2], s & 3, false, QT == GGUF_Q6_K ? 128.f : QT == GGUF_Q3_K ? 32.f : 0.f);
     };
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -520,17 +524,6 @@ __device__ __forceinline__ void with_type(int qt, F&& f) {
 
 // ---------------------------------------------------------------- the weights' ring
 
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// all but the last n groups of this thread's copies have arrived
-__device__ __forceinline__ void copies_wait(int n) {
-    if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 2;" ::: "memory");
-}
-
 // A matrix of one expert, as rows of pieces.  The rows at and after n of its last 16 stand for its last row (their results
 // are dropped).
 struct Matrix {
@@ -540,59 +533,108 @@ struct Matrix {
     int n;                          // rows
 };
 
-// The warp's lanes take the 16 bytes units of the rows one after the other: a
-// copy instruction costs a cycle for each line of memory that it meets.
+// Where this lane's 16-byte units of an aligned piece lie, from the tile's first row on.
 template <int QT>
-__device__ __forceinline__ void fetch_piece(uint32_t slot, const Matrix& m, int row0, int c, int lane) {
-    constexpr int UNITS = piece_stride(QT) / 16;            // of a row
-    row0 = min(row0, m.n - 1);                              // a tile past the last row
-    const uint8_t* const base = m.w + (int64_t)row0 * m.rb + (int64_t)c * piece_bytes(QT);
-    const int bytes = (int)min((int64_t)piece_bytes(QT), m.rb - (int64_t)c * piece_bytes(QT));   // fewer at the end of a row of 32-value blocks
-    const int last = m.n - 1 - row0, low = (int)(reinterpret_cast<uintptr_t>(base) & 15);
-    const uint32_t rb = (uint32_t)m.rb;                     // 16 rows are below 2^32 bytes
-    const bool inside = m.end - base > 16 * m.rb;           // no copy reaches the end of the experts
+struct Units {
+    static constexpr int ROW = piece_stride(QT) / 16, N = piece_aligned(QT) ? (16 * ROW + 31) / 32 : 1;
+    uint32_t rel[N];
+    __device__ __forceinline__ Units(const Matrix& m, int lane) {
+        if constexpr (piece_aligned(QT))
 #pragma unroll
-    for (int i = 0; i < (16 * UNITS + 31) / 32; ++i) {
-        const int u = 32 * i + lane, row = u / UNITS, at = 16 * (u - row * UNITS);
-        if (16 * UNITS % 32 && u >= 16 * UNITS) break;
-        const uint32_t from = (uint32_t)min(row, last) * rb;
-        if constexpr (piece_aligned(QT)) {
-            copy16(slot + 16 * u, base + from + at, 16);
-        } else {
-            const int off = (low + (int)from) & 15;
-            const uint8_t* src = base + from + (at - off);
-            if (at < off + bytes) copy16(slot + 16 * u, src, inside ? 16 : (int)min((int64_t)16, (int64_t)(m.end - src)));
+            for (int i = 0; i < N; ++i) {
+                const int u = 32 * i + lane, row = u / ROW;
+                rel[i] = (uint32_t)row * (uint32_t)m.rb + 16 * (u - row * ROW);         // 16 rows are below 2^32 bytes
+            }
+    }
+};
+// What a piece's barrier counts: the lanes, whose own copies arrive for them, or the one that announces the bulk copies.
+// A kernel whose pieces are all aligned has no barriers: each lane waits for its own copies, in order.
+__host__ __device__ constexpr int piece_arrivals(int qt) { return piece_aligned(qt) ? 32 : 1; }
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the last n groups of this thread's copies have arrived
+__device__ __forceinline__ void copies_wait(int n) {
+    if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+template <int QT>
+__device__ __forceinline__ void fetch_piece(uint8_t* slot, uint64_t* bar, const Matrix& m, const Units<QT>& units, int row0, int c, int lane) {
+    if constexpr (piece_aligned(QT)) {
+        using U = Units<QT>;
+        const bool whole = row0 + 16 <= m.n;
+        const uint8_t* const base = m.w + (int64_t)(whole ? row0 : 0) * m.rb + c * piece_bytes(QT);
+        const uint32_t to = smem_u32(slot) + 16 * lane;
+#pragma unroll
+        for (int i = 0; i < U::N; ++i) {
+            const int u = 32 * i + lane;
+            if (16 * U::ROW % 32 && u >= 16 * U::ROW) break;
+            const uint8_t* src = base + units.rel[i];
+            if (!whole) src = base + (int64_t)min(row0 + u / U::ROW, m.n - 1) * m.rb + 16 * (u % U::ROW);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512 * i), "l"(src) : "memory");
         }
+        if (bar) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    } else {
+        // Lane l copies row l's piece.  The last bytes of all experts may end inside 16: no copy goes past them, and they
+        // are moved by hand.
+        const uint8_t* src = m.w + (int64_t)min(row0 + (lane & 15), m.n - 1) * m.rb + (int64_t)c * piece_bytes(QT);
+        uint8_t* const dst = slot + (lane & 15) * piece_stride(QT);
+        const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);
+        // fewer at the end of a row of 32-value blocks
+        const int bytes = off + (int)min((int64_t)piece_bytes(QT), m.rb - (int64_t)c * piece_bytes(QT));
+        src -= off;
+        int size = (bytes + 15) & ~15;
+        if (m.end - src < size) {
+            size = (int)(m.end - src) & ~15;
+            if (lane < 16)
+                for (int i = size; i < bytes; i += 2) *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(src + i);
+        }
+        const uint32_t all = __reduce_add_sync(0xffffffffu, lane < 16 ? (uint32_t)size : 0u);
+        if (lane == 0) mbar_arrive_expect_tx(bar, all);
+        __syncwarp();
+        if (lane < 16 && size) bulk_g2s(dst, src, (uint32_t)size, bar);
     }
 }
 
-// The same with what does not change from piece to piece kept in registers.
-template <int QT>
-struct Fetcher {
-    static constexpr int UNITS = piece_stride(QT) / 16, N = (16 * UNITS + 31) / 32;
-    uint32_t rel[N];                // where this lane's units lie from the tile's first row on
-    __device__ __forceinline__ void init(const Matrix& m, int lane) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int u = 32 * i + lane, row = u / UNITS;
-            rel[i] = (uint32_t)row * (uint32_t)m.rb + 16 * (u - row * UNITS);
-        }
+// A warp's ring: where the next piece goes, which is read next, and its turn.
+// BARS: whether the pieces have barriers.
+template <bool BARS>
+struct Ring {
+    uint8_t* at;
+    uint64_t* bars;
+    int* status;
+    int slot_bytes, stages, into = 0, from = 0;
+    uint32_t parity = 0;
+    bool dead = false;              // a wait has been given up: no more copies, no more waits
+    __device__ __forceinline__ void init(int arrivals, int lane) {
+        if (BARS && lane < stages) mbar_init(bars + lane, arrivals);
+        if (BARS) fence_mbar_init();
+        __syncwarp();
     }
-    __device__ __forceinline__ void fetch(uint32_t slot, const Matrix& m, int row0, int c, int lane) const {
-        const uint8_t* const base = m.w + (int64_t)row0 * m.rb + c * piece_bytes(QT);
-        if (row0 + 16 > m.n || (!piece_aligned(QT) && m.end - base <= 16 * m.rb)) return fetch_piece<QT>(slot, m, row0, c, lane);
-        const int low = (int)(reinterpret_cast<uintptr_t>(base) & 15), bytes = min(piece_bytes(QT), (int)m.rb - c * piece_bytes(QT));
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int u = 32 * i + lane;
-            if (16 * UNITS % 32 && i == N - 1 && u >= 16 * UNITS) break;
-            if constexpr (piece_aligned(QT)) {
-                copy16(slot + 16 * u, base + rel[i], 16);
-            } else {
-                const int off = (low + (int)rel[i]) & 15, at = 16 * (u % UNITS);
-                if (at < off + bytes) copy16(slot + 16 * u, base + (int)(rel[i] - (uint32_t)off), 16);
-            }
+    __device__ __forceinline__ uint8_t* put(uint64_t*& bar) {
+        const int k = into;
+        into = into + 1 == stages ? 0 : into + 1;
+        bar = BARS ? bars + k : nullptr;
+        return at + k * slot_bytes;
+    }
+    // all lanes together
+    __device__ __forceinline__ const uint8_t* get() {
+        const int k = from;
+        if constexpr (BARS) {
+            if (!dead && !__all_sync(0xffffffffu, mbar_wait(bars + k, parity, status))) dead = true;
+        } else {
+            copies_wait(stages - 1);
+            __syncwarp();
         }
+        if (++from == stages) from = 0, parity ^= 1;
+        return at + k * slot_bytes;
+    }
+    // what was on its way when a wait was given up does not outlive the block
+    __device__ __forceinline__ void close() {
+        if (BARS && dead)
+            for (int k = 0; k < stages; ++k) mbar_wait(bars + k, (k < from ? parity ^ 1 : parity), status);
     }
 };
 
@@ -645,8 +687,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
     uint8_t* const columns = s_dyn + Routes::bytes(entries);                                // [held][tile]
     float* const scales = reinterpret_cast<float*>(columns + (size_t)held * tiles * kTileBytes);        // [held][8 * tiles]
     float* const sums = scales + held * 8 * tiles;                                          // [2][warp][16 rows][8 * tiles]
-    uint8_t* const ring = reinterpret_cast<uint8_t*>(sums + 2 * kWarps * 128 * tiles) + (size_t)warp * p.up_stages * p.up_slot;
-    const uint32_t ring_at = smem_u32(ring);
+    __shared__ uint64_t s_bars[kWarps * kMaxStages];
+    constexpr bool kBars = QT < 0 || !piece_aligned(QT);
+    Ring<kBars> ring{reinterpret_cast<uint8_t*>(sums + 2 * kWarps * 128 * tiles) + (size_t)warp * p.up_stages * p.up_slot, s_bars + warp * kMaxStages,
+              p.status, p.up_slot, p.up_stages};
     pdl_wait();
     pdl_launch_dependents();        // all blocks of this kernel are running
     const int both = make_routes(routes, reinterpret_cast<uint32_t*>(columns), p.ids, entries, p.n_expert, 8 * tiles / parts, 8 / p.h_parts, tid);
@@ -688,27 +732,28 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
     // this warp's part of a job
     const int wp = p.up_wp, teams = kWarps / (2 * wp), team = warp / (2 * wp), mat = (warp / wp) & 1, c0 = warp % wp;
     const int qt = mat ? p.up_type : p.gate_type;
+    ring.init(qt == GGUF_Q4_K || qt == GGUF_Q5_K ? piece_arrivals(GGUF_Q4_K) : piece_arrivals(GGUF_Q6_K), lane);
     Matrix m;
     m.rb = mat ? p.up_rb : p.gate_rb;
     m.n = F;
     m.end = (mat ? p.up : p.gate) + p.n_expert * p.F * m.rb;
     auto matrix_of = [&](int group) { return (mat ? p.up : p.gate) + routes.up[group].expert * p.F * m.rb; };
     // A group's jobs [begin, end) go to the teams in turn.  The ring's next piece to fetch runs ahead.
-    int fgroup = job0 / per_group, fend = min(job1, (fgroup + 1) * per_group), fjob = job0 + team, fc = c0, fslot = 0, slot = 0;
+    int fgroup = job0 / per_group, fend = min(job1, (fgroup + 1) * per_group), fjob = job0 + team, fc = c0;
     Matrix fm = m;
-    Fetcher<(QT < 0 ? GGUF_Q4_K : QT)> fetcher;
-    fetcher.init(m, lane);
+    const Units<(QT < 0 ? GGUF_Q6_K : QT)> units(m, lane);
     auto settle = [&] {             // to a job that there is
         while (fjob >= fend && fend < job1) fjob = fend + team, ++fgroup, fend = min(job1, fend + per_group);
         if (fjob < fend) fm.w = matrix_of(fgroup);
     };
     settle();
     auto fetch = [&] {
-        if (fjob < fend) {
+        if (fjob < fend && !ring.dead) {
             const int row0 = (fjob - fgroup * per_group) * 16;
-            if constexpr (QT >= 0) fetcher.fetch(ring_at + fslot * p.up_slot, fm, row0, fc, lane);
-            else with_type(qt, [&](auto q) { fetch_piece<decltype(q)::value>(ring_at + fslot * p.up_slot, fm, row0, fc, lane); });
-            fslot = fslot + 1 == p.up_stages ? 0 : fslot + 1;
+            uint64_t* bar;
+            uint8_t* const slot = ring.put(bar);
+            if constexpr (QT >= 0) fetch_piece<QT>(slot, bar, fm, units, row0, fc, lane);
+            else with_type(qt, [&](auto q) { fetch_piece<decltype(q)::value>(slot, bar, fm, Units<decltype(q)::value>(fm, lane), row0, fc, lane); });
             fc += wp;
             if (fc >= chunks) {
                 fc = c0;
@@ -716,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
                 if (fjob >= fend) settle();
             }
         }
-        copies_commit();
+        if (!kBars) copies_commit();
     };
     for (int i = 0; i < p.up_stages; ++i) fetch();
 
@@ -746,14 +791,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
             const int at = p.up_resident ? c : warp;
             if (!p.up_resident)
                 for (int k = 0; k < g.n; ++k) make(k, c, at);
-            copies_wait(p.up_stages - 1);
             __syncwarp();
+            const uint8_t* const slot = ring.get();
             const int nsub = min(8, (K - c * kChunk) / 32), t = lane & 3;
             const ColumnsInShared col{columns + (size_t)at * tiles * kTileBytes + (lane >> 2) * kColStride + t * 16, scales + at * 8 * tiles + 2 * t, t};
             auto unit = [&](auto q) {
                 constexpr int Q = decltype(q)::value;
                 Raw<Q> r[2];
-                read_piece<Q>(r, ring + slot * p.up_slot, m, row0, c, nsub, lane);
+                read_piece<Q>(r, slot, m, row0, c, nsub, lane);
                 __syncwarp();       // the piece is read: its place may be filled
                 fetch();
                 // (an instruction that a predicate turns off still takes its turn)
@@ -762,7 +807,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
             };
             if constexpr (QT >= 0) unit(std::integral_constant<int, QT>{});
             else with_type(qt, unit);
-            slot = slot + 1 == p.up_stages ? 0 : slot + 1;
             if (!p.up_resident) __syncwarp();       // the columns are read
         }
         float* const to = sums + (size_t)(buffer * kWarps + warp) * 128 * tiles;
@@ -791,6 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
       }
       begin = end;
     }
+    ring.close();
 }
 
 // ---------------------------------------------------------------- the hidden values as columns
@@ -831,8 +876,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnP
     float* const weights = reinterpret_cast<float*>(s_dyn + Routes::bytes(entries));                // [entry]
     float* const sums = weights + (entries + 3) / 4 * 4;                                            // [split][entry][16]
     constexpr int kSlot = 16 * piece_stride(QT);
-    uint8_t* const ring = reinterpret_cast<uint8_t*>(sums + (size_t)splits * entries * 16) + (size_t)warp * p.down_stages * kSlot;
-    const uint32_t ring_at = smem_u32(ring);
+    __shared__ uint64_t s_bars[kWarps * kMaxStages];
+    constexpr bool kBars = !piece_aligned(QT);
+    Ring<kBars> ring{reinterpret_cast<uint8_t*>(sums + (size_t)splits * entries * 16) + (size_t)warp * p.down_stages * kSlot, s_bars + warp * kMaxStages,
+              p.status, kSlot, p.down_stages};
+    ring.init(piece_arrivals(QT), lane);
     // The kernel before this one let it begin when up had ended, so the routes are
     // there; the columns are waited for once the first weights are on their way.
     for (int i = tid; i < (int)(Routes::bytes(entries) / 16); i += kThreads)
@@ -845,19 +893,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnP
     const int row0 = 16 * blockIdx.x, F = (int)p.F, chunks = (F + kChunk - 1) / kChunk;
     Matrix m{nullptr, p.down + p.n_expert * p.K * p.down_rb, p.down_rb, (int)p.K};
     auto matrix_of = [&](int item) { return p.down + routes.down[item / splits].expert * p.K * p.down_rb; };
-    int fitem = warp, fc = warp % splits, fslot = 0, slot = 0;
+    int fitem = warp, fc = warp % splits;
     Matrix fm = m;
-    Fetcher<QT> fetcher;
-    fetcher.init(m, lane);
+    const Units<QT> units(m, lane);
     if (fitem < items) fm.w = matrix_of(fitem);
     auto fetch = [&] {
-        if (fitem < items) {
-            fetcher.fetch(ring_at + fslot * kSlot, fm, row0, fc, lane);
-            fslot = fslot + 1 == p.down_stages ? 0 : fslot + 1;
+        if (fitem < items && !ring.dead) {
+            uint64_t* bar;
+            uint8_t* const slot = ring.put(bar);
+            fetch_piece<QT>(slot, bar, fm, units, row0, fc, lane);
             fc += splits;
             if (fc >= chunks && (fitem += kWarps) < items) fc = fitem % splits, fm.w = matrix_of(fitem);
         }
-        copies_commit();
+        if (!kBars) copies_commit();
     };
     for (int i = 0; i < p.down_stages; ++i) fetch();
     float residual = 0.f;           // of this thread's first output
@@ -882,12 +930,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnP
                 col.s[0] = make_uint2(__ldg(s + t), __ldg(s + 8 + t)), col.s[1] = make_uint2(__ldg(s + 4 + t), __ldg(s + 12 + t));
             }
             col.f = make_float2(__ldg(p.column_scales + first + c), __ldg(p.column_scales + second + c));
-            copies_wait(p.down_stages - 1);
-            __syncwarp();
+            const uint8_t* const slot = ring.get();
             const int nsub = min(8, (F - c * kChunk) / 32);
             Raw<QT> r[2];
-            read_piece<QT>(r, ring + slot * kSlot, m, row0, c, nsub, lane);
-            slot = slot + 1 == p.down_stages ? 0 : slot + 1;
+            read_piece<QT>(r, slot, m, row0, c, nsub, lane);
             __syncwarp();           // the piece is read: its place may be filled
             fetch();
             multiply<QT, 1>(r, col, nsub, lane, acc);
@@ -910,6 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnP
                 }
         }
     }
+    ring.close();
     __syncthreads();
     for (int i = tid; i < p.T * 16; i += kThreads) {
         const int r = i & 15, token = i >> 4;

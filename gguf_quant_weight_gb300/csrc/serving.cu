@@ -290,6 +290,7 @@ int gguf_moe_ffn(const gguf_moe_weights* experts, const void* x, int xdt, int64_
     p.weights = weights;
     p.residual = residual;
     p.y = y;
+    p.status = status;
     return moe_ffn_launch(p, workspace, sms, pdl_on(), (cudaStream_t)stream);
 }
 

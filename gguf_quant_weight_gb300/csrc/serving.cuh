@@ -93,6 +93,7 @@ struct MoeFfnParams {
     const float* weights;
     const void* residual;
     void* y;
+    int* status;
     // set by the launch.  In the workspace: hidden values [T * top_k][F], then as
     // the down kernel's columns, the columns' scales, and what up makes of the ids
     float* h;
