@@ -81,6 +81,32 @@ __device__ int make_routes(const Routes& r, uint32_t* scratch, const int32_t* id
                            int tid) {
     __shared__ int s_warp[kWarps];
     const int lane = tid & 31, warp = tid >> 5, words = (entries + 31) >> 5;
+    if (entries <= 32) {
+        // one warp's work, the experts in the order in which they come
+        if (warp == 0) {
+            const int id = lane < entries ? ids[lane] : -1;
+            const bool in = (unsigned)id < (unsigned)n_expert;
+            const unsigned same = __match_any_sync(0xffffffffu, in ? id : -1 - lane), before = same & ((1u << lane) - 1);
+            const int rows = in && !before ? __popc(same) : 0, ups = (rows + up_rows - 1) / up_rows, downs = (rows + down_rows - 1) / down_rows;
+            const int mine = rows | ups << 10 | downs << 20;
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const int at = upto - mine, first = at & 1023;
+            for (int k = 0; k < ups; ++k)
+                r.up[(at >> 10 & 1023) + k] = Group{(int16_t)id, (int16_t)min(up_rows, rows - k * up_rows), (int16_t)(first + k * up_rows), 0};
+            for (int k = 0; k < downs; ++k)
+                r.down[(at >> 20) + k] = Group{(int16_t)id, (int16_t)min(down_rows, rows - k * down_rows), (int16_t)(first + k * down_rows), 0};
+            const int start = __shfl_sync(0xffffffffu, first, __ffs(same) - 1);
+            if (in) r.list[start + __popc(before)] = (uint16_t)lane;
+            if (lane == 31) s_warp[0] = (upto >> 10 & 1023) | (upto >> 20) << 16;
+        }
+        __syncthreads();
+        return s_warp[0];
+    }
     uint32_t* const first = scratch + words * n_expert;
     const int id = tid < entries ? ids[tid] : -1;           // at most kThreads entries
     for (int i = tid; i < words * n_expert; i += kThreads) scratch[i] = 0;
@@ -663,7 +689,7 @@ __device__ __forceinline__ float activate(float a, int act) {
 // 2 wp, each on its own job: of each matrix wp warps take every wp-th chunk of K, and
 // their sums meet in shared memory.  Small teams meet seldom for what they do in
 // between; larger ones are for calls that have too few jobs.
-// QT: both matrices' type, or -1 where they differ.
+// QT: both matrices' type, or -1 where they differ.  TILES: of 8 columns that a group may have.
 struct ColumnsInShared {
     const uint8_t* at;              // the chunk's tiles, at this lane's column and 16 bytes
     const float* scales;            // the chunk's, at 2t
@@ -676,11 +702,12 @@ struct ColumnsInShared {
     __device__ __forceinline__ float2 back(int n) const { return *reinterpret_cast<const float2*>(scales + 8 * n); }
 };
 
-template <int QT>
+template <int QT, int TILES>
 __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnParams p) {
     extern __shared__ __align__(16) uint8_t s_dyn[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int entries = p.T * p.top_k, tiles = p.up_tiles, chunks = (int)ceil_div(p.K, kChunk), parts = p.x_parts;
+    const int entries = p.T * p.top_k, chunks = (int)ceil_div(p.K, kChunk), parts = p.x_parts;
+    constexpr int tiles = TILES;
     const Routes routes(s_dyn, entries);
     // a group's columns: of all chunks, or, where K is too long, of the one that each warp is at
     const int held = p.up_resident ? chunks : kWarps;
@@ -704,31 +731,37 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
     const int K = (int)p.K, F = (int)p.F, per_group = (F + 15) / 16, jobs = per_group * groups;
     // The blocks' shares of the jobs, where a job of two tiles counts 4 and one of one tile 3 (the blocks
     // are taken apart once either way).
-    __shared__ int s_from[2], s_wide;
-    if (tid < 2) s_from[tid] = jobs;
-    if (warp == 0) {
-        int wide = 0;
-        for (int b = 0; b < groups; b += 32) {
-            const bool two = b + lane < groups && routes.up[b + lane].n * parts > 8;
-            const unsigned on = __ballot_sync(0xffffffffu, two);
-            if (b + lane < groups) routes.up[b + lane].wide = (int16_t)(wide + __popc(on & ((1u << lane) - 1)));
-            wide += __popc(on);
+    int job0, job1;
+    if constexpr (TILES == 1) {
+        auto share = [&](unsigned b) { return jobs < 1 << 23 ? (int)((unsigned)jobs * b / gridDim.x) : (int)((int64_t)jobs * b / gridDim.x); };
+        job0 = share(blockIdx.x), job1 = share(blockIdx.x + 1);      // at most 152 blocks
+    } else {
+        __shared__ int s_from[2], s_wide;
+        if (tid < 2) s_from[tid] = jobs;
+        if (warp == 0) {
+            int wide = 0;
+            for (int b = 0; b < groups; b += 32) {
+                const bool two = b + lane < groups && routes.up[b + lane].n * parts > 8;
+                const unsigned on = __ballot_sync(0xffffffffu, two);
+                if (b + lane < groups) routes.up[b + lane].wide = (int16_t)(wide + __popc(on & ((1u << lane) - 1)));
+                wide += __popc(on);
+            }
+            if (lane == 0) s_wide = wide;
         }
-        if (lane == 0) s_wide = wide;
-    }
-    __syncthreads();
-    const int64_t whole = (int64_t)per_group * (3 * groups + s_wide);
-    if (tid < groups) {
-        const int cost = routes.up[tid].n * parts > 8 ? 4 : 3;
-        const int64_t lo = (int64_t)per_group * (3 * tid + routes.up[tid].wide);
+        __syncthreads();
+        const int64_t whole = (int64_t)per_group * (3 * groups + s_wide);
+        if (tid < groups) {
+            const int cost = routes.up[tid].n * parts > 8 ? 4 : 3;
+            const int64_t lo = (int64_t)per_group * (3 * tid + routes.up[tid].wide);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int64_t at = whole * (blockIdx.x + k) / gridDim.x - lo;
-            if (at >= 0 && at < (int64_t)per_group * cost) s_from[k] = tid * per_group + (int)at / cost;
+            for (int k = 0; k < 2; ++k) {
+                const int64_t at = whole * (blockIdx.x + k) / gridDim.x - lo;
+                if (at >= 0 && at < (int64_t)per_group * cost) s_from[k] = tid * per_group + (int)at / cost;
+            }
         }
+        __syncthreads();
+        job0 = s_from[0], job1 = s_from[1];
     }
-    __syncthreads();
-    const int job0 = s_from[0], job1 = s_from[1];
     // this warp's part of a job
     const int wp = p.up_wp, teams = kWarps / (2 * wp), team = warp / (2 * wp), mat = (warp / wp) & 1, c0 = warp % wp;
     const int qt = mat ? p.up_type : p.gate_type;
@@ -786,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
       const int n_tiles = (g.n * parts + 7) >> 3;
       for (int job = begin + team; job < end; job += teams, buffer ^= 1) {
         const int row0 = (job - group * per_group) * 16;
-        float acc[kTiles][4] = {};
+        float acc[TILES][4] = {};
         for (int c = c0; c < chunks; c += wp) {
             const int at = p.up_resident ? c : warp;
             if (!p.up_resident)
@@ -802,8 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
                 __syncwarp();       // the piece is read: its place may be filled
                 fetch();
                 // (an instruction that a predicate turns off still takes its turn)
-                if (n_tiles == 1) multiply<Q, 1>(r, col, nsub, lane, reinterpret_cast<float(&)[1][4]>(acc));
-                else multiply<Q, kTiles>(r, col, nsub, lane, acc);
+                if (TILES == 1 || n_tiles == 1) multiply<Q, 1>(r, col, nsub, lane, reinterpret_cast<float(&)[1][4]>(acc));
+                else multiply<Q, TILES>(r, col, nsub, lane, acc);
             };
             if constexpr (QT >= 0) unit(std::integral_constant<int, QT>{});
             else with_type(qt, unit);
@@ -811,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_up_kernel(const MoeFfnPar
         }
         float* const to = sums + (size_t)(buffer * kWarps + warp) * 128 * tiles;
 #pragma unroll
-        for (int k = 0; k < kTiles; ++k) {
+        for (int k = 0; k < TILES; ++k) {
             if (k >= n_tiles) continue;
             float* at = to + (lane >> 2) * 8 * tiles + 8 * k + 2 * (lane & 3);
             *reinterpret_cast<float2*>(at) = make_float2(acc[k][0], acc[k][1]);
@@ -975,11 +1008,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnP
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? GGUF_OK : GGUF_ERR_CUDA; }
 
-template <int QT>
+template <int QT, int TILES>
 int launch_up(const MoeFfnParams& p, int blocks, size_t smem, int pdl, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    if (set_once(moe_ffn_up_kernel<QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem, done) != cudaSuccess) return GGUF_ERR_CUDA;
-    return cuda_status(launch_pdl(moe_ffn_up_kernel<QT>, dim3((unsigned)blocks), dim3(kThreads), smem, s, pdl, p));
+    auto* k = moe_ffn_up_kernel<QT, TILES>;
+    if (set_once(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem, done) != cudaSuccess) return GGUF_ERR_CUDA;
+    return cuda_status(launch_pdl(k, dim3((unsigned)blocks), dim3(kThreads), smem, s, pdl, p));
+}
+template <int QT>
+int launch_up(const MoeFfnParams& p, int blocks, size_t smem, int pdl, cudaStream_t s) {
+    return p.up_tiles == 1 ? launch_up<QT, 1>(p, blocks, smem, pdl, s) : launch_up<QT, kTiles>(p, blocks, smem, pdl, s);
 }
 
 template <int QT>
