@@ -106,7 +106,8 @@ struct Shared {
     uint32_t table[32 * 32];                             // kTable, a copy for each lane's bank
     alignas(8) uint32_t count[kBins], low[kBins], high[kBins];      // of a histogram: tokens, and their weights' sums
     uint32_t cand_key[kCap], cand_idx[kCap], n_cand;
-    u64 cand_w[kCap], kept_w[kCap];
+    u64 cand_w[kCap], kept_w[kCap], cand_order[kCap];
+    uint32_t cand_pos[kCap], cand_low[kCap], cand_high[kCap];
     u64 warp_sum[kWarps];
     uint32_t warp_count[kWarps];
     float warp_f[kWarps];
@@ -464,23 +465,39 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         });
         sync();
     };
+    // A sum over the n candidates j for each candidate, f(j, candidate, count, sum): several threads share one's, as many as
+    // there are, and add their parts up in cand_pos, cand_low and cand_high.
+    auto over_candidates = [&](int n, auto&& f) {
+        int wide = 32;
+        while (wide < n) wide *= 2;
+        const int i = tid & (wide - 1), parts = kThreads / wide, per = (n + parts - 1) / parts, j0 = tid / wide * per, j1 = min(n, j0 + per);
+        if (tid < n) s.cand_pos[tid] = s.cand_low[tid] = s.cand_high[tid] = 0;
+        __syncthreads();
+        if (i < n && j0 < j1) {
+            uint32_t count = 0;
+            u64 sum = 0;
+#pragma unroll 4
+            for (int j = j0; j < j1; ++j) f(j, i, count, sum);
+            atomicAdd(&s.cand_pos[i], count);
+            const uint32_t lo = (uint32_t)sum, old = atomicAdd(&s.cand_low[i], lo);
+            atomicAdd(&s.cand_high[i], (uint32_t)(sum >> 32) + (old + lo < old ? 1u : 0u));
+        }
+        __syncthreads();
+    };
     // in the first block: this thread's candidate's place in the order and the sum of weights up to it
     auto place = [&](int n, bool with_sum, uint32_t& key, uint32_t& idx, u64& w, int& pos, u64& upto) {
         key = 0, idx = 0, w = 0, pos = 0, upto = 0;
         if (tid < n) {
             key = s.cand_key[tid], idx = s.cand_idx[tid];
-            if (with_sum) s.cand_w[tid] = w = weight(float_of(key));
+            s.cand_order[tid] = (u64)key << 32 | (uint32_t)~idx;        // the larger comes first
+            s.cand_w[tid] = w = with_sum ? weight(float_of(key)) : 0;
         }
-        __syncthreads();
-        if (tid < n) {
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) {
-                const uint32_t kj = s.cand_key[j], ij = s.cand_idx[j];
-                const bool before = kj > key || (kj == key && ij < idx);
-                pos += before;
-                if (with_sum) upto += before || j == tid ? s.cand_w[j] : 0;
-            }
-        }
+        over_candidates(n, [&](int j, int i, uint32_t& count, u64& sum) {
+            const u64 o = s.cand_order[j], mine = s.cand_order[i];
+            count += o > mine;
+            sum += o >= mine ? s.cand_w[j] : 0;
+        });
+        if (tid < n) pos = (int)s.cand_pos[tid], upto = (u64)s.cand_high[tid] << 32 | s.cand_low[tid];
     };
     const u64 least = !use_m ? 0 : min_p < 1.f ? share_of(min_p, weight(m), true) : weight(m);     // min-p's, of a weight
     // the share of W that top-p keeps, the place in W that u asks for
@@ -567,17 +584,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             keep = keep && upto - w < goal;
         }
         keep = keep && w >= least;
-        if (tid < n) s.kept_w[tid] = keep ? w : 0;
-        __syncthreads();
+        const u64 own = keep ? w : 0;
+        u64 W = own;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+        if (tid < n) s.kept_w[tid] = own;
+        if (lane == 0) s.warp_sum[warp] = W;
+        // the sums in the vocabulary's order
+        over_candidates(n, [&](int j, int i, uint32_t&, u64& sum) { sum += s.cand_idx[j] <= s.cand_idx[i] ? s.kept_w[j] : 0; });
+        W = 0;
+        for (int v = 0; v < kWarps; ++v) W += s.warp_sum[v];
         if (keep) {
-            u64 c = 0, W = 0;
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) {
-                const u64 wj = s.kept_w[j];
-                W += wj;
-                if (s.cand_idx[j] <= idx) c += wj;
-            }
-            const u64 t = target_of(W);
+            const u64 c = (u64)s.cand_high[tid] << 32 | s.cand_low[tid], t = target_of(W);
             if (c > t && c - w <= t) emit((int)idx, w, W);
         }
     };
