@@ -761,7 +761,7 @@ cudaError_t launch(const SampleParams& p, int num_sms, int pdl, cudaStream_t s) 
     // to a row where there are few rows
     const int64_t span = p.vocab + 3;
     int cluster = 1;
-    while (cluster < 8 && (span > cluster * (int64_t)(kWarps * 2175) || (p.rows * cluster < num_sms && span > cluster * 2048))) cluster *= 2;
+    while (cluster < 8 && (span > cluster * (int64_t)(kWarps * 2175) || (p.rows * cluster * 2 <= num_sms && span > cluster * 2048))) cluster *= 2;
     const int64_t seg = ceil_div(span, (int64_t)cluster * kWarps * 128) * 128;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.rows * cluster));
