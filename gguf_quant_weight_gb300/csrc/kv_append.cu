@@ -200,6 +200,34 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
     }
 }
 
+// The same for positions below 2^24, which are floats, without doubles (of which an SM does two a cycle): the frequency in
+// turns in two floats, and what the product's rounding leaves by a second product.  Off by 2^-46 of the turns and by
+// two roundings of a part below one half, 2^-24 of a turn.  (37 mixed tokens: 9.7 us with doubles, 9.2 so.)
+__device__ __forceinline__ void near_angle(const AppendParams& p, int t, int pos, int i, float& cos, float& sin) {
+    const int at = p.positions ? p.positions[t] : pos;
+    if (abs(at) >= 1 << 24) return angle(p, t, pos, i, cos, sin);
+    constexpr float kHigh = 0.15915494f, kLow = 6.4206383e-9f;      // 1 / (2 pi)
+    const float f = p.freqs[i], high = __fmul_rn(f, kHigh), low = __fmaf_rn(f, kHigh, -high) + f * kLow;
+    const float a = (float)at, turns = __fmul_rn(a, high), rest = __fmaf_rn(a, high, -turns) + a * low;
+    float sn, cs;
+    sincospif(2.f * ((turns - rintf(turns)) + rest), &sn, &cs);
+    cos = cs * p.rope_scale;
+    sin = sn * p.rope_scale;
+}
+
+// V consecutive floats of shared memory (V * 4 bytes aligned, up to 16)
+template <int V>
+__device__ __forceinline__ void read_v(const float* p, float (&f)[V]) {
+    constexpr int N = V < 4 ? V : 4;
+    struct alignas(4 * N) Pack { float v[N]; };
+#pragma unroll
+    for (int i = 0; i < V; i += N) {
+        const Pack k = *reinterpret_cast<const Pack*>(p + i);
+#pragma unroll
+        for (int j = 0; j < N; ++j) f[i + j] = k.v[j];
+    }
+}
+
 // The same with the heads of q and k normed on the way:
 //   x -> x / sqrt(mean(x^2) + eps) * weight, then turned.
 // A head is held by a group of `lanes` lanes (a power of two, its last ones
@@ -211,8 +239,7 @@ template <class X, class C, int V, bool NEOX>
 __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendParams p, int lanes) {
     constexpr int U = V >= 4 ? 1 : V == 2 ? 2 : 4;
     __shared__ Place at;
-    __shared__ float s_cos[64], s_sin[64];
-    __shared__ __align__(16) float s_wq[128], s_wk[128];
+    __shared__ __align__(16) float s_cos[64], s_sin[64], s_wq[128], s_wk[128];
     const int t = blockIdx.x, tid = threadIdx.x;
     if (tid == 0) at.found = at.disorder = 0;
     const int half = p.rot >> 1;
@@ -252,9 +279,18 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendPa
     __syncthreads();
     pdl_launch_dependents();
     if (!at.found || at.disorder) return;
-    if (tid < half) angle(p, t, at.pos, tid, s_cos[tid], s_sin[tid]);
+    if (tid < half) near_angle(p, t, at.pos, tid, s_cos[tid], s_sin[tid]);
     __syncthreads();
     const int64_t slot = at.slot;
+    // a lane's units are the same of every head, and so are their angles
+    constexpr int P = NEOX ? V : V / 2;           // pairs of a unit
+    float cs[U][P], sn[U][P];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int u = me + i * lanes;
+        if (u < turn) read_v<P>(s_cos + u * P, cs[i]), read_v<P>(s_sin + u * P, sn[i]);
+    }
+    const float per_value = 1.f / (float)D;
     // the whole warp comes here for as many heads as any of its groups has
     auto write = [&](int h, const Head& w) {
         const bool on = h < n;
@@ -265,14 +301,17 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendPa
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 a[i][k] = on && u < units ? w.a[i][k] : 0.f;
-                b[i][k] = NEOX && on && u < turn ? w.b[NEOX ? i : 0][k] : 0.f;
-                sum = fmaf(a[i][k], a[i][k], fmaf(b[i][k], b[i][k], sum));
+                sum = fmaf(a[i][k], a[i][k], sum);
+                if (NEOX) {
+                    b[i][k] = on && u < turn ? w.b[NEOX ? i : 0][k] : 0.f;
+                    sum = fmaf(b[i][k], b[i][k], sum);
+                }
             }
         }
         for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (!on || !(h < p.heads || slot >= 0)) return;
         const float* weight = h < p.heads ? (p.q_norm ? s_wq : nullptr) : h < HK && p.k_norm ? s_wk : nullptr;
-        const float inv = 1.f / sqrtf(sum / (float)D + p.eps);
+        const float inv = rsqrtf(fmaf(sum, per_value, p.eps));       // to two units in the last place
         C* dst = h < p.heads ? static_cast<C*>(p.q_out) + t * p.ldqo + h * D
                  : h < HK    ? static_cast<C*>(p.c.k) + slot + (h - p.heads) * p.c.head_stride
                              : static_cast<C*>(p.c.v) + slot + (h - HK) * p.c.head_stride;
@@ -282,10 +321,14 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendPa
             if (u >= units) continue;
             const int d = first(u);
             if (weight) {
+                float f[V];
+                read_v<V>(weight + d, f);
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    a[i][k] = a[i][k] * inv * weight[d + k];
-                    if (NEOX && u < turn) b[i][k] = b[i][k] * inv * weight[half + d + k];
+                for (int k = 0; k < V; ++k) a[i][k] *= inv * f[k];
+                if (NEOX && u < turn) {
+                    read_v<V>(weight + half + d, f);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) b[i][k] *= inv * f[k];
                 }
             }
             if (h < HK && u < turn) {
@@ -293,9 +336,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendPa
                     float y[V], z[V];
 #pragma unroll
                     for (int k = 0; k < V; ++k) {
-                        const float cs = s_cos[d + k], sn = s_sin[d + k];
-                        y[k] = a[i][k] * cs - b[i][k] * sn;
-                        z[k] = a[i][k] * sn + b[i][k] * cs;
+                        y[k] = a[i][k] * cs[i][k % P] - b[i][k] * sn[i][k % P];
+                        z[k] = a[i][k] * sn[i][k % P] + b[i][k] * cs[i][k % P];
                     }
                     store_v<V>(dst + d, y);
                     store_v<V>(dst + half + d, z);
@@ -303,9 +345,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendPa
                     float y[V];
 #pragma unroll
                     for (int k = 0; k < V / 2; ++k) {
-                        const float cs = s_cos[d / 2 + k], sn = s_sin[d / 2 + k];
-                        y[2 * k] = a[i][2 * k] * cs - a[i][2 * k + 1] * sn;
-                        y[2 * k + 1] = a[i][2 * k] * sn + a[i][2 * k + 1] * cs;
+                        y[2 * k] = a[i][2 * k] * cs[i][k] - a[i][2 * k + 1] * sn[i][k];
+                        y[2 * k + 1] = a[i][2 * k] * sn[i][k] + a[i][2 * k + 1] * cs[i][k];
                     }
                     store_v<V>(dst + d, y);
                 }
@@ -327,15 +368,20 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendPa
 }
 
 template <class X, class C, int V, bool NEOX>
+cudaError_t launch_norm(const AppendParams& p, int num_sms, int pdl, cudaStream_t s) {
+    const int half = p.rot / 2, units = (NEOX ? half / V : p.rot / V) + (p.c.dim - p.rot) / V;
+    int lanes = 1;
+    while (lanes < 32 && lanes < units) lanes *= 2;
+    const int64_t heads = p.heads + 2 * p.c.kv_heads;
+    const int64_t share = std::max<int64_t>(1, std::min(ceil_div(heads, kThreads / lanes), ceil_div(4 * num_sms, p.b.n_tokens)));
+    return launch_pdl(kv_append_norm_kernel<X, C, V, NEOX>, dim3(p.b.n_tokens, (unsigned)share), dim3(kThreads), 0, s, pdl, p, lanes);
+}
+
+template <class X, class C, int V, bool NEOX>
 cudaError_t launch(const AppendParams& p, int num_sms, int pdl, cudaStream_t s) {
-    if (p.q_norm || p.k_norm) {
-        const int half = p.rot / 2, units = (NEOX ? half / V : p.rot / V) + (p.c.dim - p.rot) / V;
-        int lanes = 1;
-        while (lanes < 32 && lanes < units) lanes *= 2;
-        const int64_t heads = p.heads + 2 * p.c.kv_heads;
-        const int64_t share = std::max<int64_t>(1, std::min(ceil_div(heads, kThreads / lanes), ceil_div(4 * num_sms, p.b.n_tokens)));
-        return launch_pdl(kv_append_norm_kernel<X, C, V, NEOX>, dim3(p.b.n_tokens, (unsigned)share), dim3(kThreads), 0, s, pdl, p, lanes);
-    }
+    // f32 rows in 16 bytes a lane: eight values and their angles take so many registers that fewer blocks fit
+    // (9,600 tokens of 40 heads: 60.5 us with eight, 57.6 so; 37 mixed tokens 9.2 either way)
+    if (p.q_norm || p.k_norm) return launch_norm<X, C, (sizeof(X) == 4 && V == 8 ? 4 : V), NEOX>(p, num_sms, pdl, s);
     const int64_t per_token = (int64_t)(p.heads + 2 * p.c.kv_heads) * p.c.dim / V;
     // enough blocks to occupy the SMs when there are few tokens
     const int64_t share = std::max<int64_t>(1, std::min(ceil_div(per_token, kThreads), ceil_div(4 * num_sms, p.b.n_tokens)));
