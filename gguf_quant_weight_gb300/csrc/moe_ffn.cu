@@ -151,6 +151,7 @@ __device__ int make_routes(const Routes& r, uint32_t* scratch, const int32_t* id
         for (int w = 0; w < warp; ++w) at += __popc(scratch[w * n_expert + id]);
         r.list[at] = (uint16_t)tid;
     }
+    fence_proxy_async_smem();                               // the scratch's place is the ring's too
     __syncthreads();
     return (done >> 10 & 1023) | (done >> 20) << 16;
 }
@@ -202,15 +203,19 @@ __device__ __forceinline__ float make_column(uint8_t* col, int parts, const void
     // powers of two by their bits, both of them normal numbers
     const int ex = max((int)(top >> 23), 10);
     const float scale = __uint_as_float((uint32_t)(263 - ex) << 23), back = __uint_as_float((uint32_t)(ex - 9) << 23);
-    float sa = 0.f, sb = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        a[i] *= scale, b[i] *= scale;
-        sa += a[i], sb += b[i];
-    }
+    for (int i = 0; i < 4; ++i) a[i] *= scale, b[i] *= scale;
     uint4 hi;
     hi.x = pack2(a[0], a[2]), hi.y = pack2(a[1], a[3]), hi.z = pack2(b[0], b[2]), hi.w = pack2(b[1], b[3]);
     *reinterpret_cast<uint4*>(col + lane * 16) = hi;
+    if (parts == 1 && dt == GGUF_DT_F32) {
+        // a min meets the values that the codes meet: what f16 rounds off counts for the
+        // weights as they are, not for their codes alone, which may be far larger
+        const float2 f[4] = {unpack2(hi.x), unpack2(hi.y), unpack2(hi.z), unpack2(hi.w)};
+        a[0] = f[0].x, a[2] = f[0].y, a[1] = f[1].x, a[3] = f[1].y;
+        b[0] = f[2].x, b[2] = f[2].y, b[1] = f[3].x, b[3] = f[3].y;
+    }
+    float sa = (a[0] + a[1]) + (a[2] + a[3]), sb = (b[0] + b[1]) + (b[2] + b[3]);
     sa += __shfl_xor_sync(0xffffffffu, sa, 1), sb += __shfl_xor_sync(0xffffffffu, sb, 1);
     sa += __shfl_xor_sync(0xffffffffu, sa, 2), sb += __shfl_xor_sync(0xffffffffu, sb, 2);
     uint32_t* sums = reinterpret_cast<uint32_t*>(col + 2 * kChunk);      // [first parts 16][second parts 16] f16
