@@ -347,6 +347,10 @@ __global__ void __launch_bounds__(kThreads) moe_router_kernel(const RouterParams
                 }
                 __syncthreads();
             }
+            // NaN, after everything else: every expert has a place of its own whatever the scores are
+            for (int c = tid; c < n; c += kThreads)
+                if (isnan(s_exact[c])) s_exact[c] = -HUGE_VAL;
+            __syncthreads();
             for (int c = tid; c < n; c += kThreads) {
                 const double mine = s_exact[c];
                 const int e = s_before[c];
@@ -394,7 +398,7 @@ cudaError_t launch(const RouterParams& p, int cluster, int pdl, cudaStream_t s) 
 }
 
 template <int TG, int EW>
-cudaError_t launch(const RouterParams& p, int num_sms, int pdl, cudaStream_t s) {
+cudaError_t launch(const RouterParams& p, int pdl, cudaStream_t s) {
     // a warp's experts a block first, so many blocks as the experts ask for
     int cluster = 1;
     while (cluster < 8 && cluster * EW * kWarps < p.n_expert) cluster *= 2;
@@ -408,9 +412,9 @@ cudaError_t moe_router_launch(const RouterParams& p, int num_sms, int pdl, cudaS
     // few tokens: one or two to a cluster, two experts to a warp, over as many SMs as
     // that gives; then four and eight tokens
     const int64_t blocks = std::min<int64_t>(8, ceil_div(p.n_expert, 2 * kWarps)), clusters = std::max<int64_t>(1, 2 * num_sms / blocks);
-    if (p.T <= clusters) return launch<1, 2>(p, num_sms, pdl, s);
-    if (p.T <= 2 * clusters) return launch<2, 2>(p, num_sms, pdl, s);
-    return p.T <= 4 * clusters ? launch<4, 4>(p, num_sms, pdl, s) : launch<8, 4>(p, num_sms, pdl, s);
+    if (p.T <= clusters) return launch<1, 2>(p, pdl, s);
+    if (p.T <= 2 * clusters) return launch<2, 2>(p, pdl, s);
+    return p.T <= 4 * clusters ? launch<4, 4>(p, pdl, s) : launch<8, 4>(p, pdl, s);
 }
 
 }  // namespace gg
