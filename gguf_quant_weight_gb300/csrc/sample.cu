@@ -113,8 +113,7 @@ struct Shared {
     float warp_f[kWarps];
     // from each block of the cluster
     uint32_t peer_max[8], peer_bad[8], peer_lo[8], peer_hi[8], peer_listed[8];
-    float peer_tail[8];
-    u64 peer_sum[3][8];
+    u64 peer_sum[3][8], peer_tail[8];
     // what one thread found, for all
     uint32_t bin, base_count, bin_count, all_count;
     u64 base_sum, all_sum;
@@ -318,7 +317,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         __syncthreads();                             // the warps' sums have been read
         const bool want_tail = use_p && !use_k;
         int n = 0;
-        float rest = 0.f;
+        // The others' weights, which are at most 2^-below, in units of 2^-(21 + below): an integer's sum is the same however
+        // the row is cut, and its rounding lies far below the weight of a token at the border.
+        uint32_t rest = 0;
+        const int below = min((int)(limit * 0.0625f), 100);
+        const float unit = __uint_as_float((uint32_t)(127 + 21 + below) << 23), farthest = fminf(300.f / ch, 3e38f);
         // the same bound for the logits themselves, a little below
         const float above = fmaxf(m - limit / bin_scale - 1e-6f * (fabsf(m) + limit / bin_scale), -3.402823466e38f);
         each_four([&](float (&f)[4], int i) {
@@ -327,9 +330,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             for (int j = 0; j < 4; ++j) {
                 in[j] = f[j] >= above;
                 if (want_tail) {
-                    const float dh = fmaxf(f[j] - m, -1e30f);        // -inf times cl would be NaN
-                    const float w = ex2(fmaf(dh, ch, dh * cl));
-                    rest += in[j] ? 0.f : w;
+                    const float dh = fmaxf(f[j] - m, -farthest);     // where the weight is 0, and dh * cl still a number
+                    const float w = fmaf(ex2(fmaf(dh, ch, dh * cl)), unit, 8388608.f);
+                    rest += in[j] || f[j] == -INFINITY ? 0u : __float_as_uint(w) - 0x4b000000u;
                 }
             }
             if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) return;
@@ -353,13 +356,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             chunks = (n + 127) >> 7;
             for (int i = n + lane; i < 128 * chunks; i += 32) list[i] = -INFINITY, offs[i] = 0;
         }
+        // below 2^32 in a lane: at most 1028 tokens of 2^21 and a half
+        u64 sum = rest;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
-        if (lane == 0) s.warp_f[warp] = rest, atomicAdd(&s.listed, n <= kList ? (uint32_t)n : 1u << 24);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) s.warp_sum[warp] = sum, atomicAdd(&s.listed, n <= kList ? (uint32_t)n : 1u << 24);
         __syncthreads();
         if (tid == 0) {
-            for (int w = 1; w < kWarps; ++w) s.warp_f[0] += s.warp_f[w];
-            if (cluster == 1) s.peer_listed[0] = s.listed, s.peer_tail[0] = s.warp_f[0];
+            for (int w = 1; w < kWarps; ++w) s.warp_sum[0] += s.warp_sum[w];
+            if (cluster == 1) s.peer_listed[0] = s.listed, s.peer_tail[0] = s.warp_sum[0];
         }
         __syncthreads();
     }
@@ -711,14 +716,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         if (cluster > 1) {
             if (tid < cluster) {
                 st_cluster(cluster_map(smem_u32(&s.peer_listed[rank]), tid), s.listed);
-                st_cluster(cluster_map(smem_u32(&s.peer_tail[rank]), tid), __float_as_uint(s.warp_f[0]));
+                st_cluster(cluster_map(smem_u32(&s.peer_tail[rank]), tid), s.warp_sum[0]);
             }
             sync();
         }
         uint32_t n = 0;
-        float others = 0.f;
+        u64 others = 0;
         for (int b = 0; b < cluster; ++b) n += s.peer_listed[b], others += s.peer_tail[b];
-        tail = (u64)(others * (float)(0.995 * 0x1p46 * 0.98922801319397548)) >> less;        // weight()'s unit
+        // in weight()'s unit, 2^-46 / kTable's factor: others is below 2^45
+        const u64 part = __umul64hi(others << 17, (u64)(0.995 * 0.98922801319397548 * 0x1p64));
+        const int down = min((int)(limit * 0.0625f), 100) + less - 8;
+        tail = down >= 0 ? down < 64 ? part >> down : 0 : part << -down;
         if (n <= kCap) {
             gather([&](float, uint32_t, int) { return true; });
             if (rank == 0) finish(use_k ? (uint32_t)k : 0xffffffffu, 0, use_k ? 0 : tail);

@@ -161,7 +161,8 @@ def sample(x, temperature, top_k, top_p, min_p, u):
         return -1, np.nan, 0
     if t == 0:
         return int(np.argmax(x)), 0.0, 1
-    order = [i for i in sorted(range(len(x)), key=lambda i: (-x[i], i)) if x[i] > -np.inf]
+    order = np.lexsort((np.arange(len(x)), -x))
+    order = order[x[order] > -np.inf]
     if top_k > 0:
         order = order[:int(top_k)]
     with np.errstate(over="ignore"):
@@ -172,10 +173,10 @@ def sample(x, temperature, top_k, top_p, min_p, u):
     if min_p > 0:
         least = top + t * math.log(min(float(min_p), 1.0)) if math.isfinite(t) else -np.inf
         n = min(n, int((x[order] >= least).sum()))
-    kept = sorted(order[:n])
+    kept = np.sort(order[:n])
     with np.errstate(over="ignore"):
         w = np.exp((x[kept] - top) / t)
     upto = np.cumsum(w)
     past = np.flatnonzero(upto > u * upto[-1]) if u < 1 else []
     at = int(past[0]) if len(past) else int(np.flatnonzero(w > 0)[-1])
-    return kept[at], float(np.log(w[at] / upto[-1])), len(kept)
+    return int(kept[at]), float(np.log(w[at] / upto[-1])), len(kept)

@@ -207,6 +207,34 @@ def test_router_scores_that_are_not_finite():
             assert np.array_equal(ids[t], ri[0]) and np.allclose(weights[t], rw[0], rtol=1e-5)
 
 
+@pytest.mark.parametrize("top_k", [1, 5, 12, 20])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_router_experts_masked_by_their_bias(top_k, sigmoid):
+    """Biases of -inf shut experts out: they come last, by index; +inf ones come first."""
+    x, w, b = router_inputs(6, 256, 20, seed=8)
+    b[[0, 3, 7, 8, 19]] = -math.inf
+    b[11] = math.inf
+    w[5] = w[4]
+    b[5] = b[4]
+    check_router(x, w, top_k, sigmoid=sigmoid, bias=b)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(sigmoid=True), dict(biased=True), dict(sigmoid=True, biased=True)])
+@pytest.mark.parametrize("top_k", [2, 15, 20])
+def test_router_ids_differ_whatever_the_scores_are(kw, top_k):
+    x, w, b = router_inputs(8, 64, 20, "f32", seed=9)
+    w[6] = w[5]                        # a tie, so that the scores are computed again
+    x[0, 3], x[1, 5], x[2], x[3, 0], x[3, 1] = math.nan, math.inf, math.nan, math.inf, -math.inf
+    x[4] = 3e38
+    w[9, 2] = math.nan
+    b[3], b[5], b[6] = math.nan, 0.1, 0.1
+    kw = dict(kw)
+    if kw.pop("biased", False):
+        kw["bias"] = b
+    ids, _ = run_router(x, w, top_k, **kw)
+    assert all(len(set(r)) == top_k and r.min() >= 0 and r.max() < 20 for r in ids)
+
+
 # ------------------------------------------------------------------ the experts' feed-forward
 
 FORMATS = {"Q4_0": syn.Q4_0, "Q4_1": syn.Q4_1, "Q5_0": syn.Q5_0, "Q5_1": syn.Q5_1, "Q8_0": syn.Q8_0, "Q2_K": syn.Q2_K, "Q3_K": syn.Q3_K,
@@ -385,6 +413,36 @@ def test_ffn_values_that_are_not_finite_stay_in_their_rows():
     assert np.array_equal(got[keep], want[keep])
 
 
+@pytest.mark.parametrize("types,K,F,E,T,top_k", [
+    (("Q4_K", "Q4_K", "Q4_K"), 16384, 256, 2, 3, 2),        # columns of all of K's chunks have no room
+    (("Q6_K", "Q6_K", "Q6_K"), 16384, 256, 2, 20, 1),
+    (("Q8_0", "Q8_0", "Q8_0"), 12832, 64, 2, 2, 1),
+    (("Q5_K", "Q2_K", "Q3_K"), 13312, 256, 2, 9, 1),
+    (("Q4_K", "Q4_K", "Q6_K"), 256, 16384, 2, 3, 1),        # many chunks of F
+    (("Q8_0", "Q8_0", "Q8_0"), 64, 12832, 2, 17, 2),
+    (("Q8_0", "Q4_0", "Q8_0"), 64, 64, 1024, 64, 8),        # as many experts and rows as there may be
+    (("Q6_K", "Q6_K", "Q6_K"), 256, 256, 7, 256, 2),
+    (("Q3_K", "Q3_K", "Q5_K"), 256, 512, 3, 1, 512),        # one token, experts many times over
+    (("Q5_0", "Q5_0", "Q4_1"), 32, 32, 1, 512, 1),
+])
+@pytest.mark.parametrize("xdt,ydt", [("bf16", "bf16"), ("f32", "f32")])
+def test_ffn_ends_of_the_ranges(types, K, F, E, T, top_k, xdt, ydt):
+    ids = np.random.default_rng(E).integers(0, E, (T, top_k))
+    check_ffn(Experts(types, K, F, E, seed=13), T, top_k, xdt=xdt, ydt=ydt, ids=ids, seed=14)
+
+
+def test_ffn_weights_at_the_end_of_their_allocation():
+    """Nothing past the last expert's bytes is read: what stands there does not matter, and they may end anywhere."""
+    for t, K, F in (("Q6_K", 256, 256), ("Q5_0", 32, 96), ("Q3_K", 256, 512), ("Q8_0", 96, 32), ("Q4_0", 64, 32)):
+        ex = Experts((t, t, t), K, F, 3, seed=15)
+        for i in range(3):
+            flat = ex.dev[i].reshape(-1)
+            room = torch.full((flat.numel() + 64,), 0xff, dtype=torch.uint8, device=DEV)
+            room[:flat.numel()] = flat
+            ex.dev[i] = room[:flat.numel()]
+        check_ffn(ex, 2, 2, xdt="f32", ydt="f32", seed=16)
+
+
 def test_ffn_in_place_and_again():
     ex = Experts(("Q4_K", "Q4_K", "Q4_K"), 512, 512, 6, seed=12)
     a = run_ffn(ex, 17, 3, seed=1)[4]
@@ -513,6 +571,35 @@ def test_sample_does_not_depend_on_the_cut():
     for r in (0, 7, 299):
         one, l1 = run_sample(x[r:r + 1], g.gguf_sampler(t, None, p), u[r:r + 1])
         assert one[0] == many[r] and l1[0] == lp[r]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_sample_top_p_of_masked_rows_at_any_temperature(dt):
+    """What lies below top-p's bound is summed without being listed: masked tokens add nothing to it."""
+    x, rs = logits_of(12, 6000, dt, seed=7)
+    x[:, 1::3] = -math.inf
+    x[6:, 2::3] = torch.finfo(x.dtype).min
+    t = [math.inf, 1e30, 1e4, 1.0, 1e-3, 1e-30] * 2
+    for p in (0.3, 0.9, 0.999):
+        check_sample(x, u=rs.random(12), temp=t, top_p=p)
+        check_sample(x, u=rs.random(12), temp=t, top_p=p, min_p=0.2)
+
+
+def test_sample_top_p_does_not_depend_on_the_cut():
+    rs = np.random.default_rng(8)
+    x = torch.tensor(rs.standard_normal((400, 20000)) * 1.5, dtype=torch.float32, device=DEV)
+    u = torch.tensor(rs.random(400), dtype=torch.float32, device=DEV)
+    p = torch.tensor(rs.uniform(0.05, 0.95, 400), dtype=torch.float32, device=DEV)
+    many, lp = run_sample(x, g.gguf_sampler(None, None, p), u)
+    for r in range(0, 400, 7):
+        one, l1 = run_sample(x[r:r + 1], g.gguf_sampler(None, None, p[r:r + 1]), u[r:r + 1])
+        assert one[0] == many[r] and l1[0] == lp[r]
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=50), dict(top_k=100000, top_p=0.8), dict(top_p=0.9), dict(min_p=0.1)])
+def test_sample_largest_vocabulary(kw):
+    x, rs = logits_of(2, 1 << 22, "bf16", seed=9, spread=2.0)
+    check_sample(x, u=rs.random(2), **kw)
 
 
 def test_sample_draws_with_the_frequencies_asked_for():
