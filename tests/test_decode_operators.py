@@ -617,3 +617,110 @@ def test_sample_without_logprob():
     x, rs = logits_of(2, 100, seed=6)
     token, lp = run_sample(x, None, torch.tensor([0.3, 0.6], device=DEV), logprob=False)
     assert (lp == -7.0).all() and (token >= 0).all()
+
+
+# ------------------------------------------------------------------ streams, graphs, calls next to each other
+
+class Work:
+    """One call of each operator on fixed buffers."""
+
+    def __init__(self, seed, T=5, ws=None):
+        rs = np.random.default_rng(seed)
+        f = lambda *s: torch.tensor(rs.standard_normal(s), dtype=torch.float32, device=DEV)      # noqa: E731
+        self.case = Case([(T, 20)], 2, 64, "bf16", seed=seed)
+        self.qkv = f(T, 8 * 64).bfloat16()
+        self.turned = torch.empty((T, 4, 64), dtype=torch.bfloat16, device=DEV)
+        self.norm, self.rope = g.gguf_head_norm(1 + f(64) / 8, 1 + f(64) / 8), g.gguf_rope(freqs_of(64), 64, 1)
+        self.batch, self.cache = self.case.batch(), g.gguf_kv_cache(self.case.k, self.case.v)
+        self.x, self.router = f(T, 512), g.gguf_router(f(9, 512) / 22, 3)
+        self.ids, self.w = torch.empty((T, 3), dtype=torch.int32, device=DEV), torch.empty((T, 3), device=DEV)
+        self.experts = Experts(("Q4_K", "Q4_K", "Q6_K"), 512, 256, 9, seed=seed)
+        self.T, self.y = T, torch.empty((T, 512), device=DEV)
+        self.size = g.gguf_moe_ffn_workspace_size(256, T, 3)
+        self.ws = torch.empty(self.size, dtype=torch.uint8, device=DEV) if ws is None else ws
+        self.logits, self.u = f(T, 9001) * 3, torch.tensor(rs.random(T), dtype=torch.float32, device=DEV)
+        self.sampler = g.gguf_sampler(None, None, torch.full((T,), 0.9, device=DEV))
+        self.token, self.lp = torch.empty(T, dtype=torch.int32, device=DEV), torch.empty(T, device=DEV)
+
+    def run(self, stream=None):
+        q, k, v = self.qkv.split((256, 128, 128), dim=1)
+        g.gguf_kv_append_norm(q, 512, k, 512, v, 512, 2, 4, self.norm, self.rope, self.batch, self.cache, self.turned, 256, stream)
+        g.gguf_moe_router(self.x, 0, self.T, 512, self.router, self.ids, self.w, stream)
+        g.gguf_moe_ffn(self.experts.struct(), self.x, 0, self.T, self.ids, self.w, 3, None, self.y, 0, self.ws, self.size, stream)
+        g.gguf_sample(self.logits, 0, 9001, self.T, 9001, self.sampler, self.u, self.token, self.lp, stream)
+
+    def outputs(self):
+        return [t.clone() for t in (self.turned, self.case.k, self.case.v, self.ids, self.w, self.y, self.token, self.lp)]
+
+    def clear(self):
+        for t in (self.turned, self.case.k, self.case.v, self.ids, self.w, self.y, self.token, self.lp, self.ws):
+            t.fill_(1)
+
+
+def expect(works):
+    out = []
+    for w in works:
+        w.clear()
+        w.run()
+        out.append(w.outputs())
+    torch.cuda.synchronize()
+    assert g.gguf_mm_check_errors() == 0
+    for w in works:
+        w.clear()
+    torch.cuda.synchronize()
+    return out
+
+
+def same(works, want):
+    torch.cuda.synchronize()
+    assert g.gguf_mm_check_errors() == 0
+    assert all(torch.equal(a, b) for w, o in zip(works, want) for a, b in zip(w.outputs(), o))
+
+
+def test_two_streams_at_once():
+    works = [Work(1), Work(2, T=40)]
+    want = expect(works)
+    streams = [torch.cuda.Stream() for _ in works]
+    for _ in range(20):
+        for w, s in zip(works, streams):
+            w.run(s)
+    same(works, want)
+
+
+def test_graphs_that_share_a_workspace():
+    """Replayed one after the other on one stream, without anything in between."""
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    works = [Work(3, T=40, ws=ws), Work(4, T=1, ws=ws), Work(5, T=2, ws=ws)]
+    want = expect(works)
+    graphs = []
+    for w in works:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            w.run()
+        graphs.append(graph)
+    for _ in range(5):
+        for graph in graphs:
+            graph.replay()
+    same(works, want)
+    # new inputs in the captured buffers
+    for w in works:
+        w.x.mul_(-0.5), w.logits.neg_(), w.qkv.mul_(2)
+    want = expect(works)
+    for graph in graphs:
+        graph.replay()
+    same(works, want)
+
+
+def test_calls_back_to_back_on_one_workspace():
+    """A call's kernels may begin before the call ahead has ended: what they write and read of the workspace does not."""
+    ws = torch.empty(1 << 21, dtype=torch.uint8, device=DEV)
+    works = [Work(6 + i, T=t, ws=ws) for i, t in enumerate((1, 64, 3, 17, 1, 30))]
+    want = expect(works)
+    for _ in range(10):
+        for w in works:
+            w.run()
+    same(works, want)
+    for _ in range(10):                      # the experts' calls alone, next to each other
+        for w in works:
+            g.gguf_moe_ffn(w.experts.struct(), w.x, 0, w.T, w.ids, w.w, 3, None, w.y, 0, ws, w.size)
+    same(works, want)
