@@ -135,11 +135,6 @@ __device__ __forceinline__ u64 share_of(float f, u64 W, bool up) {
     return v + (up && rest ? 1 : 0);
 }
 
-// logp of w of W, to f32's rounding also where it is near 0
-__device__ __forceinline__ float log_share(u64 w, u64 W) {
-    const float all = (float)W;
-    return 2 * w > W ? log1pf(-((float)(W - w) / all)) : logf((float)w / all);
-}
 
 // seg: tokens of a warp, a multiple of 128; warp w of a row's cluster has those
 // from index first + w * seg on.
@@ -262,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
     // The bounds: a token with (m - x) * bin_scale at `limit` or more is not kept.
     float limit = INFINITY;
-    const bool by_share = use_p && !use_k && top_p < 0.9999f;
+    const bool tame = ch >= 1e-30f;                  // temperatures below 1e30, at which a distance that f32 has gives no weight
+    const bool by_share = use_p && !use_k && top_p < 0.9999f && tame;
     if (greedy) {
         limit = 1e-37f;
     } else if (use_k || by_share) {
@@ -305,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         __syncthreads();
         if (s.bin < kBins - 1) limit = (float)(s.bin + 1);
     }
-    if (use_m && !(use_k && use_p)) limit = fminf(limit, 16.f * (0.01f - __log2f(fminf(min_p, 1.f))) + 1.f);
+    if (use_m && !(use_p && (use_k || !tame))) limit = fminf(limit, 16.f * (0.01f - __log2f(fminf(min_p, 1.f))) + 1.f);
 
     // the tokens above the bounds, listed by warp in the row's order; the others' weights, for top-p
     bool listed = limit < INFINITY;
@@ -321,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         // the row is cut, and its rounding lies far below the weight of a token at the border.
         uint32_t rest = 0;
         const int below = min((int)(limit * 0.0625f), 100);
-        const float unit = __uint_as_float((uint32_t)(127 + 21 + below) << 23), farthest = fminf(300.f / ch, 3e38f);
+        const float unit = __uint_as_float((uint32_t)(127 + 21 + below) << 23), farthest = 300.f / ch;
         // the same bound for the logits themselves, a little below
         const float above = fmaxf(m - limit / bin_scale - 1e-6f * (fabsf(m) + limit / bin_scale), -3.402823466e38f);
         each_four([&](float (&f)[4], int i) {
@@ -332,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 if (want_tail) {
                     const float dh = fmaxf(f[j] - m, -farthest);     // where the weight is 0, and dh * cl still a number
                     const float w = fmaf(ex2(fmaf(dh, ch, dh * cl)), unit, 8388608.f);
-                    rest += in[j] || f[j] == -INFINITY ? 0u : __float_as_uint(w) - 0x4b000000u;
+                    rest += in[j] ? 0u : __float_as_uint(w) - 0x4b000000u;
                 }
             }
             if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) return;
@@ -508,9 +504,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     // the share of W that top-p keeps, the place in W that u asks for
     auto goal_of_p = [&](u64 W) { return max((u64)1, share_of(fmaxf(top_p, 0.f), W, true)); };
     auto target_of = [&](u64 W) { return u < 1.f ? share_of(u > 0.f ? u : 0.f, W, false) : u >= 1.f ? W - 1 : (u64)0; };
-    auto emit = [&](int i, u64 w, u64 W) {
+    // logprob to f32's rounding: near 0 from what the others have, else from the logit (an unlikely token's integer has few bits)
+    auto emit = [&](int i, u64 w, u64 W, float v) {
         p.token[r] = i;
-        if (p.logprob) p.logprob[r] = log_share(w, W);
+        if (!p.logprob) return;
+        const float all = (float)W;
+        p.logprob[r] = 2 * w > W ? log1pf(-((float)(W - w) / all)) : -((m - v) / T) - logf(all / (float)weight(m));
     };
     int round = 0;
     // the first index, in the vocabulary's order, at which the sum of f(value, index) passes goal_of(the whole sum)
@@ -559,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                     u64 b = before + upto - own;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if (b <= goal && b + w[j] > goal) found(at[j], w[j], W);
+                        if (b <= goal && b + w[j] > goal) found(at[j], w[j], W, v[j]);
                         b += w[j];
                     }
                 }
@@ -601,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         for (int v = 0; v < kWarps; ++v) W += s.warp_sum[v];
         if (keep) {
             const u64 c = (u64)s.cand_high[tid] << 32 | s.cand_low[tid], t = target_of(W);
-            if (c > t && c - w <= t) emit((int)idx, w, W);
+            if (c > t && c - w <= t) emit((int)idx, w, W, float_of(key));
         }
     };
 
@@ -698,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const u64 many = (goal - (by_sum ? base_sum : (u64)base_count) + w - 1) / w;
             locate([&](float v, int i) -> u64 { const uint32_t key = key_of(v); return key == lo && kept(key, i) ? 1 : 0; },
                    [&](u64) { return many - 1; },
-                   [&](int i, u64, u64) {
+                   [&](int i, u64, u64, float) {
                        for (int c = 0; c < cluster; ++c) {
                            st_cluster(cluster_map(smem_u32(&s.K), c), lo);
                            st_cluster(cluster_map(smem_u32(&s.I), c), (uint32_t)i + 1);
