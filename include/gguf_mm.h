@@ -481,8 +481,9 @@ typedef struct {
  *   w_0 + ... + w_i > u[r] * (sum of all w),
  * u [rows] f32 uniform in [0, 1) (below 0 and NaN count as 0; at 1 and above the
  * last token that passes is taken).  The weights are accurate to about 1e-9 of
- * themselves and their sums exact, so that the token is the one that 64-bit
- * arithmetic gives but where u or top_p falls that close to a border.
+ * the largest and their sums exact (top_p without top_k: the part of the sum
+ * that it leaves out is accurate to about 1e-6 of itself), so that the token is the one
+ * that 64-bit arithmetic gives but where u or top_p falls that close to a border.
  *   logprob  f32 [rows] or NULL: log(w_token / sum of all w), 0 where the
  *            temperature is 0
  * A row without a distribution (a NaN or +inf among its logits, nothing but
@@ -525,8 +526,10 @@ typedef struct {
  * the top_k of the largest p + bias in falling order, the lower index first among equals:
  *   ids [T][top_k] int32,  weights [T][top_k] f32.
  * The choice and its order are those of 64-bit arithmetic; weights are accurate
- * to f32's rounding.  A token with a score that is not finite gets top_k
- * different experts all the same, and weights that may be NaN.  K a multiple of
+ * to f32's rounding, of scores that are neither beyond f32's range nor made of
+ * products below it.  A bias of -inf shuts an expert out: it comes after all others.
+ * A token with a score that is not finite gets top_k different
+ * experts all the same, and weights that may be NaN.  K a multiple of
  * 8; x and w 16-byte aligned, the other arrays 4-byte aligned.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, NO_DEVICE, CUDA. */
 int gguf_moe_router(const void* x, int xdt, int64_t T, int64_t K, const gguf_router* router, int32_t* ids,
@@ -552,7 +555,7 @@ typedef struct {
 /* A few tokens through their experts:
  *   y[t] = residual[t] + sum over s of weights[t][s] * Down_e(act(Gate_e x[t]) * Up_e x[t]),  e = ids[t][s]
  *   x [T][K] of xdt, ids [T][top_k] int32, weights [T][top_k] f32, residual [T][K]
- *   of ydt or NULL, y [T][K] of ydt (F32, F16 or BF16 each); y may be residual,
+ *   of ydt or NULL, y [T][K] of ydt (F32, F16 or BF16 each); y may be residual itself,
  *   and may not overlap x.
  * At most 512 routed rows (T * top_k): larger batches are gguf_mm_id's and
  * gguf_mm_id_slots'.  An id outside [0, n_expert) adds nothing; one that comes
