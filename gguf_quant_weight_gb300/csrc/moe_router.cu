@@ -410,7 +410,8 @@ cudaError_t launch(const RouterParams& p, int pdl, cudaStream_t s) {
 
 cudaError_t moe_router_launch(const RouterParams& p, int num_sms, int pdl, cudaStream_t s) {
     // few tokens: one or two to a cluster, two experts to a warp, over as many SMs as
-    // that gives; then four and eight tokens
+    // that gives; then four and eight tokens.  One token of 2048 over 128 experts takes 5.6 us so, and 7.5, 8.9 and 11.4
+    // in clusters for two, four and eight; 509 tokens 25.7 us in clusters for eight, 26.8 for four, 43 for two.
     const int64_t blocks = std::min<int64_t>(8, ceil_div(p.n_expert, 2 * kWarps)), clusters = std::max<int64_t>(1, 2 * num_sms / blocks);
     if (p.T <= clusters) return launch<1, 2>(p, pdl, s);
     if (p.T <= 2 * clusters) return launch<2, 2>(p, pdl, s);

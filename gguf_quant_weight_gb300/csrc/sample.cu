@@ -765,7 +765,8 @@ cudaError_t launch(const SampleParams& p, int num_sms, int pdl, cudaStream_t s) 
     cudaError_t e = set_once(sample_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared), done);
     if (e != cudaSuccess) return e;
     // up to 2175 tokens a warp, of which its list holds two fifths; more blocks
-    // to a row where there are few rows
+    // to a row where there are few rows.  Always as many blocks as there may be: 37 rows of 32003 take 29.6 us and not 23.1,
+    // 256 of 131072 238 and not 197; only what the lists ask for: 38.6 us, and one row of 128259 16.0 and not 12.8.
     const int64_t span = p.vocab + 3;
     int cluster = 1;
     while (cluster < 8 && (span > cluster * (int64_t)(kWarps * 2175) || (p.rows * cluster * 2 <= num_sms && span > cluster * 2048))) cluster *= 2;

@@ -413,6 +413,16 @@ def test_ffn_values_that_are_not_finite_stay_in_their_rows():
     assert np.array_equal(got[keep], want[keep])
 
 
+@pytest.mark.parametrize("types", [(t, t, t) for t in FORMATS] + [("Q4_K", "Q6_K", "Q5_0"), ("Q5_1", "Q8_0", "Q2_K")])
+@pytest.mark.parametrize("xdt,ydt", [("bf16", "f32"), ("f32", "bf16")])
+def test_ffn_many_rows_of_each_expert(types, xdt, ydt):
+    """Two tiles of columns at a time, and what an expert's last group has left of them."""
+    ex = Experts(types, 256, 256, 3, seed=17)
+    for rows in ((93, 51, 6), (49, 48, 80)):
+        ids = np.random.default_rng(18).permutation(np.repeat(np.arange(3), rows)).reshape(-1, 1)
+        check_ffn(ex, len(ids), 1, xdt=xdt, ydt=ydt, ids=ids, seed=19)
+
+
 @pytest.mark.parametrize("types,K,F,E,T,top_k", [
     (("Q4_K", "Q4_K", "Q4_K"), 16384, 256, 2, 3, 2),        # columns of all of K's chunks have no room
     (("Q6_K", "Q6_K", "Q6_K"), 16384, 256, 2, 20, 1),
