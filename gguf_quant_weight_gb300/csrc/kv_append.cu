@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
 
 // The same for positions below 2^24, which are floats, without doubles (of which an SM does two a cycle): the frequency in
 // turns in two floats, and what the product's rounding leaves by a second product.  Off by 2^-46 of the turns and by
-// two roundings of a part below one half, 2^-24 of a turn.  (37 mixed tokens: 9.7 us with doubles, 9.2 so.)
+// two roundings of a part below one half, 2^-24 of a turn.  (48 mixed sequences: 9.7 us with doubles, 9.2 so.)
 __device__ __forceinline__ void near_angle(const AppendParams& p, int t, int pos, int i, float& cos, float& sin) {
     const int at = p.positions ? p.positions[t] : pos;
     if (abs(at) >= 1 << 24) return angle(p, t, pos, i, cos, sin);
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendPa
     __syncthreads();
     pdl_wait();
     int h0 = blockIdx.y * groups + tid / lanes;
-    Head ws[kAhead];
+    Head ws[kAhead] = {};            // what a lane has no unit for stays 0, so a head's sum can take all lanes
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
         if (h0 + j * step < n) fetch(h0 + j * step, ws[j]);
@@ -293,23 +293,21 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendPa
     const float per_value = 1.f / (float)D;
     // the whole warp comes here for as many heads as any of its groups has
     auto write = [&](int h, const Head& w) {
-        const bool on = h < n;
         float a[U][V], b[U][V], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int u = me + i * lanes;
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                a[i][k] = on && u < units ? w.a[i][k] : 0.f;
+                a[i][k] = w.a[i][k];
                 sum = fmaf(a[i][k], a[i][k], sum);
                 if (NEOX) {
-                    b[i][k] = on && u < turn ? w.b[NEOX ? i : 0][k] : 0.f;
+                    b[i][k] = w.b[NEOX ? i : 0][k];
                     sum = fmaf(b[i][k], b[i][k], sum);
                 }
             }
         }
         for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (!on || !(h < p.heads || slot >= 0)) return;
+        if (h >= n || !(h < p.heads || slot >= 0)) return;
         const float* weight = h < p.heads ? (p.q_norm ? s_wq : nullptr) : h < HK && p.k_norm ? s_wk : nullptr;
         const float inv = rsqrtf(fmaf(sum, per_value, p.eps));       // to two units in the last place
         C* dst = h < p.heads ? static_cast<C*>(p.q_out) + t * p.ldqo + h * D
@@ -380,7 +378,7 @@ cudaError_t launch_norm(const AppendParams& p, int num_sms, int pdl, cudaStream_
 template <class X, class C, int V, bool NEOX>
 cudaError_t launch(const AppendParams& p, int num_sms, int pdl, cudaStream_t s) {
     // f32 rows in 16 bytes a lane: eight values and their angles take so many registers that fewer blocks fit
-    // (9,600 tokens of 40 heads: 60.5 us with eight, 57.6 so; 37 mixed tokens 9.2 either way)
+    // (9,600 tokens of 40 heads: 60.5 us with eight, 57.2 so)
     if (p.q_norm || p.k_norm) return launch_norm<X, C, (sizeof(X) == 4 && V == 8 ? 4 : V), NEOX>(p, num_sms, pdl, s);
     const int64_t per_token = (int64_t)(p.heads + 2 * p.c.kv_heads) * p.c.dim / V;
     // enough blocks to occupy the SMs when there are few tokens
