@@ -235,6 +235,11 @@ __device__ __forceinline__ void read_v(const float* p, float (&f)[V]) {
 // few shuffles and each value is still read once; a lane takes U units of the
 // head, more than one only where the rotated part's edges keep vectors below
 // four values.  Values are copied by the same groups.
+// Bytes bound it, and next to them the arithmetic of norm and turn, some 60 % of
+// the issue slots.  One head of a lane is on its way while blocks enough are on the
+// SM: with two (and 16 more registers, so fewer blocks) 9,600 tokens of 40 heads in f32 take
+// 60.5 us and not 53.0 (5.5 TB/s), in bf16 68.7 and not 52.5, and 48 mixed sequences 8.9 and not
+// 9.7; with 8 bytes a lane in bf16 54.8, and 66.8 where pairs are neighbours.
 template <class X, class C, int V, bool NEOX>
 __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendParams p, int lanes) {
     constexpr int U = V >= 4 ? 1 : V == 2 ? 2 : 4;
@@ -267,10 +272,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendPa
     __syncthreads();
     pdl_wait();
     int h0 = blockIdx.y * groups + tid / lanes;
-    Head ws[kAhead] = {};            // what a lane has no unit for stays 0, so a head's sum can take all lanes
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-        if (h0 + j * step < n) fetch(h0 + j * step, ws[j]);
+    Head w{};                        // what a lane has no unit for stays 0, so a head's sum can take all lanes
+    if (h0 < n) fetch(h0, w);
     if (tid < D) {
         if (p.q_norm) s_wq[tid] = p.q_norm[tid];
         if (p.k_norm) s_wk[tid] = p.k_norm[tid];
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendPa
     }
     const float per_value = 1.f / (float)D;
     // the whole warp comes here for as many heads as any of its groups has
-    auto write = [&](int h, const Head& w) {
+    auto write = [&](int h) {
         float a[U][V], b[U][V], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -355,13 +358,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_norm_kernel(const AppendPa
         }
     };
     // a warp's groups hold neighbouring heads, so the first of them says when it is done
-    for (int w0 = h0 - (tid & 31) / lanes; w0 < n; w0 += kAhead * step, h0 += kAhead * step) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (w0 + j * step < n) write(h0 + j * step, ws[j]);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (h0 + (kAhead + j) * step < n) fetch(h0 + (kAhead + j) * step, ws[j]);
+    for (int w0 = h0 - (tid & 31) / lanes; w0 < n; w0 += step, h0 += step) {
+        write(h0);
+        if (h0 + step < n) fetch(h0 + step, w);
     }
 }
 
@@ -377,9 +376,7 @@ cudaError_t launch_norm(const AppendParams& p, int num_sms, int pdl, cudaStream_
 
 template <class X, class C, int V, bool NEOX>
 cudaError_t launch(const AppendParams& p, int num_sms, int pdl, cudaStream_t s) {
-    // f32 rows in 16 bytes a lane: eight values and their angles take so many registers that fewer blocks fit
-    // (9,600 tokens of 40 heads: 60.5 us with eight, 57.2 so)
-    if (p.q_norm || p.k_norm) return launch_norm<X, C, (sizeof(X) == 4 && V == 8 ? 4 : V), NEOX>(p, num_sms, pdl, s);
+    if (p.q_norm || p.k_norm) return launch_norm<X, C, V, NEOX>(p, num_sms, pdl, s);
     const int64_t per_token = (int64_t)(p.heads + 2 * p.c.kv_heads) * p.c.dim / V;
     // enough blocks to occupy the SMs when there are few tokens
     const int64_t share = std::max<int64_t>(1, std::min(ceil_div(per_token, kThreads), ceil_div(4 * num_sms, p.b.n_tokens)));
