@@ -920,11 +920,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnP
               p.status, kSlot, p.down_stages};
     ring.init(piece_arrivals(QT), lane);
     // The kernel before this one let it begin when up had ended, so the routes are
-    // there; the columns are waited for once the first weights are on their way.
+    // there (read past L1, as nothing has been waited for here); the columns are waited
+    // for once the first weights are on their way.
     for (int i = tid; i < (int)(Routes::bytes(entries) / 16); i += kThreads)
-        reinterpret_cast<uint4*>(s_dyn)[i] = reinterpret_cast<const uint4*>(p.routes)[i + 1];
-    const int items = *reinterpret_cast<const int*>(p.routes) * splits;
-    if (tid < entries) weights[tid] = (unsigned)p.ids[tid] < (unsigned)p.n_expert ? p.weights[tid] : 0.f;
+        reinterpret_cast<uint4*>(s_dyn)[i] = __ldcg(reinterpret_cast<const uint4*>(p.routes) + i + 1);
+    const int items = __ldcg(reinterpret_cast<const int*>(p.routes)) * splits;
+    if (tid < entries) weights[tid] = (unsigned)__ldcg(p.ids + tid) < (unsigned)p.n_expert ? __ldcg(p.weights + tid) : 0.f;
     // an id of no expert adds 0 * 0
     for (int i = tid; i < splits * entries * 4; i += kThreads) reinterpret_cast<float4*>(sums)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
@@ -946,10 +947,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_ffn_down_kernel(const MoeFfnP
         if (!kBars) copies_commit();
     };
     for (int i = 0; i < p.down_stages; ++i) fetch();
+    pdl_wait();
     float residual = 0.f;           // of this thread's first output
     if (p.residual && tid < p.T * 16 && row0 + (tid & 15) < p.K)
         residual = load_act(p.residual, p.ydt, (tid >> 4) * p.K + row0 + (tid & 15));
-    pdl_wait();
     const int g = lane >> 2, t = lane & 3;
     for (int item = warp; item < items; item += kWarps) {
         const Group group = routes.down[item / splits];

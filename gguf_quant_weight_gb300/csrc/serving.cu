@@ -262,6 +262,12 @@ int gguf_moe_ffn(const gguf_moe_weights* experts, const void* x, int xdt, int64_
     if (!aligned16(m.gate) || !aligned16(m.up) || !aligned16(m.down) || !aligned16(x) || !aligned16(residual) || !aligned16(y) ||
         !aligned16(workspace) || !aligned4(ids) || !aligned4(weights))
         return GGUF_ERR_MISALIGNED;
+    auto overlap = [](const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+        const uintptr_t u = reinterpret_cast<uintptr_t>(a), v = reinterpret_cast<uintptr_t>(b);
+        return u < v + b_bytes && v < u + a_bytes;
+    };
+    const int64_t x_bytes = T * m.K * (xdt == GGUF_DT_F32 ? 4 : 2), y_bytes = T * m.K * (ydt == GGUF_DT_F32 ? 4 : 2);
+    if (overlap(x, x_bytes, y, y_bytes) || (residual && residual != y && overlap(residual, y_bytes, y, y_bytes))) return GGUF_ERR_INVALID_ARG;
     if (!workspace || ws_bytes < gguf_moe_ffn_workspace_size(m.F, T, top_k)) return GGUF_ERR_WORKSPACE;
     int sms = 0, *status = nullptr;
     const int st = current_device_launch_facts(&sms, &status);

@@ -556,7 +556,7 @@ typedef struct {
  *   y[t] = residual[t] + sum over s of weights[t][s] * Down_e(act(Gate_e x[t]) * Up_e x[t]),  e = ids[t][s]
  *   x [T][K] of xdt, ids [T][top_k] int32, weights [T][top_k] f32, residual [T][K]
  *   of ydt or NULL, y [T][K] of ydt (F32, F16 or BF16 each); y may be residual itself,
- *   and may not overlap x.
+ *   and overlaps neither it in part nor x.
  * At most 512 routed rows (T * top_k): larger batches are gguf_mm_id's and
  * gguf_mm_id_slots'.  An id outside [0, n_expert) adds nothing; one that comes
  * twice in a token adds twice.  The activations are not rounded to int8 codes:

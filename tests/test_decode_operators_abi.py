@@ -67,7 +67,7 @@ def experts(**kw):
 
 
 def test_ffn_refusals(lib):  # noqa: F811
-    def call(m=None, x=16, xdt=2, T=2, ids=16, weights=16, top_k=2, res=None, y=16, ydt=2, ws=16, size=1 << 20):
+    def call(m=None, x=16, xdt=2, T=2, ids=16, weights=16, top_k=2, res=None, y=1 << 40, ydt=2, ws=16, size=1 << 20):
         return lib.gguf_moe_ffn(r(m or experts()), x, xdt, T, ids, weights, top_k, res, y, ydt, ws, size, None)
 
     assert lib.gguf_moe_ffn(None, 16, 2, 1, 16, 16, 1, None, 16, 2, 16, 1 << 20, None) == INV
@@ -84,6 +84,10 @@ def test_ffn_refusals(lib):  # noqa: F811
         assert call(**kw) == MIS, kw
     for name in ("gate", "up", "down"):
         assert call(experts(**{name: 24})) == MIS
+    # y may be the residual itself, and overlaps neither it in part nor x (2 rows of 256 bf16 values: 1024 bytes)
+    assert call(y=16) == INV and call(y=16 + 1008) == INV and call(x=2048, y=16, ydt=0) == INV
+    assert call(res=(1 << 40) - 1008) == INV and call(res=(1 << 40) + 16) == INV
+    assert call(y=16 + 1024, ws=None) == WS and call(res=1 << 40, ws=None) == WS and call(res=(1 << 40) + 1024, ws=None) == WS
     assert call(ws=None) == WS and call(size=g.gguf_moe_ffn_workspace_size(512, 2, 2) - 1) == WS
 
 
