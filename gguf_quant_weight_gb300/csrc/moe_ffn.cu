@@ -10,8 +10,8 @@
 // the batch's rows that it has: the tensor cores' m16n8k16 takes 16 weight rows
 // as A and up to 8 columns of activations as B.  A's values are the blocks'
 // codes.  A code without an offset needs no conversion: an integer's bits are
-// the f16 number 2^-24 times it (a subnormal, which the tensor cores take), so a mask gives
-// two of them, and the high nibble stays where it is, 16 times as large.  Codes
+// the f16 number 2^-24 times it (a subnormal, which the tensor cores take), so a shift and a mask give
+// two of them.  Codes
 // with a zero point become 1024 + code by a byte permutation, less 1024 + zero
 // point.  The products of a sub-block are summed by the tensor cores, and its
 // scale is applied in f32.  B's columns are the activations scaled by a power of two
@@ -263,6 +263,11 @@ __host__ __device__ constexpr int zero_point(int qt) {
     return qt == GGUF_Q6_K ? 32 : qt == GGUF_Q3_K ? 4 : qt == GGUF_Q8_0 ? 128 : block32(qt) ? b32_zero_point(qt) : 0;
 }
 
+// Codes without a zero point stand this far up in their bytes (see multiply()).
+__host__ __device__ constexpr int code_shift(int qt) {
+    return qt == GGUF_Q2_K ? 6 : qt == GGUF_Q4_K || qt == GGUF_Q4_1 ? 4 : qt == GGUF_Q5_K || qt == GGUF_Q5_1 ? 3 : 0;
+}
+
 // 256 values of one weight row as lane t of four holds them.  load(): from their
 // first byte; nsub, how many of their 32-value groups exist (fewer than 8 at the
 // end of a row of 32-value blocks).
@@ -287,8 +292,7 @@ template <> struct Raw<GGUF_Q5_K> {
         for (int p = 0; p < 4; ++p) w[p][0] = ld32(b + 48 + 32 * p + 4 * t), w[p][1] = ld32(b + 64 + 32 * p + 4 * t);
     }
     __device__ __forceinline__ uint32_t codes(int j, int half, int) const {
-        const uint32_t high = j < 4 ? h[half] << (4 - j) : h[half] >> (j - 4);
-        return ((w[j >> 1][half] >> (4 * (j & 1))) & 0x0f0f0f0fu) | (high & 0x10101010u);
+        return ((j & 1 ? w[j >> 1][half] >> 1 : w[j >> 1][half] << 3) & 0x78787878u) | ((h[half] << (7 - j)) & 0x80808080u);
     }
 };
 template <> struct Raw<GGUF_Q6_K> {
@@ -318,7 +322,7 @@ template <> struct Raw<GGUF_Q2_K> {
         for (int p = 0; p < 2; ++p) w[p][0] = ld32(b + 16 + 32 * p + 4 * t), w[p][1] = ld32(b + 32 + 32 * p + 4 * t);
         dm = ld32(b + 80);
     }
-    __device__ __forceinline__ uint32_t codes(int j, int half, int) const { return (w[j >> 2][half] >> (2 * (j & 3))) & 0x03030303u; }
+    __device__ __forceinline__ uint32_t codes(int j, int half, int) const { return (w[j >> 2][half] << (6 - 2 * (j & 3))) & 0xc0c0c0c0u; }
 };
 template <> struct Raw<GGUF_Q3_K> {
     uint32_t w[2][2], h[2], sc[3], d;
@@ -364,11 +368,12 @@ template <int QT> struct Raw {
         if constexpr (QT == GGUF_Q8_0) {
             return w[j][half] ^ 0x80808080u;
         } else {
-            uint32_t c = (w[j][0] >> (4 * half)) & 0x0f0f0f0fu;
+            constexpr int up = code_shift(QT);
+            uint32_t c = (up >= 4 * half ? w[j][0] << (up - 4 * half) : w[j][0] >> (4 * half - up)) & (0x0f0f0f0fu << up);
             if constexpr (b32_has_qh(QT)) {
                 // bits 16 half + 4 t .. + 3, one to a byte: bit i times 2^7i lands on bit 8i, and no other product does
                 const uint32_t four = (qh[j] >> (16 * half + 4 * t)) & 15u;
-                c |= ((four * 0x00204081u) & 0x01010101u) << 4;
+                c |= ((four * 0x00204081u) & 0x01010101u) << (4 + up);
             }
             return c;
         }
@@ -394,10 +399,9 @@ __device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<
 __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 __device__ __forceinline__ float f16_low(uint32_t v) { return __half2float(__ushort_as_half((unsigned short)(v & 0xffffu))); }
 __device__ __forceinline__ float f16_high(uint32_t v) { return __half2float(__ushort_as_half((unsigned short)(v >> 16))); }
-// byte i of a word as a float, and (sixteenth) a sixteenth of it: the mantissa's last bits of 2^23 (2^19)
-__device__ __forceinline__ float byte_f(uint32_t w, int i, bool sixteenth = false, float less = 0.f) {
-    const uint32_t m = sixteenth ? 0x49000000u : 0x4b000000u;
-    return __uint_as_float(__byte_perm(w, m, 0x7650 | i)) - (__uint_as_float(m) + less);
+// byte i of a word as a float, less `less`: the mantissa's last bits of 2^23
+__device__ __forceinline__ float byte_f(uint32_t w, int i, float less = 0.f) {
+    return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7650 | i)) - (8388608.f + less);
 }
 
 // The 6-bit scales (lo, hi of four) and mins of Q4_K / Q5_K as words of bytes.
@@ -415,7 +419,13 @@ __device__ __forceinline__ void six_bits(const uint4& head, uint32_t (&sc)[4], u
 template <int QT, int TILES, class B>
 __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, int nsub, int lane, float (&acc)[TILES][4]) {
     const int t = lane & 3;
-    constexpr bool plain = zero_point(QT) == 0;         // codes as they are, subnormals: 2^-24 of them
+    // Codes as they are, subnormals, 2^(code_shift - 24) of them.  The tensor cores line products up by their exponents,
+    // and a subnormal's is the lowest whatever its leading bits: a sum loses as many of its last bits as there are zeros
+    // ahead of a code.  So codes and mins stand as high as shifts that are needed anyway leave them: two-bit codes in the lowest bits
+    // gave an error of 1.4e-5 of the output, four bits 3.3e-6.
+    constexpr bool plain = zero_point(QT) == 0;
+    constexpr float kCode = (float)(1 << (24 - code_shift(QT)));
+    constexpr int kMinUp = QT == GGUF_Q2_K ? 6 : 4;
     constexpr bool narrow = QT == GGUF_Q2_K || QT == GGUF_Q3_K || QT == GGUF_Q6_K;      // scales of 16 values
     const __half2 zero = __float2half2_rn(-(float)(1024 + zero_point(QT)));
     float total[TILES][4] = {};
@@ -445,8 +455,7 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
     auto scale = [&](int i, int j, int half) -> float {
         if constexpr (block32(QT)) return f16_low(r[i].d[j]);
         const int s = narrow ? 2 * j + half : j;
-        if constexpr (QT == GGUF_Q4_K) return byte_f(sc[i][s >> 2], s & 3, j & 1);        // its high nibbles are 16 times too large
-        return byte_f(sc[i][s >> 2], s & 3, false, QT == GGUF_Q6_K ? 128.f : QT == GGUF_Q3_K ? 32.f : 0.f);
+        return byte_f(sc[i][s >> 2], s & 3, QT == GGUF_Q6_K ? 128.f : QT == GGUF_Q3_K ? 32.f : 0.f);
     };
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -462,9 +471,9 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if constexpr (QT == GGUF_Q4_K) {
-                    const uint32_t w = r[i].w[j >> 1][half], m = j & 1 ? 0x00f000f0u : 0x000f000fu;
-                    a[i] = w & m;
-                    a[i + 2] = (w >> 8) & m;
+                    const uint32_t w = r[i].w[j >> 1][half], m = 0x00f000f0u;
+                    a[i] = (j & 1 ? w : w << 4) & m;
+                    a[i + 2] = (j & 1 ? w >> 8 : w >> 4) & m;
                 } else {
                     const uint32_t c = r[i].codes(j, half, t);
                     if constexpr (plain) {
@@ -494,7 +503,7 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
             }
         }
     }
-    if constexpr (plain) d[0] *= 0x1p24f, d[1] *= 0x1p24f;
+    if constexpr (plain) d[0] *= kCode, d[1] *= kCode;
 #pragma unroll
     for (int n = 0; n < TILES; ++n) {
         const float2 back = col.back(n);
@@ -508,13 +517,13 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
                     // mins are subnormals too, but those of the 32-value blocks, f16 numbers
                     if constexpr (QT == GGUF_Q2_K) {
                         const uint32_t two = (t < 2 ? mn[i][2 * k] : mn[i][2 * k + 1]) >> (16 * (t & 1));
-                        a[i] = (two & 0xffu) | (two & 0xff00u) << 8;
+                        a[i] = (two & 0xffu) << kMinUp | (two & 0xff00u) << (8 + kMinUp);
                     } else if constexpr (block32(QT)) {
                         // group 4k + t's m: no register is indexed by a lane
                         const uint32_t m = t < 2 ? (t ? r[i].d[4 * k + 1] : r[i].d[4 * k]) : (t == 2 ? r[i].d[4 * k + 2] : r[i].d[4 * k + 3]);
                         a[i] = 4 * k + t < nsub ? __byte_perm(m, 0u, 0x3232) : 0u;
                     } else {
-                        a[i] = ((mn[i][k] >> (8 * t)) & 0xffu) * 0x00010001u;
+                        a[i] = ((mn[i][k] >> (8 * t)) & 0xffu) * (0x00010001u << kMinUp);
                     }
                 }
                 const uint2 s = col.sums(n, k);         // the same mins with the sums' first part and their second
@@ -522,7 +531,8 @@ __device__ __forceinline__ void multiply(const Raw<QT> (&r)[2], const B& col, in
                 else mma(low, a[0], a[1], a[0], a[1], s.x, s.y);
             }
             // Q4_1, Q5_1 add their m
-            const float m0 = block32(QT) ? 1.f : -0x1p24f * dmin[0], m1 = block32(QT) ? 1.f : -0x1p24f * dmin[1];
+            constexpr float kMin = (float)(1 << (24 - kMinUp));
+            const float m0 = block32(QT) ? 1.f : -kMin * dmin[0], m1 = block32(QT) ? 1.f : -kMin * dmin[1];
             acc[n][0] = fmaf(fmaf(m0, low[0], d[0] * total[n][0]), back.x, acc[n][0]);
             acc[n][1] = fmaf(fmaf(m0, low[1], d[0] * total[n][1]), back.y, acc[n][1]);
             acc[n][2] = fmaf(fmaf(m1, low[2], d[1] * total[n][2]), back.x, acc[n][2]);

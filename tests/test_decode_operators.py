@@ -355,6 +355,18 @@ def test_ffn_formats(t, xdt, ydt):
     check_ffn(ex, 1, 4, xdt=xdt, ydt=ydt, residual=False, seed=3)
 
 
+@pytest.mark.parametrize("t", list(FORMATS))
+@pytest.mark.parametrize("xdt", ["bf16", "f32"])
+def test_ffn_error_by_norm(t, xdt):
+    """f32 outputs lie within 2**-20 of themselves by norm.  Some six stages round by at most 2**-22 of what they add up (an
+    activation and a hidden value to two f16 parts, the products' alignment, the sums that mins meet, the two sums), which
+    for codes centred by a min is about twice the values; apart from each other: 2**-22 * (6 * 2) ** 0.5 < 2**-20."""
+    ex = Experts((t, t, t), 512, 512, 4, seed=20)
+    x, ids, weights, _, y = run_ffn(ex, 4, 2, xdt=xdt, ydt="f32", residual=False, seed=21)
+    ref = S.moe_ffn(x, *ex.val, ids, weights, False, None)
+    assert np.linalg.norm(y - ref) <= 2.0 ** -20 * np.linalg.norm(ref)
+
+
 @pytest.mark.parametrize("types", [("Q4_K", "Q4_K", "Q6_K"), ("Q8_0", "Q5_1", "Q4_0"), ("Q2_K", "Q6_K", "Q3_K"), ("Q5_K", "Q8_0", "Q5_0"),
                                    ("Q4_1", "Q3_K", "Q4_K"), ("Q4_0", "Q2_K", "Q4_1")])
 def test_ffn_mixed_types(types):
