@@ -34,6 +34,10 @@
 // (A bulk copy of some 150 bytes holds its engine for about 19 cycles: with those
 // 64 tokens through Q4_K experts take 145 us and not 122, and without them three
 // tokens' Q6_K projection of 14336 takes 127 us and not 101.)
+//
+// Measured: one token through 8 of 128 experts of 2048 x 768 (Q4_K, Q6_K) 20.9 us, the three kernels' latency; 64 tokens
+// (Q4_K) 123 us, 2.4 TB/s, with three of five issue slots used, most by the integer instructions that take blocks
+// apart; three tokens through 2 of 8 experts of 4096 x 14336 213 us, 3.0 TB/s.
 #include <type_traits>
 
 #include "formats.cuh"
