@@ -28,7 +28,7 @@
 // distributions) and rows without a filter are read from L2 again instead.
 //
 // Measured: one row of 128259 with every filter 12.8 us, the latency of three passes and their meetings; 256 rows
-// of 131072 f32 with top-p 197 us (0.7 TB/s of logits), bound by the passes' instructions, 56 % of the issue slots.
+// of 131072 f32 with top-p 209 us (0.6 TB/s of logits), bound by the passes' instructions, 56 % of the issue slots.
 #include <type_traits>
 
 #include "serving.cuh"
@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
     // the tokens above the bounds, listed by warp in the row's order; the others' weights, for top-p
     bool listed = limit < INFINITY;
+    float above = -INFINITY;                         // what is below is not kept
     int chunks = seg >> 7;                           // of 128 tokens
     float* const list = s.value + warp * kList;
     uint16_t* const offs = s.offset + warp * kList;
@@ -316,13 +317,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         __syncthreads();                             // the warps' sums have been read
         const bool want_tail = use_p && !use_k;
         int n = 0;
-        // The others' weights, which are at most 2^-below, in units of 2^-(21 + below): an integer's sum is the same however
-        // the row is cut, and its rounding lies far below the weight of a token at the border.
+        // The others' weights, which are at most 2^-below: an integer's sum is the same however the row is cut.  Each goes into
+        // two, the first in units of 2^-(21 + below), the second in units 2^20 smaller with what rounding to the first has left.
+        // So a weight is off by 2^-(42 + below) beside its own f32 rounding, and those of a whole vocabulary of 2^22 by
+        // 2^-20 of a weight at the border.
         uint32_t rest = 0;
-        const int below = min((int)(limit * 0.0625f), 100);
-        const float unit = __uint_as_float((uint32_t)(127 + 21 + below) << 23), farthest = 300.f / ch;
+        int fine = 0;
+        const int below = min((int)(limit * 0.0625f), 80);
+        const float unit = __uint_as_float((uint32_t)(127 + 21 + below) << 23), unit2 = unit * 0x1p20f, farthest = 300.f / ch;
         // the same bound for the logits themselves, a little below
-        const float above = fmaxf(m - limit / bin_scale - 1e-6f * (fabsf(m) + limit / bin_scale), -3.402823466e38f);
+        above = fmaxf(m - limit / bin_scale - 1e-6f * (fabsf(m) + limit / bin_scale), -3.402823466e38f);
         each_four([&](float (&f)[4], int i) {
             bool in[4];
 #pragma unroll
@@ -330,8 +334,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 in[j] = f[j] >= above;
                 if (want_tail) {
                     const float dh = fmaxf(f[j] - m, -farthest);     // where the weight is 0, and dh * cl still a number
-                    const float w = fmaf(ex2(fmaf(dh, ch, dh * cl)), unit, 8388608.f);
-                    rest += in[j] ? 0u : __float_as_uint(w) - 0x4b000000u;
+                    const float w = in[j] ? 0.f : ex2(fmaf(dh, ch, dh * cl)), whole = fmaf(w, unit, 8388608.f);
+                    rest += __float_as_uint(whole) - 0x4b000000u;
+                    // 2^20 (2^23 - whole), exact, and 1.5 * 2^23 for the next one's integer
+                    const float less_whole = fmaf(whole, -0x1p20f, 0x1p43f + 12582912.f);
+                    fine += (int)(__float_as_uint(fmaf(w, unit2, less_whole)) - 0x4b400000u);
                 }
             }
             if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) return;
@@ -355,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             chunks = (n + 127) >> 7;
             for (int i = n + lane; i < 128 * chunks; i += 32) list[i] = -INFINITY, offs[i] = 0;
         }
-        // below 2^32 in a lane: at most 1028 tokens of 2^21 and a half
-        u64 sum = rest;
+        // below 2^32 in a lane: at most 1028 tokens of 2^21 and a half; of all tokens below 2^64, 2^22 of 2^41
+        u64 sum = ((u64)rest << 20) + (u64)(int64_t)fine;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) s.warp_sum[warp] = sum, atomicAdd(&s.listed, n <= kList ? (uint32_t)n : 1u << 24);
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         } else {
             load(i, v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) at[j] = first + i + 4 * lane + j;
+            for (int j = 0; j < 4; ++j) v[j] = v[j] >= above ? v[j] : -INFINITY, at[j] = first + i + 4 * lane + j;
         }
     };
     auto each = [&](auto&& f) {
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         } else {
             each_four([&](float (&v)[4], int i) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f(v[j], first + i + 4 * lane + j);
+                for (int j = 0; j < 4; ++j) f(v[j] >= above ? v[j] : -INFINITY, first + i + 4 * lane + j);
             });
         }
     };
@@ -725,16 +732,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         uint32_t n = 0;
         u64 others = 0;
         for (int b = 0; b < cluster; ++b) n += s.peer_listed[b], others += s.peer_tail[b];
-        // in weight()'s unit, 2^-46 / kTable's factor: others is below 2^45
-        const u64 part = __umul64hi(others << 17, (u64)(0.995 * 0.98922801319397548 * 0x1p64));
-        const int down = min((int)(limit * 0.0625f), 100) + less - 8;
+        // in weight()'s unit, 2^-46 / kTable's factor
+        const u64 part = __umul64hi(others, (u64)(0.995 * 0.98922801319397548 * 0x1p64));
+        const int down = min((int)(limit * 0.0625f), 80) + less - 5;
         tail = down >= 0 ? down < 64 ? part >> down : 0 : part << -down;
         if (n <= kCap) {
             gather([&](float, uint32_t, int) { return true; });
             if (rank == 0) finish(use_k ? (uint32_t)k : 0xffffffffu, 0, use_k ? 0 : tail);
             return;
         }
-        if (n >= 1u << 24) listed = false, chunks = seg >> 7, tail = 0;
+        // a list that is too long leaves the same tokens and the same rest to passes over the row
+        if (n >= 1u << 24) listed = false, chunks = seg >> 7;
         else if (limit < (float)kBins) fine_scale = bin_scale * ((float)(kBins - 1) / limit);
     } else if (use_k || by_share) {
         sync();                                              // every block has read the counts

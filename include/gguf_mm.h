@@ -482,7 +482,8 @@ typedef struct {
  * u [rows] f32 uniform in [0, 1) (below 0 and NaN count as 0; at 1 and above the
  * last token that passes is taken).  The weights are accurate to about 1e-9 of
  * the largest and their sums exact (top_p without top_k: the part of the sum
- * that it leaves out is accurate to about 1e-6 of itself), so that the token is the one
+ * that it leaves out is accurate to 4e-6 of itself and 1e-6 of the least likely
+ * token's weight that it keeps), so that the token is the one
  * that 64-bit arithmetic gives but where u or top_p falls that close to a border.
  *   logprob  f32 [rows] or NULL: log(w_token / sum of all w), 0 where the
  *            temperature is 0

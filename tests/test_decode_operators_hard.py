@@ -1,0 +1,95 @@
+"""The sampler, the router and the normed append where their arithmetic is at its ends, against the 64-bit definitions in
+oracle/serving_oracle.py.
+
+Which tokens top-p keeps shows in what u just below 1 draws where the likely tokens come first in the vocabulary and in
+falling order: the last one kept.  top_p is put next to a border between two sets, `gap` of the whole sum away from it, and
+rounded to f32, by 2**-25 of the sum at most; the expected token is that of the rounded number.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import gguf_quant_weight_gb300 as g
+from oracle import serving_oracle as S
+from tests import gpu_util as U
+from tests.test_decode_operators import check_sample, h64, run_sample
+from tests.test_serving import Case, near
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+LAST = 1 - 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    U.require_gpu()
+
+
+# ------------------------------------------------------------------ top-p: what lies far below the border
+
+def next_to_a_border(x, temp, j, gap):
+    """The top_p, as f32, `gap` of the sum beyond the weight of the first j tokens of the falling row x."""
+    w = np.exp((x.astype(np.float64) - float(x.max())) / temp)
+    return np.float32((np.sort(w)[::-1][:j].sum() + gap * w.sum()) / w.sum())
+
+
+@pytest.mark.parametrize("V", [131072, 262144, 1 << 20, 1 << 22])
+def test_sample_top_p_counts_a_flat_rest(V):
+    """Ten equal tokens over a flat rest of some percent, which no single token of shows."""
+    x = np.full(V, -15.388, np.float32)
+    at = np.sort(np.random.default_rng(V).permutation(V)[:10])
+    x[at] = 0
+    rest = (V - 10) * math.exp(-15.388)
+    x = torch.tensor(x, device=DEV).expand(3, V).contiguous()
+    check_sample(x, top_p=5.01 / (10 + rest), u=[0.07, 0.5, 0.9])       # six are kept, and five without the rest
+
+
+def test_sample_top_p_counts_a_flat_rest_of_two_tokens():
+    x = np.full(131072, -15.3, np.float32)
+    x[:2] = 0, -0.034
+    u = (np.arange(16) + 0.5) / 16
+    check_sample(torch.tensor(x, device=DEV).expand(16, -1).contiguous(), top_p=0.505, u=u)
+
+
+@pytest.mark.parametrize("V,rows,dt", [(131072, 40, "f32"), (131071, 12, "bf16"), (262144, 12, "f32"), (1 << 20, 5, "f16"), (1 << 22, 3, "f32")])
+def test_sample_top_p_over_a_bulk_far_below(V, rows, dt):
+    """A few dozen likely tokens over a bulk 15 to 20 nats lower.  The rest's weights are f32 numbers of arguments z (in bits)
+    with two roundings, up to 2**-23 z ln 2 + 2**-22 of themselves, below 4e-6 for z <= 45; the rest is a tenth of the sum at
+    most, so a gap of 1e-6 of the sum is further than what it may be off by."""
+    rs = np.random.default_rng(V)
+    x = np.empty((rows, V), np.float32)
+    temp, p = rs.choice([0.5, 1.0, 2.0], rows), np.empty(rows, np.float32)
+    for r in range(rows):
+        n = int(rs.integers(20, 60))
+        x[r] = (rs.standard_normal(V) * rs.uniform(0.2, 0.8) - rs.uniform(15, 20)) * temp[r]
+        x[r, :n] = np.sort(rs.standard_normal(n) * 0.8)[::-1] * temp[r]
+    x = torch.tensor(x, device=DEV).to(U.TORCH_DT[dt])
+    host = x.float().cpu().numpy()
+    for r in range(rows):
+        w = np.exp((host[r].astype(np.float64) - host[r].max()) / temp[r])
+        assert 1e-7 < np.sort(w)[:-60].sum() / w.sum() < 0.1
+        p[r] = next_to_a_border(host[r], temp[r], int(rs.integers(3, 18)), float(rs.choice([-1e-6, 1e-6])))
+    check_sample(x, temp=temp, top_p=p, u=np.full(rows, LAST))
+
+
+@pytest.mark.parametrize("depth", [15.0, 15.4])
+def test_sample_top_p_where_one_cut_overflows_its_lists(depth):
+    """A thousand neighbours near the top: more than a warp lists where few blocks share a row, and not where many do."""
+    rs = np.random.default_rng(5)
+    V, rows = 32003, 200
+    x = np.full((rows, V), -depth, np.float32)
+    x[:, :1000] = np.linspace(0, -0.02, 1000)
+    p = np.array([next_to_a_border(x[r], 1.0, int(rs.integers(100, 900)), float(rs.choice([-1e-6, 1e-6]))) for r in range(rows)])
+    x = torch.tensor(x, device=DEV)
+    f = lambda a: torch.tensor(a, dtype=torch.float32, device=DEV)      # noqa: E731
+    u = np.full(rows, LAST)
+    many, lp = run_sample(x, g.gguf_sampler(None, None, f(p)), f(u))
+    for r in range(0, rows, 9):
+        one, l1 = run_sample(x[r:r + 1].clone(), g.gguf_sampler(None, None, f(p[r:r + 1])), f(u[r:r + 1]))
+        assert one[0] == many[r] and l1[0] == lp[r]
+    keep = slice(0, 30)
+    check_sample(x[keep].contiguous(), top_p=p[keep], u=u[keep])
+    want = [S.sample(x[r].double().cpu().numpy(), 1.0, 0, float(np.float32(p[r])), 0.0, float(u[r]))[0] for r in range(0, rows, 10)]
+    assert np.array_equal(many[::10], want)
