@@ -297,8 +297,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             const uint32_t before = upto - n[0] - n[1];
             if (before < (uint32_t)k && upto >= (uint32_t)k) s.bin = 2 * tid + (before + n[0] < (uint32_t)k ? 1 : 0);
         } else {
-            // a share r of weights known to 2.2 % either way is off by at most 0.0434 r (1 - r)
-            const float share = fmaxf(top_p, 0.f), goal = (share + 0.0435f * share * (1.f - share)) * all, before = mass - w0 - w1;
+            // Weights stand for themselves to a factor 2^(1/32) either way.  So where tokens have the share r, the bins up to
+            // theirs have at most r q / (r q + 1 - r), q = 2^(1/16) = 1.04427.  1.0444 covers the rounding of a token's place in
+            // the bins and the rest's (1e-5 and 4e-6 of the ratio of the two parts), 4e-6 that of these sums, some 25 operations deep.
+            const float share = fmaxf(top_p, 0.f), heavy = 1.0444f * share, goal = heavy / (heavy + 1.f - share) * 1.000004f * all, before = mass - w0 - w1;
             if (before < goal && mass >= goal) s.bin = 2 * tid + (before + w0 < goal ? 1 : 0);
         }
         __syncthreads();

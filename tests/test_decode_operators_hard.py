@@ -93,3 +93,23 @@ def test_sample_top_p_where_one_cut_overflows_its_lists(depth):
     check_sample(x[keep].contiguous(), top_p=p[keep], u=u[keep])
     want = [S.sample(x[r].double().cpu().numpy(), 1.0, 0, float(np.float32(p[r])), 0.0, float(u[r]))[0] for r in range(0, rows, 10)]
     assert np.array_equal(many[::10], want)
+
+
+# ------------------------------------------------------------------ top-p: weights at the edges of a bin
+
+@pytest.mark.parametrize("share", [0.0099, 0.05, 0.1, 0.2, 0.3, 0.5, 0.8])
+@pytest.mark.parametrize("n", [100, 299, 1500])
+def test_sample_top_p_between_the_edges_of_two_bins(share, n):
+    """The likely tokens at the far edge of the first sixteenth of a bit, the others at the near edge of the next: counted by
+    sixteenths, the first look heavier than they are and the others lighter.  One of the others is kept."""
+    others = int(n / share)
+    x = np.empty(1 + n + others, np.float32)
+    x[0], x[1:n + 1], x[n + 1:] = 0, -0.99995 / 16 * math.log(2), -1.00005 / 16 * math.log(2)
+    p = next_to_a_border(x, 1.0, 1 + n, 1e-6)
+    check_sample(torch.tensor(x, device=DEV)[None].contiguous(), top_p=p, u=[LAST])
+
+
+def test_sample_top_p_at_the_edge_of_a_bin_in_a_long_row():
+    x = np.empty(101002, np.float32)
+    x[0], x[1:1001], x[1001:] = 0, -0.99995 / 16 * math.log(2), -1.00005 / 16 * math.log(2)
+    check_sample(torch.tensor(x, device=DEV)[None].contiguous(), top_p=0.009914, u=[LAST])
