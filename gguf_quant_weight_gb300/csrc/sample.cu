@@ -227,11 +227,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     const float bin_scale = 16.f * (greedy ? 1.4426950f : fminf(ch, 1e36f));
     float fine_scale = bin_scale;                    // of the histograms: all bins for what is listed
     const int less = V > (1 << 18) ? 32 - __clz(V - 1) - 18 : 0;         // V weights below 2^46 stay below 2^64
+    const float last_grid = 393216.f + 46.f - max(less, 1);               // at most 63 bits are shifted off
 
     auto weight = [&](float v) -> u64 {
         const float dh = m - v, bb = dh - m, dl = (m - (dh - bb)) - (v + bb);          // m - v = dh + dl exactly
         const float grid = __fmaf_rn(dh, ch, 393216.f);  // 1.5 * 2^18: its last bit stands for 1 / 32
-        if (!(grid < 393216.f + 45.f)) return 0;
+        if (!(grid < last_grid)) return 0;
         const float f = __fmaf_rn(dl, ch, __fmaf_rn(dh, cl, __fmaf_rn(dh, ch, -__fsub_rn(grid, 393216.f))));
         const float e = f * fmaf(f, fmaf(f, fmaf(f, 0.0096181291f, -0.055504109f), 0.24022651f), -0.69314718f);    // 2^-f - 1
         const uint32_t bits = __float_as_uint(grid), t = s.table[(bits & 31u) * 32 + lane];

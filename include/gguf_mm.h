@@ -480,8 +480,10 @@ typedef struct {
  * the filters, the first i in the order of the vocabulary with
  *   w_0 + ... + w_i > u[r] * (sum of all w),
  * u [rows] f32 uniform in [0, 1) (below 0 and NaN count as 0; at 1 and above the
- * last token that passes is taken).  The weights are accurate to about 1e-9 of
- * the largest and their sums exact (top_p without top_k: the part of the sum
+ * last token that passes and has a weight is taken).  The weights are accurate to
+ * about 1e-9 of themselves and 2^-45 of the largest (2^-41 in vocabularies above
+ * 2^18; what is below, or further from the largest logit than f32's largest
+ * number, has none) and their sums exact (top_p without top_k: the part of the sum
  * that it leaves out is accurate to 4e-6 of itself and 1e-6 of the least likely
  * token's weight that it keeps), so that the token is the one
  * that 64-bit arithmetic gives but where u or top_p falls that close to a border.

@@ -113,3 +113,14 @@ def test_sample_top_p_at_the_edge_of_a_bin_in_a_long_row():
     x = np.empty(101002, np.float32)
     x[0], x[1:1001], x[1001:] = 0, -0.99995 / 16 * math.log(2), -1.00005 / 16 * math.log(2)
     check_sample(torch.tensor(x, device=DEV)[None].contiguous(), top_p=0.009914, u=[LAST])
+
+
+# ------------------------------------------------------------------ weights at the end of their integers
+
+@pytest.mark.parametrize("V", [1 << 20, 1 << 22])
+@pytest.mark.parametrize("kw", [dict(), dict(top_p=0.9999), dict(top_k=1000), dict(min_p=1e-13)])
+def test_sample_tokens_at_the_last_bits(V, kw):
+    """Tokens 40 to 47 bits below the largest, where integers of so large a vocabulary end."""
+    x = -torch.linspace(40, 47, V, device=DEV) * math.log(2)
+    x[V // 3] = 0
+    check_sample(x.expand(2, V).contiguous(), u=[0.0, 0.99999], **kw)
