@@ -248,18 +248,22 @@ __global__ void __launch_bounds__(kThreads) moe_router_kernel(const RouterParams
         const int t = t0 + k;
         if (t >= p.T) break;
         const float* z = s_z + k / cluster * E4;
-        // the largest score and |W[e]|, and the softmax's sum: every warp for itself
+        // the largest score and |W[e]|, and the softmax's sum where it is asked for: every warp for itself
         float m = -INFINITY, ww = 0.f, sum = 0.f;
         for (int e = lane; e < E; e += 32) m = fmaxf(m, z[e]), ww = fmaxf(ww, s_ww[e]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o)), ww = fmaxf(ww, __shfl_xor_sync(0xffffffffu, ww, o));
-        if (soft) {
+        if (soft && (p.bias || !p.renormalize)) {
             for (int e = lane; e < E; e += 32) sum += expf(z[e] - m);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
-        auto prob = [&](float v) { return soft ? expf(v - m) / sum : 1.f / (1.f + expf(-v)); };
+        // (a sigmoid's exponential overflows nowhere)
+        auto prob = [&](float v) {
+            const float e = expf(soft ? v - m : -fabsf(v));
+            return soft ? e / sum : (v < 0.f ? e : 1.f) / (1.f + e);
+        };
         // without a bias the scores themselves have the order
         auto rank_of = [&](int e) { return p.bias ? prob(z[e]) + p.bias[e] : z[e]; };
         // A score's error: a lane's every other product in a row, the two halves, the lanes'.  A
@@ -363,7 +367,23 @@ __global__ void __launch_bounds__(kThreads) moe_router_kernel(const RouterParams
             }
             __syncthreads();
         }
-        if (tid < top_k) s_p[tid] = prob(z[s_id[tid]]);
+        // Where only the chosen experts' shares count, p is scaled by what makes the largest of them 1 or near it: it may be
+        // far below f32's range (sigmoids of very negative scores, a softmax whose largest score a bias shuts out).
+        float best = z[s_id[0]];
+        if (p.renormalize && p.bias) {                   // not the first: every warp looks at them all
+            uint32_t key = lane < top_k ? ordered(z[s_id[lane]]) : 0u;
+            if (lane + 32 < top_k) key = max(key, ordered(z[s_id[lane + 32]]));
+            key = __reduce_max_sync(0xffffffffu, key);
+            best = __uint_as_float(key >> 31 ? key & 0x7fffffffu : ~key);
+        }
+        if (tid < top_k) {
+            const float v = z[s_id[tid]];
+            if (p.renormalize) {
+                s_p[tid] = soft ? expf(v - best) : expf(fminf(v, 0.f) - fminf(best, 0.f)) / (1.f + expf(-fabsf(v)));
+            } else {
+                s_p[tid] = prob(v);
+            }
+        }
         __syncthreads();
         if (tid < top_k) {
             float v = s_p[tid];

@@ -124,3 +124,63 @@ def test_sample_tokens_at_the_last_bits(V, kw):
     x = -torch.linspace(40, 47, V, device=DEV) * math.log(2)
     x[V // 3] = 0
     check_sample(x.expand(2, V).contiguous(), u=[0.0, 0.99999], **kw)
+
+
+# ------------------------------------------------------------------ router: weights of small scores
+
+def router_of(z):
+    """A router and a token whose scores are z, exactly (multiples of 1/64 below 2**10, each from one product)."""
+    z = np.asarray(z, np.float64)
+    assert np.array_equal(z, np.round(z * 64) / 64) and np.abs(z).max() < 1024
+    w = np.zeros((len(z), 8), np.float32)
+    w[np.arange(len(z)), 0] = z
+    x = torch.zeros((1, 8), device=DEV)
+    x[0, 0] = 1
+    return x, torch.tensor(w, device=DEV)
+
+
+def check_exact_scores(z, top_k, sigmoid, bias, renorm, scale=1.0):
+    """Scores are exact here, so weights are off by two exponentials (2 units of 2**-23 each), a sum of top_k (or of all
+    experts) positive terms, a quotient and two products: 2**-19 of themselves; 8 of
+    the smallest f32 where exponentials (2 of them, times scale) and quotients are subnormal."""
+    x, w = router_of(z)
+    b = None if bias is None else torch.tensor(np.asarray(bias), dtype=torch.float32, device=DEV)
+    ids, weights = torch.empty((1, top_k), dtype=torch.int32, device=DEV), torch.empty((1, top_k), device=DEV)
+    g.gguf_moe_router(x, 0, 1, 8, g.gguf_router(w, top_k, int(sigmoid), b, renorm, scale), ids, weights)
+    assert g.gguf_mm_check_errors() == 0
+    ri, rw = S.router(x.double().cpu().numpy(), w.double().cpu().numpy(), None if b is None else b.double().cpu().numpy(), top_k,
+                      sigmoid, renorm, scale)
+    assert np.array_equal(ids.cpu().numpy(), ri)
+    got = weights.double().cpu().numpy()
+    assert np.all(np.abs(got - rw) <= 2.0 ** -19 * np.abs(rw) + 2.0 ** -146), (got, rw)
+
+
+def scores(n, at, spread, seed):
+    return at + np.round(np.random.default_rng(seed).uniform(-spread, spread, n) * 64) / 64
+
+
+@pytest.mark.parametrize("at", [-60, -87, -88, -95, -103, -200, -690])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_router_sigmoids_of_very_negative_scores(at, biased, renorm):
+    z = scores(40, at, 5, 1)
+    check_exact_scores(z, 6, True, np.random.default_rng(2).standard_normal(40) if biased else None, renorm, 2.5)
+
+
+@pytest.mark.parametrize("above", [20, 87, 95, 104, 150, 600])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_router_softmax_beside_an_expert_that_is_shut_out(above, renorm):
+    """The softmax goes over all experts, the weights' sum over the chosen: a shut-out expert far above leaves them their digits."""
+    z, b = scores(30, 0, 3, 3), np.zeros(30)
+    z[7], b[7] = above, -math.inf
+    check_exact_scores(z, 5, False, b, renorm)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_router_weights_of_scores_far_apart(sigmoid):
+    for at in (-150, -40, 0, 40):
+        z = scores(24, at, 3, 4)
+        z[::5] -= 30
+        b = np.random.default_rng(6).standard_normal(24)
+        for bias in (None, b):
+            check_exact_scores(z, 24, sigmoid, bias, True)
