@@ -4,13 +4,14 @@
 //   the top_k experts of the largest p (+ bias), the lower index first among
 //   equals;  weights p of those, divided by their sum if asked, times scale.
 //
-// Which experts a token takes is decided exactly.  The products are summed in
+// Which experts a token takes is decided to twice f32's digits.  The products are summed in
 // f32, whose error is at most n 2^-24 |x| |W[e]| (n additions deep, norms by
 // Cauchy and Schwarz).  Where two
 // neighbours in the order lie closer than that allows, the scores of the experts
 // that could be among the first top_k are computed again with compensated sums
-// (the exact products' and additions' rounding errors carried along, as good as
-// twice the digits) and ordered by those in double.  That meets about one token in a
+// (the exact products' and additions' rounding errors carried along in a second
+// float: off by n^2 2^-48 of the n = K / 32 magnitudes that a lane adds up) and
+// ordered by those in double.  That meets about one token in a
 // hundred; going through all products with compensated sums would cost nine
 // operations for one.
 //
@@ -266,10 +267,11 @@ __global__ void __launch_bounds__(kThreads) moe_router_kernel(const RouterParams
         };
         // without a bias the scores themselves have the order
         auto rank_of = [&](int e) { return p.bias ? prob(z[e]) + p.bias[e] : z[e]; };
-        // A score's error: a lane's every other product in a row, the two halves, the lanes'.  A
-        // sigmoid's slope is a quarter; a softmax's p moves by twice the scores' error times p.
-        const float deep = (float)(K / 64 + 10);
-        const float err = deep * 0x1p-24f * sqrtf(s_xx[k]) * sqrtf(ww) * 1.01f;
+        // A score's error: a lane's every other product in a row, the two halves, the lanes'; what products and squares lose
+        // that are subnormal, at most 2^-150 each.  A sigmoid's slope is a quarter; a softmax's p moves by twice the scores'
+        // error times p.
+        const float deep = (float)(K / 64 + 10), lost = (float)K * 0x1p-149f;
+        const float err = fmaf(deep * 0x1p-24f * sqrtf(s_xx[k] + lost), sqrtf(ww + lost) * 1.01f, lost);
         const float off = !p.bias ? 2.f * err : soft ? 4.f * err / sum : 0.5f * err;    // of two ranks
         auto slack = [&](float a, float b) { return p.bias ? off + 0x1p-20f * (fabsf(a) + fabsf(b) + 1.f) : off; };
         for (int e = tid; e < E4; e += kThreads) s_key[e] = e < E ? ordered(rank_of(e)) : 0u, s_before[e] = 0;

@@ -528,8 +528,10 @@ typedef struct {
 /* The experts of each token: scores x [T][K] (of xdt: F32, F16 or BF16) . w^T,
  * the top_k of the largest p + bias in falling order, the lower index first among equals:
  *   ids [T][top_k] int32,  weights [T][top_k] f32.
- * The choice and its order are those of 64-bit arithmetic; weights are accurate
- * to f32's rounding, of scores that are neither beyond f32's range nor made of
+ * The choice and its order are those of scores computed to twice f32's digits
+ * (to (K / 32)^2 2^-48 of |x| |w[e]|) and compared in 64 bits; without a bias the
+ * scores themselves are compared.  Weights are those of f32 scores, accurate to
+ * f32's rounding of those.  Both of scores that are neither beyond f32's range nor made of
  * products below it.  A bias of -inf shuts an expert out: it comes after all others.
  * A token with a score that is not finite gets top_k different
  * experts all the same, and weights that may be NaN.  K a multiple of

@@ -184,3 +184,20 @@ def test_router_weights_of_scores_far_apart(sigmoid):
         b = np.random.default_rng(6).standard_normal(24)
         for bias in (None, b):
             check_exact_scores(z, 24, sigmoid, bias, True)
+
+
+# ------------------------------------------------------------------ router: the order of small scores
+
+@pytest.mark.parametrize("power", [-60, -80, -90])
+@pytest.mark.parametrize("side", ["x", "w"])
+def test_router_orders_small_scores_that_f32_cannot_tell(power, side):
+    """Families of copies whose values differ in their last bits, of activations or weights whose squares f32 does not hold."""
+    rs = np.random.default_rng(7)
+    x, w = rs.standard_normal((20, 2048)).astype(np.float32), (rs.standard_normal((64, 2048)) / 45).astype(np.float32)
+    for e in range(16, 64):
+        w[e] = w[e % 16] * (1 + rs.integers(-2, 3, 2048) * 2.0 ** -23)
+    x, w = (x * np.float32(2.0 ** power), w) if side == "x" else (x, w * np.float32(2.0 ** power))
+    ids, weights = torch.empty((20, 12), dtype=torch.int32, device=DEV), torch.empty((20, 12), device=DEV)
+    g.gguf_moe_router(torch.tensor(x, device=DEV), 0, 20, 2048, g.gguf_router(torch.tensor(w, device=DEV), 12), ids, weights)
+    ri, _ = S.router(x.astype(np.float64), w.astype(np.float64), None, 12, False, True, 1.0)
+    assert np.array_equal(ids.cpu().numpy(), ri)
