@@ -200,15 +200,15 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
     }
 }
 
-// The same for positions below 2^24, which are floats, without doubles (of which an SM does two a cycle): the frequency in
-// turns in two floats, and what the product's rounding leaves by a second product.  Off by 2^-46 of the turns and by
-// two roundings of a part below one half, 2^-24 of a turn.  (48 mixed sequences: 9.7 us with doubles, 9.2 so.)
+// The same for positions below 2^24, which are floats, and angles below 2^22 turns, without doubles (of which an SM does two a
+// cycle): the frequency in turns in two floats, and what the product's rounding leaves by a second product.  Off by 2^-46 of
+// the turns and by two roundings of a part below one half, 2^-24 of a turn.  (48 mixed sequences: 9.7 us with doubles, 9.2 so.)
 __device__ __forceinline__ void near_angle(const AppendParams& p, int t, int pos, int i, float& cos, float& sin) {
     const int at = p.positions ? p.positions[t] : pos;
-    if (abs(at) >= 1 << 24) return angle(p, t, pos, i, cos, sin);
     constexpr float kHigh = 0.15915494f, kLow = 6.4206383e-9f;      // 1 / (2 pi)
     const float f = p.freqs[i], high = __fmul_rn(f, kHigh), low = __fmaf_rn(f, kHigh, -high) + f * kLow;
     const float a = (float)at, turns = __fmul_rn(a, high), rest = __fmaf_rn(a, high, -turns) + a * low;
+    if (!(fabsf(a) < 0x1p24f && fabsf(turns) < 0x1p22f)) return angle(p, t, pos, i, cos, sin);
     float sn, cs;
     sincospif(2.f * ((turns - rintf(turns)) + rest), &sn, &cs);
     cos = cs * p.rope_scale;

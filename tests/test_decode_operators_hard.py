@@ -201,3 +201,37 @@ def test_router_orders_small_scores_that_f32_cannot_tell(power, side):
     g.gguf_moe_router(torch.tensor(x, device=DEV), 0, 20, 2048, g.gguf_router(torch.tensor(w, device=DEV), 12), ids, weights)
     ri, _ = S.router(x.astype(np.float64), w.astype(np.float64), None, 12, False, True, 1.0)
     assert np.array_equal(ids.cpu().numpy(), ri)
+
+
+# ------------------------------------------------------------------ normed append: angles
+
+@pytest.mark.parametrize("style", [0, 1])
+@pytest.mark.parametrize("freqs", ["rope", "near 1", "large"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_append_norm_far_and_given_positions(style, freqs, dt):
+    """Angles are good to 2**-24 of a turn, 2 pi 2**-24, twice where f64 takes over, cos and sin to 2 units of 2**-23 and the turn
+    to 3 roundings; the norm of 16 values to (16 / 2 + 4) * 2**-24: below 32 * 2**-24 of |a| + |b| <= 2 max |x|."""
+    rs = np.random.default_rng(8)
+    D, heads, KV = 16, 24, 8
+    f = {"rope": 10000.0 ** (-np.arange(8) / 8), "near 1": 1 - np.arange(8) / 77, "large": np.geomspace(3, 100, 8)}[freqs].astype(np.float32)
+    lowest = -2 ** 31
+    at = np.array([0, 1, -1, 2 ** 24 - 1, 2 ** 24, 2 ** 24 + 1, 1 - 2 ** 24, -2 ** 24, -2 ** 24 - 1, lowest, lowest + 1, 2 ** 31 - 1,
+                   9999999, -9999999, 123456789, 4095, 131071, 1048575, -7, 16000001], np.int32)
+    if freqs == "large":        # of farther ones f64 keeps too few digits
+        at = np.clip(at, -2 ** 24 - 1, 2 ** 24 + 1)
+    T = len(at)
+    c = Case([(T, T)], KV, D, dt, seed=1)
+    q, k, v = (c.values((T, h, D), "f32") for h in (heads, KV, KV))
+    wq, wk = (torch.tensor(1 + 0.3 * rs.standard_normal(D), dtype=torch.float32, device=DEV) for _ in range(2))
+    out = torch.empty((T, heads, D), dtype=U.TORCH_DT[dt], device=DEV)
+    kc, vc = h64(c.k), h64(c.v)
+    rope = g.gguf_rope(torch.tensor(f, device=DEV), D, style, 1.0, torch.tensor(at, device=DEV))
+    g.gguf_kv_append_norm(q, heads * D, k, KV * D, v, KV * D, 0, heads, g.gguf_head_norm(wq, wk), rope, c.batch(),
+                          g.gguf_kv_cache(c.k, c.v), out, heads * D)
+    assert g.gguf_mm_check_errors() == 0
+    nq, nk = S.head_norm(h64(q), h64(wq), 1e-6), S.head_norm(h64(k), h64(wk), 1e-6)
+    qo, kc, vc = S.append(nq, nk, h64(v), f, D, style, 1.0, c.q_start, c.kv_len, c.pages, kc, vc, at)
+    u = 32 * 2.0 ** -24 * 2
+    near(h64(out), qo, dt, u * np.abs(nq).max(-1, keepdims=True), "q")
+    near(h64(c.k), kc, dt, u * np.abs(nk).max(), "k")
+    near(h64(c.v), vc, dt, 0.0, "v")
