@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
 
 // The same for positions below 2^24, which are floats, and angles below 2^22 turns, without doubles (of which an SM does two a
 // cycle): the frequency in turns in two floats, and what the product's rounding leaves by a second product.  Off by 2^-46 of
-// the turns and by two roundings of a part below one half, 2^-24 of a turn.  (48 mixed sequences: 9.7 us with doubles, 9.2 so.)
+// the turns and by two roundings of a part below one half, 2^-24 of a turn.  (48 mixed sequences: 10.1 us with doubles, 9.5
+// so; 9,600 tokens 55.1 and 52.5.)
 __device__ __forceinline__ void near_angle(const AppendParams& p, int t, int pos, int i, float& cos, float& sin) {
     const int at = p.positions ? p.positions[t] : pos;
     constexpr float kHigh = 0.15915494f, kLow = 6.4206383e-9f;      // 1 / (2 pi)

@@ -32,10 +32,10 @@
 // boundary (Q4_K, Q5_K) the lanes copy 16 bytes each; where they do not, which
 // costs the lanes the arithmetic of every row's offset, one bulk copy moves a row.
 // (A bulk copy of some 150 bytes holds its engine for about 19 cycles: with those
-// 64 tokens through Q4_K experts take 145 us and not 122, and without them three
-// tokens' Q6_K projection of 14336 takes 127 us and not 101.)
+// 64 tokens through Q4_K experts take 167 us and not 123.  Before the codes were moved up
+// in their subnormals, lanes' own copies made three tokens' Q6_K projection of 14336 take 127 us and not 101.)
 //
-// Measured: one token through 8 of 128 experts of 2048 x 768 (Q4_K, Q6_K) 20.9 us, the three kernels' latency; 64 tokens
+// Measured: one token through 8 of 128 experts of 2048 x 768 (Q4_K, Q6_K) 20.7 us, the three kernels' latency; 64 tokens
 // (Q4_K) 123 us, 2.4 TB/s, with three of five issue slots used, most by the integer instructions that take blocks
 // apart; three tokens through 2 of 8 experts of 4096 x 14336 213 us, 3.0 TB/s.
 #include <type_traits>
@@ -1096,26 +1096,32 @@ int moe_ffn_launch(MoeFfnParams p, void* workspace, int num_sms, int pdl, cudaSt
     p.column_scales = reinterpret_cast<float*>(p.columns + column_bytes(entries, p.F));
     p.routes = reinterpret_cast<uint8_t*>(p.column_scales) + scale_bytes(entries, p.F);
     p.x_parts = p.xdt == GGUF_DT_F32 ? 2 : 1;           // the 16-bit types' values are f16 numbers, scaled
-    // the hidden values' rounding to f16 is below what a bf16 output rounds, and would not be below an f16 output's
+    // the hidden values' rounding to f16 is below what a bf16 output rounds, and would not be below an f16 output's (two columns
+    // for bf16 as well: 64 tokens through 8 of 128 experts 133 us and not 123, 64 rows of each of 8 experts 150 and not 107; the
+    // error against 64 bits is bf16's own, 1.7e-3 by norm, either way)
     p.h_parts = p.ydt == GGUF_DT_BF16 ? 1 : 2;
     const size_t routes = Routes::bytes(entries);
 
     // up: two tiles of columns where the experts have 48 columns and more each, by the mean, and there is room for two
     // pieces to a warp beside them.  A second tile saves taking the blocks apart again, and leaves half as many jobs to
-    // share out, each with more to add up at its end.  2048 x 768 through 8 experts, one tile / two: 16 columns each 36 /
-    // 45 us, 32 60 / 63, 64 106 / 104, 64 of Q5_0 and Q5_1 142 / 123; 4 each of 128 experts 119 / 123.
+    // share out, each with more to add up at its end.  2048 x 768 through 8 experts, one tile / two: 16 columns each 37 /
+    // 46 us, 32 61 / 65, 64 109 / 108, 64 of Q5_0 and Q5_1 142 / 124; 4 each of 128 experts 123 / 127.
     const int64_t chunks = ceil_div(p.K, kChunk);
     p.up_slot = std::max(slot_bytes(p.gate_type), slot_bytes(p.up_type));
     auto fixed = [&](int64_t held, int tiles) { return routes + (size_t)(held * tiles * (kTileBytes + 32) + 2 * kWarps * 128 * tiles * 4); };
     auto stages = [&](size_t used, size_t slot) { return used > kSmem ? 0 : (int)std::min<size_t>(kMaxStages, (kSmem - used) / (kWarps * slot)); };
     p.up_tiles = entries * p.x_parts >= 48 * std::min(entries, p.n_expert) && stages(fixed(chunks, 2), p.up_slot) >= 2 ? 2 : 1;
+    // The columns of all of K stay in shared memory while one piece a warp still fits: making them again for every job costs
+    // more than a ring of one piece.  8 tokens through 2 of 8 experts of K x 2048, held / one chunk a warp at a time with two or
+    // three pieces: Q6_K, 5120 108 / 173 us, 7168 133 / 225, 8192 155 / 261; Q8_0, 5120 110 / 163, 7168 135 / 213; Q5_K, 7168
+    // 99 / 193; Q4_K, 8192 106 / 211.  One token, Q6_K: 38 / 41, 45 / 50, 52 / 57.
     p.up_resident = stages(fixed(chunks, p.up_tiles), p.up_slot) >= 1;
     const size_t up_fixed = fixed(p.up_resident ? chunks : kWarps, p.up_tiles);
     p.up_stages = stages(up_fixed, p.up_slot);
     // what making the routes takes is shared with the columns and the ring
     const size_t up_smem = std::max(up_fixed + (size_t)kWarps * p.up_stages * p.up_slot, routes + routes_scratch(entries, p.n_expert));
-    // Few jobs, larger teams: one token's one expert of 2048 x 768 takes 12.9 us with teams of 4 warps, 12.0 with 16;
-    // 64 tokens through 8 of 128 experts take 138 us with teams of 16, 122 with 4.
+    // Few jobs, larger teams: one token's one expert of 2048 x 768 takes 13.3 us with teams of 4 warps, 12.6 with 16;
+    // 64 tokens through 8 of 128 experts take 139 us with teams of 16, 123 with 4.
     const int64_t jobs = ceil_div(p.F, 16) * std::min(entries, p.n_expert);
     p.up_wp = jobs <= num_sms ? 8 : jobs <= 2 * num_sms ? 4 : 2;
     while (p.up_wp > chunks) p.up_wp /= 2;
@@ -1129,8 +1135,9 @@ int moe_ffn_launch(MoeFfnParams p, void* workspace, int num_sms, int pdl, cudaSt
     if (st != GGUF_OK) return st;
 
     // down: with few experts, several warps share one's chunks, so that each warp has some three shares to take, as
-    // far as there is room for their sums and two pieces to a warp (three tokens through 14336 x 4096: 289 us with one
-    // warp to an expert's row tile, 208 so; 64 tokens through 8 of 128 experts: 122 either way)
+    // far as there is room for their sums and two pieces to a warp (three tokens through 14336 x 4096: 299 us with one
+    // warp to an expert's row tile, 213 so; 64 tokens through 8 of 128 experts: 123 either way; 64 rows of each of 8 experts: 97 with
+    // one, 107 so)
     const size_t slot = slot_bytes(p.down_type), one = (size_t)entries * 16 * 4, down_fixed = routes + (entries + 3) / 4 * 16;
     const int64_t room = ((int64_t)kSmem - (int64_t)down_fixed - (int64_t)(kWarps * 2 * slot)) / (int64_t)one;
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(3 * kWarps, std::min(entries, p.n_expert)), fchunks, room}));

@@ -28,7 +28,7 @@
 // distributions) and rows without a filter are read from L2 again instead.
 //
 // Measured: one row of 128259 with every filter 12.8 us, the latency of three passes and their meetings; 256 rows
-// of 131072 f32 with top-p 209 us (0.6 TB/s of logits), bound by the passes' instructions, 56 % of the issue slots.
+// of 131072 f32 with top-p 210 us (0.6 TB/s of logits), bound by the passes' instructions, 56 % of the issue slots.
 #include <type_traits>
 
 #include "serving.cuh"
@@ -779,8 +779,9 @@ cudaError_t launch(const SampleParams& p, int num_sms, int pdl, cudaStream_t s) 
     cudaError_t e = set_once(sample_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared), done);
     if (e != cudaSuccess) return e;
     // up to 2175 tokens a warp, of which its list holds two fifths; more blocks
-    // to a row where there are few rows.  Always as many blocks as there may be: 37 rows of 32003 take 29.6 us and not 23.1,
-    // 256 of 131072 238 and not 197; only what the lists ask for: 38.6 us, and one row of 128259 16.0 and not 12.8.
+    // to a row where there are few rows.  Always as many blocks as there may be: 37 rows of 32003 take 31.5 us and not 26.1,
+    // 256 of 131072 242 and not 215; only what the lists ask for: 47 us, and one row of 128259 16.4 and not 13.0.  152064
+    // tokens, 2385 a warp with four blocks: 64 rows take 129 us so and 84 with eight, 256 rows 229 and 250.
     const int64_t span = p.vocab + 3;
     int cluster = 1;
     while (cluster < 8 && (span > cluster * (int64_t)(kWarps * 2175) || (p.rows * cluster * 2 <= num_sms && span > cluster * 2048))) cluster *= 2;
