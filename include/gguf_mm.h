@@ -389,10 +389,11 @@ typedef struct {
 
 /* gguf_kv_append with the heads of q and k normed first, in the same pass: the
  * sum of squares, the norm and the rotation are computed in f32 (a head's sum of
- * squares has to be within its range) and each value is rounded once; angles are good to 2^-24 of a turn, or where they are beyond
- * 2^22 turns to f64's product.  All other arguments, the rules for tokens out of range and
- * the errors as gguf_kv_append; norm may not be NULL (INVALID_ARG), and where q
- * is NULL norm->q is not read. */
+ * squares has to be within its range) and each value is rounded once; angles are
+ * good to 2^-24 of a turn, or where they are beyond 2^22 turns to f64's product.
+ * All other arguments, the rules for tokens out of range and the errors as
+ * gguf_kv_append; norm may not be NULL (INVALID_ARG), and where q is NULL norm->q
+ * is not read. */
 int gguf_kv_append_norm(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv, int xdt,
                         int64_t heads, const gguf_head_norm* norm, const gguf_rope* rope, const gguf_kv_batch* batch,
                         const gguf_kv_cache* cache, void* q_out, int64_t ldqo, gguf_stream_t stream);
